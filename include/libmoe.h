@@ -317,6 +317,109 @@ moe_status_t moe_router_aux_bwd(const float* logits, const float* load_frac, con
                                 void* dx_router, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Norms before and after the block, with its gate and residual scale                           */
+/* The residual stream x around one block (the MoE layer or any other):
+ *   xn  = rmsnorm(x) * w_in                                   before: the block's input
+ *   out = res_scale * x + gate * (rmsnorm(y) * w_out)         after: y is the block's output
+ *   rmsnorm(v) = v / sqrt(mean_j v_j^2 + eps)
+ * gate [ceil(T / gate_rows), d] (dt) or NULL (no gate): token t uses row t / gate_rows, so
+ * gate_rows = T is one learned vector, the sequence length one row per sequence, 1 one row per token.
+ * Norms, sums and statistics are fp32; every output is rounded once.  T >= 0 (0: no rows; the
+ * parameter gradients are written as zeros); d must be a multiple of 8, at most 16384; eps >= 0;
+ * gate_rows >= 1 (ignored without a gate).  Outputs must not overlap inputs.
+ * Source: the pages train this layer inside residual blocks ("Olmo-core DDP MoE examples",
+ * "Production throughput runs") without printing the norm; the formulas above are the reading. */
+
+/* Before the block:  xn [T, d] (dt) OUTPUT;  rstd [T] float OUTPUT or NULL: 1 / sqrt(mean x^2 + eps),
+ * which the backward reads.  x [T, d], w [d] (dt) INPUT. */
+moe_status_t moe_norm_in(const void* x, const void* w, int64_t T, int64_t d, float eps, moe_dtype_t dt,
+                         void* xn, float* rstd, moe_stream_t stream);
+/* After the block:  out [T, d] (dt) OUTPUT;  rstd [T] float OUTPUT or NULL.
+ * y, x [T, d], w [d], gate (dt) INPUT. */
+moe_status_t moe_norm_out(const void* y, const void* x, const void* w, const void* gate, int64_t gate_rows,
+                          float res_scale, float eps, int64_t T, int64_t d, moe_dtype_t dt, void* out,
+                          float* rstd, moe_stream_t stream);
+/* moe_combine and moe_norm_out in one pass: the combined row is summed in fp32 and normalised as it
+ * is, without the rounding that moe_combine's output has.
+ *   y_perm, topk_gate, dest_pos, shared_out, k: as for moe_combine
+ *   y [T, d] (dt) OUTPUT or NULL: the combined rows, rounded (the backward reads them). */
+moe_status_t moe_combine_norm_out(const void* y_perm, const float* topk_gate, const int32_t* dest_pos,
+                                  const void* shared_out, const void* x, const void* w, const void* gate,
+                                  int64_t gate_rows, float res_scale, float eps, int64_t T, int64_t d, int32_t k,
+                                  moe_dtype_t dt, void* y, void* out, float* rstd, moe_stream_t stream);
+/* Workspace of both backward calls. */
+size_t moe_norm_bwd_workspace_size(int64_t T, int64_t d);
+/* Backward of moe_norm_out (and of the norm of moe_combine_norm_out) with respect to y, w and gate;
+ * with n = y rstd and u = w gate dout:
+ *   dy [T, d] (dt) OUTPUT = rstd (u - n mean_j(u n))
+ *   dw [d] float OUTPUT = sum_t gate dout n
+ *   dgate float, the shape of gate, OUTPUT (NULL exactly when gate is) = w sum_{t of the row} dout n
+ * The gradient with respect to x, res_scale * dout, is what moe_norm_in_bwd adds through dres. */
+moe_status_t moe_norm_out_bwd(const void* dout, const void* y, const void* w, const void* gate, int64_t gate_rows,
+                              const float* rstd, int64_t T, int64_t d, moe_dtype_t dt, void* dy, float* dw,
+                              float* dgate, void* ws, size_t ws_bytes, moe_stream_t stream);
+/* Backward of moe_norm_in, and the residual's gradient; with n = x rstd and u = w dxn:
+ *   dx [T, d] (dt) OUTPUT = res_scale * dres + rstd (u - n mean_j(u n));  dres [T, d] (dt) INPUT or NULL
+ *   dw [d] float OUTPUT = sum_t dxn n */
+moe_status_t moe_norm_in_bwd(const void* dxn, const void* x, const void* w, const float* rstd, const void* dres,
+                             float res_scale, int64_t T, int64_t d, moe_dtype_t dt, void* dx, float* dw, void* ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Softmax cross entropy over a vocabulary                                                      */
+/* The loss that starts the backward pass, from the last hidden states and the output projection:
+ *   logits = h w^T;  lse[t] = log sum_v exp(logits[t, v]);  loss[t] = lse[t] - logits[t, target[t]]
+ * in pieces of the vocabulary; no buffer ever holds the logits.
+ *   h [T, d] (dt), w [V, d] (dt), target [T] int32   INPUT.  A target outside [0, V) (such as -100)
+ *     marks a token without loss: loss 0 and no gradient.  Its row of h is still read and must be finite.
+ *   loss, lse [T] float                              OUTPUT
+ * Products of bf16 data accumulate in fp32, exponentials and sums are fp32.  d must be a multiple of
+ * 8, at most 65536; T and V at most 2^22; T may be 0.
+ * Source: "Olmo-core DDP MoE examples", "Production throughput runs" (language-model training runs;
+ * the pages do not print the loss). */
+size_t moe_vocab_loss_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt);
+moe_status_t moe_vocab_loss(const void* h, const void* w, const int32_t* target, int64_t T, int64_t d, int64_t V,
+                            moe_dtype_t dt, float* loss, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream);
+/* Backward.  dloss [T] float INPUT is the gradient of each token's loss (for the mean over n tokens
+ * with a loss, 1 / n; not read where target is outside [0, V)); lse [T] from moe_vocab_loss.  With
+ * P[t, v] = dloss[t] (exp(logits[t, v] - lse[t]) - [v = target[t]]):
+ *   dh = P w   [T, d] (dt) OUTPUT;   dw = P^T h   [V, d] (dt) OUTPUT (every row is written)
+ * The logits are formed again piece by piece; P of one piece is kept in dt between the products, dh
+ * accumulates in fp32 over the pieces. */
+size_t moe_vocab_loss_bwd_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt);
+moe_status_t moe_vocab_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse,
+                                const float* dloss, int64_t T, int64_t d, int64_t V, moe_dtype_t dt, void* dh,
+                                void* dw, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Global gradient norm and clipping                                                            */
+/* Over a list of gradient tensors (a HOST array; what it points to is device memory, read when the
+ * call's kernels run).  Every tensor is contiguous, 16-byte aligned, and may be empty. */
+typedef struct {
+  const void* grad; /* [n] (dt) */
+  void* out;        /* [n] (dt) scaled gradient; may be grad itself (in place); moe_grad_norm ignores it */
+  int64_t n;
+  moe_dtype_t dt;
+} moe_grad_t;
+
+/* Workspace of the calls below. */
+size_t moe_grad_workspace_size(const moe_grad_t* grads, int32_t count);
+/* sumsq [1] double OUTPUT = sum of g^2 over every tensor; norm [1] float OUTPUT or NULL = its root.
+ * Squares and sums are double and added in a fixed order. */
+moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t count, double* sumsq, float* norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+/* out = c grad with c = min(1, max_norm / (sqrt(sumsq) + 1e-6)) in fp32, rounded once; sumsq [1]
+ * double INPUT: from moe_grad_norm, after a sum over ranks where the gradients are sharded.  When c
+ * is 1, out is a copy (nothing is written in place).  An infinite or NaN norm scales nothing (c = 1):
+ * read the norm and skip the step.  norm [1] float OUTPUT or NULL.  max_norm > 0.  An out may overlap
+ * no other tensor of the list (MOE_ERR_INVALID_VALUE), so no tensor is scaled twice. */
+moe_status_t moe_grad_scale(const moe_grad_t* grads, int32_t count, const double* sumsq, float max_norm,
+                            float* norm, moe_stream_t stream);
+/* Both: clip to a global norm of max_norm.  norm [1] float OUTPUT or NULL (the norm before clipping). */
+moe_status_t moe_grad_clip(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
 /* MXFP8 grouped GEMMs                                                                          */
 /* The pages train their largest operating points with an MXFP8 recipe ("Olmo-core DDP MoE
  * examples", "Production throughput runs", operating-point table; "Other experiments in the
@@ -421,7 +524,8 @@ typedef enum {
   MOE_OP_ROUTER_AUX = 9,      /* moe_router_aux */
   MOE_OP_ROUTER_AUX_BWD = 10, /* moe_router_aux_bwd */
   MOE_OP_MX_GEMM_ROWS = 11,   /* moe_mx_gemm_rows over the routed experts (and the shared expert) */
-  MOE_OP_MX_GEMM_K = 12       /* moe_mx_gemm_k, both weight-gradient products of each set */
+  MOE_OP_MX_GEMM_K = 12,      /* moe_mx_gemm_k, both weight-gradient products of each set */
+  MOE_OP_NORM_BWD = 13        /* moe_norm_out_bwd, moe_norm_in_bwd */
 } moe_op_t;
 
 /* Device workspace bytes that call `op` needs in a layer of T tokens of width d, each routed to

@@ -8,7 +8,9 @@
 #include <cstdint>
 #include <cstdio>
 #include <initializer_list>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 
 #include "common.h"
@@ -576,6 +578,324 @@ moe_status_t moe_router_aux_bwd(const float* logits, const float* load_frac, con
 }
 
 // ---------------------------------------------------------------------------------------------
+// Norms around the block
+
+namespace {
+
+constexpr int64_t kNormMaxWidth = 16384;
+
+moe_status_t check_norm(int64_t T, int64_t d, moe_dtype_t dt) {
+  moe_status_t st = check_dtype(dt);
+  if (st != MOE_OK) return st;
+  CHECK(T >= 0, MOE_ERR_INVALID_VALUE, "T must be >= 0 (got %lld)", (long long)T);
+  CHECK(d > 0, MOE_ERR_INVALID_VALUE, "d must be > 0 (got %lld)", (long long)d);
+  CHECK(d % 8 == 0 && d <= kNormMaxWidth, MOE_ERR_UNSUPPORTED,
+        "d must be a multiple of 8, at most %lld (got %lld)", (long long)kNormMaxWidth, (long long)d);
+  CHECK(T <= kMaxInt / 2, MOE_ERR_UNSUPPORTED, "T must be < 2^30 (got %lld)", (long long)T);
+  return MOE_OK;
+}
+
+// eps >= 0 (a NaN fails the comparison).
+#define CHECK_EPS(eps) CHECK((eps) >= 0.0f, MOE_ERR_INVALID_VALUE, "eps must be >= 0")
+
+moe_status_t check_gate(const void* gate, int64_t& gate_rows, int64_t T) {
+  if (!gate) {
+    gate_rows = 1;
+    return MOE_OK;
+  }
+  CHECK(gate_rows >= 1, MOE_ERR_INVALID_VALUE, "gate_rows must be >= 1 (got %lld)", (long long)gate_rows);
+  gate_rows = std::min(gate_rows, std::max<int64_t>(T, 1));
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_norm_in(const void* x, const void* w, int64_t T, int64_t d, float eps, moe_dtype_t dt, void* xn,
+                         float* rstd, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_norm(T, d, dt);
+  if (st != MOE_OK) return st;
+  CHECK_EPS(eps);
+  if (T == 0) return MOE_OK;
+  CHECK(x && w && xn, MOE_ERR_INVALID_VALUE, "x/w/xn is NULL");
+  CHECK_ALIGN16(x, w, xn, rstd);
+  return hip_check(moe::launch_norm_in(x, w, (int)T, (int)d, eps, dt == MOE_BF16, xn, rstd, S(stream)), "norm before");
+}
+
+moe_status_t moe_norm_out(const void* y, const void* x, const void* w, const void* gate, int64_t gate_rows,
+                          float res_scale, float eps, int64_t T, int64_t d, moe_dtype_t dt, void* out, float* rstd,
+                          moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_norm(T, d, dt);
+  if (st != MOE_OK) return st;
+  CHECK_EPS(eps);
+  if ((st = check_gate(gate, gate_rows, T)) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  CHECK(y && x && w && out, MOE_ERR_INVALID_VALUE, "y/x/w/out is NULL");
+  CHECK_ALIGN16(y, x, w, gate, out, rstd);
+  return hip_check(moe::launch_norm_out(y, nullptr, nullptr, nullptr, 0, x, w, gate, (int)gate_rows, res_scale, eps,
+                                        (int)T, (int)d, dt == MOE_BF16, nullptr, out, rstd, S(stream)),
+                   "norm after");
+}
+
+moe_status_t moe_combine_norm_out(const void* y_perm, const float* topk_gate, const int32_t* dest_pos,
+                                  const void* shared_out, const void* x, const void* w, const void* gate,
+                                  int64_t gate_rows, float res_scale, float eps, int64_t T, int64_t d, int32_t k,
+                                  moe_dtype_t dt, void* y, void* out, float* rstd, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_norm(T, d, dt);
+  if (st != MOE_OK) return st;
+  CHECK(k > 0, MOE_ERR_INVALID_VALUE, "k must be > 0 (got %d)", k);
+  CHECK(k <= 8, MOE_ERR_UNSUPPORTED, "k > 8 is not supported (got %d)", k);
+  CHECK(T * k <= kMaxInt - 8, MOE_ERR_UNSUPPORTED, "T*k must be < 2^31");
+  CHECK_EPS(eps);
+  if ((st = check_gate(gate, gate_rows, T)) != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  CHECK(y_perm && topk_gate && dest_pos, MOE_ERR_INVALID_VALUE, "y_perm/topk_gate/dest_pos is NULL");
+  CHECK(x && w && out, MOE_ERR_INVALID_VALUE, "x/w/out is NULL");
+  CHECK_ALIGN16(y_perm, topk_gate, dest_pos, shared_out, x, w, gate, y, out, rstd);
+  return hip_check(moe::launch_norm_out(y_perm, topk_gate, dest_pos, shared_out, k, x, w, gate, (int)gate_rows,
+                                        res_scale, eps, (int)T, (int)d, dt == MOE_BF16, y, out, rstd, S(stream)),
+                   "combine and norm after");
+}
+
+size_t moe_norm_bwd_workspace_size(int64_t T, int64_t d) {
+  if (T < 0 || d <= 0 || d > kNormMaxWidth || T > kMaxInt / 2) return 0;
+  return align256(moe::norm_bwd_ws_bytes(T, (int)d));
+}
+
+moe_status_t moe_norm_out_bwd(const void* dout, const void* y, const void* w, const void* gate, int64_t gate_rows,
+                              const float* rstd, int64_t T, int64_t d, moe_dtype_t dt, void* dy, float* dw,
+                              float* dgate, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_norm(T, d, dt);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(gate, gate_rows, T)) != MOE_OK) return st;
+  CHECK(w && dw && (T == 0 || (dout && y && rstd && dy)), MOE_ERR_INVALID_VALUE, "dout/y/w/rstd/dy/dw is NULL");
+  CHECK((gate == nullptr) == (dgate == nullptr), MOE_ERR_INVALID_VALUE,
+        "gate and dgate must both be given or both be NULL");
+  const size_t need = moe_norm_bwd_workspace_size(T, d);
+  CHECK(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(dout, y, w, gate, rstd, dy, dw, dgate, ws);
+  return hip_check(moe::launch_norm_out_bwd(dout, y, w, gate, (int)gate_rows, rstd, (int)T, (int)d, dt == MOE_BF16, dy,
+                                            dw, dgate, ws, S(stream)),
+                   "norm after, backward");
+}
+
+moe_status_t moe_norm_in_bwd(const void* dxn, const void* x, const void* w, const float* rstd, const void* dres,
+                             float res_scale, int64_t T, int64_t d, moe_dtype_t dt, void* dx, float* dw, void* ws,
+                             size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_norm(T, d, dt);
+  if (st != MOE_OK) return st;
+  CHECK(w && dw && (T == 0 || (dxn && x && rstd && dx)), MOE_ERR_INVALID_VALUE, "dxn/x/w/rstd/dx/dw is NULL");
+  const size_t need = moe_norm_bwd_workspace_size(T, d);
+  CHECK(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(dxn, x, w, rstd, dres, dx, dw, ws);
+  return hip_check(moe::launch_norm_in_bwd(dxn, x, w, rstd, dres, res_scale, (int)T, (int)d, dt == MOE_BF16, dx, dw, ws,
+                                           S(stream)),
+                   "norm before, backward");
+}
+
+// ---------------------------------------------------------------------------------------------
+// Softmax cross entropy over a vocabulary
+
+namespace {
+
+constexpr int64_t kVocabMax = int64_t(1) << 22;
+
+moe_status_t check_vocab(int64_t T, int64_t d, int64_t V, moe_dtype_t dt) {
+  moe_status_t st = check_dtype(dt);
+  if (st != MOE_OK) return st;
+  CHECK(T >= 0, MOE_ERR_INVALID_VALUE, "T must be >= 0 (got %lld)", (long long)T);
+  CHECK(d > 0 && V > 0, MOE_ERR_INVALID_VALUE, "d and V must be > 0 (got d=%lld, V=%lld)", (long long)d, (long long)V);
+  CHECK(d % 8 == 0 && d <= 65536, MOE_ERR_UNSUPPORTED, "d must be a multiple of 8, at most 65536 (got %lld)",
+        (long long)d);
+  CHECK(T <= kVocabMax && V <= kVocabMax, MOE_ERR_UNSUPPORTED, "T and V must be at most 2^22 (got T=%lld, V=%lld)",
+        (long long)T, (long long)V);
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_vocab_loss_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt) {
+  if (check_vocab(T, d, V, dt) != MOE_OK) return 0;
+  return align256(moe::vocab_loss_ws_bytes(T, d, V, dt == MOE_BF16));
+}
+
+moe_status_t moe_vocab_loss(const void* h, const void* w, const int32_t* target, int64_t T, int64_t d, int64_t V,
+                            moe_dtype_t dt, float* loss, float* lse, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_vocab(T, d, V, dt);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  CHECK(h && w && target && loss && lse, MOE_ERR_INVALID_VALUE, "h/w/target/loss/lse is NULL");
+  const size_t need = moe_vocab_loss_workspace_size(T, d, V, dt);
+  CHECK(ws && ws_bytes >= need, MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(h, w, target, loss, lse, ws);
+  return hip_check(moe::launch_vocab_loss(h, w, target, (int)T, (int)d, (int)V, dt == MOE_BF16, loss, lse, ws, S(stream)),
+                   "vocabulary loss");
+}
+
+size_t moe_vocab_loss_bwd_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt) {
+  if (check_vocab(T, d, V, dt) != MOE_OK) return 0;
+  return align256(moe::vocab_loss_bwd_ws_bytes(T, d, V, dt == MOE_BF16));
+}
+
+moe_status_t moe_vocab_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse,
+                                const float* dloss, int64_t T, int64_t d, int64_t V, moe_dtype_t dt, void* dh, void* dw,
+                                void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_vocab(T, d, V, dt);
+  if (st != MOE_OK) return st;
+  CHECK(w && dw && (T == 0 || (h && target && lse && dloss && dh)), MOE_ERR_INVALID_VALUE,
+        "h/w/target/lse/dloss/dh/dw is NULL");
+  const size_t need = moe_vocab_loss_bwd_workspace_size(T, d, V, dt);
+  CHECK(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(h, w, target, lse, dloss, dh, dw, ws);
+  return hip_check(moe::launch_vocab_loss_bwd(h, w, target, lse, dloss, (int)T, (int)d, (int)V, dt == MOE_BF16, dh, dw,
+                                              ws, S(stream)),
+                   "vocabulary loss, backward");
+}
+
+// ---------------------------------------------------------------------------------------------
+// Gradient norm and clipping
+
+namespace {
+
+// The list in the launchers' form, and its checks.  `scale`: the call writes out.
+struct GradList {
+  std::unique_ptr<moe::GradItem[]> items;
+  long long chunks = 0;
+};
+
+constexpr int64_t kGradMaxElements = int64_t(1) << 48;
+
+moe_status_t grad_list(const moe_grad_t* grads, int32_t count, bool scale, GradList& list) {
+  CHECK(count >= 0, MOE_ERR_INVALID_VALUE, "count must be >= 0 (got %d)", count);
+  CHECK(count == 0 || grads, MOE_ERR_INVALID_VALUE, "grads is NULL");
+  CHECK(count <= 1 << 20, MOE_ERR_UNSUPPORTED, "count must be at most 2^20 (got %d)", count);
+  list.items.reset(new (std::nothrow) moe::GradItem[std::max(count, 1)]);
+  CHECK(list.items, MOE_ERR_UNSUPPORTED, "no host memory for a list of %d gradients", count);
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_grad_t& g = grads[i];
+    moe_status_t st = check_dtype(g.dt);
+    if (st != MOE_OK) return st;
+    CHECK(g.n >= 0, MOE_ERR_INVALID_VALUE, "gradient %d has n = %lld", i, (long long)g.n);
+    CHECK(g.n <= kGradMaxElements - total, MOE_ERR_UNSUPPORTED, "more than 2^48 gradient elements");
+    total += g.n;
+    CHECK(g.n == 0 || (g.grad && (!scale || g.out)), MOE_ERR_INVALID_VALUE, "gradient %d: grad/out is NULL", i);
+    CHECK(aligned16({g.grad, scale ? g.out : nullptr}), MOE_ERR_INVALID_VALUE,
+          "device pointers must be 16-byte aligned (gradient %d)", i);
+    list.items[i] = moe::GradItem{g.grad, g.out, (long long)g.n, g.dt == MOE_BF16};
+  }
+  list.chunks = moe::grad_chunks(list.items.get(), count);
+  if (!scale) return MOE_OK;
+  // No output may overlap another tensor of the list: sweep the address ranges in order of their
+  // starts, keeping the furthest end of an output and of any range so far.
+  struct Range {
+    uintptr_t begin, end;
+    bool out;
+  };
+  std::unique_ptr<Range[]> r(new (std::nothrow) Range[2 * (size_t)std::max(count, 1)]);
+  CHECK(r, MOE_ERR_UNSUPPORTED, "no host memory for a list of %d gradients", count);
+  size_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    if (grads[i].n == 0) continue;
+    const size_t bytes = (size_t)grads[i].n * esize(grads[i].dt);
+    const uintptr_t o = reinterpret_cast<uintptr_t>(grads[i].out), g = reinterpret_cast<uintptr_t>(grads[i].grad);
+    r[n++] = Range{o, o + bytes, true};
+    if (g != o) r[n++] = Range{g, g + bytes, false};
+  }
+  std::sort(r.get(), r.get() + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t end_out = 0, end_any = 0;
+  for (size_t i = 0; i < n; ++i) {
+    CHECK(r[i].begin >= end_out && (!r[i].out || r[i].begin >= end_any), MOE_ERR_INVALID_VALUE,
+          "an out overlaps another tensor of the list");
+    end_any = std::max(end_any, r[i].end);
+    if (r[i].out) end_out = std::max(end_out, r[i].end);
+  }
+  return MOE_OK;
+}
+
+moe_status_t check_max_norm(float max_norm) {
+  CHECK(max_norm > 0.0f, MOE_ERR_INVALID_VALUE, "max_norm must be > 0");
+  return MOE_OK;
+}
+
+// Partial sums, and one double for a total behind them.
+size_t grad_ws_bytes(long long chunks) { return align256(((size_t)chunks + 1) * sizeof(double)); }
+
+}  // namespace
+
+size_t moe_grad_workspace_size(const moe_grad_t* grads, int32_t count) {
+  GradList list;
+  if (grad_list(grads, count, false, list) != MOE_OK) return 0;
+  return grad_ws_bytes(list.chunks);
+}
+
+moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t count, double* sumsq, float* norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  GradList list;
+  moe_status_t st = grad_list(grads, count, false, list);
+  if (st != MOE_OK) return st;
+  CHECK(sumsq, MOE_ERR_INVALID_VALUE, "sumsq is NULL");
+  const size_t need = grad_ws_bytes(list.chunks);
+  CHECK(ws && ws_bytes >= need, MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(sumsq, norm, ws);
+  double* partial = reinterpret_cast<double*>(ws);
+  st = hip_check(moe::launch_grad_sumsq(list.items.get(), count, partial, S(stream)), "gradient sum of squares");
+  if (st != MOE_OK) return st;
+  return hip_check(moe::launch_grad_total(partial, (int)list.chunks, sumsq, norm, S(stream)), "gradient norm");
+}
+
+moe_status_t moe_grad_scale(const moe_grad_t* grads, int32_t count, const double* sumsq, float max_norm, float* norm,
+                            moe_stream_t stream) {
+  g_err.clear();
+  GradList list;
+  moe_status_t st = grad_list(grads, count, true, list);
+  if (st != MOE_OK) return st;
+  if ((st = check_max_norm(max_norm)) != MOE_OK) return st;
+  CHECK(sumsq, MOE_ERR_INVALID_VALUE, "sumsq is NULL");
+  CHECK_ALIGN16(sumsq, norm);
+  if (list.chunks == 0) {   // nothing to scale: the norm alone
+    if (!norm) return MOE_OK;
+    return hip_check(moe::launch_grad_total(sumsq, 1, nullptr, norm, S(stream)), "gradient norm");
+  }
+  return hip_check(moe::launch_grad_scale(list.items.get(), count, sumsq, 1, max_norm, norm, S(stream)),
+                   "gradient scaling");
+}
+
+moe_status_t moe_grad_clip(const moe_grad_t* grads, int32_t count, float max_norm, float* norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  GradList list;
+  moe_status_t st = grad_list(grads, count, true, list);
+  if (st != MOE_OK) return st;
+  if ((st = check_max_norm(max_norm)) != MOE_OK) return st;
+  const size_t need = grad_ws_bytes(list.chunks);
+  CHECK(ws && ws_bytes >= need, MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(norm, ws);
+  double* partial = reinterpret_cast<double*>(ws);
+  if (list.chunks == 0) {   // no elements: a norm of zero
+    if (!norm) return MOE_OK;
+    return hip_check(moe::launch_grad_total(partial, 0, nullptr, norm, S(stream)), "gradient norm");
+  }
+  st = hip_check(moe::launch_grad_sumsq(list.items.get(), count, partial, S(stream)), "gradient sum of squares");
+  if (st != MOE_OK) return st;
+  return hip_check(moe::launch_grad_scale(list.items.get(), count, partial, (int)list.chunks, max_norm, norm, S(stream)),
+                   "gradient scaling");
+}
+
+// ---------------------------------------------------------------------------------------------
 // MXFP8
 
 moe_status_t moe_mx_quantize_rows(const void* x, int64_t R, int64_t K, int64_t ldx, uint8_t* codes,
@@ -784,6 +1104,7 @@ size_t moe_workspace_bytes(int32_t op, int64_t T, int64_t d, int32_t E, int32_t 
                                        moe_mx_gemm_k_workspace_size(1, 2 * fs, d)));
       return need;
     }
+    case MOE_OP_NORM_BWD: return moe_norm_bwd_workspace_size(T, d);
     default:
       fail(MOE_ERR_INVALID_VALUE, "unknown op %d", op);
       return 0;

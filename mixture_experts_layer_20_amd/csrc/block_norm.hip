@@ -1,0 +1,525 @@
+// Norms before and after the MoE block, with the block's gate and residual scale, and their backward.
+//
+//   before   xn  = x r w,                     r = 1 / sqrt(mean_j x_j^2 + eps)
+//   after    out = a x + g * (y r w),         r = 1 / sqrt(mean_j y_j^2 + eps)
+// The block's output y comes as a tensor, or is the layer's weighted combine, summed here: the
+// normalised row is then read once from the experts' rows and never stored.
+//
+// Backward, with n = y r (or x r) and u = w * g * dout (or w * dxn):
+//   dy = r (u - n mean_j(u_j n_j)),  dg_s = w * S_s,  dw = sum_s g_s * S_s,
+//   S_s = sum over the rows t of gate row s of dout_t * n_t
+// so one column sum S per gate row gives both parameter gradients.
+//
+// Every sum, norm and statistic is fp32; a value is rounded to the storage type once, at its store.
+#include "common.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+// 8 consecutive elements, as loaded and widened.
+template <typename T> struct Seg8;
+template <> struct Seg8<bf16_t> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const bf16_t* p) { w = *reinterpret_cast<const u32x4_t*>(p); }
+  __device__ __forceinline__ void zero() { w = u32x4_t{0, 0, 0, 0}; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static __forceinline__ void put(bf16_t* p, const float (&v)[8]) {
+    u32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
+    *reinterpret_cast<u32x4_t*>(p) = r;
+  }
+};
+template <> struct Seg8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ static __forceinline__ void put(float* p, const float (&v)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+constexpr int NT = 256;   // threads of a workgroup
+
+// Sum over the L lanes that share a row (L = 64: a wave; L = 256: the workgroup, one row at a time).
+// `red` holds one value per wave and slot; two slots alternate, so one barrier per sum is enough.
+template <int L>
+__device__ __forceinline__ float row_sum(float s, float (&red)[2][NT / 64], int& slot) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+  if constexpr (L == NT) {
+    if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
+    slot ^= 1;
+  }
+  return s;
+}
+
+// Lane `lane` of the L lanes of a row holds the 8-element segments lane + i L, i < NV.
+struct Cols {
+  int c;
+  bool in;
+};
+template <int L>
+__device__ __forceinline__ Cols cols(int lane, int i, int d) {
+  const int c = 8 * (lane + i * L);
+  return Cols{c, c < d};
+}
+
+template <typename T, int L, int NV>
+__global__ __launch_bounds__(NT) void norm_in_kernel(const T* x, const T* w, int rows, int d, float eps, T* xn,
+                                                     float* rstd) {
+  __shared__ float red[2][NT / 64];
+  const int lane = threadIdx.x % L;
+  const int t = blockIdx.x * (NT / L) + threadIdx.x / L;
+  if (t >= rows) return;   // L = NT: the whole workgroup; L = 64: whole waves, no barrier below
+  int slot = 0;
+  Seg8<T> xr[NV], wr[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const Cols k = cols<L>(lane, i, d);
+    if (k.in) {
+      xr[i].load(x + (size_t)t * d + k.c);
+      wr[i].load(w + k.c);
+    } else {
+      xr[i].zero();
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    float v[8];
+    xr[i].get(v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += v[e] * v[e];
+  }
+  const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
+  if (rstd && lane == 0) rstd[t] = r;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const Cols k = cols<L>(lane, i, d);
+    if (!k.in) continue;
+    float v[8], wv[8];
+    xr[i].get(v);
+    wr[i].get(wv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * r * wv[e];
+    Seg8<T>::put(xn + (size_t)t * d + k.c, v);
+  }
+}
+
+// The norm after the block.  COMBINE: y is the layer's weighted combine of k rows of y_perm and the
+// shared expert's row, summed in fp32 in the order of combine_kernel (slots, then the shared row) and
+// normalised unrounded; y_out (if given) gets it rounded, for the backward.
+template <typename T, int L, int NV, bool COMBINE>
+__global__ __launch_bounds__(NT) void norm_out_kernel(const T* y, const float* topk_gate, const int32_t* dest_pos,
+                                                      const T* shared, int k, const T* x, const T* w, const T* gate,
+                                                      int gate_rows, float res_scale, int rows, int d, float eps,
+                                                      T* y_out, T* out, float* rstd) {
+  __shared__ float red[2][NT / 64];
+  const int lane = threadIdx.x % L;
+  const int t = blockIdx.x * (NT / L) + threadIdx.x / L;
+  if (t >= rows) return;
+  int slot = 0;
+  float yv[NV][8];
+  if constexpr (COMBINE) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) yv[i][e] = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const size_t row = (size_t)dest_pos[(size_t)t * k + j] * d;
+      const float g = topk_gate[(size_t)t * k + j];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        if (!q.in) continue;
+        Seg8<T> seg;
+        float v[8];
+        seg.load(y + row + q.c);
+        seg.get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) yv[i][e] += g * v[e];
+      }
+    }
+    if (shared) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        if (!q.in) continue;
+        Seg8<T> seg;
+        float v[8];
+        seg.load(shared + (size_t)t * d + q.c);
+        seg.get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) yv[i][e] += v[e];
+      }
+    }
+    if (y_out) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        if (q.in) Seg8<T>::put(y_out + (size_t)t * d + q.c, yv[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Cols q = cols<L>(lane, i, d);
+      Seg8<T> seg;
+      seg.zero();
+      if (q.in) seg.load(y + (size_t)t * d + q.c);
+      seg.get(yv[i]);
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += yv[i][e] * yv[i][e];
+  const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
+  if (rstd && lane == 0) rstd[t] = r;
+  const T* grow = gate ? gate + (size_t)(t / gate_rows) * d : nullptr;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const Cols q = cols<L>(lane, i, d);
+    if (!q.in) continue;
+    Seg8<T> seg;
+    float xv[8], wv[8], o[8];
+    seg.load(x + (size_t)t * d + q.c);
+    seg.get(xv);
+    seg.load(w + q.c);
+    seg.get(wv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = yv[i][e] * r * wv[e];
+    if (grow) {
+      seg.load(grow + q.c);
+      seg.get(wv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= wv[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] += res_scale * xv[e];
+    Seg8<T>::put(out + (size_t)t * d + q.c, o);
+  }
+}
+
+// Row block of the backward: workgroup b owns rows b R .. min(T, (b + 1) R), walked piece by piece
+// (a piece: the block's rows of one gate row).  At a piece's end the column sum S of its rows goes
+//   to dgate directly when the gate row lies inside the block,
+//   else to the block's `head` partial (the gate row began before the block or at its start) or its
+//   `tail` partial (it began inside and goes on in the next block): a block has at most one of each.
+struct BwdArgs {
+  int rows, d, R, gate_rows;
+  float res_scale;
+  float* part;   // [3][blocks][d]: dw partials, head, tail
+  float* dw;
+  float* dgate;
+};
+
+// IN: dxn (as dout), x (as y), dres.  Otherwise: dout, y, gate.
+template <typename T, int L, int NV, bool IN>
+__global__ __launch_bounds__(NT) void norm_bwd_kernel(const T* dout, const T* y, const T* w, const T* gate,
+                                                      const T* dres, const float* rstd, T* dy, BwdArgs p) {
+  constexpr int NS = NT / L;   // rows in flight of a workgroup
+  __shared__ float red[2][NT / 64];
+  extern __shared__ float sums[];   // [NS - 1][8 NV L] column sums of the other waves (L = 64)
+  const int lane = threadIdx.x % L, me = threadIdx.x / L;
+  const int d = p.d;
+  const int r0 = blockIdx.x * p.R, r1 = min(p.rows, r0 + p.R);
+  const int blocks = gridDim.x;
+  int slot = 0;
+  float dwacc[NV][8] = {};
+  for (int p0 = r0; p0 < r1;) {
+    const int seg = gate ? p0 / p.gate_rows : 0;
+    const long long seg_end = gate ? (long long)(seg + 1) * p.gate_rows : (long long)p.rows;
+    const int p1 = (int)min((long long)r1, seg_end);
+    float gw[NV][8], S[NV][8] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Cols q = cols<L>(lane, i, d);
+      Seg8<T> sg;
+      sg.zero();
+      if (q.in) sg.load(w + q.c);
+      sg.get(gw[i]);
+      if (gate && q.in) {
+        float gv[8];
+        sg.load(gate + (size_t)seg * d + q.c);
+        sg.get(gv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gw[i][e] *= gv[e];
+      }
+    }
+    for (int t = p0 + me; t < p1; t += NS) {
+      Seg8<T> yr[NV], dr[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        yr[i].zero();
+        dr[i].zero();
+        if (q.in) {
+          yr[i].load(y + (size_t)t * d + q.c);
+          dr[i].load(dout + (size_t)t * d + q.c);
+        }
+      }
+      const float r = rstd[t];
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float n[8], g[8];
+        yr[i].get(n);
+        dr[i].get(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          n[e] *= r;
+          S[i][e] += g[e] * n[e];
+          dot += g[e] * gw[i][e] * n[e];
+        }
+      }
+      const float m = row_sum<L>(dot, red, slot) / (float)d;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        if (!q.in) continue;
+        float n[8], g[8];
+        yr[i].get(n);
+        dr[i].get(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = r * (g[e] * gw[i][e] - n[e] * r * m);
+        if (IN && dres) {
+          Seg8<T> sg;
+          float v[8];
+          sg.load(dres + (size_t)t * d + q.c);
+          sg.get(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] += p.res_scale * v[e];
+        }
+        Seg8<T>::put(dy + (size_t)t * d + q.c, g);
+      }
+    }
+    // S over the workgroup's waves, into wave 0 (L = 64)
+    if constexpr (NS > 1) {
+      if (me > 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sums[((me - 1) * NV * 8 + i * 8 + e) * L + lane] = S[i][e];
+      }
+      __syncthreads();
+      if (me == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int o = 0; o < NS - 1; ++o) S[i][e] += sums[(o * NV * 8 + i * 8 + e) * L + lane];
+      }
+      __syncthreads();
+    }
+    if (me == 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        if (!q.in) continue;
+        if (gate) {
+          const long long seg_begin = (long long)seg * p.gate_rows;
+          const bool whole = seg_begin >= r0 && min(seg_end, (long long)p.rows) <= r1;
+          Seg8<T> sg;
+          float wv[8], gv[8];
+          sg.load(w + q.c);
+          sg.get(wv);
+          sg.load(gate + (size_t)seg * d + q.c);
+          sg.get(gv);
+          float* to = whole ? p.dgate + (size_t)seg * d
+                            : p.part + ((size_t)(seg_begin <= r0 ? 1 : 2) * blocks + blockIdx.x) * d;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            to[q.c + e] = whole ? wv[e] * S[i][e] : S[i][e];
+            dwacc[i][e] += gv[e] * S[i][e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dwacc[i][e] += S[i][e];
+        }
+      }
+    }
+    p0 = p1;
+  }
+  if (me == 0) {
+    float* to = blocks == 1 ? p.dw : p.part + (size_t)blockIdx.x * d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Cols q = cols<L>(lane, i, d);
+      if (!q.in) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) to[q.c + e] = dwacc[i][e];
+    }
+  }
+}
+
+// Joins the row blocks' partials in block order.  blockIdx.y = 0: dw.  blockIdx.y = b + 1: the gate
+// row that the end of block b cuts, if b is the first block of that gate row.
+template <typename T>
+__global__ __launch_bounds__(NT) void norm_bwd_join_kernel(const T* w, bool gated, BwdArgs p, int blocks) {
+  __shared__ float red[NT / 16][64 + 1];
+  const int d = p.d;
+  const int c = blockIdx.x * 64 + (threadIdx.x % 16) * 4, slice = threadIdx.x / 16;
+  int b0 = 0, b1 = blocks;   // blocks whose partials are added
+  int seg = 0;
+  long long seg_begin = 0;
+  if (blockIdx.y > 0) {
+    const int b = blockIdx.y - 1;
+    const int row = (b + 1) * p.R - 1;   // last row of block b; row + 1 exists (b is not the last block)
+    seg = row / p.gate_rows;
+    if ((row + 1) / p.gate_rows != seg) return;   // the cut falls between gate rows
+    seg_begin = (long long)seg * p.gate_rows;
+    b0 = (int)(seg_begin / p.R);
+    if (b0 != b) return;                           // an earlier cut handles it
+    const long long last = min((long long)p.rows, seg_begin + p.gate_rows) - 1;
+    b1 = (int)(last / p.R) + 1;
+  }
+  float a[4] = {0, 0, 0, 0};
+  if (c < d) {
+    for (int b = b0 + slice; b < b1; b += NT / 16) {
+      const int kind = blockIdx.y == 0 ? 0 : (seg_begin <= (long long)b * p.R ? 1 : 2);
+      const float4 v = *reinterpret_cast<const float4*>(p.part + ((size_t)kind * blocks + b) * d + c);
+      a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[slice][(threadIdx.x % 16) * 4 + e] = a[e];
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int col = blockIdx.x * 64 + threadIdx.x;
+    if (col >= d) return;
+    float s = 0.0f;
+    for (int i = 0; i < NT / 16; ++i) s += red[i][threadIdx.x];
+    if (blockIdx.y == 0) p.dw[col] = s;
+    else p.dgate[(size_t)seg * d + col] = to_f32<T>(w[col]) * s;
+  }
+}
+
+__global__ __launch_bounds__(NT) void zero_f32_kernel(float* p, int n) {
+  const int i = blockIdx.x * NT + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
+// Lanes per row and segments per lane for a width of d: one wave up to 2048 columns (no barrier in
+// the row loop), the workgroup above.
+template <typename F>
+hipError_t by_width(int d, F&& f) {
+  if (d <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+  if (d <= 2048) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  if (d <= 8192) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 8>{});
+}
+
+// Rows per workgroup of the backward: about 512 workgroups (two per CU), at least one row per wave.
+int bwd_rows(long long T, int d) {
+  const int ns = d <= 2048 ? 4 : 1;
+  const long long r = (T + 511) / 512;
+  return (int)std::max<long long>(ns, (r + ns - 1) / ns * ns);
+}
+
+template <typename T, bool IN>
+hipError_t norm_bwd(const T* dout, const T* y, const T* w, const T* gate, const T* dres, const float* rstd, T* dy,
+                    BwdArgs p, hipStream_t s) {
+  if (p.rows == 0) {
+    zero_f32_kernel<<<dim3(ceil_div(p.d, NT)), dim3(NT), 0, s>>>(p.dw, p.d);
+    return hipGetLastError();
+  }
+  p.R = bwd_rows(p.rows, p.d);
+  const int blocks = ceil_div(p.rows, p.R);
+  hipError_t e = by_width(p.d, [&](auto L, auto NV) {
+    constexpr int ns = NT / decltype(L)::value;
+    const size_t lds = (size_t)(ns - 1) * 8 * decltype(NV)::value * decltype(L)::value * sizeof(float);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(L)::value, decltype(NV)::value, IN>), dim3(blocks), dim3(NT), lds, s,
+                       dout, y, w, gate, dres, rstd, dy, p);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || blocks == 1) return e;
+  norm_bwd_join_kernel<T><<<dim3(ceil_div(p.d, 64), gate ? blocks : 1), dim3(NT), 0, s>>>(w, gate != nullptr, p, blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_in(const void* x, const void* w, int T, int d, float eps, bool bf16, void* xn, float* rstd,
+                          hipStream_t s) {
+  auto go = [&](auto tag) {
+    typedef decltype(tag) E;
+    return by_width(d, [&](auto L, auto NV) {
+      hipLaunchKernelGGL((norm_in_kernel<E, decltype(L)::value, decltype(NV)::value>),
+                         dim3(ceil_div(T, NT / decltype(L)::value)), dim3(NT), 0, s, (const E*)x, (const E*)w, T, d, eps,
+                         (E*)xn, rstd);
+      return hipGetLastError();
+    });
+  };
+  return bf16 ? go(bf16_t{}) : go(float{});
+}
+
+hipError_t launch_norm_out(const void* y, const float* topk_gate, const int32_t* dest_pos, const void* shared, int k,
+                           const void* x, const void* w, const void* gate, int gate_rows, float res_scale, float eps,
+                           int T, int d, bool bf16, void* y_out, void* out, float* rstd, hipStream_t s) {
+  auto go = [&](auto tag, auto comb) {
+    typedef decltype(tag) E;
+    return by_width(d, [&](auto L, auto NV) {
+      hipLaunchKernelGGL((norm_out_kernel<E, decltype(L)::value, decltype(NV)::value, decltype(comb)::value>),
+                         dim3(ceil_div(T, NT / decltype(L)::value)), dim3(NT), 0, s, (const E*)y, topk_gate, dest_pos,
+                         (const E*)shared, k, (const E*)x, (const E*)w, (const E*)gate, gate_rows, res_scale, T, d, eps,
+                         (E*)y_out, (E*)out, rstd);
+      return hipGetLastError();
+    });
+  };
+  if (dest_pos) return bf16 ? go(bf16_t{}, std::true_type{}) : go(float{}, std::true_type{});
+  return bf16 ? go(bf16_t{}, std::false_type{}) : go(float{}, std::false_type{});
+}
+
+size_t norm_bwd_ws_bytes(long long T, int d) {
+  if (T <= 0) return 0;
+  return (size_t)3 * ((T + bwd_rows(T, d) - 1) / bwd_rows(T, d)) * d * sizeof(float);
+}
+
+hipError_t launch_norm_in_bwd(const void* dxn, const void* x, const void* w, const float* rstd, const void* dres,
+                              float res_scale, int T, int d, bool bf16, void* dx, float* dw, void* ws, hipStream_t s) {
+  BwdArgs p{T, d, 0, 1, res_scale, (float*)ws, dw, nullptr};
+  if (bf16)
+    return norm_bwd<bf16_t, true>((const bf16_t*)dxn, (const bf16_t*)x, (const bf16_t*)w, nullptr, (const bf16_t*)dres,
+                                  rstd, (bf16_t*)dx, p, s);
+  return norm_bwd<float, true>((const float*)dxn, (const float*)x, (const float*)w, nullptr, (const float*)dres, rstd,
+                               (float*)dx, p, s);
+}
+
+hipError_t launch_norm_out_bwd(const void* dout, const void* y, const void* w, const void* gate, int gate_rows,
+                               const float* rstd, int T, int d, bool bf16, void* dy, float* dw, float* dgate, void* ws,
+                               hipStream_t s) {
+  BwdArgs p{T, d, 0, gate_rows, 0.0f, (float*)ws, dw, dgate};
+  if (bf16)
+    return norm_bwd<bf16_t, false>((const bf16_t*)dout, (const bf16_t*)y, (const bf16_t*)w, (const bf16_t*)gate, nullptr,
+                                   rstd, (bf16_t*)dy, p, s);
+  return norm_bwd<float, false>((const float*)dout, (const float*)y, (const float*)w, (const float*)gate, nullptr, rstd,
+                                (float*)dy, p, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,382 @@
+// Softmax cross entropy over a vocabulary and its gradient, in pieces of the vocabulary.
+//
+//   l = h w^T (T x V),  lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l[t, target_t]
+//   P = dloss_t (exp(l_tv - lse_t) - [v = target_t]),  dh = P w,  dw = P^T h
+//
+// The logits are never stored.  Forward: each tile of the product keeps, per row, the maximum and
+// the sum of exponentials of its columns (and the target's logit where the target lies in it); a
+// second kernel joins a row's tiles in order.  Backward: the product is formed again one piece of
+// the vocabulary at a time, its epilogue writes P of the piece (in the storage type: the operand of
+// the two gradient products), and dh accumulates over the pieces in fp32.
+// A target outside [0, V) marks a row without loss: loss 0, P = 0 exactly.
+#include "common.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+struct VocabArgs {
+  const void* h;
+  const void* w;
+  const int32_t* target;
+  const float* lse;
+  const float* dloss;
+  int T, d, V;
+  int v0, vn;         // the piece: words v0 .. v0 + vn - 1
+  int ldp;            // row length of P
+  void* p;            // [T, ldp]
+  float* pmax;        // [T, tiles] per-tile maxima, then [T, tiles] sums
+  float* psum;
+  int tiles;
+  float* tlogit;      // [T] logit of the target
+  float* dh_acc;      // [T, d] fp32
+  void* dh;
+  void* dw;
+  bool first, last;   // the piece is the first / the last one
+};
+
+enum VocabMode { VL_STATS = 0, VL_GRAD = 1, VL_DH = 2, VL_DW = 3 };
+
+// ---------------------------------------------------------------------------------------------
+// 128x128 tiles, four waves of 64x64, operands staged through registers: any T, V and d (a multiple
+// of 8), both types.
+
+constexpr int TM = 128, TN = 128, NT = 256;
+
+template <typename T> struct Cfg;
+template <> struct Cfg<bf16_t> {
+  static constexpr int BK = 32, E = 8, LD = BK + 8;   // E: elements of a 16-byte chunk
+};
+template <> struct Cfg<float> {
+  static constexpr int BK = 16, E = 4, LD = BK + 4;
+};
+
+// Operand chunk c (0..511) of the K step at k0 into its LDS tile [128][LD].  KC: rows of K
+// consecutive elements; otherwise K rows of consecutive tile rows.  Elements outside are zero.
+template <typename T, bool KC>
+struct Stage {
+  static constexpr int E = Cfg<T>::E, BK = Cfg<T>::BK, LD = Cfg<T>::LD;
+  u32x4_t v[2];
+  __device__ __forceinline__ void load(const T* base, size_t ld, int row0, int rows, int k0, int K) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = threadIdx.x + i * NT;
+      const int r = KC ? c / (BK / E) : (c % (TM / E)) * E;
+      const int k = k0 + (KC ? (c % (BK / E)) * E : c / (TM / E));
+      v[i] = u32x4_t{0, 0, 0, 0};
+      if (row0 + r < rows && k < K) v[i] = *reinterpret_cast<const u32x4_t*>(KC ? base + (size_t)(row0 + r) * ld + k : base + (size_t)k * ld + row0 + r);
+    }
+  }
+  __device__ __forceinline__ void store(T* lds) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = threadIdx.x + i * NT;
+      if constexpr (KC) {
+        *reinterpret_cast<u32x4_t*>(lds + (c / (BK / E)) * LD + (c % (BK / E)) * E) = v[i];
+      } else {
+        const int r = (c % (TM / E)) * E, k = c / (TM / E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if constexpr (E == 8) lds[(r + e) * LD + k] = (bf16_t)(v[i][e / 2] >> (16 * (e & 1)));
+          else lds[(r + e) * LD + k] = __uint_as_float(v[i][e]);
+        }
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void store4(bf16_t* p, const float (&v)[4]) {
+  uint2 w;
+  w.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
+  w.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+  *reinterpret_cast<uint2*>(p) = w;
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// MODE's operands.  STATS, GRAD: rows of h against words of the piece, K = d.  DH: rows of P against
+// columns of w, K = the piece's words.  DW: the piece's words against columns of h, K = T.
+template <typename T, int MODE>
+__global__ __launch_bounds__(NT) void vocab_tile_kernel(VocabArgs p) {
+  constexpr int BK = Cfg<T>::BK, LD = Cfg<T>::LD;
+  __shared__ __attribute__((aligned(16))) T sa[TM * LD];
+  __shared__ __attribute__((aligned(16))) T sb[TN * LD];
+  __shared__ float red[2][2][TM];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wm = wave >> 1, wn = wave & 1;
+  const T* h = reinterpret_cast<const T*>(p.h);
+  const T* w = reinterpret_cast<const T*>(p.w) + (size_t)p.v0 * p.d;
+  const T* P = reinterpret_cast<const T*>(p.p);
+  constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
+  const int M = MODE == VL_DW ? p.vn : p.T;
+  const int N = LOGITS ? p.vn : p.d;
+  // P's columns past the piece's words are zero up to the next multiple of 8
+  const int K = LOGITS ? p.d : (MODE == VL_DH ? p.vn : p.T);
+  const int m0 = blockIdx.y * TM, n0 = blockIdx.x * TN;
+
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+  Stage<T, MODE != VL_DW> a;
+  Stage<T, LOGITS> b;
+  auto load = [&](int k0) {
+    if constexpr (LOGITS) {
+      a.load(h, p.d, m0, M, k0, K);
+      b.load(w, p.d, n0, N, k0, K);
+    } else if constexpr (MODE == VL_DH) {
+      a.load(P, p.ldp, m0, M, k0, K);
+      b.load(w, p.d, n0, N, k0, K);
+    } else {
+      a.load(P, p.ldp, m0, M, k0, K);
+      b.load(h, p.d, n0, N, k0, K);
+    }
+  };
+  load(0);
+  for (int k0 = 0; k0 < K; k0 += BK) {
+    __syncthreads();
+    a.store(sa);
+    b.store(sb);
+    __syncthreads();
+    if (k0 + BK < K) load(k0 + BK);
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int s = 0; s < BK / 16; ++s) {
+        bf16x8_t fa[2], fb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fa[i] = *reinterpret_cast<const bf16x8_t*>(sa + (wm * 64 + i * 32 + (lane & 31)) * LD + s * 16 + (lane >> 5) * 8);
+          fb[i] = *reinterpret_cast<const bf16x8_t*>(sb + (wn * 64 + i * 32 + (lane & 31)) * LD + s * 16 + (lane >> 5) * 8);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < BK / 2; ++s) {
+        float fa[2], fb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          fa[i] = sa[(wm * 64 + i * 32 + (lane & 31)) * LD + s * 2 + (lane >> 5)];
+          fb[i] = sb[(wn * 64 + i * 32 + (lane & 31)) * LD + s * 2 + (lane >> 5)];
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      }
+    }
+  }
+
+  // Lane l holds row l % 32 of block i and, in element v, column 8 (v / 4) + 4 (l / 32) + v % 4 of
+  // block j.
+  if constexpr (MODE == VL_STATS) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int rl = wm * 64 + i * 32 + (lane & 31), row = m0 + rl;
+      const int tgt = row < M ? p.target[row] - p.v0 : -1;
+      float mx = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int n = n0 + wn * 64 + j * 32 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+          if (n < N) mx = fmaxf(mx, acc[i][j][e]);
+          if (n < N && n == tgt && row < M) p.tlogit[row] = acc[i][j][e];
+        }
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      float sm = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int n = n0 + wn * 64 + j * 32 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
+          if (n < N) sm += expf(acc[i][j][e] - mx);
+        }
+      sm += __shfl_xor(sm, 32, 64);
+      if (lane < 32) {
+        red[0][wn][rl] = mx;
+        red[1][wn][rl] = sm;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < TM && m0 + threadIdx.x < M) {
+      const int r = threadIdx.x;
+      const float m1 = red[0][0][r], m2 = red[0][1][r], mx = fmaxf(m1, m2);
+      float sm = red[1][0][r] * expf(m1 - mx);
+      if (n0 + 64 < N) sm += red[1][1][r] * expf(m2 - mx);   // the second half holds words at all
+      const size_t at = (size_t)(m0 + r) * p.tiles + blockIdx.x;
+      p.pmax[at] = mx;
+      p.psum[at] = sm;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = m0 + wm * 64 + i * 32 + (lane & 31);
+    if (row >= M) continue;
+    float lse = 0.0f, dl = 0.0f;
+    int tgt = -1;
+    if constexpr (MODE == VL_GRAD) {
+      lse = p.lse[row];
+      tgt = p.target[row];
+      dl = tgt >= 0 && tgt < p.V ? p.dloss[row] : 0.0f;
+      tgt -= p.v0;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int n = n0 + wn * 64 + j * 32 + 8 * g + 4 * (lane >> 5);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * g + e];
+        if constexpr (MODE == VL_GRAD) {
+          if (n >= p.ldp) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float q = expf(v[e] - lse) - (n + e == tgt ? 1.0f : 0.0f);
+            v[e] = dl == 0.0f || n + e >= N ? 0.0f : dl * q;
+          }
+          store4(reinterpret_cast<T*>(p.p) + (size_t)row * p.ldp + n, v);
+        } else {
+          if (n >= N) continue;   // N = d, a multiple of 8
+          if constexpr (MODE == VL_DH) {
+            float* acc_row = p.dh_acc + (size_t)row * p.d + n;
+            if (!p.first) {
+              const float4 o = *reinterpret_cast<const float4*>(acc_row);
+              v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+            }
+            if (p.last) store4(reinterpret_cast<T*>(p.dh) + (size_t)row * p.d + n, v);
+            else store4(acc_row, v);
+          } else {
+            store4(reinterpret_cast<T*>(p.dw) + (size_t)(p.v0 + row) * p.d + n, v);
+          }
+        }
+      }
+  }
+}
+
+// Joins the tiles of a row in tile order, one wave per row.
+__global__ __launch_bounds__(NT) void vocab_lse_kernel(const float* pmax, const float* psum, const float* tlogit,
+                                                       const int32_t* target, int T, int V, int tiles, float* loss,
+                                                       float* lse) {
+  const int row = blockIdx.x * (NT / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (row >= T) return;
+  const float* m = pmax + (size_t)row * tiles;
+  const float* s = psum + (size_t)row * tiles;
+  float mx = -__builtin_inff();
+  for (int i = lane; i < tiles; i += 64) mx = fmaxf(mx, m[i]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  float sum = 0.0f;
+  for (int i = lane; i < tiles; i += 64) sum += s[i] * expf(m[i] - mx);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (lane == 0) {
+    const float l = mx + logf(sum);
+    const int t = target[row];
+    lse[row] = l;
+    loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(NT) void fill_zero_kernel(T* p, size_t n) {
+  for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < n; i += (size_t)gridDim.x * NT) p[i] = T(0);
+}
+
+inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Words per piece of the backward: P of about 2^26 elements, at least 4096 words.
+long long piece_words(long long T, long long V) {
+  const long long want = std::max<long long>(4096, ((1LL << 26) / std::max<long long>(T, 1)) / 256 * 256);
+  return std::min(want, (V + 255) / 256 * 256);
+}
+
+template <typename T, int MODE>
+hipError_t launch_tiles(const VocabArgs& p, hipStream_t s) {
+  const int M = MODE == VL_DW ? p.vn : p.T;
+  const int N = MODE == VL_DW || MODE == VL_DH ? p.d : (MODE == VL_GRAD ? std::min(p.ldp, ceil_div(p.vn, 8) * 8) : p.vn);
+  hipLaunchKernelGGL((vocab_tile_kernel<T, MODE>), dim3(ceil_div(N, TN), ceil_div(M, TM)), dim3(NT), 0, s, p);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t s) {
+  p.tiles = ceil_div(p.V, TN);
+  p.tlogit = reinterpret_cast<float*>(ws);
+  p.pmax = p.tlogit + align256((size_t)p.T * 4) / 4;
+  p.psum = p.pmax + (size_t)p.T * p.tiles;
+  p.v0 = 0;
+  p.vn = p.V;
+  hipError_t e = launch_tiles<T, VL_STATS>(p, s);
+  if (e != hipSuccess) return e;
+  vocab_lse_kernel<<<dim3(ceil_div(p.T, NT / 64)), dim3(NT), 0, s>>>(p.pmax, p.psum, p.tlogit, p.target, p.T, p.V,
+                                                                     p.tiles, loss, lse);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
+  if (p.T == 0) {
+    const size_t n = (size_t)p.V * p.d;
+    fill_zero_kernel<T><<<dim3((unsigned)std::min<size_t>((n + NT - 1) / NT, 8192)), dim3(NT), 0, s>>>((T*)p.dw, n);
+    return hipGetLastError();
+  }
+  const int words = (int)piece_words(p.T, p.V);
+  p.ldp = words;
+  p.dh_acc = reinterpret_cast<float*>(ws);
+  p.p = reinterpret_cast<char*>(ws) + align256((size_t)p.T * p.d * 4);
+  for (int v0 = 0; v0 < p.V; v0 += words) {
+    p.v0 = v0;
+    p.vn = std::min(words, p.V - v0);
+    p.first = v0 == 0;
+    p.last = v0 + words >= p.V;
+    hipError_t e = launch_tiles<T, VL_GRAD>(p, s);
+    if (e == hipSuccess) e = launch_tiles<T, VL_DH>(p, s);
+    if (e == hipSuccess) e = launch_tiles<T, VL_DW>(p, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t vocab_loss_ws_bytes(long long T, long long d, long long V, bool bf16) {
+  return align256((size_t)T * 4) + 2 * (size_t)T * ((V + TN - 1) / TN) * 4;
+}
+
+hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target, int T, int d, int V, bool bf16,
+                             float* loss, float* lse, void* ws, hipStream_t s) {
+  VocabArgs p{};
+  p.h = h; p.w = w; p.target = target; p.T = T; p.d = d; p.V = V;
+  return bf16 ? loss_fwd<bf16_t>(p, loss, lse, ws, s) : loss_fwd<float>(p, loss, lse, ws, s);
+}
+
+size_t vocab_loss_bwd_ws_bytes(long long T, long long d, long long V, bool bf16) {
+  if (T <= 0) return 0;
+  return align256((size_t)T * d * 4) + (size_t)T * piece_words(T, V) * (bf16 ? 2 : 4);
+}
+
+hipError_t launch_vocab_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse,
+                                 const float* dloss, int T, int d, int V, bool bf16, void* dh, void* dw, void* ws,
+                                 hipStream_t s) {
+  VocabArgs p{};
+  p.h = h; p.w = w; p.target = target; p.lse = lse; p.dloss = dloss; p.T = T; p.d = d; p.V = V; p.dh = dh; p.dw = dw;
+  return bf16 ? loss_bwd<bf16_t>(p, ws, s) : loss_bwd<float>(p, ws, s);
+}
+
+}  // namespace moe

@@ -147,14 +147,28 @@ class MoELayer:
     reuse them until ``refresh_mx_weights()`` is called, as when the weights change once per
     optimizer step and several micro-batches pass through the layer in between; otherwise every
     pass quantizes them.
+    ``block_norm``: the layer as a residual block: the router, the experts and the shared expert read
+    ``xn = rmsnorm(x) * norm_in``, and the output is ``res_scale * x + gate * (rmsnorm(y) * norm_out)``
+    with y the combined expert outputs.  ``params`` then holds ``norm_in``, ``norm_out`` [d] and, if
+    the block has a gate, ``norm_gate`` [ceil(T / gate_rows), d] (``gate_rows``: tokens per gate row,
+    by default all of them).  The backward adds the residual's gradient to dx and writes
+    ``dnorm_in``, ``dnorm_out`` and ``dnorm_gate`` (float).
     """
 
     def __init__(self, cfg: MoEConfig, params: dict, bufs: Buffers | None = None, renormalize: int = 1,
                  merge_shared: bool = True, recompute: bool = False, lbl_weight: float = 0.0,
-                 precision: str = "bf16", mx_cached_weights: bool = False):
+                 precision: str = "bf16", mx_cached_weights: bool = False, block_norm: bool = False,
+                 gate_rows: int | None = None, res_scale: float = 1.0, norm_eps: float = 1e-6):
         self.cfg = cfg
         self.p = params
         self.bufs = bufs or Buffers.allocate(cfg, params["x"].device)
+        self.norm = bool(block_norm)
+        self.gate_rows = cfg.T if gate_rows is None else int(gate_rows)
+        self.res_scale = float(res_scale)
+        self.norm_eps = float(norm_eps)
+        self._grads: L.GradList | None = None   # clip_gradients
+        if self.norm:
+            self._allocate_norm()
         self.renorm = renormalize
         self.merge = merge_shared
         self.recompute = recompute
@@ -187,6 +201,34 @@ class MoELayer:
             if cfg.fs > 0:
                 self.mx.append(MxSet(b["shared_offsets"], 1, cfg.T, cfg.d, cfg.fs, dev, cfg.backward))
 
+    @property
+    def x(self) -> torch.Tensor:
+        """What the router and the experts read."""
+        return self.bufs["xn"] if self.norm else self.p["x"]
+
+    def _allocate_norm(self):
+        c, p, t = self.cfg, self.p, self.bufs.t
+        dev = p["x"].device
+        f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=dev)
+        gate = p.get("norm_gate")
+        if self.gate_rows < 1:
+            raise ValueError("gate_rows must be >= 1")
+        if gate is not None and tuple(gate.shape) != (-(-c.T // self.gate_rows), c.d):
+            raise ValueError(f"norm_gate must be [ceil(T / gate_rows), d], got {tuple(gate.shape)}")
+        for name in ("norm_in", "norm_out"):
+            if tuple(p[name].shape) != (c.d,):
+                raise ValueError(f"{name} must be [d], got {tuple(p[name].shape)}")
+        for w in (p["norm_in"], p["norm_out"], gate):
+            if w is not None and w.dtype != p["x"].dtype:
+                raise ValueError("the norms' weights and gate must have x's dtype")
+        t["xn"] = torch.empty_like(p["x"])
+        t["rstd_in"], t["rstd_out"] = f32(c.T), f32(c.T)
+        if c.backward:
+            t["y_block"], t["dblock"], t["dxn"] = (torch.empty_like(p["x"]) for _ in range(3))
+            t["dnorm_in"], t["dnorm_out"] = f32(c.d), f32(c.d)
+            t["dnorm_gate"] = None if gate is None else f32(*gate.shape)
+            t["ws_norm"] = torch.empty(max(256, L.moe_norm_bwd_workspace_size(c.T, c.d)), dtype=torch.uint8, device=dev)
+
     def _sets(self, dout=None, stash=True):
         """The routed experts and (if any) the shared expert as expert sets; stash=False leaves out
         the pre-activation outputs A and B."""
@@ -200,7 +242,7 @@ class MoELayer:
                               dw2=g("dw2"))
         if fs == 0:
             return [routed]
-        shared = L.expert_set(b["shared_offsets"], 1, T, fs, x=p["x"], w1=p["ws1"], w3=p["ws3"], w2=p["ws2"],
+        shared = L.expert_set(b["shared_offsets"], 1, T, fs, x=self.x, w1=p["ws1"], w3=p["ws3"], w2=p["ws2"],
                               a=b["as"] if bw else None, b=b["bs"] if bw else None, h=b["hs"], y=b["s"],
                               dy=dout, dab=g("dabs"), dx=g("dx_shared"), dw1=g("dws1"), dw3=g("dws3"),
                               dw2=g("dws2"))
@@ -232,10 +274,12 @@ class MoELayer:
         Tk = T * k
         learned = c.routing == "learned"
         logits = b["logits"] if learned else p["logits"]
-        self._stage("route", L.moe_route, p["x"], p.get("w_router") if learned else None,
+        if self.norm:
+            self._stage("norm_in", L.moe_norm_in, p["x"], p["norm_in"], T, d, self.norm_eps, dt, b["xn"], b["rstd_in"])
+        self._stage("route", L.moe_route, self.x, p.get("w_router") if learned else None,
                     p.get("bias") if learned else None, logits, T, d, E, k, self.renorm, dt,
                     b["topk_idx"], b["gate"])
-        self._stage("permute", L.moe_permute, p["x"], b["topk_idx"], T, d, E, k, dt, b["counts"],
+        self._stage("permute", L.moe_permute, self.x, b["topk_idx"], T, d, E, k, dt, b["counts"],
                     b["offsets"], b["dest_pos"], b["src_row"], b["x_perm"], b["ws_perm"],
                     b["ws_perm"].numel())
         if self.lbl > 0:
@@ -248,6 +292,11 @@ class MoELayer:
             self._gemm("gate_up_fwd", L.MOE_STAGE_GATE_UP_FWD, sets, b["ws_fwd"])
             self._gemm("down_fwd", L.MOE_STAGE_DOWN_FWD, sets, b["ws_fwd"])
         shared = b["s"] if fs > 0 else None
+        if self.norm:
+            self._stage("combine_norm_out", L.moe_combine_norm_out, b["y"], b["gate"], b["dest_pos"], shared, p["x"],
+                        p["norm_out"], p.get("norm_gate"), self.gate_rows, self.res_scale, self.norm_eps, T, d, k, dt,
+                        b["y_block"] if c.backward else None, b["out"], b["rstd_out"])
+            return b["out"]
         self._stage("combine", L.moe_combine, b["y"], b["gate"], b["dest_pos"], shared, T, d, k, dt, b["out"])
         return b["out"]
 
@@ -257,25 +306,41 @@ class MoELayer:
         Tk = T * k
         dout = p["dout"] if dout is None else dout
         learned = c.routing == "learned"
+        if not self.norm:
+            return self._block_backward(dout, b["dx"])
+        self._stage("norm_out_bwd", L.moe_norm_out_bwd, dout, b["y_block"], p["norm_out"], p.get("norm_gate"),
+                    self.gate_rows, b["rstd_out"], T, d, dt, b["dblock"], b["dnorm_out"], b["dnorm_gate"], b["ws_norm"],
+                    b["ws_norm"].numel())
+        self._block_backward(b["dblock"], b["dxn"])
+        self._stage("norm_in_bwd", L.moe_norm_in_bwd, b["dxn"], p["x"], p["norm_in"], b["rstd_in"], dout,
+                    self.res_scale, T, d, dt, b["dx"], b["dnorm_in"], b["ws_norm"], b["ws_norm"].numel())
+        return b["dx"]
+
+    def _block_backward(self, dout, dx):
+        """The layer's own backward: dout is the gradient of the combined output, dx gets that of the
+        layer's input."""
+        c, p, b, dt = self.cfg, self.p, self.bufs, self.dt
+        T, d, E, k, f, fs = c.T, c.d, c.E, c.k, c.f, c.fs
+        learned = c.routing == "learned"
         self._stage("combine_bwd", L.moe_combine_bwd, dout, b["y"], b["gate"], b["dest_pos"], T, d, k, dt,
                     b["dy"], b["dgate"] if learned else None)
         dx_router = None
         if learned:
             self._stage("route_bwd", L.moe_route_bwd, b["dgate"], b["gate"], b["topk_idx"], b["offsets"],
-                        b["src_row"], p["x"], p["w_router"], T, d, E, k, self.renorm, dt, b["dwr"],
+                        b["src_row"], self.x, p["w_router"], T, d, E, k, self.renorm, dt, b["dwr"],
                         b["dx_router"], b["ws_route"], b["ws_route"].numel())
             dx_router = b["dx_router"]
             if self.lbl > 0:
-                self._stage("router_aux_bwd", L.moe_router_aux_bwd, b["logits"], b["load_frac"], p["x"],
+                self._stage("router_aux_bwd", L.moe_router_aux_bwd, b["logits"], b["load_frac"], self.x,
                             p["w_router"], T, d, E, self.lbl, dt, b["dwr"], b["dx_router"], b["ws_aux_bwd"],
                             b["ws_aux_bwd"].numel())
         dx_shared = b["dx_shared"] if fs > 0 else None
         if self.mx is not None:
             self._mx_dgrad(dout)
             self._stage("permute_bwd", L.moe_permute_bwd, b["dx_perm"], b["dest_pos"], dx_shared, dx_router, T,
-                        d, k, dt, b["dx"])
+                        d, k, dt, dx)
             self._mx_wgrad(dout)
-            return b["dx"]
+            return dx
         ws = b["ws_bwd"]
         sets = self._sets(dout)
         if self.recompute:
@@ -286,10 +351,10 @@ class MoELayer:
         self._gemm("down_bwd", L.MOE_STAGE_DOWN_BWD, sets, ws)
         self._gemm("gate_up_dgrad", L.MOE_STAGE_GATE_UP_DGRAD, sets, ws)
         self._stage("permute_bwd", L.moe_permute_bwd, b["dx_perm"], b["dest_pos"], dx_shared, dx_router, T, d,
-                    k, dt, b["dx"])
+                    k, dt, dx)
         self._gemm("down_wgrad", L.MOE_STAGE_DOWN_WGRAD, sets, ws)
         self._gemm("gate_up_wgrad", L.MOE_STAGE_GATE_UP_WGRAD, sets, ws)
-        return b["dx"]
+        return dx
 
     # ---- MXFP8 expert products -------------------------------------------------------------
     def _mx_tensors(self, i, dout=None):
@@ -299,7 +364,7 @@ class MoELayer:
             return dict(x=b["x_perm"], w1=p["w1"], w3=p["w3"], w2=p["w2"], a=t.get("a"), b=t.get("b"), h=b["h"],
                         y=b["y"], dy=t.get("dy"), dab=t.get("dab"), dx=t.get("dx_perm"), dw1=t.get("dw1"),
                         dw3=t.get("dw3"), dw2=t.get("dw2"))
-        return dict(x=p["x"], w1=p["ws1"], w3=p["ws3"], w2=p["ws2"], a=t.get("as"), b=t.get("bs"), h=b["hs"],
+        return dict(x=self.x, w1=p["ws1"], w3=p["ws3"], w2=p["ws2"], a=t.get("as"), b=t.get("bs"), h=b["hs"],
                     y=b["s"], dy=dout, dab=t.get("dabs"), dx=t.get("dx_shared"), dw1=t.get("dws1"),
                     dw3=t.get("dws3"), dw2=t.get("dws2"))
 
@@ -377,6 +442,33 @@ class MoELayer:
             self._stage(self._pfx(i, "gate_up_wgrad"), L.moe_mx_gemm_k, m.abc[0], m.abc[1], m.ld, m.xc[0],
                         m.xc[1], m.ld, m.kbase, G, 2 * f, d, f, t["dw1"], t["dw3"], m.ws_k,
                         m.ws_k.numel())
+
+    def gradients(self) -> list[torch.Tensor]:
+        """Every parameter gradient the backward writes (dx, the input's, is not among them)."""
+        t, c = self.bufs.t, self.cfg
+        names = ["dw1", "dw3", "dw2"]
+        if c.fs > 0:
+            names += ["dws1", "dws3", "dws2"]
+        if c.routing == "learned":
+            names.append("dwr")
+        if self.norm:
+            names += ["dnorm_in", "dnorm_out", "dnorm_gate"]
+        return [t[n] for n in names if t.get(n) is not None]
+
+    def clip_gradients(self, max_norm: float) -> torch.Tensor:
+        """Scale the gradients in place to a global norm of at most max_norm; returns the norm before
+        that ([1] float, on the device)."""
+        if not self.cfg.backward:
+            raise ValueError("the layer has no backward")
+        b, grads = self.bufs.t, self.gradients()
+        if self._grads is None or any(g is not h for g, h in zip(grads, self._grads.tensors[0])):
+            self._grads = L.grad_list(grads)
+            dev = self.p["x"].device
+            b["grad_norm"] = torch.empty(1, dtype=torch.float32, device=dev)
+            b["ws_grad"] = torch.empty(L.moe_grad_workspace_size(self._grads), dtype=torch.uint8, device=dev)
+        self._stage("grad_clip", L.moe_grad_clip, self._grads, max_norm, b["grad_norm"], b["ws_grad"],
+                    b["ws_grad"].numel())
+        return b["grad_norm"]
 
     def step(self):
         """One pass of the whole path: forward, then backward when the workload has one."""

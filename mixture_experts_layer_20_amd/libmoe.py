@@ -40,6 +40,7 @@ MOE_OP_ROUTER_AUX = 9
 MOE_OP_ROUTER_AUX_BWD = 10
 MOE_OP_MX_GEMM_ROWS = 11
 MOE_OP_MX_GEMM_K = 12
+MOE_OP_NORM_BWD = 13
 
 MOE_MX_EPI_STORE = 0
 MOE_MX_EPI_SWIGLU = 1
@@ -52,6 +53,7 @@ _P = _c.c_void_p
 _I64 = _c.c_int64
 _I32 = _c.c_int32
 _SZ = _c.c_size_t
+_F = _c.c_float
 
 
 
@@ -61,6 +63,11 @@ class ExpertSet(ctypes.Structure):
                 ("f", ctypes.c_int64)] + [(n, ctypes.c_void_p) for n in
                                           ("x", "w1", "w3", "w2", "a", "b", "h", "y", "dy", "dab", "dx", "dw1",
                                            "dw3", "dw2")]
+
+
+class Grad(ctypes.Structure):
+    """moe_grad_t: one tensor of a gradient list."""
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dt", ctypes.c_int32)]
 
 
 # name -> (restype, argtypes); mirrors include/libmoe.h
@@ -95,6 +102,21 @@ _SIGS = {
     "moe_router_aux_bwd": (_I32, [_P, _P, _P, _P, _I64, _I64, _I32, _c.c_float, _I32, _P, _P, _P, _SZ, _P]),
     "moe_route_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P,
                              _P, _SZ, _P]),
+    "moe_norm_in": (_I32, [_P, _P, _I64, _I64, _F, _I32, _P, _P, _P]),
+    "moe_norm_out": (_I32, [_P, _P, _P, _P, _I64, _F, _F, _I64, _I64, _I32, _P, _P, _P]),
+    "moe_combine_norm_out": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I64, _F, _F, _I64, _I64, _I32, _I32, _P, _P, _P,
+                                    _P]),
+    "moe_norm_bwd_workspace_size": (_SZ, [_I64, _I64]),
+    "moe_norm_out_bwd": (_I32, [_P, _P, _P, _P, _I64, _P, _I64, _I64, _I32, _P, _P, _P, _P, _SZ, _P]),
+    "moe_norm_in_bwd": (_I32, [_P, _P, _P, _P, _P, _F, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
+    "moe_vocab_loss_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "moe_vocab_loss": (_I32, [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
+    "moe_vocab_loss_bwd_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
+    "moe_vocab_loss_bwd": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
+    "moe_grad_workspace_size": (_SZ, [_P, _I32]),
+    "moe_grad_norm": (_I32, [_P, _I32, _P, _P, _P, _SZ, _P]),
+    "moe_grad_scale": (_I32, [_P, _I32, _P, _F, _P, _P]),
+    "moe_grad_clip": (_I32, [_P, _I32, _F, _P, _P, _SZ, _P]),
     "moe_mx_quantize_rows": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P]),
     "moe_mx_quantize_cols_ld": (_I64, [_I64, _I32, _I32]),
     "moe_mx_quantize_cols": (_I32, [_P, _I64, _I64, _I64, _P, _I32, _I64, _I32, _P, _P, _I64, _P, _P]),
@@ -326,6 +348,92 @@ def moe_router_aux_bwd(logits, load_frac, x, w_router, T, d, E, weight, dt, dw_r
                        stream=None):
     _call("moe_router_aux_bwd", _ptr(logits), _ptr(load_frac), _ptr(x), _ptr(w_router), T, d, E, weight, dt,
           _ptr(dw_router), _ptr(dx_router), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_norm_in(x, w, T, d, eps, dt, xn, rstd, stream=None):
+    _call("moe_norm_in", _ptr(x), _ptr(w), T, d, eps, dt, _ptr(xn), _ptr(rstd), _stream(stream))
+
+
+def moe_norm_out(y, x, w, gate, gate_rows, res_scale, eps, T, d, dt, out, rstd, stream=None):
+    _call("moe_norm_out", _ptr(y), _ptr(x), _ptr(w), _ptr(gate), gate_rows, res_scale, eps, T, d, dt, _ptr(out),
+          _ptr(rstd), _stream(stream))
+
+
+def moe_combine_norm_out(y_perm, topk_gate, dest_pos, shared_out, x, w, gate, gate_rows, res_scale, eps, T, d, k, dt,
+                         y, out, rstd, stream=None):
+    _call("moe_combine_norm_out", _ptr(y_perm), _ptr(topk_gate), _ptr(dest_pos), _ptr(shared_out), _ptr(x), _ptr(w),
+          _ptr(gate), gate_rows, res_scale, eps, T, d, k, dt, _ptr(y), _ptr(out), _ptr(rstd), _stream(stream))
+
+
+def moe_norm_bwd_workspace_size(T, d) -> int:
+    return lib().moe_norm_bwd_workspace_size(T, d)
+
+
+def moe_norm_out_bwd(dout, y, w, gate, gate_rows, rstd, T, d, dt, dy, dw, dgate, ws, ws_bytes, stream=None):
+    _call("moe_norm_out_bwd", _ptr(dout), _ptr(y), _ptr(w), _ptr(gate), gate_rows, _ptr(rstd), T, d, dt, _ptr(dy),
+          _ptr(dw), _ptr(dgate), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_norm_in_bwd(dxn, x, w, rstd, dres, res_scale, T, d, dt, dx, dw, ws, ws_bytes, stream=None):
+    _call("moe_norm_in_bwd", _ptr(dxn), _ptr(x), _ptr(w), _ptr(rstd), _ptr(dres), res_scale, T, d, dt, _ptr(dx),
+          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_vocab_loss_workspace_size(T, d, V, dt) -> int:
+    return lib().moe_vocab_loss_workspace_size(T, d, V, dt)
+
+
+def moe_vocab_loss(h, w, target, T, d, V, dt, loss, lse, ws, ws_bytes, stream=None):
+    _call("moe_vocab_loss", _ptr(h), _ptr(w), _ptr(target), T, d, V, dt, _ptr(loss), _ptr(lse), _ptr(ws), ws_bytes,
+          _stream(stream))
+
+
+def moe_vocab_loss_bwd_workspace_size(T, d, V, dt) -> int:
+    return lib().moe_vocab_loss_bwd_workspace_size(T, d, V, dt)
+
+
+def moe_vocab_loss_bwd(h, w, target, lse, dloss, T, d, V, dt, dh, dw, ws, ws_bytes, stream=None):
+    _call("moe_vocab_loss_bwd", _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), T, d, V, dt, _ptr(dh),
+          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream))
+
+
+class GradList:
+    """A list of gradient tensors in the form the moe_grad_* calls take.  It holds the tensors, so
+    their memory lives as long as the list; values are read when a call's kernels run."""
+
+    def __init__(self, grads, outs):
+        self.tensors = (list(grads), list(outs))
+        self.count = len(self.tensors[0])
+        if len(self.tensors[1]) != self.count:
+            raise ValueError("grads and outs differ in length")
+        self.array = (Grad * max(1, self.count))()
+        for e, g, o in zip(self.array, *self.tensors):
+            if o is not None and (o.dtype != g.dtype or o.numel() != g.numel()):
+                raise ValueError("an out must have its gradient's dtype and size")
+            e.grad, e.out, e.n, e.dt = _ptr(g), _ptr(o), g.numel(), dtype_code(g)
+        self.ptr = ctypes.cast(self.array, _P)
+
+
+def grad_list(grads, outs=None) -> GradList:
+    """The gradient tensors, with the tensors their scaled values go to (default: in place)."""
+    grads = list(grads)
+    return GradList(grads, grads if outs is None else outs)
+
+
+def moe_grad_workspace_size(grads: GradList) -> int:
+    return lib().moe_grad_workspace_size(grads.ptr, grads.count)
+
+
+def moe_grad_norm(grads: GradList, sumsq, norm, ws, ws_bytes, stream=None):
+    _call("moe_grad_norm", grads.ptr, grads.count, _ptr(sumsq), _ptr(norm), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_grad_scale(grads: GradList, sumsq, max_norm, norm, stream=None):
+    _call("moe_grad_scale", grads.ptr, grads.count, _ptr(sumsq), max_norm, _ptr(norm), _stream(stream))
+
+
+def moe_grad_clip(grads: GradList, max_norm, norm, ws, ws_bytes, stream=None):
+    _call("moe_grad_clip", grads.ptr, grads.count, max_norm, _ptr(norm), _ptr(ws), ws_bytes, _stream(stream))
 
 
 def moe_mx_quantize_rows(x, R, K, ldx, codes, scales, stream=None):
