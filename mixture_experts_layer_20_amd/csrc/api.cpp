@@ -13,6 +13,7 @@
 #include <new>
 #include <string>
 
+#include "block_step.h"
 #include "common.h"
 #include "mxfp8.h"
 

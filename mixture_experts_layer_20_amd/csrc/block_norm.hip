@@ -11,7 +11,7 @@
 // so one column sum S per gate row gives both parameter gradients.
 //
 // Every sum, norm and statistic is fp32; a value is rounded to the storage type once, at its store.
-#include "common.h"
+#include "block_step.h"
 
 #include <algorithm>
 

@@ -10,7 +10,7 @@
 //
 // The tensor list travels in the kernel arguments (kTable tensors per launch), so a call needs no
 // copy to the device and can be captured.
-#include "common.h"
+#include "block_step.h"
 
 #include <algorithm>
 

@@ -9,7 +9,7 @@
 // the vocabulary at a time, its epilogue writes P of the piece (in the storage type: the operand of
 // the two gradient products), and dh accumulates over the pieces in fp32.
 // A target outside [0, V) marks a row without loss: loss 0, P = 0 exactly.
-#include "common.h"
+#include "block_step.h"
 
 #include <algorithm>
 
