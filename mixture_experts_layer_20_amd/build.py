@@ -20,7 +20,8 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libmoe.so")
 
 SOURCES = ["api.cpp", "route.hip", "router_aux.hip", "dispatch.hip", "combine.hip", "grouped_gemm.hip",
-           "grouped_gemm_pipe.hip", "mxfp8.hip", "block_norm.hip", "vocab_loss.hip", "grad_clip.hip"]
+           "grouped_gemm_pipe.hip", "mxfp8.hip", "block_norm.hip", "vocab_loss.hip",
+           "vocab_loss_pipe.hip", "grad_clip.hip"]
 
 ARCH = "gfx950"
 # Packed fp32 instructions stay off: plain scalar fp32 code only.

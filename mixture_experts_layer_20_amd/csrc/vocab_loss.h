@@ -1,0 +1,41 @@
+// Shared by the two kernels of the vocabulary loss.
+#pragma once
+
+#include "block_step.h"
+
+namespace moe {
+namespace vocab {
+
+struct VocabArgs {
+  const void* h;
+  const void* w;
+  const int32_t* target;
+  const float* lse;
+  const float* dloss;
+  int T, d, V;
+  int v0, vn;         // the piece: words v0 .. v0 + vn - 1
+  int ldp;            // row length of P, a multiple of 256
+  void* p;            // [T, ldp]; columns vn.. of a piece are zero as far as its last tile reaches
+  float2* part;       // [ceil(V / 64)][T] maximum and sum of exponentials of 64 words
+  float* dh_acc;      // dh of the pieces so far, fp32
+  void* dh;
+  void* dw;
+  bool first, last;   // the piece is the first / the last one
+};
+
+enum VocabMode { VL_STATS = 0, VL_GRAD = 1, VL_DH = 2, VL_DW = 3 };
+
+constexpr int WORDS_PER_PART = 64;
+constexpr int NUM_CUS = 256;
+
+inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
+
+// The pipelined bf16 kernel (256x256 tiles).  dh_acc holds the accumulator tiles of pipe_splits()
+// partial products in the kernel's own order; pipe_join adds them into dh.
+int pipe_splits(int T, int d, int words);
+size_t pipe_acc_bytes(int T, int d, int words);
+hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s);
+hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s);
+
+}  // namespace vocab
+}  // namespace moe

@@ -4,12 +4,11 @@
 //   P = dloss_t (exp(l_tv - lse_t) - [v = target_t]),  dh = P w,  dw = P^T h
 //
 // The logits are never stored.  Forward: each tile of the product keeps, per row, the maximum and
-// the sum of exponentials of its columns (and the target's logit where the target lies in it); a
-// second kernel joins a row's tiles in order.  Backward: the product is formed again one piece of
+// the sum of exponentials of each 64 of its columns; a second kernel joins a row's parts in order.  Backward: the product is formed again one piece of
 // the vocabulary at a time, its epilogue writes P of the piece (in the storage type: the operand of
 // the two gradient products), and dh accumulates over the pieces in fp32.
 // A target outside [0, V) marks a row without loss: loss 0, P = 0 exactly.
-#include "block_step.h"
+#include "vocab_loss.h"
 
 #include <algorithm>
 
@@ -20,27 +19,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-struct VocabArgs {
-  const void* h;
-  const void* w;
-  const int32_t* target;
-  const float* lse;
-  const float* dloss;
-  int T, d, V;
-  int v0, vn;         // the piece: words v0 .. v0 + vn - 1
-  int ldp;            // row length of P
-  void* p;            // [T, ldp]
-  float* pmax;        // [T, tiles] per-tile maxima, then [T, tiles] sums
-  float* psum;
-  int tiles;
-  float* tlogit;      // [T] logit of the target
-  float* dh_acc;      // [T, d] fp32
-  void* dh;
-  void* dw;
-  bool first, last;   // the piece is the first / the last one
-};
-
-enum VocabMode { VL_STATS = 0, VL_GRAD = 1, VL_DH = 2, VL_DW = 3 };
+using namespace vocab;
 
 // ---------------------------------------------------------------------------------------------
 // 128x128 tiles, four waves of 64x64, operands staged through registers: any T, V and d (a multiple
@@ -107,7 +86,6 @@ __global__ __launch_bounds__(NT) void vocab_tile_kernel(VocabArgs p) {
   constexpr int BK = Cfg<T>::BK, LD = Cfg<T>::LD;
   __shared__ __attribute__((aligned(16))) T sa[TM * LD];
   __shared__ __attribute__((aligned(16))) T sb[TN * LD];
-  __shared__ float red[2][2][TM];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int wm = wave >> 1, wn = wave & 1;
   const T* h = reinterpret_cast<const T*>(p.h);
@@ -183,43 +161,27 @@ __global__ __launch_bounds__(NT) void vocab_tile_kernel(VocabArgs p) {
   // Lane l holds row l % 32 of block i and, in element v, column 8 (v / 4) + 4 (l / 32) + v % 4 of
   // block j.
   if constexpr (MODE == VL_STATS) {
+    const int c0 = n0 + wn * 64;   // this wave's part: 64 words
+    if (c0 >= N) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int rl = wm * 64 + i * 32 + (lane & 31), row = m0 + rl;
-      const int tgt = row < M ? p.target[row] - p.v0 : -1;
+      const int row = m0 + wm * 64 + i * 32 + (lane & 31);
       float mx = -__builtin_inff();
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int n = n0 + wn * 64 + j * 32 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-          if (n < N) mx = fmaxf(mx, acc[i][j][e]);
-          if (n < N && n == tgt && row < M) p.tlogit[row] = acc[i][j][e];
+          if (c0 + j * 32 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4 >= N) acc[i][j][e] = -__builtin_inff();
+          mx = fmaxf(mx, acc[i][j][e]);
         }
       mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
       float sm = 0.0f;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int n = n0 + wn * 64 + j * 32 + 8 * (e / 4) + 4 * (lane >> 5) + e % 4;
-          if (n < N) sm += expf(acc[i][j][e] - mx);
-        }
+        for (int e = 0; e < 16; ++e) sm += expf(acc[i][j][e] - mx);
       sm += __shfl_xor(sm, 32, 64);
-      if (lane < 32) {
-        red[0][wn][rl] = mx;
-        red[1][wn][rl] = sm;
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < TM && m0 + threadIdx.x < M) {
-      const int r = threadIdx.x;
-      const float m1 = red[0][0][r], m2 = red[0][1][r], mx = fmaxf(m1, m2);
-      float sm = red[1][0][r] * expf(m1 - mx);
-      if (n0 + 64 < N) sm += red[1][1][r] * expf(m2 - mx);   // the second half holds words at all
-      const size_t at = (size_t)(m0 + r) * p.tiles + blockIdx.x;
-      p.pmax[at] = mx;
-      p.psum[at] = sm;
+      if (lane < 32 && row < M) p.part[(size_t)((p.v0 + c0) / WORDS_PER_PART) * p.T + row] = make_float2(mx, sm);
     }
     return;
   }
@@ -269,28 +231,61 @@ __global__ __launch_bounds__(NT) void vocab_tile_kernel(VocabArgs p) {
   }
 }
 
-// Joins the tiles of a row in tile order, one wave per row.
-__global__ __launch_bounds__(NT) void vocab_lse_kernel(const float* pmax, const float* psum, const float* tlogit,
-                                                       const int32_t* target, int T, int V, int tiles, float* loss,
-                                                       float* lse) {
-  const int row = blockIdx.x * (NT / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (row >= T) return;
-  const float* m = pmax + (size_t)row * tiles;
-  const float* s = psum + (size_t)row * tiles;
-  float mx = -__builtin_inff();
-  for (int i = lane; i < tiles; i += 64) mx = fmaxf(mx, m[i]);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
-  float sum = 0.0f;
-  for (int i = lane; i < tiles; i += 64) sum += s[i] * expf(m[i] - mx);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
-  if (lane == 0) {
-    const float l = mx + logf(sum);
-    const int t = target[row];
-    lse[row] = l;
-    loss[row] = t >= 0 && t < V ? l - tlogit[row] : 0.0f;
+// Joins a row's parts, 16 rows of 16 slices per workgroup (slice s takes parts s, s + 16, ..., and the
+// slices are joined in order), and forms the target's logit as a product of its own, which spares
+// the tiles a search for it: 2 T d elements read beside the product's V d.
+constexpr int JR = 16;
+template <typename T>
+__global__ __launch_bounds__(JR * 16) void vocab_lse_kernel(VocabArgs p, int parts, float* loss, float* lse) {
+  __shared__ float2 sl[16][JR + 1];
+  __shared__ float dot[JR];
+  const int r0 = blockIdx.x * JR;
+  {
+    const int r = threadIdx.x % JR, slice = threadIdx.x / JR, row = min(r0 + r, p.T - 1);
+    float mx = -__builtin_inff(), sum = 0.0f;
+    for (int i = slice; i < parts; i += 16) {
+      const float2 v = p.part[(size_t)i * p.T + row];
+      const float m = fmaxf(mx, v.x);
+      sum = sum * expf(mx - m) + v.y * expf(v.x - m);
+      mx = m;
+    }
+    sl[slice][r] = make_float2(mx, sum);
   }
+  {
+    const int r = threadIdx.x / 16, s = threadIdx.x % 16, row = min(r0 + r, p.T - 1);
+    const int t = p.target[row];
+    constexpr int E = 16 / sizeof(T);
+    float a = 0.0f;
+    if (t >= 0 && t < p.V) {
+      const T* h = reinterpret_cast<const T*>(p.h) + (size_t)row * p.d;
+      const T* w = reinterpret_cast<const T*>(p.w) + (size_t)t * p.d;
+      for (int c = s * E; c < p.d; c += 16 * E) {
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(h + c), y = *reinterpret_cast<const u32x4_t*>(w + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (E == 8) {
+            a += __uint_as_float(x[e] << 16) * __uint_as_float(y[e] << 16);
+            a += __uint_as_float(x[e] & 0xffff0000u) * __uint_as_float(y[e] & 0xffff0000u);
+          } else {
+            a += __uint_as_float(x[e]) * __uint_as_float(y[e]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
+    if (s == 0) dot[r] = a;
+  }
+  __syncthreads();
+  const int row = r0 + threadIdx.x;
+  if (threadIdx.x >= JR || row >= p.T) return;
+  float mx = -__builtin_inff(), sum = 0.0f;
+  for (int s = 0; s < min(16, parts); ++s) mx = fmaxf(mx, sl[s][threadIdx.x].x);
+  for (int s = 0; s < min(16, parts); ++s) sum += sl[s][threadIdx.x].y * expf(sl[s][threadIdx.x].x - mx);
+  const float l = mx + logf(sum);
+  const int t = p.target[row];
+  lse[row] = l;
+  loss[row] = t >= 0 && t < p.V ? l - dot[threadIdx.x] : 0.0f;
 }
 
 template <typename T>
@@ -298,13 +293,17 @@ __global__ __launch_bounds__(NT) void fill_zero_kernel(T* p, size_t n) {
   for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < n; i += (size_t)gridDim.x * NT) p[i] = T(0);
 }
 
-inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
-
-// Words per piece of the backward: P of about 2^26 elements, at least 4096 words.
-long long piece_words(long long T, long long V) {
-  const long long want = std::max<long long>(4096, ((1LL << 26) / std::max<long long>(T, 1)) / 256 * 256);
-  return std::min(want, (V + 255) / 256 * 256);
+// Words per piece of the backward, a multiple of 256: pieces of one size, P of about 2^26 elements
+// and at least 4096 words.
+int piece_words(long long T, long long V) {
+  const long long want = std::max<long long>(4096, (1LL << 26) / std::max<long long>(T, 1));
+  const long long pieces = (V + want - 1) / want;
+  return (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
 }
+
+int parts_of(long long V) { return (int)((V + WORDS_PER_PART - 1) / WORDS_PER_PART); }
+
+bool use_pipe(int T, int d, int V, bool bf16) { return bf16; }
 
 template <typename T, int MODE>
 hipError_t launch_tiles(const VocabArgs& p, hipStream_t s) {
@@ -316,17 +315,18 @@ hipError_t launch_tiles(const VocabArgs& p, hipStream_t s) {
 
 template <typename T>
 hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t s) {
-  p.tiles = ceil_div(p.V, TN);
-  p.tlogit = reinterpret_cast<float*>(ws);
-  p.pmax = p.tlogit + align256((size_t)p.T * 4) / 4;
-  p.psum = p.pmax + (size_t)p.T * p.tiles;
+  p.part = reinterpret_cast<float2*>(ws);
   p.v0 = 0;
   p.vn = p.V;
-  hipError_t e = launch_tiles<T, VL_STATS>(p, s);
+  const hipError_t e = use_pipe(p.T, p.d, p.V, sizeof(T) == 2) ? launch_pipe(VL_STATS, p, s) : launch_tiles<T, VL_STATS>(p, s);
   if (e != hipSuccess) return e;
-  vocab_lse_kernel<<<dim3(ceil_div(p.T, NT / 64)), dim3(NT), 0, s>>>(p.pmax, p.psum, p.tlogit, p.target, p.T, p.V,
-                                                                     p.tiles, loss, lse);
+  vocab_lse_kernel<T><<<dim3(ceil_div(p.T, JR)), dim3(JR * 16), 0, s>>>(p, parts_of(p.V), loss, lse);
   return hipGetLastError();
+}
+
+// Bytes of the accumulated dh.
+size_t acc_bytes(int T, int d, int V, bool bf16) {
+  return align256(use_pipe(T, d, V, bf16) ? pipe_acc_bytes(T, d, piece_words(T, V)) : (size_t)T * d * 4);
 }
 
 template <typename T>
@@ -336,27 +336,28 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
     fill_zero_kernel<T><<<dim3((unsigned)std::min<size_t>((n + NT - 1) / NT, 8192)), dim3(NT), 0, s>>>((T*)p.dw, n);
     return hipGetLastError();
   }
-  const int words = (int)piece_words(p.T, p.V);
+  const int words = piece_words(p.T, p.V);
+  const bool pipe = use_pipe(p.T, p.d, p.V, sizeof(T) == 2);
   p.ldp = words;
   p.dh_acc = reinterpret_cast<float*>(ws);
-  p.p = reinterpret_cast<char*>(ws) + align256((size_t)p.T * p.d * 4);
+  p.p = reinterpret_cast<char*>(ws) + acc_bytes(p.T, p.d, p.V, sizeof(T) == 2);
   for (int v0 = 0; v0 < p.V; v0 += words) {
     p.v0 = v0;
     p.vn = std::min(words, p.V - v0);
     p.first = v0 == 0;
     p.last = v0 + words >= p.V;
-    hipError_t e = launch_tiles<T, VL_GRAD>(p, s);
-    if (e == hipSuccess) e = launch_tiles<T, VL_DH>(p, s);
-    if (e == hipSuccess) e = launch_tiles<T, VL_DW>(p, s);
+    hipError_t e = pipe ? launch_pipe(VL_GRAD, p, s) : launch_tiles<T, VL_GRAD>(p, s);
+    if (e == hipSuccess) e = pipe ? launch_pipe(VL_DH, p, s) : launch_tiles<T, VL_DH>(p, s);
+    if (e == hipSuccess) e = pipe ? launch_pipe(VL_DW, p, s) : launch_tiles<T, VL_DW>(p, s);
     if (e != hipSuccess) return e;
   }
-  return hipSuccess;
+  return pipe ? launch_pipe_join(p, s) : hipSuccess;
 }
 
 }  // namespace
 
 size_t vocab_loss_ws_bytes(long long T, long long d, long long V, bool bf16) {
-  return align256((size_t)T * 4) + 2 * (size_t)T * ((V + TN - 1) / TN) * 4;
+  return (size_t)T * parts_of(V) * sizeof(float2);
 }
 
 hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target, int T, int d, int V, bool bf16,
@@ -368,7 +369,7 @@ hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target
 
 size_t vocab_loss_bwd_ws_bytes(long long T, long long d, long long V, bool bf16) {
   if (T <= 0) return 0;
-  return align256((size_t)T * d * 4) + (size_t)T * piece_words(T, V) * (bf16 ? 2 : 4);
+  return acc_bytes((int)T, (int)d, (int)V, bf16) + (size_t)T * piece_words(T, V) * (bf16 ? 2 : 4);
 }
 
 hipError_t launch_vocab_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse,
