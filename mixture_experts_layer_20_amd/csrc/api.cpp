@@ -774,7 +774,7 @@ struct GradList {
   long long chunks = 0;
 };
 
-constexpr int64_t kGradMaxElements = int64_t(1) << 48;
+constexpr int64_t kGradMaxElements = int64_t(1) << 41;   // a chunk then has fewer than 2^31
 
 moe_status_t grad_list(const moe_grad_t* grads, int32_t count, bool scale, GradList& list) {
   CHECK(count >= 0, MOE_ERR_INVALID_VALUE, "count must be >= 0 (got %d)", count);
@@ -788,7 +788,7 @@ moe_status_t grad_list(const moe_grad_t* grads, int32_t count, bool scale, GradL
     moe_status_t st = check_dtype(g.dt);
     if (st != MOE_OK) return st;
     CHECK(g.n >= 0, MOE_ERR_INVALID_VALUE, "gradient %d has n = %lld", i, (long long)g.n);
-    CHECK(g.n <= kGradMaxElements - total, MOE_ERR_UNSUPPORTED, "more than 2^48 gradient elements");
+    CHECK(g.n <= kGradMaxElements - total, MOE_ERR_UNSUPPORTED, "more than 2^41 gradient elements");
     total += g.n;
     CHECK(g.n == 0 || (g.grad && (!scale || g.out)), MOE_ERR_INVALID_VALUE, "gradient %d: grad/out is NULL", i);
     CHECK(aligned16({g.grad, scale ? g.out : nullptr}), MOE_ERR_INVALID_VALUE,
@@ -870,7 +870,7 @@ moe_status_t moe_grad_scale(const moe_grad_t* grads, int32_t count, const double
     if (!norm) return MOE_OK;
     return hip_check(moe::launch_grad_total(sumsq, 1, nullptr, norm, S(stream)), "gradient norm");
   }
-  return hip_check(moe::launch_grad_scale(list.items.get(), count, sumsq, 1, max_norm, norm, S(stream)),
+  return hip_check(moe::launch_grad_scale(list.items.get(), count, const_cast<double*>(sumsq), 1, max_norm, norm, S(stream)),
                    "gradient scaling");
 }
 

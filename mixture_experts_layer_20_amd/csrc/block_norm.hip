@@ -20,11 +20,15 @@ namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-// 8 consecutive elements, as loaded and widened.
+// 8 consecutive elements, as loaded and widened.  load_once: a stream that nothing reads again soon (a
+// nontemporal load).
 template <typename T> struct Seg8;
 template <> struct Seg8<bf16_t> {
   u32x4_t w;
   __device__ __forceinline__ void load(const bf16_t* p) { w = *reinterpret_cast<const u32x4_t*>(p); }
+  __device__ __forceinline__ void load_once(const bf16_t* p) {
+    w = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  }
   __device__ __forceinline__ void zero() { w = u32x4_t{0, 0, 0, 0}; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
@@ -46,6 +50,7 @@ template <> struct Seg8<float> {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
   }
+  __device__ __forceinline__ void load_once(const float* p) { load(p); }
   __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -57,18 +62,23 @@ template <> struct Seg8<float> {
   }
 };
 
-constexpr int NT = 256;   // threads of a workgroup
+constexpr int NT = 256;   // threads of a workgroup, or L where a row takes more
+template <int L>
+constexpr int threads() { return L < NT ? NT : L; }
 
-// Sum over the L lanes that share a row (L = 64: a wave; L = 256: the workgroup, one row at a time).
+// Sum over the L lanes that share a row (L = 64: a wave; otherwise the workgroup, one row at a time).
 // `red` holds one value per wave and slot; two slots alternate, so one barrier per sum is enough.
 template <int L>
-__device__ __forceinline__ float row_sum(float s, float (&red)[2][NT / 64], int& slot) {
+__device__ __forceinline__ float row_sum(float s, float (&red)[2][16], int& slot) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
-  if constexpr (L == NT) {
+  if constexpr (L > 64) {
     if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = s;
     __syncthreads();
-    s = (red[slot][0] + red[slot][1]) + (red[slot][2] + red[slot][3]);
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < L / 64; i += 4)
+      s += (red[slot][i] + red[slot][i + 1]) + (red[slot][i + 2] + red[slot][i + 3]);
     slot ^= 1;
   }
   return s;
@@ -86,12 +96,12 @@ __device__ __forceinline__ Cols cols(int lane, int i, int d) {
 }
 
 template <typename T, int L, int NV>
-__global__ __launch_bounds__(NT) void norm_in_kernel(const T* x, const T* w, int rows, int d, float eps, T* xn,
+__global__ __launch_bounds__(threads<L>()) void norm_in_kernel(const T* x, const T* w, int rows, int d, float eps, T* xn,
                                                      float* rstd) {
-  __shared__ float red[2][NT / 64];
+  __shared__ float red[2][16];
   const int lane = threadIdx.x % L;
-  const int t = blockIdx.x * (NT / L) + threadIdx.x / L;
-  if (t >= rows) return;   // L = NT: the whole workgroup; L = 64: whole waves, no barrier below
+  const int t = blockIdx.x * (threads<L>() / L) + threadIdx.x / L;
+  if (t >= rows) return;   // L = 64: whole waves, no barrier below; otherwise there are no such rows
   int slot = 0;
   Seg8<T> xr[NV], wr[NV];
 #pragma unroll
@@ -129,47 +139,72 @@ __global__ __launch_bounds__(NT) void norm_in_kernel(const T* x, const T* w, int
 
 // The norm after the block.  COMBINE: y is the layer's weighted combine of k rows of y_perm and the
 // shared expert's row, summed in fp32 in the order of combine_kernel (slots, then the shared row) and
-// normalised unrounded; y_out (if given) gets it rounded, for the backward.
+// normalised unrounded; y_out (if given) gets it rounded, for the backward.  Up to four expert rows
+// are loaded before the first is used, and the residual, weight and gate before the row's statistic
+// is known.
 template <typename T, int L, int NV, bool COMBINE>
-__global__ __launch_bounds__(NT) void norm_out_kernel(const T* y, const float* topk_gate, const int32_t* dest_pos,
+__global__ __launch_bounds__(threads<L>()) void norm_out_kernel(const T* y, const float* topk_gate, const int32_t* dest_pos,
                                                       const T* shared, int k, const T* x, const T* w, const T* gate,
                                                       int gate_rows, float res_scale, int rows, int d, float eps,
                                                       T* y_out, T* out, float* rstd) {
-  __shared__ float red[2][NT / 64];
+  __shared__ float red[2][16];
   const int lane = threadIdx.x % L;
-  const int t = blockIdx.x * (NT / L) + threadIdx.x / L;
+  const int t = blockIdx.x * (threads<L>() / L) + threadIdx.x / L;
   if (t >= rows) return;
   int slot = 0;
   float yv[NV][8];
+  Seg8<T> xr[NV], wr[NV], gr[NV], sr[NV];
+  const T* grow = gate ? gate + (size_t)(t / gate_rows) * d : nullptr;
+  auto load = [&](Seg8<T> (&r)[NV], const T* from) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Cols q = cols<L>(lane, i, d);
+      if (q.in) r[i].load(from + q.c);
+      else r[i].zero();
+    }
+  };
   if constexpr (COMBINE) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) yv[i][e] = 0.0f;
-    for (int j = 0; j < k; ++j) {
-      const size_t row = (size_t)dest_pos[(size_t)t * k + j] * d;
-      const float g = topk_gate[(size_t)t * k + j];
+    constexpr int G = 4;   // rows in flight
+    for (int j0 = 0; j0 < k; j0 += G) {
+      Seg8<T> r[G][NV];
+      float g[G];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Cols q = cols<L>(lane, i, d);
-        if (!q.in) continue;
-        Seg8<T> seg;
-        float v[8];
-        seg.load(y + row + q.c);
-        seg.get(v);
+      for (int u = 0; u < G; ++u)
+        if (j0 + u < k) {
+          g[u] = topk_gate[(size_t)t * k + j0 + u];
+          const T* row = y + (size_t)dest_pos[(size_t)t * k + j0 + u] * d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) yv[i][e] += g * v[e];
+          for (int i = 0; i < NV; ++i) {
+            const Cols q = cols<L>(lane, i, d);
+            if (q.in) r[u][i].load_once(row + q.c);
+            else r[u][i].zero();
+          }
+        }
+      if (j0 == 0) {
+        if (shared) load(sr, shared + (size_t)t * d);
+        load(xr, x + (size_t)t * d);
       }
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+        if (j0 + u < k) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            float v[8];
+            r[u][i].get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) yv[i][e] += g[u] * v[e];
+          }
+        }
     }
     if (shared) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const Cols q = cols<L>(lane, i, d);
-        if (!q.in) continue;
-        Seg8<T> seg;
         float v[8];
-        seg.load(shared + (size_t)t * d + q.c);
-        seg.get(v);
+        sr[i].get(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) yv[i][e] += v[e];
       }
@@ -182,15 +217,13 @@ __global__ __launch_bounds__(NT) void norm_out_kernel(const T* y, const float* t
       }
     }
   } else {
+    load(sr, y + (size_t)t * d);
+    load(xr, x + (size_t)t * d);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const Cols q = cols<L>(lane, i, d);
-      Seg8<T> seg;
-      seg.zero();
-      if (q.in) seg.load(y + (size_t)t * d + q.c);
-      seg.get(yv[i]);
-    }
+    for (int i = 0; i < NV; ++i) sr[i].get(yv[i]);
   }
+  load(wr, w);
+  if (grow) load(gr, grow);
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -198,22 +231,17 @@ __global__ __launch_bounds__(NT) void norm_out_kernel(const T* y, const float* t
     for (int e = 0; e < 8; ++e) s += yv[i][e] * yv[i][e];
   const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
   if (rstd && lane == 0) rstd[t] = r;
-  const T* grow = gate ? gate + (size_t)(t / gate_rows) * d : nullptr;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const Cols q = cols<L>(lane, i, d);
     if (!q.in) continue;
-    Seg8<T> seg;
     float xv[8], wv[8], o[8];
-    seg.load(x + (size_t)t * d + q.c);
-    seg.get(xv);
-    seg.load(w + q.c);
-    seg.get(wv);
+    xr[i].get(xv);
+    wr[i].get(wv);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] = yv[i][e] * r * wv[e];
     if (grow) {
-      seg.load(grow + q.c);
-      seg.get(wv);
+      gr[i].get(wv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] *= wv[e];
     }
@@ -228,30 +256,56 @@ __global__ __launch_bounds__(NT) void norm_out_kernel(const T* y, const float* t
 //   to dgate directly when the gate row lies inside the block,
 //   else to the block's `head` partial (the gate row began before the block or at its start) or its
 //   `tail` partial (it began inside and goes on in the next block): a block has at most one of each.
+// Gated by several gate rows (MULTI), the block's dw is summed over its pieces; otherwise the one
+// column sum S, or its join over the blocks, gives both.
 struct BwdArgs {
   int rows, d, R, gate_rows;
   float res_scale;
-  float* part;   // [3][blocks][d]: dw partials, head, tail
+  float* part;   // [3][blocks][d]: dw partials (MULTI), head (the only ones otherwise), tail
   float* dw;
   float* dgate;
 };
 
-// IN: dxn (as dout), x (as y), dres.  Otherwise: dout, y, gate.
-template <typename T, int L, int NV, bool IN>
-__global__ __launch_bounds__(NT) void norm_bwd_kernel(const T* dout, const T* y, const T* w, const T* gate,
-                                                      const T* dres, const float* rstd, T* dy, BwdArgs p) {
-  constexpr int NS = NT / L;   // rows in flight of a workgroup
-  __shared__ float red[2][NT / 64];
+// IN: dxn (as dout), x (as y), dres.  Otherwise: dout, y, gate.  The next row is loaded while the
+// current one is reduced: without it the loads of a row waited for the statistic of the row before.
+template <typename T, int L, int NV, bool IN, bool MULTI>
+__global__ __launch_bounds__(threads<L>()) void norm_bwd_kernel(const T* dout, const T* y, const T* w, const T* gate,
+                                                                const T* dres, const float* rstd, T* dy, BwdArgs p) {
+  constexpr int NS = threads<L>() / L;   // rows in flight of a workgroup
+  constexpr bool AHEAD = L < 1024;       // (a workgroup of 1024 has 128 registers a lane: no room)
+  __shared__ float red[2][16];
   extern __shared__ float sums[];   // [NS - 1][8 NV L] column sums of the other waves (L = 64)
   const int lane = threadIdx.x % L, me = threadIdx.x / L;
   const int d = p.d;
   const int r0 = blockIdx.x * p.R, r1 = min(p.rows, r0 + p.R);
   const int blocks = gridDim.x;
+  const float inv_d = 1.0f / (float)d;
   int slot = 0;
-  float dwacc[NV][8] = {};
+  struct Row {
+    Seg8<T> y[NV], g[NV], e[IN ? NV : 1];
+    float r;
+  };
+  auto load = [&](Row& q, int t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Cols c = cols<L>(lane, i, d);
+      if (c.in) {
+        q.y[i].load(y + (size_t)t * d + c.c);
+        q.g[i].load(dout + (size_t)t * d + c.c);
+        if constexpr (IN) {
+          if (dres) q.e[i].load(dres + (size_t)t * d + c.c);
+        }
+      } else {
+        q.y[i].zero();
+        q.g[i].zero();
+      }
+    }
+    q.r = rstd[t];
+  };
+  float dwacc[MULTI ? NV : 1][8] = {};
   for (int p0 = r0; p0 < r1;) {
     const int seg = gate ? p0 / p.gate_rows : 0;
-    const long long seg_end = gate ? (long long)(seg + 1) * p.gate_rows : (long long)p.rows;
+    const long long seg_end = MULTI ? (long long)(seg + 1) * p.gate_rows : (long long)p.rows;
     const int p1 = (int)min((long long)r1, seg_end);
     float gw[NV][8], S[NV][8] = {};
 #pragma unroll
@@ -269,25 +323,22 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(const T* dout, const T* y,
         for (int e = 0; e < 8; ++e) gw[i][e] *= gv[e];
       }
     }
+    Row cur, next;
+    if (AHEAD && p0 + me < p1) load(next, p0 + me);
     for (int t = p0 + me; t < p1; t += NS) {
-      Seg8<T> yr[NV], dr[NV];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Cols q = cols<L>(lane, i, d);
-        yr[i].zero();
-        dr[i].zero();
-        if (q.in) {
-          yr[i].load(y + (size_t)t * d + q.c);
-          dr[i].load(dout + (size_t)t * d + q.c);
-        }
+      if constexpr (AHEAD) {
+        cur = next;
+        if (t + NS < p1) load(next, t + NS);
+      } else {
+        load(cur, t);
       }
-      const float r = rstd[t];
+      const float r = cur.r;
       float dot = 0.0f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float n[8], g[8];
-        yr[i].get(n);
-        dr[i].get(g);
+        cur.y[i].get(n);
+        cur.g[i].get(g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           n[e] *= r;
@@ -295,23 +346,23 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(const T* dout, const T* y,
           dot += g[e] * gw[i][e] * n[e];
         }
       }
-      const float m = row_sum<L>(dot, red, slot) / (float)d;
+      const float m = row_sum<L>(dot, red, slot) * inv_d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const Cols q = cols<L>(lane, i, d);
         if (!q.in) continue;
         float n[8], g[8];
-        yr[i].get(n);
-        dr[i].get(g);
+        cur.y[i].get(n);
+        cur.g[i].get(g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[e] = r * (g[e] * gw[i][e] - n[e] * r * m);
-        if (IN && dres) {
-          Seg8<T> sg;
-          float v[8];
-          sg.load(dres + (size_t)t * d + q.c);
-          sg.get(v);
+        if constexpr (IN) {
+          if (dres) {
+            float v[8];
+            cur.e[i].get(v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) g[e] += p.res_scale * v[e];
+            for (int e = 0; e < 8; ++e) g[e] += p.res_scale * v[e];
+          }
         }
         Seg8<T>::put(dy + (size_t)t * d + q.c, g);
       }
@@ -336,85 +387,100 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(const T* dout, const T* y,
       __syncthreads();
     }
     if (me == 0) {
+      const long long seg_begin = MULTI ? (long long)seg * p.gate_rows : 0;
+      const bool whole = seg_begin >= r0 && min(seg_end, (long long)p.rows) <= r1;
+      float* head = p.part + ((size_t)(seg_begin <= r0 ? 1 : 2) * blocks + blockIdx.x) * d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const Cols q = cols<L>(lane, i, d);
         if (!q.in) continue;
+        if (!whole) Seg8<float>::put(head + q.c, S[i]);
+        if (!MULTI && !whole) continue;   // the join forms dw and dgate from the blocks' sums
+        Seg8<T> sg;
+        float wv[8], gv[8];
+        sg.load(w + q.c);
+        sg.get(wv);
         if (gate) {
-          const long long seg_begin = (long long)seg * p.gate_rows;
-          const bool whole = seg_begin >= r0 && min(seg_end, (long long)p.rows) <= r1;
-          Seg8<T> sg;
-          float wv[8], gv[8];
-          sg.load(w + q.c);
-          sg.get(wv);
           sg.load(gate + (size_t)seg * d + q.c);
           sg.get(gv);
-          float* to = whole ? p.dgate + (size_t)seg * d
-                            : p.part + ((size_t)(seg_begin <= r0 ? 1 : 2) * blocks + blockIdx.x) * d;
+        }
+        float o[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            to[q.c + e] = whole ? wv[e] * S[i][e] : S[i][e];
-            dwacc[i][e] += gv[e] * S[i][e];
-          }
+        for (int e = 0; e < 8; ++e) o[e] = wv[e] * S[i][e];
+        if (whole && gate) Seg8<float>::put(p.dgate + (size_t)seg * d + q.c, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = gate ? gv[e] * S[i][e] : S[i][e];
+        if constexpr (MULTI) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dwacc[i][e] += o[e];
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) dwacc[i][e] += S[i][e];
+          Seg8<float>::put(p.dw + q.c, o);
         }
       }
     }
     p0 = p1;
   }
-  if (me == 0) {
-    float* to = blocks == 1 ? p.dw : p.part + (size_t)blockIdx.x * d;
+  if constexpr (MULTI) {
+    if (me == 0) {
+      float* to = blocks == 1 ? p.dw : p.part + (size_t)blockIdx.x * d;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const Cols q = cols<L>(lane, i, d);
-      if (!q.in) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) to[q.c + e] = dwacc[i][e];
+      for (int i = 0; i < NV; ++i) {
+        const Cols q = cols<L>(lane, i, d);
+        if (q.in) Seg8<float>::put(to + q.c, dwacc[i]);
+      }
     }
   }
 }
 
-// Joins the row blocks' partials in block order.  blockIdx.y = 0: dw.  blockIdx.y = b + 1: the gate
-// row that the end of block b cuts, if b is the first block of that gate row.
-template <typename T>
-__global__ __launch_bounds__(NT) void norm_bwd_join_kernel(const T* w, bool gated, BwdArgs p, int blocks) {
-  __shared__ float red[NT / 16][64 + 1];
+// Joins the row blocks' partials in a fixed order, 16 columns by 64 slices of the blocks per
+// workgroup.  One gate row or none: dw = gate S and dgate = w S of the joined sum.  Several (MULTI):
+// blockIdx.y = 0 joins dw; the others dgate, one gate row each where there are few gate rows
+// (y = row + 1), else the gate row that the end of block y - 1 cuts, if that is its first cut.
+template <typename T, bool MULTI>
+__global__ __launch_bounds__(NT) void norm_bwd_join_kernel(const T* w, const T* gate, BwdArgs p, int blocks, bool by_row) {
+  constexpr int SL = NT / 4;
+  __shared__ float red[SL][16 + 1];
   const int d = p.d;
-  const int c = blockIdx.x * 64 + (threadIdx.x % 16) * 4, slice = threadIdx.x / 16;
+  const int c = blockIdx.x * 16 + (threadIdx.x % 4) * 4, slice = threadIdx.x / 4;
   int b0 = 0, b1 = blocks;   // blocks whose partials are added
   int seg = 0;
   long long seg_begin = 0;
-  if (blockIdx.y > 0) {
-    const int b = blockIdx.y - 1;
-    const int row = (b + 1) * p.R - 1;   // last row of block b; row + 1 exists (b is not the last block)
-    seg = row / p.gate_rows;
-    if ((row + 1) / p.gate_rows != seg) return;   // the cut falls between gate rows
+  if (MULTI && blockIdx.y > 0) {
+    seg = by_row ? blockIdx.y - 1 : (int)((long long)blockIdx.y * p.R - 1) / p.gate_rows;   // block y - 1's last row
     seg_begin = (long long)seg * p.gate_rows;
+    const long long seg_last = min((long long)p.rows, seg_begin + p.gate_rows) - 1;
     b0 = (int)(seg_begin / p.R);
-    if (b0 != b) return;                           // an earlier cut handles it
-    const long long last = min((long long)p.rows, seg_begin + p.gate_rows) - 1;
-    b1 = (int)(last / p.R) + 1;
+    b1 = (int)(seg_last / p.R) + 1;
+    if (b1 - b0 < 2) return;                                 // inside one block: written there
+    if (!by_row && b0 != (int)blockIdx.y - 1) return;        // an earlier cut handles it
   }
   float a[4] = {0, 0, 0, 0};
   if (c < d) {
-    for (int b = b0 + slice; b < b1; b += NT / 16) {
-      const int kind = blockIdx.y == 0 ? 0 : (seg_begin <= (long long)b * p.R ? 1 : 2);
+    const bool dw = MULTI && blockIdx.y == 0;
+#pragma unroll 4
+    for (int b = b0 + slice; b < b1; b += SL) {
+      const int kind = dw ? 0 : (seg_begin <= (long long)b * p.R ? 1 : 2);
       const float4 v = *reinterpret_cast<const float4*>(p.part + ((size_t)kind * blocks + b) * d + c);
       a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
     }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) red[slice][(threadIdx.x % 16) * 4 + e] = a[e];
+  for (int e = 0; e < 4; ++e) red[slice][(threadIdx.x % 4) * 4 + e] = a[e];
   __syncthreads();
-  if (threadIdx.x < 64) {
-    const int col = blockIdx.x * 64 + threadIdx.x;
-    if (col >= d) return;
-    float s = 0.0f;
-    for (int i = 0; i < NT / 16; ++i) s += red[i][threadIdx.x];
-    if (blockIdx.y == 0) p.dw[col] = s;
-    else p.dgate[(size_t)seg * d + col] = to_f32<T>(w[col]) * s;
+  // 16 threads per column add 4 slices each, then a tree
+  const int col = threadIdx.x / 16, part = threadIdx.x % 16;
+  float s = (red[part][col] + red[part + 16][col]) + (red[part + 32][col] + red[part + 48][col]);
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) s += __shfl_xor(s, off, 64);
+  const int at = blockIdx.x * 16 + col;
+  if (part != 0 || at >= d) return;
+  if (MULTI && blockIdx.y == 0) {
+    p.dw[at] = s;
+  } else if (MULTI) {
+    p.dgate[(size_t)seg * d + at] = to_f32<T>(w[at]) * s;
+  } else {
+    p.dw[at] = gate ? to_f32<T>(gate[at]) * s : s;
+    if (gate) p.dgate[at] = to_f32<T>(w[at]) * s;
   }
 }
 
@@ -423,23 +489,44 @@ __global__ __launch_bounds__(NT) void zero_f32_kernel(float* p, int n) {
   if (i < n) p[i] = 0.0f;
 }
 
-// Lanes per row and segments per lane for a width of d: one wave up to 2048 columns (no barrier in
-// the row loop), the workgroup above.
+// Lanes per row and segments per lane for a width of d.  At most two segments a lane: with four the
+// backward's registers spilled (fp32: 200 of them).
 template <typename F>
 hipError_t by_width(int d, F&& f) {
   if (d <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
   if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (d <= 2048) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+  if (d <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
   if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-  if (d <= 8192) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 8>{});
+  if (d <= 8192) return f(std::integral_constant<int, 512>{}, std::integral_constant<int, 2>{});
+  return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
 
-// Rows per workgroup of the backward: about 512 workgroups (two per CU), at least one row per wave.
+// Rows per workgroup of the backward: about BLOCKS workgroups, at least one row per wave or
+// workgroup that walks rows.
+constexpr int BLOCKS = 1024;
 int bwd_rows(long long T, int d) {
-  const int ns = d <= 2048 ? 4 : 1;
-  const long long r = (T + 511) / 512;
+  const int ns = d <= 1024 ? 4 : 1;
+  const long long r = (T + BLOCKS - 1) / BLOCKS;
   return (int)std::max<long long>(ns, (r + ns - 1) / ns * ns);
+}
+
+template <typename T, bool IN, bool MULTI>
+hipError_t norm_bwd_rows(const T* dout, const T* y, const T* w, const T* gate, const T* dres, const float* rstd, T* dy,
+                         const BwdArgs& p, hipStream_t s) {
+  const int blocks = ceil_div(p.rows, p.R);
+  hipError_t e = by_width(p.d, [&](auto L, auto NV) {
+    constexpr int th = threads<decltype(L)::value>(), ns = th / decltype(L)::value;
+    const size_t lds = (size_t)(ns - 1) * 8 * decltype(NV)::value * decltype(L)::value * sizeof(float);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(L)::value, decltype(NV)::value, IN, MULTI>), dim3(blocks), dim3(th),
+                       lds, s, dout, y, w, gate, dres, rstd, dy, p);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || blocks == 1) return e;
+  const int gate_rows = MULTI ? ceil_div(p.rows, p.gate_rows) : 0;
+  const bool by_row = gate_rows < blocks;
+  norm_bwd_join_kernel<T, MULTI><<<dim3(ceil_div(p.d, 16), 1 + (MULTI ? (by_row ? gate_rows : blocks - 1) : 0)), dim3(NT), 0,
+                                   s>>>(w, gate, p, blocks, by_row);
+  return hipGetLastError();
 }
 
 template <typename T, bool IN>
@@ -450,17 +537,10 @@ hipError_t norm_bwd(const T* dout, const T* y, const T* w, const T* gate, const 
     return hipGetLastError();
   }
   p.R = bwd_rows(p.rows, p.d);
-  const int blocks = ceil_div(p.rows, p.R);
-  hipError_t e = by_width(p.d, [&](auto L, auto NV) {
-    constexpr int ns = NT / decltype(L)::value;
-    const size_t lds = (size_t)(ns - 1) * 8 * decltype(NV)::value * decltype(L)::value * sizeof(float);
-    hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(L)::value, decltype(NV)::value, IN>), dim3(blocks), dim3(NT), lds, s,
-                       dout, y, w, gate, dres, rstd, dy, p);
-    return hipGetLastError();
-  });
-  if (e != hipSuccess || blocks == 1) return e;
-  norm_bwd_join_kernel<T><<<dim3(ceil_div(p.d, 64), gate ? blocks : 1), dim3(NT), 0, s>>>(w, gate != nullptr, p, blocks);
-  return hipGetLastError();
+  if constexpr (!IN) {
+    if (gate && p.gate_rows < p.rows) return norm_bwd_rows<T, IN, true>(dout, y, w, gate, dres, rstd, dy, p, s);
+  }
+  return norm_bwd_rows<T, IN, false>(dout, y, w, gate, dres, rstd, dy, p, s);
 }
 
 }  // namespace
@@ -469,12 +549,16 @@ hipError_t launch_norm_in(const void* x, const void* w, int T, int d, float eps,
                           hipStream_t s) {
   auto go = [&](auto tag) {
     typedef decltype(tag) E;
-    return by_width(d, [&](auto L, auto NV) {
+    auto run = [&](auto L, auto NV) {
       hipLaunchKernelGGL((norm_in_kernel<E, decltype(L)::value, decltype(NV)::value>),
-                         dim3(ceil_div(T, NT / decltype(L)::value)), dim3(NT), 0, s, (const E*)x, (const E*)w, T, d, eps,
+                         dim3(ceil_div(T, threads<decltype(L)::value>() / decltype(L)::value)),
+                         dim3(threads<decltype(L)::value>()), 0, s, (const E*)x, (const E*)w, T, d, eps,
                          (E*)xn, rstd);
       return hipGetLastError();
-    });
+    };
+    // a wave per row as far as its registers go: 24.3 us against 27.6 at 16384 x 2048
+    if (d > 1024 && d <= 2048) return run(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
+    return by_width(d, run);
   };
   return bf16 ? go(bf16_t{}) : go(float{});
 }
@@ -486,7 +570,8 @@ hipError_t launch_norm_out(const void* y, const float* topk_gate, const int32_t*
     typedef decltype(tag) E;
     return by_width(d, [&](auto L, auto NV) {
       hipLaunchKernelGGL((norm_out_kernel<E, decltype(L)::value, decltype(NV)::value, decltype(comb)::value>),
-                         dim3(ceil_div(T, NT / decltype(L)::value)), dim3(NT), 0, s, (const E*)y, topk_gate, dest_pos,
+                         dim3(ceil_div(T, threads<decltype(L)::value>() / decltype(L)::value)),
+                         dim3(threads<decltype(L)::value>()), 0, s, (const E*)y, topk_gate, dest_pos,
                          (const E*)shared, k, (const E*)x, (const E*)w, (const E*)gate, gate_rows, res_scale, T, d, eps,
                          (E*)y_out, (E*)out, rstd);
       return hipGetLastError();

@@ -27,22 +27,21 @@ struct GradItem {
   long long n;
   bool bf16;
 };
-constexpr int kGradTable = 96;   // tensors per launch: the table stays within 4 KiB of kernel arguments
+constexpr int kGradTable = 160;   // tensors per launch: the table stays within 4 KiB of kernel arguments
 struct GradTable {
   const void* grad[kGradTable];
   void* out[kGradTable];
-  long long n[kGradTable];
-  int first[kGradTable + 1];   // first chunk of each tensor, among this launch's chunks
-  bool bf16[kGradTable];
+  int first[kGradTable + 1];     // first chunk of each tensor, among this launch's chunks
+  uint32_t tail[kGradTable];     // elements of its last chunk; bit 31: bf16
   int count;
-  int base;                    // chunks of the launches before this one
+  int base;                      // chunks of the launches before this one
 };
 long long grad_chunks(const GradItem* g, int count);
 hipError_t launch_grad_sumsq(const GradItem* g, int count, double* partial, hipStream_t s);
 // sumsq, norm: either may be NULL.
 hipError_t launch_grad_total(const double* partial, int count, double* sumsq, float* norm, hipStream_t s);
-// sums[0..nsums): their sum is the sum of squares.
-hipError_t launch_grad_scale(const GradItem* g, int count, const double* sums, int nsums, float max_norm, float* norm,
+// sums[0..nsums): their sum is the sum of squares; nsums > 1: one more double behind them is written.
+hipError_t launch_grad_scale(const GradItem* g, int count, double* sums, int nsums, float max_norm, float* norm,
                              hipStream_t s);
 
 // Softmax cross entropy over a vocabulary

@@ -231,35 +231,51 @@ __global__ __launch_bounds__(NT) void vocab_tile_kernel(VocabArgs p) {
   }
 }
 
-// Joins a row's parts, 16 rows of 16 slices per workgroup (slice s takes parts s, s + 16, ..., and the
-// slices are joined in order), and forms the target's logit as a product of its own, which spares
-// the tiles a search for it: 2 T d elements read beside the product's V d.
-constexpr int JR = 16;
-template <typename T>
-__global__ __launch_bounds__(JR * 16) void vocab_lse_kernel(VocabArgs p, int parts, float* loss, float* lse) {
-  __shared__ float2 sl[16][JR + 1];
-  __shared__ float dot[JR];
-  const int r0 = blockIdx.x * JR;
+int parts_of(long long V) { return (int)((V + WORDS_PER_PART - 1) / WORDS_PER_PART); }
+
+// Joins a row's parts and forms the target's logit as a product of its own, which spares the tiles a
+// search for it (2 T d elements read beside the product's V d).  JR rows per workgroup, the parts of
+// a row dealt to its NT / JR threads and joined in a fixed tree.
+__device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  // a part of nothing has a maximum of -inf and adds nothing
+  const float u = a.x == m ? a.y : a.y * expf(a.x - m), v = b.x == m ? b.y : b.y * expf(b.x - m);
+  return make_float2(m, u + v);
+}
+template <typename T, int JR>
+__global__ __launch_bounds__(NT) void vocab_lse_kernel(VocabArgs p, int parts, float* loss, float* lse) {
+  constexpr int TPR = NT / JR, NWV = NT / 64;
+  __shared__ float2 sl[NWV][JR];
+  __shared__ float dots[NWV][JR];
+  const int r0 = blockIdx.x * JR, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   {
-    const int r = threadIdx.x % JR, slice = threadIdx.x / JR, row = min(r0 + r, p.T - 1);
-    float mx = -__builtin_inff(), sum = 0.0f;
-    for (int i = slice; i < parts; i += 16) {
-      const float2 v = p.part[(size_t)i * p.T + row];
-      const float m = fmaxf(mx, v.x);
-      sum = sum * expf(mx - m) + v.y * expf(v.x - m);
-      mx = m;
+    // consecutive threads take consecutive rows: a part's statistics are contiguous over the rows
+    const int r = threadIdx.x % JR, row = min(r0 + r, p.T - 1);
+    const float2* part = p.part + row;
+    float2 acc = make_float2(-__builtin_inff(), 0.0f);
+    int i = threadIdx.x / JR;
+    for (; i + 3 * TPR < parts; i += 4 * TPR) {
+      float2 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = part[(size_t)(i + u * TPR) * p.T];
+      acc = join_parts(acc, join_parts(join_parts(v[0], v[1]), join_parts(v[2], v[3])));
     }
-    sl[slice][r] = make_float2(mx, sum);
+    for (; i < parts; i += TPR) acc = join_parts(acc, part[(size_t)i * p.T]);
+#pragma unroll
+    for (int off = 32; off >= JR; off >>= 1)
+      acc = join_parts(acc, make_float2(__shfl_xor(acc.x, off, 64), __shfl_xor(acc.y, off, 64)));
+    if (lane < JR) sl[wave][lane] = acc;
   }
   {
-    const int r = threadIdx.x / 16, s = threadIdx.x % 16, row = min(r0 + r, p.T - 1);
+    // consecutive threads share a row: TPR of them, 16 bytes each
+    const int r = threadIdx.x / TPR, s = threadIdx.x % TPR, row = min(r0 + r, p.T - 1);
     const int t = p.target[row];
     constexpr int E = 16 / sizeof(T);
     float a = 0.0f;
     if (t >= 0 && t < p.V) {
       const T* h = reinterpret_cast<const T*>(p.h) + (size_t)row * p.d;
       const T* w = reinterpret_cast<const T*>(p.w) + (size_t)t * p.d;
-      for (int c = s * E; c < p.d; c += 16 * E) {
+      for (int c = s * E; c < p.d; c += TPR * E) {
         const u32x4_t x = *reinterpret_cast<const u32x4_t*>(h + c), y = *reinterpret_cast<const u32x4_t*>(w + c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -273,19 +289,35 @@ __global__ __launch_bounds__(JR * 16) void vocab_lse_kernel(VocabArgs p, int par
       }
     }
 #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
-    if (s == 0) dot[r] = a;
+    for (int off = (TPR < 64 ? TPR : 64) / 2; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
+    if (lane % TPR == 0) dots[wave][r] = a;   // TPR > 64: one partial per wave
   }
   __syncthreads();
-  const int row = r0 + threadIdx.x;
-  if (threadIdx.x >= JR || row >= p.T) return;
-  float mx = -__builtin_inff(), sum = 0.0f;
-  for (int s = 0; s < min(16, parts); ++s) mx = fmaxf(mx, sl[s][threadIdx.x].x);
-  for (int s = 0; s < min(16, parts); ++s) sum += sl[s][threadIdx.x].y * expf(sl[s][threadIdx.x].x - mx);
-  const float l = mx + logf(sum);
+  const int r = threadIdx.x, row = r0 + r;
+  if (r >= JR || row >= p.T) return;
+  float2 acc = sl[0][r];
+#pragma unroll
+  for (int w = 1; w < NWV; ++w) acc = join_parts(acc, sl[w][r]);
+  float dot = 0.0f;
+  if constexpr (TPR > 64) {
+    for (int w = 0; w < NWV; ++w) dot += dots[w][0];
+  } else {
+    dot = dots[r * TPR / 64][r];
+  }
+  const float l = acc.x + logf(acc.y);
   const int t = p.target[row];
   lse[row] = l;
-  loss[row] = t >= 0 && t < p.V ? l - dot[threadIdx.x] : 0.0f;
+  loss[row] = t >= 0 && t < p.V ? l - dot : 0.0f;
+}
+
+// As many rows per workgroup as still fill the CUs: few rows have their parts dealt to more threads.
+template <typename T>
+hipError_t launch_lse(const VocabArgs& p, float* loss, float* lse, hipStream_t s) {
+  const int parts = parts_of(p.V);
+  if (p.T >= 16 * NUM_CUS) vocab_lse_kernel<T, 16><<<dim3(ceil_div(p.T, 16)), dim3(NT), 0, s>>>(p, parts, loss, lse);
+  else if (p.T >= 4 * NUM_CUS) vocab_lse_kernel<T, 4><<<dim3(ceil_div(p.T, 4)), dim3(NT), 0, s>>>(p, parts, loss, lse);
+  else vocab_lse_kernel<T, 1><<<dim3(p.T), dim3(NT), 0, s>>>(p, parts, loss, lse);
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -300,8 +332,6 @@ int piece_words(long long T, long long V) {
   const long long pieces = (V + want - 1) / want;
   return (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
 }
-
-int parts_of(long long V) { return (int)((V + WORDS_PER_PART - 1) / WORDS_PER_PART); }
 
 bool use_pipe(int T, int d, int V, bool bf16) { return bf16; }
 
@@ -320,8 +350,7 @@ hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t 
   p.vn = p.V;
   const hipError_t e = use_pipe(p.T, p.d, p.V, sizeof(T) == 2) ? launch_pipe(VL_STATS, p, s) : launch_tiles<T, VL_STATS>(p, s);
   if (e != hipSuccess) return e;
-  vocab_lse_kernel<T><<<dim3(ceil_div(p.T, JR)), dim3(JR * 16), 0, s>>>(p, parts_of(p.V), loss, lse);
-  return hipGetLastError();
+  return launch_lse<T>(p, loss, lse, s);
 }
 
 // Bytes of the accumulated dh.
