@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libmoe.so")
 
 SOURCES = ["api.cpp", "route.hip", "router_aux.hip", "dispatch.hip", "combine.hip", "grouped_gemm.hip",
            "grouped_gemm_pipe.hip", "mxfp8.hip", "block_norm.hip", "vocab_loss.hip",
-           "vocab_loss_pipe.hip", "grad_clip.hip"]
+           "vocab_loss_pipe.hip", "vocab_loss_tile.hip", "grad_clip.hip"]
 
 ARCH = "gfx950"
 # Packed fp32 instructions stay off: plain scalar fp32 code only.

@@ -716,6 +716,7 @@ moe_status_t check_vocab(int64_t T, int64_t d, int64_t V, moe_dtype_t dt) {
         (long long)d);
   CHECK(T <= kVocabMax && V <= kVocabMax, MOE_ERR_UNSUPPORTED, "T and V must be at most 2^22 (got T=%lld, V=%lld)",
         (long long)T, (long long)V);
+  CHECK(((T + 63) / 64) * ((V + 63) / 64) < kMaxInt, MOE_ERR_UNSUPPORTED, "grid too large");
   return MOE_OK;
 }
 

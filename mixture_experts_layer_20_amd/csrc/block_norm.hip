@@ -19,9 +19,13 @@ namespace moe {
 namespace {
 
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 // 8 consecutive elements, as loaded and widened.  load_once: a stream that nothing reads again soon (a
-// nontemporal load).
+// nontemporal load: the experts' rows at 6.6 TB/s instead of 4.9).  Stores are nontemporal: the four
+// calls of a forward and backward pass at 16384 x 2048 take 140 us with them and 161 without, where
+// the inputs they read in common then stay in the last-level cache; inside the layer, with its
+// products between the calls, both take the same time.
 template <typename T> struct Seg8;
 template <> struct Seg8<bf16_t> {
   u32x4_t w;
@@ -41,7 +45,7 @@ template <> struct Seg8<bf16_t> {
     u32x4_t r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) r[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
-    *reinterpret_cast<u32x4_t*>(p) = r;
+    __builtin_nontemporal_store(r, reinterpret_cast<u32x4_t*>(p));
   }
 };
 template <> struct Seg8<float> {
@@ -57,8 +61,8 @@ template <> struct Seg8<float> {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
   __device__ static __forceinline__ void put(float* p, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4_t*>(p));
+    __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4_t*>(p) + 1);
   }
 };
 

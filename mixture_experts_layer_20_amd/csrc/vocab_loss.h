@@ -16,8 +16,9 @@ struct VocabArgs {
   int v0, vn;         // the piece: words v0 .. v0 + vn - 1
   int ldp;            // row length of P, a multiple of 256
   void* p;            // [T, ldp]; columns vn.. of a piece are zero as far as its last tile reaches
-  float2* part;       // [ceil(V / 64)][T] maximum and sum of exponentials of 64 words
+  float2* part;       // [parts][T] maximum and sum of exponentials of PIPE_PART or TILE_PART words
   float* dh_acc;      // dh of the pieces so far, fp32
+  float* dw_acc;      // partial products of a piece's dw, fp32
   void* dh;
   void* dw;
   bool first, last;   // the piece is the first / the last one
@@ -25,7 +26,7 @@ struct VocabArgs {
 
 enum VocabMode { VL_STATS = 0, VL_GRAD = 1, VL_DH = 2, VL_DW = 3 };
 
-constexpr int WORDS_PER_PART = 64;
+constexpr int PIPE_PART = 64, TILE_PART = 32;   // words of a row's part, by the kernel that writes it
 constexpr int NUM_CUS = 256;
 
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -36,6 +37,12 @@ int pipe_splits(int T, int d, int words);
 size_t pipe_acc_bytes(int T, int d, int words);
 hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s);
 hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s);
+
+// 64x64 tiles, both types.  dh_acc and dw_acc hold tile_splits() partial products of all outputs.
+int tile_splits(int M, int N, int K);
+size_t tile_acc_bytes(int M, int N, int K);
+hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s);
+hipError_t launch_tile_join(const VocabArgs& p, bool bf16, hipStream_t s);
 
 }  // namespace vocab
 }  // namespace moe

@@ -380,7 +380,7 @@ __device__ __forceinline__ void stats_epilogue(const VocabArgs& p, const Geo& g,
       for (int e = 0; e < 16; ++e) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -m2));
     s = other_half_sum(s);
     const int row = row0 + 32 * i + (lane & 31);
-    if (lane < 32 && row < g.M) p.part[(size_t)((p.v0 + col0) / WORDS_PER_PART) * p.T + row] = make_float2(mx, s);
+    if (lane < 32 && row < g.M) p.part[(size_t)((p.v0 + col0) / PIPE_PART) * p.T + row] = make_float2(mx, s);
   }
 }
 

@@ -1,0 +1,370 @@
+// The products of the vocabulary loss (vocab_loss.hip has the formulas) in 64x64 tiles, both types:
+// fp32, and bf16 where the 256x256 tiles of vocab_loss_pipe.hip are too few to fill the CUs.
+//
+// A workgroup of 4 waves takes one tile, 32x32 per wave, two workgroups per CU.  K goes through two
+// LDS stages of 256 bytes per row and operand (128 bf16 or 64 fp32 values), filled by direct-to-LDS
+// loads two steps ahead.  An operand contiguous along K is kept [64 rows][256 bytes], 16-byte chunks
+// XOR-swizzled by the row; one contiguous along its rows is kept [k][64 rows] and read transposed
+// (bf16) or value by value (fp32).  fp32 products run on v_mfma_f32_32x32x2_f32, which multiplies and
+// adds in fp32; the two k of an instruction are 4 apart, so one 16-byte read feeds four of them.
+// Rows past the end are read clamped and not stored, K and columns past the end read zeros.
+#include "vocab_loss.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace vocab {
+namespace {
+
+constexpr int TS = 64;                  // tile rows and columns
+constexpr int NT = 256, LP = 4;         // threads; direct loads per wave, stage and operand
+constexpr int OPB = 64 * 256, STAGE = 2 * OPB;
+constexpr int NF = 8;                   // fragment groups of a stage: 16 bf16 or 8 fp32 k each
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(1))) void gvoid_t;
+typedef __attribute__((address_space(3))) void lvoid_t;
+
+__device__ __attribute__((aligned(16))) uint4 g_zeros[4];
+
+template <int MODE> struct Tr {
+  static constexpr bool a_kc = MODE != VL_DW;
+  static constexpr bool b_kc = MODE == VL_STATS || MODE == VL_GRAD;
+};
+
+__device__ __forceinline__ uint32_t lds_addr_of(const void* ptr) {
+  return (uint32_t)(uintptr_t)((const __attribute__((address_space(3))) char*)ptr);
+}
+
+// One operand's part of a stage: where each lane's loads read, and the LDS layout.
+template <typename T, bool KC>
+struct Operand {
+  static constexpr int E = 16 / sizeof(T), BK = 256 / sizeof(T);
+  static constexpr int CPR = KC ? 16 : 64 / E;   // 16-byte chunks of an LDS row
+  const char* src[LP];
+  int k[LP];       // first k of the lane's piece, from the tile's first
+  bool in[LP];     // columns inside (not KC)
+
+  __device__ __forceinline__ static int logical(int row, int chunk) {
+    if constexpr (KC) return chunk ^ (row & 15);
+    else if constexpr (E == 8) return chunk ^ (((row >> 1) & 1) << 2);
+    else return chunk ^ (((row >> 2) & 1) << 3);
+  }
+  // base: element (row 0, k 0) of the operand; r0, k0: the tile's first row and k.
+  __device__ __forceinline__ void init(const T* base, size_t ld, int r0, int rows, int k0, int wave, int lane) {
+#pragma unroll
+    for (int j = 0; j < LP; ++j) {
+      const int q = (wave * LP + j) * 64 + lane;
+      const int row = q / CPR, c = logical(row, q % CPR) * E;
+      if constexpr (KC) {
+        src[j] = reinterpret_cast<const char*>(base + (size_t)min(r0 + row, rows - 1) * ld + k0 + c);
+        k[j] = c;
+        in[j] = true;
+      } else {
+        in[j] = r0 + c < rows;
+        src[j] = reinterpret_cast<const char*>(base + (size_t)(k0 + row) * ld + (in[j] ? r0 + c : 0));
+        k[j] = row;
+      }
+    }
+  }
+  // The stage whose first k is `at`, of k_end in the tile; then the sources move one stage on.
+  __device__ __forceinline__ void issue(char* lds, int at, int k_end, size_t ld, int wave) {
+#pragma unroll
+    for (int j = 0; j < LP; ++j) {
+      const char* from = in[j] && at + k[j] < k_end ? src[j] : reinterpret_cast<const char*>(g_zeros);
+      __builtin_amdgcn_global_load_lds((gvoid_t*)from, (lvoid_t*)(lds + (wave * LP + j) * 1024), 16, 0, 0);
+      src[j] += KC ? (size_t)256 : (size_t)BK * ld * sizeof(T);
+    }
+  }
+};
+
+// A wave's fragments of a stage.  Group s, lane l: row l % 32 of the block and, bf16: k 16 s + 8 (l / 32)
+// + 0..7; fp32: k 8 s + 4 (l / 32) + 0..3.
+template <typename T, bool KC>
+struct Frags {
+  static constexpr int E = 16 / sizeof(T);
+  u32x4_t v[NF];
+  u32x2_t h[NF][2];   // bf16, not KC: two transposed reads of 4 k
+
+  __device__ __forceinline__ void read(uint32_t base, int rb, int lane) {
+    if constexpr (KC) {
+      const int row = rb + (lane & 31);
+      const uint32_t a = base + row * 256 + (((lane >> 5) ^ (row & 15)) << 4);
+#pragma unroll
+      for (int s = 0; s < NF; ++s) asm volatile("ds_read_b128 %0, %1" : "=v"(v[s]) : "v"(a ^ (uint32_t)(32 * s)));
+    } else if constexpr (E == 8) {
+      const int b = lane >> 4, c = (lane & 15) >> 2, k = (b >> 1) * 8 + c, col = rb + 16 * (b & 1) + 4 * (lane & 3);
+      const uint32_t a = base + k * 128 + (((col >> 3) ^ (((k >> 1) & 1) << 2)) << 4) + (col & 7) * 2;
+#pragma unroll
+      for (int s = 0; s < NF; ++s) {
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(h[s][0]) : "v"(a), "i"(2048 * s));
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(h[s][1]) : "v"(a), "i"(2048 * s + 512));
+      }
+    } else {
+      const int col = rb + (lane & 31), half = lane >> 5;
+      const uint32_t a = base + half * 1024 + (((col >> 2) ^ (half << 3)) << 4) + (col & 3) * 4;
+#pragma unroll
+      for (int s = 0; s < NF; ++s) {
+        uint32_t x0, x1, x2, x3;
+        asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(x0) : "v"(a), "i"(2048 * s));
+        asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(x1) : "v"(a), "i"(2048 * s + 256));
+        asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(x2) : "v"(a), "i"(2048 * s + 512));
+        asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(x3) : "v"(a), "i"(2048 * s + 768));
+        f[s][0] = x0; f[s][1] = x1; f[s][2] = x2; f[s][3] = x3;
+      }
+    }
+  }
+  uint32_t f[NF][4];   // fp32, not KC
+
+  // After a wait: the values are in-out operands here, so no use of them moves above it.
+  __device__ __forceinline__ void landed() {
+#pragma unroll
+    for (int s = 0; s < NF; ++s) {
+      if constexpr (KC) asm volatile("" : "+v"(v[s]));
+      else if constexpr (E == 8) asm volatile("" : "+v"(h[s][0]), "+v"(h[s][1]));
+      else asm volatile("" : "+v"(f[s][0]), "+v"(f[s][1]), "+v"(f[s][2]), "+v"(f[s][3]));
+    }
+  }
+  __device__ __forceinline__ bf16x8_t get16(int s) const {
+    if constexpr (KC) return __builtin_bit_cast(bf16x8_t, v[s]);
+    const u32x4_t u = {h[s][0].x, h[s][0].y, h[s][1].x, h[s][1].y};
+    return __builtin_bit_cast(bf16x8_t, u);
+  }
+  __device__ __forceinline__ float get32(int s, int e) const {
+    return __uint_as_float(KC ? v[s][e] : f[s][e]);
+  }
+};
+
+constexpr int waitcnt_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0xf70; }   // vmcnt alone
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm(N));
+}
+__device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+__device__ __forceinline__ void store4(bf16_t* p, const float (&v)[4]) {
+  u32x2_t w;
+  w.x = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
+  w.y = (uint32_t)f32_to_bf16(v[2]) | ((uint32_t)f32_to_bf16(v[3]) << 16);
+  *reinterpret_cast<u32x2_t*>(p) = w;
+}
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// Workgroup b runs on XCD b % 8: each XCD walks one run of the tile order, rows first, so the tiles
+// that read one panel of the large operand run together.
+template <typename T, int MODE>
+__global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, int kchunk, bool direct) {
+  constexpr bool AK = Tr<MODE>::a_kc, BKC = Tr<MODE>::b_kc;
+  constexpr int BK = 256 / sizeof(T);
+  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave >> 1, wn = wave & 1;
+  constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
+  const int M = MODE == VL_DW ? p.vn : p.T;
+  const int N = LOGITS ? p.vn : p.d;
+  const int K = LOGITS ? p.d : (MODE == VL_DH ? p.vn : p.T);
+  const T* h = reinterpret_cast<const T*>(p.h);
+  const T* w = reinterpret_cast<const T*>(p.w) + (size_t)p.v0 * p.d;
+  const T* P = reinterpret_cast<const T*>(p.p);
+  const T* abase = LOGITS ? h : P;
+  const T* bbase = MODE == VL_DW ? h : w;
+  const size_t lda = LOGITS ? p.d : p.ldp, ldb = p.d;
+
+  const int MT = (M + TS - 1) / TS, NTL = (N + TS - 1) / TS, total = MT * NTL * ks;
+  const int per = (total + 7) >> 3;
+  const int L = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if ((int)(blockIdx.x >> 3) >= per || L >= total) return;
+  const int split = L / (MT * NTL), l = L - split * (MT * NTL);
+  const int nt = l / MT, mt = l - nt * MT;
+  const int m0 = mt * TS, n0 = nt * TS;
+  const int k0 = split * kchunk, k_end = min(K - k0, kchunk);
+  const int nk = (k_end + BK - 1) / BK;
+
+  Operand<T, AK> oa;
+  Operand<T, BKC> ob;
+  oa.init(abase, lda, m0, M, k0, wave, lane);
+  ob.init(bbase, ldb, n0, N, k0, wave, lane);
+  // Past the last stage the loads read zeros into slots that nobody reads.
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    oa.issue(lds + s * STAGE, s * BK, k_end, lda, wave);
+    ob.issue(lds + s * STAGE + OPB, s * BK, k_end, ldb, wave);
+  }
+  f32x16_t acc;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  const uint32_t lds0 = lds_addr_of(lds);
+  for (int j = 0; j < nk; ++j) {
+    char* slot = lds + (j & 1) * STAGE;
+    const uint32_t sb = lds0 + (j & 1) * STAGE;
+    wait_vm<2 * LP>();   // stage j has landed, stage j + 1 may be in flight
+    barrier();
+    Frags<T, AK> fa;
+    Frags<T, BKC> fb;
+    fa.read(sb, wm * 32, lane);
+    fb.read(sb + OPB, wn * 32, lane);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    fa.landed();
+    fb.landed();
+    barrier();           // every wave has read stage j
+    oa.issue(slot, (j + 2) * BK, k_end, lda, wave);
+    ob.issue(slot + OPB, (j + 2) * BK, k_end, ldb, wave);
+#pragma unroll
+    for (int s = 0; s < NF; ++s) {
+      if constexpr (sizeof(T) == 2) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb.get16(s), fa.get16(s), acc, 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fb.get32(s, e), fa.get32(s, e), acc, 0, 0, 0);
+      }
+    }
+  }
+  wait_vm<0>();   // no direct load may still be writing when the workgroup's LDS is released
+
+  // Lane l holds row l % 32 and, in element e, column 8 (e / 4) + 4 (l / 32) + e % 4 of the block.
+  const int row = m0 + wm * 32 + (lane & 31), c0 = n0 + wn * 32, half = lane >> 5;
+  if constexpr (MODE == VL_STATS) {
+    if (c0 >= N) return;
+    float mx = -__builtin_inff();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      if (c0 + 8 * (e >> 2) + 4 * half + (e & 3) >= N) acc[e] = -__builtin_inff();
+      mx = fmaxf(mx, acc[e]);
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    float sm = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sm += expf(acc[e] - mx);
+    sm += __shfl_xor(sm, 32, 64);
+    if (half == 0 && row < M) p.part[(size_t)((p.v0 + c0) / TILE_PART) * p.T + row] = make_float2(mx, sm);
+    return;
+  }
+  if (row >= M) return;
+  float lse = 0.0f, dl = 0.0f;
+  int tgt = -1;
+  if constexpr (MODE == VL_GRAD) {
+    lse = p.lse[row];
+    tgt = p.target[row];
+    dl = tgt >= 0 && tgt < p.V ? p.dloss[row] : 0.0f;
+    tgt -= p.v0;
+  }
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int n = c0 + 8 * g + 4 * half;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = acc[4 * g + e];
+    if constexpr (MODE == VL_GRAD) {   // columns up to the tile's end, inside P's row of a multiple of 256
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float q = expf(v[e] - lse) - (n + e == tgt ? 1.0f : 0.0f);
+        v[e] = dl == 0.0f || n + e >= N ? 0.0f : dl * q;
+      }
+      store4(reinterpret_cast<T*>(p.p) + (size_t)row * p.ldp + n, v);
+    } else if (n < N) {   // N = d, a multiple of 8
+      if constexpr (MODE == VL_DH) {
+        if (direct) {
+          store4(reinterpret_cast<T*>(p.dh) + (size_t)row * p.d + n, v);
+        } else {   // dh: partial product `split` of the pieces so far
+          float* to = p.dh_acc + ((size_t)split * p.T + row) * p.d + n;
+          if (!p.first) {
+            const float4 o = *reinterpret_cast<const float4*>(to);
+            v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+          }
+          store4(to, v);
+        }
+      } else if (direct) {
+        store4(reinterpret_cast<T*>(p.dw) + (size_t)(p.v0 + row) * p.d + n, v);
+      } else {
+        store4(p.dw_acc + ((size_t)split * M + row) * p.d + n, v);
+      }
+    }
+  }
+}
+
+// out = the sum of ks partial products of n elements in split order, rounded.
+template <typename T>
+__global__ __launch_bounds__(NT) void vocab_tile_join_kernel(const float* parts, T* out, size_t n, int ks) {
+  const size_t at = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
+  if (at >= n) return;   // n is a multiple of 8
+  float v[4] = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < ks; ++s) {
+    const float4 o = *reinterpret_cast<const float4*>(parts + s * n + at);
+    v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+  }
+  store4(out + at, v);
+}
+template <typename T>
+hipError_t launch_join(const float* parts, T* out, size_t n, int ks, hipStream_t s) {
+  vocab_tile_join_kernel<T><<<dim3((unsigned)((n / 4 + NT - 1) / NT)), dim3(NT), 0, s>>>(parts, out, n, ks);
+  return hipGetLastError();
+}
+
+// K per split of dh or dw, a multiple of a stage; dh's is the same for every piece of a call.
+template <typename T>
+int split_chunk(int M, int N, int K) {
+  constexpr int BK = 256 / sizeof(T);
+  return ceil_div(ceil_div(K, tile_splits(M, N, K)), BK) * BK;
+}
+
+template <typename T, int MODE>
+hipError_t launch(const VocabArgs& p, hipStream_t s) {
+  const int M = MODE == VL_DW ? p.vn : p.T;
+  const int N = MODE == VL_DW || MODE == VL_DH ? p.d : p.vn;
+  const int K = MODE == VL_DW ? p.T : (MODE == VL_DH ? p.vn : p.d);
+  const int kchunk = MODE == VL_DH ? split_chunk<T>(M, N, p.ldp) : (MODE == VL_DW ? split_chunk<T>(M, N, K) : K);
+  const int ks = ceil_div(K, kchunk);
+  // dh of a single piece and dw are stored in place unless they are split
+  const bool direct = ks == 1 && (MODE == VL_DW || (p.first && p.last));
+  const long long total = (long long)ceil_div(M, TS) * ceil_div(N, TS) * ks;
+  hipLaunchKernelGGL((vocab_tile_kernel<T, MODE>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(NT), 0, s, p, ks, kchunk, direct);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || MODE != VL_DW || direct) return e;
+  return launch_join<T>(p.dw_acc, reinterpret_cast<T*>(p.dw) + (size_t)p.v0 * p.d, (size_t)p.vn * p.d, ks, s);
+}
+
+template <typename T>
+hipError_t launch_mode(int mode, const VocabArgs& p, hipStream_t s) {
+  switch (mode) {
+    case VL_STATS: return launch<T, VL_STATS>(p, s);
+    case VL_GRAD: return launch<T, VL_GRAD>(p, s);
+    case VL_DH: return launch<T, VL_DH>(p, s);
+    case VL_DW: return launch<T, VL_DW>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t join_dh(const VocabArgs& p, hipStream_t s) {
+  // the first piece, the widest, used every split
+  const int ks = ceil_div(std::min(p.V, p.ldp), split_chunk<T>(p.T, p.d, p.ldp));
+  if (p.V <= p.ldp && ks == 1) return hipSuccess;   // written in place
+  return launch_join<T>(p.dh_acc, reinterpret_cast<T*>(p.dh), (size_t)p.T * p.d, ks, s);
+}
+
+}  // namespace
+
+// Splits of the K of an M x N product: as many as fill two workgroups per CU, at least 256 k each.
+int tile_splits(int M, int N, int K) {
+  const long long tiles = (long long)ceil_div(M, TS) * ceil_div(N, TS);
+  return (int)std::max<long long>(1, std::min<long long>(2 * NUM_CUS / tiles, K / 256));
+}
+
+size_t tile_acc_bytes(int M, int N, int K) { return (size_t)tile_splits(M, N, K) * M * N * sizeof(float); }
+
+hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s) {
+  return bf16 ? launch_mode<bf16_t>(mode, p, s) : launch_mode<float>(mode, p, s);
+}
+
+hipError_t launch_tile_join(const VocabArgs& p, bool bf16, hipStream_t s) {
+  return bf16 ? join_dh<bf16_t>(p, s) : join_dh<float>(p, s);
+}
+
+}  // namespace vocab
+}  // namespace moe
