@@ -15,6 +15,7 @@ struct VocabArgs {
   int T, d, V;
   int v0, vn;         // the piece: words v0 .. v0 + vn - 1
   int ldp;            // row length of P, a multiple of 256
+  const float* scale; // [1] the largest |dloss|: P is kept relative to it
   void* p;            // [T, ldp]; columns vn.. of a piece are zero as far as its last tile reaches
   float2* part;       // [parts][T] maximum and sum of exponentials of PIPE_PART or TILE_PART words
   float* dh_acc;      // dh of the pieces so far, fp32

@@ -1,7 +1,7 @@
 // Softmax cross entropy over a vocabulary and its gradient, in pieces of the vocabulary.
 //
 //   l = h w^T (T x V),  lse_t = log sum_v exp(l_tv),  loss_t = lse_t - l[t, target_t]
-//   P = dloss_t (exp(l_tv - lse_t) - [v = target_t]),  dh = P w,  dw = P^T h
+//   P = (dloss_t / s) (exp(l_tv - lse_t) - [v = target_t]),  dh = s P w,  dw = s P^T h
 //
 // The logits are never stored.  Forward: each tile of the product keeps, per row, the maximum and
 // the sum of exponentials of each 64 (or 32) of its columns; a second kernel joins a row's parts in a
@@ -9,6 +9,10 @@
 // epilogue writes P of the piece (in the storage type: the operand of the two gradient products; one
 // more rounding of its elements than an fp32 P would have, at four times the products' rate), and dh
 // accumulates over the pieces in fp32.
+// s is the largest |dloss| of a row with a loss.  Of the mean's gradient, where every dloss is 1 / n,
+// the target's element of P is then near -1, not near -1 / n, whose rounding to bf16 would be the same
+// in every row and add up in dw: at 8192 x 4096 x 65536 the gradients are 0.21% off the exact ones
+// instead of 0.27% (0.17% is the rounding of the outputs themselves).
 // A target outside [0, V) marks a row without loss: loss 0, P = 0 exactly.
 #include "vocab_loss.h"
 
@@ -110,6 +114,27 @@ hipError_t launch_lse(const VocabArgs& p, int parts, float* loss, float* lse, hi
   return hipGetLastError();
 }
 
+// The largest finite |dloss| of a row with a loss, 1 if there is none.
+__global__ __launch_bounds__(1024) void vocab_scale_kernel(VocabArgs p, float* scale) {
+  __shared__ float red[16];
+  float m = 0.0f;
+#pragma unroll 4
+  for (int t = threadIdx.x; t < p.T; t += 1024) {
+    const int v = p.target[t];
+    const float a = fabsf(p.dloss[t]);
+    if (v >= 0 && v < p.V && a <= 3.4028234664e38f) m = fmaxf(m, a);
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, red[i]);
+    *scale = m > 0.0f ? m : 1.0f;
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(NT) void fill_zero_kernel(T* p, size_t n) {
   for (size_t i = (size_t)blockIdx.x * NT + threadIdx.x; i < n; i += (size_t)gridDim.x * NT) p[i] = T(0);
@@ -160,11 +185,11 @@ hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t 
   return launch_lse<T>(p, ceil_div(p.V, pipe ? PIPE_PART : TILE_PART), loss, lse, s);
 }
 
-// The workspace of the backward: dh's accumulators, dw's partial products (64x64 tiles only; the last
+// The workspace of the backward: the scale, dh's accumulators, dw's partial products (64x64 tiles only; the last
 // piece may be narrower and split further), then P.
 struct BwdSpace {
-  size_t dh, dw, p;
-  size_t total() const { return dh + dw + p; }
+  size_t scale = 256, dh, dw, p;
+  size_t total() const { return scale + dh + dw + p; }
 };
 BwdSpace bwd_space(int T, int d, int V, bool bf16) {
   const int words = piece_words(T, V), wide = std::min(words, V), last = V - (V - 1) / words * words;
@@ -187,17 +212,23 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
   constexpr bool bf16 = sizeof(T) == 2;
   const int words = piece_words(p.T, p.V);
   const bool dhp = dh_pipe(p.T, p.d, words, bf16);
-  p.ldp = words;
   const BwdSpace space = bwd_space(p.T, p.d, p.V, bf16);
-  p.dh_acc = reinterpret_cast<float*>(ws);
-  p.dw_acc = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + space.dh);
-  p.p = reinterpret_cast<char*>(ws) + space.dh + space.dw;
+  p.ldp = words;
+  char* at = reinterpret_cast<char*>(ws);
+  float* scale = reinterpret_cast<float*>(at);
+  p.scale = scale;
+  p.dh_acc = reinterpret_cast<float*>(at += space.scale);
+  p.dw_acc = reinterpret_cast<float*>(at += space.dh);
+  p.p = at += space.dw;
+  vocab_scale_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, scale);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   for (int v0 = 0; v0 < p.V; v0 += words) {
     p.v0 = v0;
     p.vn = std::min(words, p.V - v0);
     p.first = v0 == 0;
     p.last = v0 + words >= p.V;
-    hipError_t e = launch_product(logits_pipe(p.T, p.d, p.vn, bf16), VL_GRAD, p, bf16, s);
+    e = launch_product(logits_pipe(p.T, p.d, p.vn, bf16), VL_GRAD, p, bf16, s);
     if (e == hipSuccess) e = launch_product(dhp, VL_DH, p, bf16, s);
     if (e == hipSuccess) e = launch_product(dw_pipe(p.T, p.d, p.vn, bf16), VL_DW, p, bf16, s);
     if (e != hipSuccess) return e;

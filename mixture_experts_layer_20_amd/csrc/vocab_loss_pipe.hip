@@ -1,7 +1,7 @@
 // Pipelined bf16 products of the vocabulary loss for gfx950, 256x256 tiles, with the loss's
 // epilogues (vocab_loss.hip has the formulas):
 //   VL_STATS  l = h w^T of all words -> maximum and sum of exponentials of each row's 64-word groups
-//   VL_GRAD   l of the piece's words again -> P = dloss (exp(l - lse) - [word = target]), bf16
+//   VL_GRAD   l of the piece's words again -> P = dloss / s (exp(l - lse) - [word = target]), bf16
 //   VL_DH     P w: accumulated over the pieces in fp32
 //   VL_DW     P^T h: the piece's rows of dw
 //
@@ -476,6 +476,7 @@ __device__ __forceinline__ void store_rows(const OutWin& w, const f32x16_t (&acc
 __device__ __forceinline__ void grad_epilogue(const VocabArgs& p, const Geo& g, f32x16_t (&acc)[MI][NI], int row0,
                                               int col0, int lane) {
   const bool edge = g.N - col0 < 64;
+  const float scale = *p.scale;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int row = row0 + 32 * i + (lane & 31);
@@ -484,7 +485,7 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& p, const Geo& g, 
     if (row < g.M) {
       tgt = p.target[row];
       if (tgt >= 0 && tgt < p.V) {
-        dl = p.dloss[row];
+        dl = p.dloss[row] / scale;
         l2 = dl == 0.0f ? l2 : p.lse[row] * LOG2E;
       }
     }
@@ -529,6 +530,13 @@ __device__ __forceinline__ void epilogue(const VocabArgs& p, const Geo& g, f32x1
         for (int q = 0; q < 4; ++q)
           to[((i * NI + j) * 4 + q) * 64] = f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
   } else {
+    const float scale = *p.scale;
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] *= scale;
     store_rows<0, true>(out_win(p.dw, ((size_t)p.v0 + row0) * p.d + col0, rows, p.d, g.N - col0), acc, lane);
   }
 }
@@ -616,7 +624,7 @@ __global__ __launch_bounds__(NTH, 1) void vocab_pipe_kernel(VocabArgs p, int ks,
   wait_vm<0>();   // no direct load may still be writing when the workgroup's LDS is released
 }
 
-// dh = the sum of the splits' accumulators, rounded.  A thread takes 4 columns of one row.
+// dh = the scaled sum of the splits' accumulators, rounded.  A thread takes 4 columns of one row.
 __global__ __launch_bounds__(256) void vocab_join_kernel(VocabArgs p, int ks, int MT, int NT) {
   const int per = MI * NI * 4 * 64;   // vectors of a wave
   const size_t slabs = (size_t)MT * NT * NW * per;
@@ -630,6 +638,7 @@ __global__ __launch_bounds__(256) void vocab_join_kernel(VocabArgs p, int ks, in
   const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.dh_acc) + at;
   f32x4_t s = from[0];
   for (int k = 1; k < ks; ++k) s += from[(size_t)k * slabs];
+  s *= *p.scale;
   u32x2_t w;
   w.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
   w.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);

@@ -245,12 +245,13 @@ __global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, 
     return;
   }
   if (row >= M) return;
+  const float out_scale = MODE != VL_GRAD && direct ? *p.scale : 1.0f;   // else the join scales
   float lse = 0.0f, dl = 0.0f;
   int tgt = -1;
   if constexpr (MODE == VL_GRAD) {
     lse = p.lse[row];
     tgt = p.target[row];
-    dl = tgt >= 0 && tgt < p.V ? p.dloss[row] : 0.0f;
+    dl = tgt >= 0 && tgt < p.V ? p.dloss[row] / *p.scale : 0.0f;
     tgt -= p.v0;
   }
 #pragma unroll
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, 
     const int n = c0 + 8 * g + 4 * half;
     float v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = acc[4 * g + e];
+    for (int e = 0; e < 4; ++e) v[e] = acc[4 * g + e] * out_scale;
     if constexpr (MODE == VL_GRAD) {   // columns up to the tile's end, inside P's row of a multiple of 256
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -287,9 +288,9 @@ __global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, 
   }
 }
 
-// out = the sum of ks partial products of n elements in split order, rounded.
+// out = the scaled sum of ks partial products of n elements in split order, rounded.
 template <typename T>
-__global__ __launch_bounds__(NT) void vocab_tile_join_kernel(const float* parts, T* out, size_t n, int ks) {
+__global__ __launch_bounds__(NT) void vocab_tile_join_kernel(const float* parts, T* out, size_t n, int ks, const float* scale) {
   const size_t at = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
   if (at >= n) return;   // n is a multiple of 8
   float v[4] = {0, 0, 0, 0};
@@ -298,11 +299,13 @@ __global__ __launch_bounds__(NT) void vocab_tile_join_kernel(const float* parts,
     const float4 o = *reinterpret_cast<const float4*>(parts + s * n + at);
     v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] *= *scale;
   store4(out + at, v);
 }
 template <typename T>
-hipError_t launch_join(const float* parts, T* out, size_t n, int ks, hipStream_t s) {
-  vocab_tile_join_kernel<T><<<dim3((unsigned)((n / 4 + NT - 1) / NT)), dim3(NT), 0, s>>>(parts, out, n, ks);
+hipError_t launch_join(const float* parts, T* out, size_t n, int ks, const float* scale, hipStream_t s) {
+  vocab_tile_join_kernel<T><<<dim3((unsigned)((n / 4 + NT - 1) / NT)), dim3(NT), 0, s>>>(parts, out, n, ks, scale);
   return hipGetLastError();
 }
 
@@ -326,7 +329,7 @@ hipError_t launch(const VocabArgs& p, hipStream_t s) {
   hipLaunchKernelGGL((vocab_tile_kernel<T, MODE>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(NT), 0, s, p, ks, kchunk, direct);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || MODE != VL_DW || direct) return e;
-  return launch_join<T>(p.dw_acc, reinterpret_cast<T*>(p.dw) + (size_t)p.v0 * p.d, (size_t)p.vn * p.d, ks, s);
+  return launch_join<T>(p.dw_acc, reinterpret_cast<T*>(p.dw) + (size_t)p.v0 * p.d, (size_t)p.vn * p.d, ks, p.scale, s);
 }
 
 template <typename T>
@@ -345,7 +348,7 @@ hipError_t join_dh(const VocabArgs& p, hipStream_t s) {
   // the first piece, the widest, used every split
   const int ks = ceil_div(std::min(p.V, p.ldp), split_chunk<T>(p.T, p.d, p.ldp));
   if (p.V <= p.ldp && ks == 1) return hipSuccess;   // written in place
-  return launch_join<T>(p.dh_acc, reinterpret_cast<T*>(p.dh), (size_t)p.T * p.d, ks, s);
+  return launch_join<T>(p.dh_acc, reinterpret_cast<T*>(p.dh), (size_t)p.T * p.d, ks, p.scale, s);
 }
 
 }  // namespace

@@ -236,7 +236,8 @@ def check_loss(h, w, target, dloss, dtype, got):
 
 
 LOSS_SIZES = [(1, 8, 1, 0.0), (1, 4096, 1000, 0.0), (2, 64, 127, 0.0), (5, 72, 129, 0.3), (63, 256, 257, 0.0),
-              (130, 136, 1000, 0.5), (257, 512, 513, 0.1), (300, 1000, 301, 0.0), (64, 2048, 4099, 0.2), (513, 64, 8200, 0.0)]
+              (130, 136, 1000, 0.5), (257, 512, 513, 0.1), (300, 1000, 301, 0.0), (64, 2048, 4099, 0.2), (513, 64, 8200, 0.0),
+              (700, 200, 16421, 0.1), (2500, 72, 4001, 0.2), (4097, 136, 300, 0.1), (1030, 1032, 3000, 0.1)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -271,6 +272,43 @@ def test_vocab_loss_with_no_target_at_all_and_confident_rows():
     dloss[5] = np.nan
     loss, lse, dh, dw = run_loss(h, w, target, dloss, "bf16")
     assert torch.isfinite(dh).all() and torch.isfinite(dw).all() and not dh[5].any()
+
+
+def test_vocab_loss_gradient_of_the_mean_is_not_biased():
+    """Every token's dloss is 1 / n and no target is likely: the gradient is the targets' rows, and the
+    rounding of 1 / n in P (up to 2^-9, the same in every row) must not show in it.  P's element of a
+    target is 1 - p with its sign: bf16 steps by 2^-8 below 1, so for p < 2^-9 it rounds to 1 and is off
+    by p, always outwards; for the other words and the outputs the roundings go either way."""
+    log("vocab loss: mean's gradient")
+    T, d, V = 300, 64, 5000
+    h, w, _, _ = loss_data(T, d, V, "bf16", 0.0, 12)
+    target = np.random.default_rng(1).permutation(V)[:T].astype(np.int32)
+    for n in (T, 307, 509):   # 1 / n rounds to bf16 by up to half a step
+        dloss = np.full(T, 1.0 / n, np.float32)
+        _, _, _, dw = run_loss(h, w, target, dloss, "bf16")
+        _, ref = S.vocab_loss_bwd(h, w, target, dloss)
+        got, ref = tnp(dw)[target].astype(np.float64), ref[target]
+        p = np.exp(-S.vocab_loss(h, w, target)[0])
+        assert p.max() < 2.0 ** -9
+        # the signed mean error of 300 x 64 independent roundings, each under 2^-8, stays below 6 sigma
+        signed = ((got - ref) * np.sign(ref)).sum() / np.abs(ref).sum()
+        assert abs(signed) < 6 * 2.0 ** -8 / np.sqrt(3 * T * d) + p.mean() * 1.5, signed   # |h| differs by row
+
+
+def test_vocab_loss_scales_of_dloss():
+    """dloss of very different sizes among the rows, tiny everywhere, infinite in one row."""
+    log("vocab loss: dloss scales")
+    T, d, V = 66, 64, 300
+    h, w, target, dloss = loss_data(T, d, V, "f32", 0.0, 13)
+    for f in (10.0 ** np.linspace(-12, 0, T), np.full(T, 1e-30)):
+        data = (h, w, target, (dloss * f).astype(np.float32))
+        check_loss(*data, "f32", run_loss(*data, "f32"))
+    dloss[7] = np.inf
+    _, _, dh, _ = run_loss(h, w, target, dloss, "f32")
+    ref, _ = S.vocab_loss_bwd(h, w, target, np.where(np.arange(T) == 7, 0.0, dloss))
+    rows = np.arange(T) != 7
+    assert not np.isfinite(tnp(dh)[7]).all()
+    assert_close("dh of the other rows", tnp(dh)[rows], ref[rows], 1e-5)
 
 
 def test_vocab_loss_without_tokens():
