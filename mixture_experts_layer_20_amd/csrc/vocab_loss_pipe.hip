@@ -171,6 +171,18 @@ __device__ __forceinline__ void set_tile(Producer& pr, const Geo& g, const Tile&
   pr.s.edge = (!Tr<MODE>::a_kc && g.M - t.m0 < BM) || (!Tr<MODE>::b_kc && g.N - t.n0 < BN);
 }
 
+// The stream's position in scalar registers: the compiler does not always see that it is the same in
+// every lane, and would then keep it per lane and branch on masks.
+__device__ __forceinline__ void scalar(Producer& pr, int& j) {
+  pr.k = uniform(pr.k);
+  pr.i = uniform(pr.i);
+  pr.t.nk = uniform(pr.t.nk);
+  pr.s.k_left = uniform(pr.s.k_left);
+  pr.s.sa = uniform_ptr(pr.s.sa);
+  pr.s.sb = uniform_ptr(pr.s.sb);
+  j = uniform(j);
+}
+
 // The next stage of the stream; past the last one it stays there (valid memory, into slots that
 // nobody reads again).
 template <int MODE>
@@ -185,14 +197,15 @@ __device__ __forceinline__ void advance(Producer& pr, const Geo& g, int hi, int 
   }
 }
 
-template <int MODE, int IDX>
+// EXACT: every tile and K step of the product is whole, so no piece needs a check.
+template <int MODE, bool EXACT, int IDX>
 __device__ __forceinline__ void issue(char* stage, const Producer& pr, const Geo& g, int wave, int lane) {
   constexpr bool A_OP = IDX < LP;
   constexpr int J = IDX % LP;
   constexpr bool KC = A_OP ? Tr<MODE>::a_kc : Tr<MODE>::b_kc;
   lvoid_t* to = (lvoid_t*)(stage + (A_OP ? 0 : OPB) + (LP * wave + J) * 1024);
   const char* src = (A_OP ? pr.s.sa : pr.s.sb) + (A_OP ? pr.o.a[J] : pr.o.b[J]);
-  if (pr.s.edge || pr.s.k_left < BKS) {   // the same in every lane
+  if (!EXACT && (pr.s.edge || pr.s.k_left < BKS)) {   // the same in every lane
     bool in;
     if constexpr (KC) in = kc_col(J, lane) < pr.s.k_left;
     else in = mc_krow(J, wave, lane) < pr.s.k_left && mc_col(J, lane) < (A_OP ? g.M - pr.t.m0 : g.N - pr.t.n0);
@@ -203,11 +216,11 @@ __device__ __forceinline__ void issue(char* stage, const Producer& pr, const Geo
   }
 }
 
-template <int MODE, int IDX>
+template <int MODE, bool EXACT, int IDX>
 __device__ __forceinline__ void issue_all(char* stage, const Producer& pr, const Geo& g, int wave, int lane) {
   if constexpr (IDX < 2 * LP) {
-    issue<MODE, IDX>(stage, pr, g, wave, lane);
-    issue_all<MODE, IDX + 1>(stage, pr, g, wave, lane);
+    issue<MODE, EXACT, IDX>(stage, pr, g, wave, lane);
+    issue_all<MODE, EXACT, IDX + 1>(stage, pr, g, wave, lane);
   }
 }
 
@@ -291,7 +304,7 @@ __device__ __forceinline__ void read_all(FragA<MODE>& a, FragB<MODE>& b, uint32_
 
 // One phase: the MFMAs of the current substep, between them the fragment reads of the next one and
 // (LOADS) the loads of the stage two steps ahead.  ACT = false: a wave without rows, loads only.
-template <int MODE, bool ACT, bool LOADS, int Q>
+template <int MODE, bool EXACT, bool ACT, bool LOADS, int Q>
 __device__ __forceinline__ void phase(f32x16_t (&acc)[MI][NI], const FragA<MODE>& ac, const FragB<MODE>& bc,
                                       FragA<MODE>& an, FragB<MODE>& bn, uint32_t ra, uint32_t rb, char* stage,
                                       const Producer& pr, const Geo& g, int wave, int lane) {
@@ -303,9 +316,9 @@ __device__ __forceinline__ void phase(f32x16_t (&acc)[MI][NI], const FragA<MODE>
       read_slot<MODE, Q>(an, bn, ra, rb);
       read_slot<MODE, Q + SLOTS>(an, bn, ra, rb);
     }
-    if constexpr (LOADS) issue<MODE, Q>(stage, pr, g, wave, lane);
+    if constexpr (LOADS) issue<MODE, EXACT, Q>(stage, pr, g, wave, lane);
     __builtin_amdgcn_sched_barrier(0);
-    phase<MODE, ACT, LOADS, Q + 1>(acc, ac, bc, an, bn, ra, rb, stage, pr, g, wave, lane);
+    phase<MODE, EXACT, ACT, LOADS, Q + 1>(acc, ac, bc, an, bn, ra, rb, stage, pr, g, wave, lane);
   }
 }
 
@@ -320,24 +333,24 @@ __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory
 template <int MODE>
 constexpr int epilogue_stores() { return MODE == VL_STATS ? 0 : 16; }
 
-template <int MODE, bool ACT>
+template <int MODE, bool EXACT, bool ACT>
 __device__ __forceinline__ void kstep(f32x16_t (&acc)[MI][NI], uint32_t fa, uint32_t fb, FragA<MODE>& a0,
                                       FragB<MODE>& b0, FragA<MODE>& a1, FragB<MODE>& b1, int j, bool after_epilogue,
                                       Producer& pr, const Geo& g, int hi, int step, int wave, int lane, char* lds) {
   constexpr bool AK = Tr<MODE>::a_kc, BK = Tr<MODE>::b_kc;
   const uint32_t sb = (j & 1) * STAGE, sn = ((j + 1) & 1) * STAGE;
-  phase<MODE, ACT, false, 0>(acc, a0, b0, a1, b1, sub_addr<AK, 1>(fa, sb), sub_addr<BK, 1>(fb, sb), nullptr, pr, g, wave, lane);
+  phase<MODE, EXACT, ACT, false, 0>(acc, a0, b0, a1, b1, sub_addr<AK, 1>(fa, sb), sub_addr<BK, 1>(fb, sb), nullptr, pr, g, wave, lane);
   if constexpr (ACT) frag_wait<MODE>(a1, b1);
-  phase<MODE, ACT, false, 0>(acc, a1, b1, a0, b0, sub_addr<AK, 2>(fa, sb), sub_addr<BK, 2>(fb, sb), nullptr, pr, g, wave, lane);
+  phase<MODE, EXACT, ACT, false, 0>(acc, a1, b1, a0, b0, sub_addr<AK, 2>(fa, sb), sub_addr<BK, 2>(fb, sb), nullptr, pr, g, wave, lane);
   if constexpr (ACT) frag_wait<MODE>(a0, b0);
-  phase<MODE, ACT, false, 0>(acc, a0, b0, a1, b1, sub_addr<AK, 3>(fa, sb), sub_addr<BK, 3>(fb, sb), nullptr, pr, g, wave, lane);
+  phase<MODE, EXACT, ACT, false, 0>(acc, a0, b0, a1, b1, sub_addr<AK, 3>(fa, sb), sub_addr<BK, 3>(fb, sb), nullptr, pr, g, wave, lane);
   if constexpr (ACT) frag_wait<MODE>(a1, b1);
   // Stage j + 1 has landed (the first step after an epilogue: only that epilogue's stores may still
   // be out, which were issued after the stage's loads), and every wave is done with slot j & 1.
   if (after_epilogue) wait_vm<epilogue_stores<MODE>()>();
   else wait_vm<0>();
   barrier();
-  phase<MODE, ACT, true, 0>(acc, a1, b1, a0, b0, sub_addr<AK, 0>(fa, sn), sub_addr<BK, 0>(fb, sn), lds + sb, pr, g, wave, lane);
+  phase<MODE, EXACT, ACT, true, 0>(acc, a1, b1, a0, b0, sub_addr<AK, 0>(fa, sn), sub_addr<BK, 0>(fb, sn), lds + sb, pr, g, wave, lane);
   advance<MODE>(pr, g, hi, step, wave, lane);
   if constexpr (ACT) frag_wait<MODE>(a0, b0);
 }
@@ -360,7 +373,16 @@ __device__ __forceinline__ float other_half_sum(float x) {
 __device__ __forceinline__ void stats_epilogue(const VocabArgs& p, const Geo& g, f32x16_t (&acc)[MI][NI], int row0,
                                                int col0, int lane) {
   if (col0 >= g.N) return;
-  const bool edge = g.N - col0 < 64;
+  if (g.N - col0 < 64) {         // words past the end
+    asm volatile("");
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (col0 + 32 * j + block_col(e, lane) >= g.N) acc[i][j][e] = -__builtin_inff();
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     float mx = -__builtin_inff();
@@ -368,7 +390,6 @@ __device__ __forceinline__ void stats_epilogue(const VocabArgs& p, const Geo& g,
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        if (edge && col0 + 32 * j + block_col(e, lane) >= g.N) acc[i][j][e] = -__builtin_inff();
         mx = fmaxf(mx, acc[i][j][e]);
       }
     mx = other_half_max(mx);
@@ -475,7 +496,6 @@ __device__ __forceinline__ void store_rows(const OutWin& w, const f32x16_t (&acc
 // Logits to P, in place.  A row without loss has lse = +inf and dl = 0: exactly zero.
 __device__ __forceinline__ void grad_epilogue(const VocabArgs& p, const Geo& g, f32x16_t (&acc)[MI][NI], int row0,
                                               int col0, int lane) {
-  const bool edge = g.N - col0 < 64;
   const float scale = *p.scale;
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -490,18 +510,30 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& p, const Geo& g, 
       }
     }
     const int tc = tgt - p.v0 - col0;   // the target's column in the wave's 64
-    const bool mine = tgt < p.V && tc >= 0 && tc < 64;
-    const bool any = __ballot(mine) != 0;
+    const bool mine = dl != 0.0f && tc >= 0 && tc < 64;
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float q = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -l2));
-        if (any && mine && 32 * j + block_col(e, lane) == tc) q -= 1.0f;
-        q *= dl;
-        if (edge && col0 + 32 * j + block_col(e, lane) >= g.N) q = 0.0f;
-        acc[i][j][e] = q;
-      }
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = dl * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], LOG2E, -l2));
+    if (__ballot(mine) != 0) {   // one wave in eight has a target at 128 rows x 64 of 65536 words
+      asm volatile("");          // a branch, not 32 selects for everybody
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (mine && 32 * j + block_col(e, lane) == tc) acc[i][j][e] -= dl;
+        }
+    }
+  }
+  if (g.N - col0 < 64) {         // words past the piece's end
+    asm volatile("");
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (col0 + 32 * j + block_col(e, lane) >= g.N) acc[i][j][e] = 0.0f;
   }
 }
 
@@ -541,7 +573,7 @@ __device__ __forceinline__ void epilogue(const VocabArgs& p, const Geo& g, f32x1
   }
 }
 
-template <int MODE, bool ACT>
+template <int MODE, bool EXACT, bool ACT>
 __device__ __forceinline__ void run_tile(const VocabArgs& p, const Geo& g, const Tile& t, uint32_t fa, uint32_t fb,
                                          FragA<MODE>& a0, FragB<MODE>& b0, FragA<MODE>& a1, FragB<MODE>& b1, int& j,
                                          bool& after_epilogue, Producer& pr, int hi, int step, int wm, int wn, int wave,
@@ -568,7 +600,8 @@ __device__ __forceinline__ void run_tile(const VocabArgs& p, const Geo& g, const
         for (int e = 0; e < 16; ++e) acc[i][jj][e] = 0.0f;
   }
   for (int k = 0; k < t.nk; ++k, ++j) {
-    kstep<MODE, ACT>(acc, fa, fb, a0, b0, a1, b1, j, after_epilogue, pr, g, hi, step, wave, lane, lds);
+    scalar(pr, j);
+    kstep<MODE, EXACT, ACT>(acc, fa, fb, a0, b0, a1, b1, j, after_epilogue, pr, g, hi, step, wave, lane, lds);
     after_epilogue = false;
   }
   // per-lane addressing of the epilogue is computed here, not kept in registers through the K loop
@@ -577,7 +610,7 @@ __device__ __forceinline__ void run_tile(const VocabArgs& p, const Geo& g, const
   after_epilogue = true;
 }
 
-template <int MODE>
+template <int MODE, bool EXACT>
 __global__ __launch_bounds__(NTH, 1) void vocab_pipe_kernel(VocabArgs p, int ks, int kchunk) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -599,7 +632,7 @@ __global__ __launch_bounds__(NTH, 1) void vocab_pipe_kernel(VocabArgs p, int ks,
   Tile t = pr.t;
 #pragma unroll 1
   for (int s = 0; s < 2; ++s) {
-    issue_all<MODE, 0>(lds + s * STAGE, pr, g, wave, lane);
+    issue_all<MODE, EXACT, 0>(lds + s * STAGE, pr, g, wave, lane);
     advance<MODE>(pr, g, hi, step, wave, lane);
   }
   wait_vm<2 * LP>();   // the first stage has landed
@@ -610,12 +643,12 @@ __global__ __launch_bounds__(NTH, 1) void vocab_pipe_kernel(VocabArgs p, int ks,
   bool after_epilogue = false;
   for (;;) {
     if (t.half && wm == 1) {
-      run_tile<MODE, false>(p, g, t, fa, fb, a0, b0, a1, b1, j, after_epilogue, pr, hi, step, wm, wn, wave, lane, lds);
+      run_tile<MODE, EXACT, false>(p, g, t, fa, fb, a0, b0, a1, b1, j, after_epilogue, pr, hi, step, wm, wn, wave, lane, lds);
     } else {
       const uint32_t sb = (j & 1) * STAGE;
       read_all<MODE, 0>(a0, b0, sub_addr<Tr<MODE>::a_kc, 0>(fa, sb), sub_addr<Tr<MODE>::b_kc, 0>(fb, sb));
       frag_wait<MODE>(a0, b0);
-      run_tile<MODE, true>(p, g, t, fa, fb, a0, b0, a1, b1, j, after_epilogue, pr, hi, step, wm, wn, wave, lane, lds);
+      run_tile<MODE, EXACT, true>(p, g, t, fa, fb, a0, b0, a1, b1, j, after_epilogue, pr, hi, step, wm, wn, wave, lane, lds);
     }
     i += step;
     if (i >= hi) break;
@@ -653,7 +686,9 @@ hipError_t launch(const VocabArgs& p, int M, int N, int K, int kchunk, hipStream
   const int ks = ceil_div(K, kchunk);
   const long long total = (long long)ceil_div(M, BM) * ceil_div(N, BN) * ks;
   const int grid = (int)std::min<long long>((total + 7) / 8 * 8, NUM_CUS);
-  hipLaunchKernelGGL(vocab_pipe_kernel<MODE>, dim3(grid), dim3(NTH), 0, s, p, ks, kchunk);
+  const bool exact = K % BKS == 0 && (MODE == VL_STATS || MODE == VL_GRAD || (N % BN == 0 && (MODE == VL_DH || M % BM == 0)));
+  if (exact) hipLaunchKernelGGL((vocab_pipe_kernel<MODE, true>), dim3(grid), dim3(NTH), 0, s, p, ks, kchunk);
+  else hipLaunchKernelGGL((vocab_pipe_kernel<MODE, false>), dim3(grid), dim3(NTH), 0, s, p, ks, kchunk);
   return hipGetLastError();
 }
 

@@ -1,25 +1,28 @@
 // The products of the vocabulary loss (vocab_loss.hip has the formulas) in 64x64 tiles, both types:
 // fp32, and bf16 where the 256x256 tiles of vocab_loss_pipe.hip are too few to fill the CUs.
 //
-// A workgroup of 4 waves takes one tile, 32x32 per wave, two workgroups per CU.  K goes through two
-// LDS stages of 256 bytes per row and operand (128 bf16 or 64 fp32 values), filled by direct-to-LDS
-// loads two steps ahead.  An operand contiguous along K is kept [64 rows][256 bytes], 16-byte chunks
-// XOR-swizzled by the row; one contiguous along its rows is kept [k][64 rows] and read transposed
+// A workgroup of 4 waves takes one tile, 32x32 per wave, two or four workgroups per CU.  K goes through
+// two LDS stages of 256 or 128 bytes per row and operand (64 bf16 or 32 fp32 values in 128 bytes),
+// filled by direct-to-LDS loads two steps ahead.  An operand contiguous along K is kept [64 rows][256
+// or 128 bytes], 16-byte chunks XOR-swizzled by the row; one contiguous along its rows is kept [k][64 rows] and read transposed
 // (bf16) or value by value (fp32).  fp32 products run on v_mfma_f32_32x32x2_f32, which multiplies and
 // adds in fp32; the two k of an instruction are 4 apart, so one 16-byte read feeds four of them.
 // Rows past the end are read clamped and not stored, K and columns past the end read zeros.
 #include "vocab_loss.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace vocab {
 namespace {
 
 constexpr int TS = 64;                  // tile rows and columns
-constexpr int NT = 256, LP = 4;         // threads; direct loads per wave, stage and operand
-constexpr int OPB = 64 * 256, STAGE = 2 * OPB;
-constexpr int NF = 8;                   // fragment groups of a stage: 16 bf16 or 8 fp32 k each
+constexpr int NT = 256;
+// NF: fragment groups of a stage, 16 bf16 or 8 fp32 k each, so 32 NF bytes of a row.
+constexpr int row_bytes(int nf) { return 32 * nf; }
+constexpr int loads(int nf) { return nf / 2; }           // direct loads per wave, stage and operand
+constexpr int op_bytes(int nf) { return 64 * row_bytes(nf); }
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
@@ -39,17 +42,25 @@ __device__ __forceinline__ uint32_t lds_addr_of(const void* ptr) {
   return (uint32_t)(uintptr_t)((const __attribute__((address_space(3))) char*)ptr);
 }
 
-// One operand's part of a stage: where each lane's loads read, and the LDS layout.
-template <typename T, bool KC>
+// Rows of 256 bytes: 16 rows read at one chunk hit 16 bank groups; of 128 bytes: two rows share one.
+template <int NF>
+__device__ __forceinline__ int swizzle(int row) {
+  return NF == 8 ? row & 15 : (row >> 1) & 7;
+}
+
+// One operand's part of a stage: where each lane's loads read, and the LDS layout.  ONCE: the operand
+// is read by this tile alone (nontemporal loads).
+template <typename T, bool KC, int NF, bool ONCE>
 struct Operand {
-  static constexpr int E = 16 / sizeof(T), BK = 256 / sizeof(T);
-  static constexpr int CPR = KC ? 16 : 64 / E;   // 16-byte chunks of an LDS row
+  static constexpr int ROWB = row_bytes(NF), LP = loads(NF);
+  static constexpr int E = 16 / sizeof(T), BK = ROWB / sizeof(T);
+  static constexpr int CPR = KC ? ROWB / 16 : 64 / E;   // 16-byte chunks of an LDS row
   const char* src[LP];
   int k[LP];       // first k of the lane's piece, from the tile's first
   bool in[LP];     // columns inside (not KC)
 
   __device__ __forceinline__ static int logical(int row, int chunk) {
-    if constexpr (KC) return chunk ^ (row & 15);
+    if constexpr (KC) return chunk ^ swizzle<NF>(row);
     else if constexpr (E == 8) return chunk ^ (((row >> 1) & 1) << 2);
     else return chunk ^ (((row >> 2) & 1) << 3);
   }
@@ -75,24 +86,24 @@ struct Operand {
 #pragma unroll
     for (int j = 0; j < LP; ++j) {
       const char* from = in[j] && at + k[j] < k_end ? src[j] : reinterpret_cast<const char*>(g_zeros);
-      __builtin_amdgcn_global_load_lds((gvoid_t*)from, (lvoid_t*)(lds + (wave * LP + j) * 1024), 16, 0, 0);
-      src[j] += KC ? (size_t)256 : (size_t)BK * ld * sizeof(T);
+      __builtin_amdgcn_global_load_lds((gvoid_t*)from, (lvoid_t*)(lds + (wave * LP + j) * 1024), 16, 0, ONCE ? 2 : 0);
+      src[j] += KC ? (size_t)ROWB : (size_t)BK * ld * sizeof(T);
     }
   }
 };
 
 // A wave's fragments of a stage.  Group s, lane l: row l % 32 of the block and, bf16: k 16 s + 8 (l / 32)
 // + 0..7; fp32: k 8 s + 4 (l / 32) + 0..3.
-template <typename T, bool KC>
+template <typename T, bool KC, int NF>
 struct Frags {
-  static constexpr int E = 16 / sizeof(T);
+  static constexpr int E = 16 / sizeof(T), ROWB = row_bytes(NF);
   u32x4_t v[NF];
   u32x2_t h[NF][2];   // bf16, not KC: two transposed reads of 4 k
 
   __device__ __forceinline__ void read(uint32_t base, int rb, int lane) {
     if constexpr (KC) {
       const int row = rb + (lane & 31);
-      const uint32_t a = base + row * 256 + (((lane >> 5) ^ (row & 15)) << 4);
+      const uint32_t a = base + row * ROWB + (((lane >> 5) ^ swizzle<NF>(row)) << 4);
 #pragma unroll
       for (int s = 0; s < NF; ++s) asm volatile("ds_read_b128 %0, %1" : "=v"(v[s]) : "v"(a ^ (uint32_t)(32 * s)));
     } else if constexpr (E == 8) {
@@ -157,10 +168,10 @@ __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
 
 // Workgroup b runs on XCD b % 8: each XCD walks one run of the tile order, rows first, so the tiles
 // that read one panel of the large operand run together.
-template <typename T, int MODE>
-__global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, int kchunk, bool direct) {
+template <typename T, int MODE, int NF, bool ONCE>
+__global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabArgs p, int ks, int kchunk, bool direct) {
   constexpr bool AK = Tr<MODE>::a_kc, BKC = Tr<MODE>::b_kc;
-  constexpr int BK = 256 / sizeof(T);
+  constexpr int BK = row_bytes(NF) / sizeof(T), LP = loads(NF), OPB = op_bytes(NF), STAGE = 2 * OPB;
   __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave >> 1, wn = wave & 1;
@@ -185,8 +196,8 @@ __global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, 
   const int k0 = split * kchunk, k_end = min(K - k0, kchunk);
   const int nk = (k_end + BK - 1) / BK;
 
-  Operand<T, AK> oa;
-  Operand<T, BKC> ob;
+  Operand<T, AK, NF, false> oa;
+  Operand<T, BKC, NF, ONCE> ob;
   oa.init(abase, lda, m0, M, k0, wave, lane);
   ob.init(bbase, ldb, n0, N, k0, wave, lane);
   // Past the last stage the loads read zeros into slots that nobody reads.
@@ -204,8 +215,8 @@ __global__ __launch_bounds__(NT, 2) void vocab_tile_kernel(VocabArgs p, int ks, 
     const uint32_t sb = lds0 + (j & 1) * STAGE;
     wait_vm<2 * LP>();   // stage j has landed, stage j + 1 may be in flight
     barrier();
-    Frags<T, AK> fa;
-    Frags<T, BKC> fb;
+    Frags<T, AK, NF> fa;
+    Frags<T, BKC, NF> fb;
     fa.read(sb, wm * 32, lane);
     fb.read(sb + OPB, wn * 32, lane);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -326,7 +337,22 @@ hipError_t launch(const VocabArgs& p, hipStream_t s) {
   // dh of a single piece and dw are stored in place unless they are split
   const bool direct = ks == 1 && (MODE == VL_DW || (p.first && p.last));
   const long long total = (long long)ceil_div(M, TS) * ceil_div(N, TS) * ks;
-  hipLaunchKernelGGL((vocab_tile_kernel<T, MODE>), dim3((unsigned)((total + 7) / 8 * 8)), dim3(NT), 0, s, p, ks, kchunk, direct);
+  const dim3 grid((unsigned)((total + 7) / 8 * 8));
+  // 256 bytes of each word's row at a time where a single row tile reads the words once (bound by that
+  // stream), 128 otherwise (four workgroups per CU): 64 tokens x 12485 words x d 3472 forward 26.6 us
+  // against 33.3, 500 x 4000 x 2048 21.3 against 19.7.
+  constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
+  // That stream is nontemporal in the forward where it would displace most of the last-level cache:
+  // 7 tokens against 205 MB of words 45.5 us instead of 52.5; 87 MB, which the backward then finds in
+  // the cache, would take 12 us longer there.
+  auto run = [&](auto nf, auto once) {
+    hipLaunchKernelGGL((vocab_tile_kernel<T, MODE, decltype(nf)::value, decltype(once)::value>), grid, dim3(NT), 0, s, p, ks, kchunk, direct);
+  };
+  typedef std::integral_constant<int, LOGITS ? 8 : 4> Stream;
+  typedef std::integral_constant<bool, MODE == VL_STATS> Once;
+  if (LOGITS && M <= TS && (size_t)N * K * sizeof(T) >= size_t(128) << 20) run(Stream{}, Once{});
+  else if (LOGITS && M <= TS) run(Stream{}, std::false_type{});
+  else run(std::integral_constant<int, 4>{}, std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || MODE != VL_DW || direct) return e;
   return launch_join<T>(p.dw_acc, reinterpret_cast<T*>(p.dw) + (size_t)p.v0 * p.d, (size_t)p.vn * p.d, ks, p.scale, s);
