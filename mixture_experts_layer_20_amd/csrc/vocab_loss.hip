@@ -119,11 +119,7 @@ __global__ __launch_bounds__(1024) void vocab_scale_kernel(VocabArgs p, float* s
   __shared__ float red[16];
   float m = 0.0f;
 #pragma unroll 4
-  for (int t = threadIdx.x; t < p.T; t += 1024) {
-    const int v = p.target[t];
-    const float a = fabsf(p.dloss[t]);
-    if (v >= 0 && v < p.V && a <= 3.4028234664e38f) m = fmaxf(m, a);
-  }
+  for (int t = threadIdx.x; t < p.T; t += 1024) m = fmaxf(m, dloss_size(p, t));
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
@@ -185,8 +181,8 @@ hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t 
   return launch_lse<T>(p, ceil_div(p.V, pipe ? PIPE_PART : TILE_PART), loss, lse, s);
 }
 
-// The workspace of the backward: the scale, dh's accumulators, dw's partial products (64x64 tiles only; the last
-// piece may be narrower and split further), then P.
+// The workspace of the backward: the scale, dh's accumulators, dw's partial products (64x64 tiles only;
+// the last piece may be narrower and split further), then P.
 struct BwdSpace {
   size_t scale = 256, dh, dw, p;
   size_t total() const { return scale + dh + dw + p; }
@@ -220,20 +216,32 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
   p.dh_acc = reinterpret_cast<float*>(at += space.scale);
   p.dw_acc = reinterpret_cast<float*>(at += space.dh);
   p.p = at += space.dw;
-  vocab_scale_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, scale);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (p.T <= SCALE_ROWS && !logits_pipe(p.T, p.d, std::min(words, p.V), bf16)) {
+    p.scale_out = scale;   // the first piece's tiles find it
+  } else {
+    vocab_scale_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, scale);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   for (int v0 = 0; v0 < p.V; v0 += words) {
     p.v0 = v0;
     p.vn = std::min(words, p.V - v0);
     p.first = v0 == 0;
     p.last = v0 + words >= p.V;
     e = launch_product(logits_pipe(p.T, p.d, p.vn, bf16), VL_GRAD, p, bf16, s);
+    p.scale_out = nullptr;
+    const bool dwp = dw_pipe(p.T, p.d, p.vn, bf16);
+    if (!dhp && !dwp) {
+      if (e == hipSuccess) e = launch_tile_pair(p, bf16, s);
+      if (e != hipSuccess) return e;
+      continue;
+    }
     if (e == hipSuccess) e = launch_product(dhp, VL_DH, p, bf16, s);
-    if (e == hipSuccess) e = launch_product(dw_pipe(p.T, p.d, p.vn, bf16), VL_DW, p, bf16, s);
+    if (e == hipSuccess) e = launch_product(dwp, VL_DW, p, bf16, s);
+    if (e == hipSuccess && p.last) e = dhp ? launch_pipe_join(p, s) : launch_tile_join(p, bf16, s);
     if (e != hipSuccess) return e;
   }
-  return dhp ? launch_pipe_join(p, s) : launch_tile_join(p, bf16, s);
+  return hipSuccess;
 }
 
 }  // namespace

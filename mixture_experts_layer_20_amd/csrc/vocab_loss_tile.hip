@@ -166,13 +166,38 @@ __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// Workgroup b runs on XCD b % 8: each XCD walks one run of the tile order, rows first, so the tiles
-// that read one panel of the large operand run together.
+// How a product is cut: splits of K, K per split, whether the tiles store the result itself (else
+// partial products, which a join adds up).
+struct Cut {
+  int ks, kchunk;
+  bool direct;
+};
+
+// The largest finite |dloss| of a row with a loss, 1 if there is none, for at most SCALE_ROWS rows.
+__device__ __forceinline__ float scale_of_rows(const VocabArgs& p) {
+  __shared__ float red[NT / 64];
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < SCALE_ROWS / NT; ++i) {
+    const int t = threadIdx.x + i * NT;
+    if (t < p.T) m = fmaxf(m, dloss_size(p, t));
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  return m > 0.0f ? m : 1.0f;
+}
+
+// One tile.  Workgroup `block` of the product runs on XCD block % 8: each XCD walks one run of the tile
+// order, rows first, so the tiles that read one panel of the large operand run together.
 template <typename T, int MODE, int NF, bool ONCE>
-__global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabArgs p, int ks, int kchunk, bool direct) {
+__device__ __forceinline__ void run_tile(const VocabArgs& p, const Cut& cut, int block, char* lds) {
   constexpr bool AK = Tr<MODE>::a_kc, BKC = Tr<MODE>::b_kc;
   constexpr int BK = row_bytes(NF) / sizeof(T), LP = loads(NF), OPB = op_bytes(NF), STAGE = 2 * OPB;
-  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+  const int ks = cut.ks, kchunk = cut.kchunk;
+  const bool direct = cut.direct;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave >> 1, wn = wave & 1;
   constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
@@ -188,8 +213,8 @@ __global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabAr
 
   const int MT = (M + TS - 1) / TS, NTL = (N + TS - 1) / TS, total = MT * NTL * ks;
   const int per = (total + 7) >> 3;
-  const int L = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if ((int)(blockIdx.x >> 3) >= per || L >= total) return;
+  const int L = (block & 7) * per + (block >> 3);
+  if ((block >> 3) >= per || L >= total) return;
   const int split = L / (MT * NTL), l = L - split * (MT * NTL);
   const int nt = l / MT, mt = l - nt * MT;
   const int m0 = mt * TS, n0 = nt * TS;
@@ -255,6 +280,15 @@ __global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabAr
     if (half == 0 && row < M) p.part[(size_t)((p.v0 + c0) / TILE_PART) * p.T + row] = make_float2(mx, sm);
     return;
   }
+  float scale = 1.0f;
+  if constexpr (MODE == VL_GRAD) {
+    if (p.scale_out) {   // few rows: every tile finds the scale itself, one writes it for the kernels after
+      scale = scale_of_rows(p);
+      if (L == 0 && threadIdx.x == 0) *p.scale_out = scale;
+    } else {
+      scale = *p.scale;
+    }
+  }
   if (row >= M) return;
   const float out_scale = MODE != VL_GRAD && direct ? *p.scale : 1.0f;   // else the join scales
   float lse = 0.0f, dl = 0.0f;
@@ -262,7 +296,7 @@ __global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabAr
   if constexpr (MODE == VL_GRAD) {
     lse = p.lse[row];
     tgt = p.target[row];
-    dl = tgt >= 0 && tgt < p.V ? p.dloss[row] / *p.scale : 0.0f;
+    dl = tgt >= 0 && tgt < p.V ? p.dloss[row] / scale : 0.0f;
     tgt -= p.v0;
   }
 #pragma unroll
@@ -299,24 +333,52 @@ __global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabAr
   }
 }
 
-// out = the scaled sum of ks partial products of n elements in split order, rounded.
+template <typename T, int MODE, int NF, bool ONCE>
+__global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabArgs p, Cut cut) {
+  __shared__ __attribute__((aligned(1024))) char lds[4 * op_bytes(NF)];
+  run_tile<T, MODE, NF, ONCE>(p, cut, blockIdx.x, lds);
+}
+
+// dh's and dw's products side by side: neither needs the other, and of few rows and words neither
+// fills the CUs alone (257 x 256 against 1000 words in fp32: 10 us together, 10 us each apart).
 template <typename T>
-__global__ __launch_bounds__(NT) void vocab_tile_join_kernel(const float* parts, T* out, size_t n, int ks, const float* scale) {
-  const size_t at = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
-  if (at >= n) return;   // n is a multiple of 8
+__global__ __launch_bounds__(NT, 4) void vocab_tile_pair_kernel(VocabArgs p, Cut dh, Cut dw, int dh_blocks) {
+  __shared__ __attribute__((aligned(1024))) char lds[4 * op_bytes(4)];
+  if ((int)blockIdx.x < dh_blocks) run_tile<T, VL_DH, 4, false>(p, dh, blockIdx.x, lds);
+  else run_tile<T, VL_DW, 4, false>(p, dw, blockIdx.x - dh_blocks, lds);
+}
+
+// out = the scaled sum of ks partial products of n elements in split order, rounded; two such sums in
+// one launch (n = 0: none).
+template <typename T>
+struct Join {
+  const float* parts;
+  T* out;
+  size_t n;   // a multiple of 8
+  int ks;
+};
+template <typename T>
+__global__ __launch_bounds__(NT) void vocab_tile_join_kernel(Join<T> a, Join<T> b, const float* scale) {
+  size_t at = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
+  if (at >= a.n) {
+    at -= a.n;
+    a = b;
+    if (at >= a.n) return;
+  }
   float v[4] = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = 0; s < ks; ++s) {
-    const float4 o = *reinterpret_cast<const float4*>(parts + s * n + at);
+  for (int s = 0; s < a.ks; ++s) {
+    const float4 o = *reinterpret_cast<const float4*>(a.parts + s * a.n + at);
     v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] *= *scale;
-  store4(out + at, v);
+  store4(a.out + at, v);
 }
 template <typename T>
-hipError_t launch_join(const float* parts, T* out, size_t n, int ks, const float* scale, hipStream_t s) {
-  vocab_tile_join_kernel<T><<<dim3((unsigned)((n / 4 + NT - 1) / NT)), dim3(NT), 0, s>>>(parts, out, n, ks, scale);
+hipError_t launch_join(const Join<T>& a, const Join<T>& b, const float* scale, hipStream_t s) {
+  if (a.n + b.n == 0) return hipSuccess;
+  vocab_tile_join_kernel<T><<<dim3((unsigned)(((a.n + b.n) / 4 + NT - 1) / NT)), dim3(NT), 0, s>>>(a, b, scale);
   return hipGetLastError();
 }
 
@@ -327,35 +389,60 @@ int split_chunk(int M, int N, int K) {
   return ceil_div(ceil_div(K, tile_splits(M, N, K)), BK) * BK;
 }
 
+template <typename T>
+Cut cut_of(int mode, const VocabArgs& p) {
+  Cut c{1, mode == VL_DW ? p.T : p.d, true};
+  if (mode == VL_DH) {
+    c.kchunk = split_chunk<T>(p.T, p.d, p.ldp);
+    c.ks = ceil_div(p.vn, c.kchunk);
+    c.direct = c.ks == 1 && p.first && p.last;   // dh of several pieces is accumulated in fp32
+  } else if (mode == VL_DW) {
+    c.kchunk = split_chunk<T>(p.vn, p.d, p.T);
+    c.ks = ceil_div(p.T, c.kchunk);
+    c.direct = c.ks == 1;
+  }
+  return c;
+}
+
+// Workgroups of a product, a multiple of the XCDs.
+unsigned blocks_of(int mode, const VocabArgs& p, const Cut& c) {
+  const int M = mode == VL_DW ? p.vn : p.T, N = mode == VL_DW || mode == VL_DH ? p.d : p.vn;
+  return (unsigned)(((long long)ceil_div(M, TS) * ceil_div(N, TS) * c.ks + 7) / 8 * 8);
+}
+
+template <typename T>
+Join<T> join_dw(const VocabArgs& p, const Cut& c) {
+  return Join<T>{p.dw_acc, reinterpret_cast<T*>(p.dw) + (size_t)p.v0 * p.d, c.direct ? 0 : (size_t)p.vn * p.d, c.ks};
+}
+// The sum over all pieces: the first one, the widest, used every split.
+template <typename T>
+Join<T> join_dh(const VocabArgs& p) {
+  const int wide = std::min(p.V, p.ldp), ks = ceil_div(wide, split_chunk<T>(p.T, p.d, p.ldp));
+  return Join<T>{p.dh_acc, reinterpret_cast<T*>(p.dh), ks == 1 && p.V <= p.ldp ? 0 : (size_t)p.T * p.d, ks};
+}
+
 template <typename T, int MODE>
 hipError_t launch(const VocabArgs& p, hipStream_t s) {
-  const int M = MODE == VL_DW ? p.vn : p.T;
-  const int N = MODE == VL_DW || MODE == VL_DH ? p.d : p.vn;
-  const int K = MODE == VL_DW ? p.T : (MODE == VL_DH ? p.vn : p.d);
-  const int kchunk = MODE == VL_DH ? split_chunk<T>(M, N, p.ldp) : (MODE == VL_DW ? split_chunk<T>(M, N, K) : K);
-  const int ks = ceil_div(K, kchunk);
-  // dh of a single piece and dw are stored in place unless they are split
-  const bool direct = ks == 1 && (MODE == VL_DW || (p.first && p.last));
-  const long long total = (long long)ceil_div(M, TS) * ceil_div(N, TS) * ks;
-  const dim3 grid((unsigned)((total + 7) / 8 * 8));
+  const Cut c = cut_of<T>(MODE, p);
+  const dim3 grid(blocks_of(MODE, p, c));
   // 256 bytes of each word's row at a time where a single row tile reads the words once (bound by that
   // stream), 128 otherwise (four workgroups per CU): 64 tokens x 12485 words x d 3472 forward 26.6 us
   // against 33.3, 500 x 4000 x 2048 21.3 against 19.7.
-  constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
   // That stream is nontemporal in the forward where it would displace most of the last-level cache:
   // 7 tokens against 205 MB of words 45.5 us instead of 52.5; 87 MB, which the backward then finds in
   // the cache, would take 12 us longer there.
+  constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
   auto run = [&](auto nf, auto once) {
-    hipLaunchKernelGGL((vocab_tile_kernel<T, MODE, decltype(nf)::value, decltype(once)::value>), grid, dim3(NT), 0, s, p, ks, kchunk, direct);
+    hipLaunchKernelGGL((vocab_tile_kernel<T, MODE, decltype(nf)::value, decltype(once)::value>), grid, dim3(NT), 0, s, p, c);
   };
   typedef std::integral_constant<int, LOGITS ? 8 : 4> Stream;
   typedef std::integral_constant<bool, MODE == VL_STATS> Once;
-  if (LOGITS && M <= TS && (size_t)N * K * sizeof(T) >= size_t(128) << 20) run(Stream{}, Once{});
-  else if (LOGITS && M <= TS) run(Stream{}, std::false_type{});
+  if (LOGITS && p.T <= TS && (size_t)p.vn * p.d * sizeof(T) >= size_t(128) << 20) run(Stream{}, Once{});
+  else if (LOGITS && p.T <= TS) run(Stream{}, std::false_type{});
   else run(std::integral_constant<int, 4>{}, std::false_type{});
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || MODE != VL_DW || direct) return e;
-  return launch_join<T>(p.dw_acc, reinterpret_cast<T*>(p.dw) + (size_t)p.v0 * p.d, (size_t)p.vn * p.d, ks, p.scale, s);
+  if (e != hipSuccess || MODE != VL_DW) return e;
+  return launch_join(join_dw<T>(p, c), Join<T>{}, p.scale, s);
 }
 
 template <typename T>
@@ -370,11 +457,13 @@ hipError_t launch_mode(int mode, const VocabArgs& p, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t join_dh(const VocabArgs& p, hipStream_t s) {
-  // the first piece, the widest, used every split
-  const int ks = ceil_div(std::min(p.V, p.ldp), split_chunk<T>(p.T, p.d, p.ldp));
-  if (p.V <= p.ldp && ks == 1) return hipSuccess;   // written in place
-  return launch_join<T>(p.dh_acc, reinterpret_cast<T*>(p.dh), (size_t)p.T * p.d, ks, p.scale, s);
+hipError_t launch_both(const VocabArgs& p, hipStream_t s) {
+  const Cut dh = cut_of<T>(VL_DH, p), dw = cut_of<T>(VL_DW, p);
+  const unsigned nh = blocks_of(VL_DH, p, dh), nw = blocks_of(VL_DW, p, dw);
+  hipLaunchKernelGGL(vocab_tile_pair_kernel<T>, dim3(nh + nw), dim3(NT), 0, s, p, dh, dw, (int)nh);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_join(join_dw<T>(p, dw), p.last ? join_dh<T>(p) : Join<T>{}, p.scale, s);
 }
 
 }  // namespace
@@ -391,8 +480,12 @@ hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s) {
   return bf16 ? launch_mode<bf16_t>(mode, p, s) : launch_mode<float>(mode, p, s);
 }
 
+hipError_t launch_tile_pair(const VocabArgs& p, bool bf16, hipStream_t s) {
+  return bf16 ? launch_both<bf16_t>(p, s) : launch_both<float>(p, s);
+}
+
 hipError_t launch_tile_join(const VocabArgs& p, bool bf16, hipStream_t s) {
-  return bf16 ? join_dh<bf16_t>(p, s) : join_dh<float>(p, s);
+  return bf16 ? launch_join(join_dh<bf16_t>(p), Join<bf16_t>{}, p.scale, s) : launch_join(join_dh<float>(p), Join<float>{}, p.scale, s);
 }
 
 }  // namespace vocab
