@@ -41,10 +41,12 @@ __device__ __forceinline__ float dloss_size(const VocabArgs& p, int t) {
 
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
-// The pipelined bf16 kernel (256x256 tiles).  dh_acc holds the accumulator tiles of pipe_splits()
-// partial products in the kernel's own order; pipe_join adds them into dh.
-int pipe_splits(int T, int d, int words);
-size_t pipe_acc_bytes(int T, int d, int words);
+// The pipelined bf16 kernel (256x256 tiles).  dh_acc and dw_acc hold the accumulator tiles of the
+// splits' partial products in the kernel's own order; VL_DW joins its own, launch_pipe_join dh's.
+int pipe_dh_splits(int T, int d, int words);
+int pipe_dw_splits(int T, int d, int words);
+size_t pipe_dh_bytes(int T, int d, int words);
+size_t pipe_dw_bytes(int T, int d, int words);
 hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s);
 hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s);
 

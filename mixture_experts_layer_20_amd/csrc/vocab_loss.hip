@@ -159,10 +159,10 @@ bool use_pipe(int M, int N, int K, int pipe_ks, int tile_ks, bool bf16) {
 }
 bool logits_pipe(int T, int d, int words, bool bf16) { return use_pipe(T, words, d, 1, 1, bf16); }
 bool dw_pipe(int T, int d, int words, bool bf16) {
-  return use_pipe(words, d, T, 1, tile_splits(words, d, T), bf16);
+  return use_pipe(words, d, T, pipe_dw_splits(T, d, words), tile_splits(words, d, T), bf16);
 }
 bool dh_pipe(int T, int d, int words, bool bf16) {
-  return use_pipe(T, d, words, pipe_splits(T, d, words), tile_splits(T, d, words), bf16);
+  return use_pipe(T, d, words, pipe_dh_splits(T, d, words), tile_splits(T, d, words), bf16);
 }
 
 hipError_t launch_product(bool pipe, int mode, const VocabArgs& p, bool bf16, hipStream_t s) {
@@ -181,8 +181,8 @@ hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t 
   return launch_lse<T>(p, ceil_div(p.V, pipe ? PIPE_PART : TILE_PART), loss, lse, s);
 }
 
-// The workspace of the backward: the scale, dh's accumulators, dw's partial products (64x64 tiles only;
-// the last piece may be narrower and split further), then P.
+// The workspace of the backward: the scale, dh's accumulators, dw's partial products (where its rows
+// are split; the last piece may be narrower and split further), then P.
 struct BwdSpace {
   size_t scale = 256, dh, dw, p;
   size_t total() const { return scale + dh + dw + p; }
@@ -190,10 +190,12 @@ struct BwdSpace {
 BwdSpace bwd_space(int T, int d, int V, bool bf16) {
   const int words = piece_words(T, V), wide = std::min(words, V), last = V - (V - 1) / words * words;
   BwdSpace s;
-  s.dh = align256(dh_pipe(T, d, words, bf16) ? pipe_acc_bytes(T, d, words) : tile_acc_bytes(T, d, words));
+  s.dh = align256(dh_pipe(T, d, words, bf16) ? pipe_dh_bytes(T, d, words) : tile_acc_bytes(T, d, words));
   s.dw = 0;
-  for (int vn : {wide, last})
-    if (!dw_pipe(T, d, vn, bf16) && tile_splits(vn, d, T) > 1) s.dw = std::max(s.dw, align256(tile_acc_bytes(vn, d, T)));
+  for (int vn : {wide, last}) {
+    const size_t tile = tile_splits(vn, d, T) > 1 ? tile_acc_bytes(vn, d, T) : 0;
+    s.dw = std::max(s.dw, align256(dw_pipe(T, d, vn, bf16) ? pipe_dw_bytes(T, d, vn) : tile));
+  }
   s.p = (size_t)T * words * (bf16 ? 2 : 4);
   return s;
 }

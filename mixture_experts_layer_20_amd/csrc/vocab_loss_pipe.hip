@@ -41,8 +41,10 @@ typedef __attribute__((address_space(3))) void lvoid_t;
 
 __device__ __attribute__((aligned(16))) uint4 g_zeros[64];
 
+constexpr int VL_DW_SPLIT = 4;   // VL_DW with its K split: partial products to the workspace
+
 template <int MODE> struct Tr {
-  static constexpr bool a_kc = MODE != VL_DW;
+  static constexpr bool a_kc = MODE != VL_DW && MODE != VL_DW_SPLIT;
   static constexpr bool b_kc = MODE == VL_STATS || MODE == VL_GRAD;
 };
 
@@ -538,8 +540,17 @@ __device__ __forceinline__ void grad_epilogue(const VocabArgs& p, const Geo& g, 
 }
 
 // The wave's accumulators in the workspace: 128 x 64 floats, one KiB per store of 4 elements.
-__device__ __forceinline__ f32x4_t* acc_slab(const VocabArgs& p, const Tile& t, int wave) {
-  return reinterpret_cast<f32x4_t*>(p.dh_acc) + ((size_t)t.slab * NW + wave) * (MI * NI * 4 * 64);
+__device__ __forceinline__ f32x4_t* acc_slab(float* acc, const Tile& t, int wave) {
+  return reinterpret_cast<f32x4_t*>(acc) + ((size_t)t.slab * NW + wave) * (MI * NI * 4 * 64);
+}
+__device__ __forceinline__ void store_slab(f32x4_t* to, const f32x16_t (&acc)[MI][NI]) {
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        to[((i * NI + j) * 4 + q) * 64] = f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
 }
 
 template <int MODE>
@@ -553,14 +564,9 @@ __device__ __forceinline__ void epilogue(const VocabArgs& p, const Geo& g, f32x1
     grad_epilogue(p, g, acc, row0, col0, lane);
     store_rows<0, false>(out_win(p.p, (size_t)row0 * p.ldp + col0, rows, p.ldp, 64), acc, lane);
   } else if constexpr (MODE == VL_DH) {
-    f32x4_t* to = acc_slab(p, t, wave) + lane;
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          to[((i * NI + j) * 4 + q) * 64] = f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    store_slab(acc_slab(p.dh_acc, t, wave) + lane, acc);
+  } else if constexpr (MODE == VL_DW_SPLIT) {
+    store_slab(acc_slab(p.dw_acc, t, wave) + lane, acc);
   } else {
     const float scale = *p.scale;
 #pragma unroll
@@ -580,7 +586,7 @@ __device__ __forceinline__ void run_tile(const VocabArgs& p, const Geo& g, const
                                          int lane, char* lds) {
   f32x16_t acc[MI][NI];
   if (MODE == VL_DH && !p.first) {
-    const f32x4_t* from = acc_slab(p, t, wave) + lane;
+    const f32x4_t* from = acc_slab(p.dh_acc, t, wave) + lane;
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -657,8 +663,9 @@ __global__ __launch_bounds__(NTH, 1) void vocab_pipe_kernel(VocabArgs p, int ks,
   wait_vm<0>();   // no direct load may still be writing when the workgroup's LDS is released
 }
 
-// dh = the scaled sum of the splits' accumulators, rounded.  A thread takes 4 columns of one row.
-__global__ __launch_bounds__(256) void vocab_join_kernel(VocabArgs p, int ks, int MT, int NT) {
+// out [M, N] = the scaled sum of the splits' accumulators, rounded.  A thread takes 4 columns of a row.
+__global__ __launch_bounds__(256) void vocab_join_kernel(const float* acc, bf16_t* out, int M, int N, int ks, const float* scale) {
+  const int MT = (M + BM - 1) / BM, NT = (N + BN - 1) / BN;
   const int per = MI * NI * 4 * 64;   // vectors of a wave
   const size_t slabs = (size_t)MT * NT * NW * per;
   const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
@@ -667,19 +674,24 @@ __global__ __launch_bounds__(256) void vocab_join_kernel(VocabArgs p, int ks, in
   const int tile = (int)(at / ((size_t)per * NW));
   const int row = tile / NT * BM + wave / WGN * 32 * MI + blk / NI * 32 + (lane & 31);
   const int col = tile % NT * BN + wave % WGN * 32 * NI + blk % NI * 32 + 8 * q + 4 * (lane >> 5);
-  if (row >= p.T || col >= p.d) return;
-  const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.dh_acc) + at;
+  if (row >= M || col >= N) return;
+  const f32x4_t* from = reinterpret_cast<const f32x4_t*>(acc) + at;
   f32x4_t s = from[0];
   for (int k = 1; k < ks; ++k) s += from[(size_t)k * slabs];
-  s *= *p.scale;
+  s *= *scale;
   u32x2_t w;
   w.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
   w.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
-  *reinterpret_cast<u32x2_t*>(reinterpret_cast<bf16_t*>(p.dh) + (size_t)row * p.d + col) = w;
+  *reinterpret_cast<u32x2_t*>(out + (size_t)row * N + col) = w;
+}
+hipError_t launch_join(const float* acc, bf16_t* out, int M, int N, int ks, const float* scale, hipStream_t s) {
+  const size_t vectors = (size_t)ceil_div(M, BM) * ceil_div(N, BN) * (BM * BN / 4);
+  hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)(vectors / 256)), dim3(256), 0, s, acc, out, M, N, ks, scale);
+  return hipGetLastError();
 }
 
-// K per split: a multiple of the K step, the same for every piece of a call.
-int split_chunk(const VocabArgs& p) { return ceil_div(ceil_div(p.ldp, pipe_splits(p.T, p.d, p.ldp)), BKS) * BKS; }
+// K per split of dh or dw: a multiple of the K step; dh's is the same for every piece of a call.
+int split_chunk(int K, int splits) { return ceil_div(ceil_div(K, splits), BKS) * BKS; }
 
 template <int MODE>
 hipError_t launch(const VocabArgs& p, int M, int N, int K, int kchunk, hipStream_t s) {
@@ -694,33 +706,46 @@ hipError_t launch(const VocabArgs& p, int M, int N, int K, int kchunk, hipStream
 
 }  // namespace
 
-// Splits of dh's sum over a piece's words: as many as the CUs hold beside the output tiles, at least
-// 512 words each.
-int pipe_splits(int T, int d, int words) {
-  const int tiles = ceil_div(T, BM) * ceil_div(d, BN);
-  return std::max(1, std::min(NUM_CUS / tiles, words / 512));
+namespace {
+// As many splits as the CUs hold beside the output tiles, at least least_k k each.
+int splits(int M, int N, int K, int least_k) {
+  const long long tiles = (long long)ceil_div(M, BM) * ceil_div(N, BN);
+  return (int)std::max<long long>(1, std::min<long long>(NUM_CUS / tiles, K / least_k));
 }
+size_t acc_bytes(int M, int N, int ks) { return (size_t)ks * ceil_div(M, BM) * ceil_div(N, BN) * BM * BN * sizeof(float); }
+}  // namespace
 
-size_t pipe_acc_bytes(int T, int d, int words) {
-  return (size_t)pipe_splits(T, d, words) * ceil_div(T, BM) * ceil_div(d, BN) * BM * BN * sizeof(float);
+// dh passes through fp32 memory anyway (it is accumulated over the pieces); dw only where its sum is
+// split, which pays from some 1500 rows per split on: 5000 rows x d 400 x 40000 words, forward and
+// backward, 1220 -> 1036 us; 2048 x 1024 x 8000 split in two 176 -> 182.
+int pipe_dh_splits(int T, int d, int words) { return splits(T, d, words, 512); }
+int pipe_dw_splits(int T, int d, int words) { return splits(words, d, T, 1536); }
+size_t pipe_dh_bytes(int T, int d, int words) { return acc_bytes(T, d, pipe_dh_splits(T, d, words)); }
+size_t pipe_dw_bytes(int T, int d, int words) {
+  const int ks = pipe_dw_splits(T, d, words);
+  return ks > 1 ? acc_bytes(words, d, ks) : 0;
 }
 
 hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s) {
   switch (mode) {
     case VL_STATS: return launch<VL_STATS>(p, p.T, p.vn, p.d, p.d, s);
     case VL_GRAD: return launch<VL_GRAD>(p, p.T, p.vn, p.d, p.d, s);
-    case VL_DH: return launch<VL_DH>(p, p.T, p.d, p.vn, split_chunk(p), s);
-    case VL_DW: return launch<VL_DW>(p, p.vn, p.d, p.T, p.T, s);
+    case VL_DH: return launch<VL_DH>(p, p.T, p.d, p.vn, split_chunk(p.ldp, pipe_dh_splits(p.T, p.d, p.ldp)), s);
+    case VL_DW: {
+      const int kchunk = split_chunk(p.T, pipe_dw_splits(p.T, p.d, p.vn)), ks = ceil_div(p.T, kchunk);
+      if (ks == 1) return launch<VL_DW>(p, p.vn, p.d, p.T, kchunk, s);
+      const hipError_t e = launch<VL_DW_SPLIT>(p, p.vn, p.d, p.T, kchunk, s);
+      if (e != hipSuccess) return e;
+      return launch_join(p.dw_acc, reinterpret_cast<bf16_t*>(p.dw) + (size_t)p.v0 * p.d, p.vn, p.d, ks, p.scale, s);
+    }
   }
   return hipErrorInvalidValue;
 }
 
 hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s) {
   // the first piece, the widest, used every split
-  const int ks = ceil_div(std::min(p.V, p.ldp), split_chunk(p));
-  const int MT = ceil_div(p.T, BM), NT = ceil_div(p.d, BN);
-  hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)((size_t)MT * NT * (BM * BN / 4) / 256)), dim3(256), 0, s, p, ks, MT, NT);
-  return hipGetLastError();
+  const int ks = ceil_div(std::min(p.V, p.ldp), split_chunk(p.ldp, pipe_dh_splits(p.T, p.d, p.ldp)));
+  return launch_join(p.dh_acc, reinterpret_cast<bf16_t*>(p.dh), p.T, p.d, ks, p.scale, s);
 }
 
 }  // namespace vocab

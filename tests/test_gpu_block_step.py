@@ -257,6 +257,14 @@ def test_vocab_loss_over_several_pieces(dtype):
     check_loss(*data, dtype, run_loss(*data, dtype))
 
 
+def test_vocab_loss_with_dw_split_over_the_rows():
+    """Many rows against few words and columns: the large tiles split dw's sum as well as dh's."""
+    T, d, V = 4100, 520, 9001
+    log(f"vocab loss bf16 dw split T={T} d={d} V={V}")
+    data = loss_data(T, d, V, "bf16", 0.1, 6)
+    check_loss(*data, "bf16", run_loss(*data, "bf16"))
+
+
 def test_vocab_loss_with_no_target_at_all_and_confident_rows():
     log("vocab loss: all ignored; confident rows")
     T, d, V = 70, 128, 500
