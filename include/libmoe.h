@@ -374,7 +374,7 @@ moe_status_t moe_norm_in_bwd(const void* dxn, const void* x, const void* w, cons
  *     marks a token without loss: loss 0 and no gradient.  Its row of h is still read and must be finite.
  *   loss, lse [T] float                              OUTPUT
  * Products of bf16 data accumulate in fp32, exponentials and sums are fp32.  d must be a multiple of
- * 8, at most 65536; T and V at most 2^22, T V at most about 2^43; T may be 0.
+ * 8, at most 65536; T and V at most 2^22, T V, V d and T d at most 2^35; T may be 0.
  * Source: "Olmo-core DDP MoE examples", "Production throughput runs" (language-model training runs;
  * the pages do not print the loss). */
 size_t moe_vocab_loss_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt);

@@ -716,7 +716,10 @@ moe_status_t check_vocab(int64_t T, int64_t d, int64_t V, moe_dtype_t dt) {
         (long long)d);
   CHECK(T <= kVocabMax && V <= kVocabMax, MOE_ERR_UNSUPPORTED, "T and V must be at most 2^22 (got T=%lld, V=%lld)",
         (long long)T, (long long)V);
-  CHECK(((T + 63) / 64) * ((V + 63) / 64) < kMaxInt, MOE_ERR_UNSUPPORTED, "grid too large");
+  // Tiles of 64 x 64 outputs with 256 threads each: a grid has fewer than 2^32 threads.
+  const int64_t most = int64_t(1) << 35;
+  CHECK(T * V <= most && V * d <= most && T * d <= most, MOE_ERR_UNSUPPORTED,
+        "T V, V d and T d must be at most 2^35 (got T=%lld, d=%lld, V=%lld)", (long long)T, (long long)d, (long long)V);
   return MOE_OK;
 }
 

@@ -104,40 +104,41 @@ __global__ __launch_bounds__(threads<L>()) void norm_in_kernel(const T* x, const
                                                      float* rstd) {
   __shared__ float red[2][16];
   const int lane = threadIdx.x % L;
-  const int t = blockIdx.x * (threads<L>() / L) + threadIdx.x / L;
-  if (t >= rows) return;   // L = 64: whole waves, no barrier below; otherwise there are no such rows
   int slot = 0;
-  Seg8<T> xr[NV], wr[NV];
+  // (a wave, or a workgroup whose row sum has barriers, leaves the loop as a whole)
+  for (int t = blockIdx.x * (threads<L>() / L) + threadIdx.x / L; t < rows; t += gridDim.x * (threads<L>() / L)) {
+    Seg8<T> xr[NV], wr[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const Cols k = cols<L>(lane, i, d);
-    if (k.in) {
-      xr[i].load(x + (size_t)t * d + k.c);
-      wr[i].load(w + k.c);
-    } else {
-      xr[i].zero();
+    for (int i = 0; i < NV; ++i) {
+      const Cols k = cols<L>(lane, i, d);
+      if (k.in) {
+        xr[i].load(x + (size_t)t * d + k.c);
+        wr[i].load(w + k.c);
+      } else {
+        xr[i].zero();
+      }
     }
-  }
-  float s = 0.0f;
+    float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float v[8];
-    xr[i].get(v);
+    for (int i = 0; i < NV; ++i) {
+      float v[8];
+      xr[i].get(v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += v[e] * v[e];
-  }
-  const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
-  if (rstd && lane == 0) rstd[t] = r;
+      for (int e = 0; e < 8; ++e) s += v[e] * v[e];
+    }
+    const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
+    if (rstd && lane == 0) rstd[t] = r;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const Cols k = cols<L>(lane, i, d);
-    if (!k.in) continue;
-    float v[8], wv[8];
-    xr[i].get(v);
-    wr[i].get(wv);
+    for (int i = 0; i < NV; ++i) {
+      const Cols k = cols<L>(lane, i, d);
+      if (!k.in) continue;
+      float v[8], wv[8];
+      xr[i].get(v);
+      wr[i].get(wv);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * r * wv[e];
-    Seg8<T>::put(xn + (size_t)t * d + k.c, v);
+      for (int e = 0; e < 8; ++e) v[e] = v[e] * r * wv[e];
+      Seg8<T>::put(xn + (size_t)t * d + k.c, v);
+    }
   }
 }
 
@@ -153,105 +154,105 @@ __global__ __launch_bounds__(threads<L>()) void norm_out_kernel(const T* y, cons
                                                       T* y_out, T* out, float* rstd) {
   __shared__ float red[2][16];
   const int lane = threadIdx.x % L;
-  const int t = blockIdx.x * (threads<L>() / L) + threadIdx.x / L;
-  if (t >= rows) return;
   int slot = 0;
-  float yv[NV][8];
-  Seg8<T> xr[NV], wr[NV], gr[NV], sr[NV];
-  const T* grow = gate ? gate + (size_t)(t / gate_rows) * d : nullptr;
-  auto load = [&](Seg8<T> (&r)[NV], const T* from) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const Cols q = cols<L>(lane, i, d);
-      if (q.in) r[i].load(from + q.c);
-      else r[i].zero();
-    }
-  };
-  if constexpr (COMBINE) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) yv[i][e] = 0.0f;
-    constexpr int G = 4;   // rows in flight
-    for (int j0 = 0; j0 < k; j0 += G) {
-      Seg8<T> r[G][NV];
-      float g[G];
-#pragma unroll
-      for (int u = 0; u < G; ++u)
-        if (j0 + u < k) {
-          g[u] = topk_gate[(size_t)t * k + j0 + u];
-          const T* row = y + (size_t)dest_pos[(size_t)t * k + j0 + u] * d;
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const Cols q = cols<L>(lane, i, d);
-            if (q.in) r[u][i].load_once(row + q.c);
-            else r[u][i].zero();
-          }
-        }
-      if (j0 == 0) {
-        if (shared) load(sr, shared + (size_t)t * d);
-        load(xr, x + (size_t)t * d);
-      }
-#pragma unroll
-      for (int u = 0; u < G; ++u)
-        if (j0 + u < k) {
-#pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            float v[8];
-            r[u][i].get(v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) yv[i][e] += g[u] * v[e];
-          }
-        }
-    }
-    if (shared) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float v[8];
-        sr[i].get(v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) yv[i][e] += v[e];
-      }
-    }
-    if (y_out) {
+  for (int t = blockIdx.x * (threads<L>() / L) + threadIdx.x / L; t < rows; t += gridDim.x * (threads<L>() / L)) {
+    float yv[NV][8];
+    Seg8<T> xr[NV], wr[NV], gr[NV], sr[NV];
+    const T* grow = gate ? gate + (size_t)(t / gate_rows) * d : nullptr;
+    auto load = [&](Seg8<T> (&r)[NV], const T* from) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const Cols q = cols<L>(lane, i, d);
-        if (q.in) Seg8<T>::put(y_out + (size_t)t * d + q.c, yv[i]);
+        if (q.in) r[i].load(from + q.c);
+        else r[i].zero();
       }
+    };
+    if constexpr (COMBINE) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) yv[i][e] = 0.0f;
+      constexpr int G = 4;   // rows in flight
+      for (int j0 = 0; j0 < k; j0 += G) {
+        Seg8<T> r[G][NV];
+        float g[G];
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+          if (j0 + u < k) {
+            g[u] = topk_gate[(size_t)t * k + j0 + u];
+            const T* row = y + (size_t)dest_pos[(size_t)t * k + j0 + u] * d;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              const Cols q = cols<L>(lane, i, d);
+              if (q.in) r[u][i].load_once(row + q.c);
+              else r[u][i].zero();
+            }
+          }
+        if (j0 == 0) {
+          if (shared) load(sr, shared + (size_t)t * d);
+          load(xr, x + (size_t)t * d);
+        }
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+          if (j0 + u < k) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+              float v[8];
+              r[u][i].get(v);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) yv[i][e] += g[u] * v[e];
+            }
+          }
+      }
+      if (shared) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float v[8];
+          sr[i].get(v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) yv[i][e] += v[e];
+        }
+      }
+      if (y_out) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const Cols q = cols<L>(lane, i, d);
+          if (q.in) Seg8<T>::put(y_out + (size_t)t * d + q.c, yv[i]);
+        }
+      }
+    } else {
+      load(sr, y + (size_t)t * d);
+      load(xr, x + (size_t)t * d);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sr[i].get(yv[i]);
     }
-  } else {
-    load(sr, y + (size_t)t * d);
-    load(xr, x + (size_t)t * d);
+    load(wr, w);
+    if (grow) load(gr, grow);
+    float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sr[i].get(yv[i]);
-  }
-  load(wr, w);
-  if (grow) load(gr, grow);
-  float s = 0.0f;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+      for (int e = 0; e < 8; ++e) s += yv[i][e] * yv[i][e];
+    const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
+    if (rstd && lane == 0) rstd[t] = r;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += yv[i][e] * yv[i][e];
-  const float r = 1.0f / sqrtf(row_sum<L>(s, red, slot) / (float)d + eps);
-  if (rstd && lane == 0) rstd[t] = r;
+    for (int i = 0; i < NV; ++i) {
+      const Cols q = cols<L>(lane, i, d);
+      if (!q.in) continue;
+      float xv[8], wv[8], o[8];
+      xr[i].get(xv);
+      wr[i].get(wv);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const Cols q = cols<L>(lane, i, d);
-    if (!q.in) continue;
-    float xv[8], wv[8], o[8];
-    xr[i].get(xv);
-    wr[i].get(wv);
+      for (int e = 0; e < 8; ++e) o[e] = yv[i][e] * r * wv[e];
+      if (grow) {
+        gr[i].get(wv);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = yv[i][e] * r * wv[e];
-    if (grow) {
-      gr[i].get(wv);
+        for (int e = 0; e < 8; ++e) o[e] *= wv[e];
+      }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] *= wv[e];
+      for (int e = 0; e < 8; ++e) o[e] += res_scale * xv[e];
+      Seg8<T>::put(out + (size_t)t * d + q.c, o);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] += res_scale * xv[e];
-    Seg8<T>::put(out + (size_t)t * d + q.c, o);
   }
 }
 
@@ -505,6 +506,9 @@ hipError_t by_width(int d, F&& f) {
   return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
 }
 
+// One workgroup for each turn of rows, as far as a grid of 2^32 threads goes.
+int fwd_blocks(int T, int rows) { return std::min(ceil_div(T, rows), 1 << 20); }
+
 // Rows per workgroup of the backward: about BLOCKS workgroups, at least one row per wave or
 // workgroup that walks rows.
 constexpr int BLOCKS = 1024;
@@ -555,7 +559,7 @@ hipError_t launch_norm_in(const void* x, const void* w, int T, int d, float eps,
     typedef decltype(tag) E;
     auto run = [&](auto L, auto NV) {
       hipLaunchKernelGGL((norm_in_kernel<E, decltype(L)::value, decltype(NV)::value>),
-                         dim3(ceil_div(T, threads<decltype(L)::value>() / decltype(L)::value)),
+                         dim3(fwd_blocks(T, threads<decltype(L)::value>() / decltype(L)::value)),
                          dim3(threads<decltype(L)::value>()), 0, s, (const E*)x, (const E*)w, T, d, eps,
                          (E*)xn, rstd);
       return hipGetLastError();
@@ -574,7 +578,7 @@ hipError_t launch_norm_out(const void* y, const float* topk_gate, const int32_t*
     typedef decltype(tag) E;
     return by_width(d, [&](auto L, auto NV) {
       hipLaunchKernelGGL((norm_out_kernel<E, decltype(L)::value, decltype(NV)::value, decltype(comb)::value>),
-                         dim3(ceil_div(T, threads<decltype(L)::value>() / decltype(L)::value)),
+                         dim3(fwd_blocks(T, threads<decltype(L)::value>() / decltype(L)::value)),
                          dim3(threads<decltype(L)::value>()), 0, s, (const E*)y, topk_gate, dest_pos,
                          (const E*)shared, k, (const E*)x, (const E*)w, (const E*)gate, gate_rows, res_scale, T, d, eps,
                          (E*)y_out, (E*)out, rstd);

@@ -249,7 +249,7 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
 }  // namespace
 
 size_t vocab_loss_ws_bytes(long long T, long long d, long long V, bool bf16) {
-  return (size_t)T * ((V + TILE_PART - 1) / TILE_PART) * sizeof(float2);
+  return (size_t)T * ceil_div(V, logits_pipe((int)T, (int)d, (int)V, bf16) ? PIPE_PART : TILE_PART) * sizeof(float2);
 }
 
 hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target, int T, int d, int V, bool bf16,

@@ -668,25 +668,25 @@ __global__ __launch_bounds__(256) void vocab_join_kernel(const float* acc, bf16_
   const int MT = (M + BM - 1) / BM, NT = (N + BN - 1) / BN;
   const int per = MI * NI * 4 * 64;   // vectors of a wave
   const size_t slabs = (size_t)MT * NT * NW * per;
-  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= slabs) return;
-  const int lane = at % 64, q = at / 64 % 4, blk = at / 256 % (MI * NI), wave = at / per % NW;
-  const int tile = (int)(at / ((size_t)per * NW));
-  const int row = tile / NT * BM + wave / WGN * 32 * MI + blk / NI * 32 + (lane & 31);
-  const int col = tile % NT * BN + wave % WGN * 32 * NI + blk % NI * 32 + 8 * q + 4 * (lane >> 5);
-  if (row >= M || col >= N) return;
-  const f32x4_t* from = reinterpret_cast<const f32x4_t*>(acc) + at;
-  f32x4_t s = from[0];
-  for (int k = 1; k < ks; ++k) s += from[(size_t)k * slabs];
-  s *= *scale;
-  u32x2_t w;
-  w.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
-  w.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
-  *reinterpret_cast<u32x2_t*>(out + (size_t)row * N + col) = w;
+  for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < slabs; at += (size_t)gridDim.x * 256) {
+    const int lane = at % 64, q = at / 64 % 4, blk = at / 256 % (MI * NI), wave = at / per % NW;
+    const int tile = (int)(at / ((size_t)per * NW));
+    const int row = tile / NT * BM + wave / WGN * 32 * MI + blk / NI * 32 + (lane & 31);
+    const int col = tile % NT * BN + wave % WGN * 32 * NI + blk % NI * 32 + 8 * q + 4 * (lane >> 5);
+    if (row >= M || col >= N) continue;
+    const f32x4_t* from = reinterpret_cast<const f32x4_t*>(acc) + at;
+    f32x4_t s = from[0];
+    for (int k = 1; k < ks; ++k) s += from[(size_t)k * slabs];
+    s *= *scale;
+    u32x2_t w;
+    w.x = (uint32_t)f32_to_bf16(s[0]) | ((uint32_t)f32_to_bf16(s[1]) << 16);
+    w.y = (uint32_t)f32_to_bf16(s[2]) | ((uint32_t)f32_to_bf16(s[3]) << 16);
+    *reinterpret_cast<u32x2_t*>(out + (size_t)row * N + col) = w;
+  }
 }
 hipError_t launch_join(const float* acc, bf16_t* out, int M, int N, int ks, const float* scale, hipStream_t s) {
   const size_t vectors = (size_t)ceil_div(M, BM) * ceil_div(N, BN) * (BM * BN / 4);
-  hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)(vectors / 256)), dim3(256), 0, s, acc, out, M, N, ks, scale);
+  hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)std::min<size_t>(vectors / 256, 1 << 20)), dim3(256), 0, s, acc, out, M, N, ks, scale);
   return hipGetLastError();
 }
 

@@ -359,26 +359,25 @@ struct Join {
 };
 template <typename T>
 __global__ __launch_bounds__(NT) void vocab_tile_join_kernel(Join<T> a, Join<T> b, const float* scale) {
-  size_t at = ((size_t)blockIdx.x * NT + threadIdx.x) * 4;
-  if (at >= a.n) {
-    at -= a.n;
-    a = b;
-    if (at >= a.n) return;
-  }
-  float v[4] = {0, 0, 0, 0};
+  const size_t step = (size_t)gridDim.x * NT * 4;
+  for (size_t i = ((size_t)blockIdx.x * NT + threadIdx.x) * 4; i < a.n + b.n; i += step) {
+    const Join<T>& j = i < a.n ? a : b;
+    const size_t at = i < a.n ? i : i - a.n;
+    float v[4] = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int s = 0; s < a.ks; ++s) {
-    const float4 o = *reinterpret_cast<const float4*>(a.parts + s * a.n + at);
-    v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
-  }
+    for (int s = 0; s < j.ks; ++s) {
+      const float4 o = *reinterpret_cast<const float4*>(j.parts + s * j.n + at);
+      v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+    }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] *= *scale;
-  store4(a.out + at, v);
+    for (int e = 0; e < 4; ++e) v[e] *= *scale;
+    store4(j.out + at, v);
+  }
 }
 template <typename T>
 hipError_t launch_join(const Join<T>& a, const Join<T>& b, const float* scale, hipStream_t s) {
   if (a.n + b.n == 0) return hipSuccess;
-  vocab_tile_join_kernel<T><<<dim3((unsigned)(((a.n + b.n) / 4 + NT - 1) / NT)), dim3(NT), 0, s>>>(a, b, scale);
+  vocab_tile_join_kernel<T><<<dim3((unsigned)std::min<size_t>(((a.n + b.n) / 4 + NT - 1) / NT, 1 << 20)), dim3(NT), 0, s>>>(a, b, scale);
   return hipGetLastError();
 }
 

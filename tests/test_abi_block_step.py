@@ -80,7 +80,9 @@ def test_vocab_loss_refusals():
     expect(UNSUPPORTED, f, *args(d=1 << 17))
     expect(UNSUPPORTED, f, *args(V=(1 << 22) + 1))
     expect(UNSUPPORTED, f, *args(T=(1 << 22) + 1))
-    expect(UNSUPPORTED, f, *args(T=1 << 22, V=1 << 22))
+    expect(UNSUPPORTED, f, *args(T=1 << 20, V=1 << 16))
+    expect(UNSUPPORTED, f, *args(d=1 << 16, V=1 << 20))
+    expect(UNSUPPORTED, f, *args(d=1 << 16, T=1 << 20))
     expect(INVALID, f, *args(V=0))
     expect(INVALID, f, *args(T=-1))
     expect(INVALID, f, *args(dt=3))

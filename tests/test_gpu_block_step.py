@@ -168,6 +168,41 @@ def test_norm_rows_of_zeros_and_extreme_scales():
         assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
 
 
+def test_norms_of_more_rows_than_one_grid():
+    """2^20 workgroups of four rows, and five rows more."""
+    log("norms: many rows")
+    T, d = (1 << 22) + 5, 8
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((T, d)).astype(np.float32)
+    w = (1 + 0.1 * rng.standard_normal(d)).astype(np.float32)
+    xd, xn, out, r = f32(x), empty(T, d), empty(T, d), empty(T)
+    L.moe_norm_in(xd, f32(w), T, d, EPS, L.MOE_F32, xn, r)
+    ref, _ = S.norm_in(x, w, EPS)
+    within("xn", tnp(xn), ref, (STAT + 4 * U) * np.abs(ref))
+    L.moe_norm_out(xd, xn, f32(w), None, 1, 0.0, EPS, T, d, L.MOE_F32, out, None)
+    assert torch.equal(out, xn)
+
+
+def test_norm_offsets_beyond_32_bits():
+    log("norms: 4.9e9 elements")
+    T, d, n = 600_000, 8192, 3
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    xn, r = torch.empty_like(x), empty(T)
+    c, t = norm_data(n, d, "bf16", 0, 5)
+    x[-n:] = t["x"]
+    L.moe_norm_in(x, t["w_in"], T, d, EPS, L.MOE_BF16, xn, r)
+    ref, ref_r = S.norm_in(c["x"], c["w_in"], EPS)
+    within("xn", tnp(xn[-n:]), ref, (STAT + 4 * U + HALF["bf16"]) * np.abs(ref))
+    assert not xn[:10].any()
+    g = torch.zeros_like(x)
+    g[-n:] = t["dxn"]
+    dw, ws = empty(d), ws_of(L.moe_norm_bwd_workspace_size(T, d))
+    L.moe_norm_in_bwd(g, x, t["w_in"], r, None, 1.0, T, d, L.MOE_BF16, xn, dw, ws, ws.numel())
+    _, ref_dw = S.norm_in_bwd(c["dxn"], c["x"], c["w_in"], ref_r, None, 1.0)
+    # three rows have terms: the sums add at most those, whatever their order, and zeros exactly
+    within("dw", tnp(dw), ref_dw, (n * U + STAT) * np.abs(c["dxn"] * c["x"] * ref_r[:, None]).sum(axis=0))
+
+
 def test_norms_without_rows():
     log("norms: no rows")
     d = 64
@@ -263,6 +298,51 @@ def test_vocab_loss_with_dw_split_over_the_rows():
     log(f"vocab loss bf16 dw split T={T} d={d} V={V}")
     data = loss_data(T, d, V, "bf16", 0.1, 6)
     check_loss(*data, "bf16", run_loss(*data, "bf16"))
+
+
+def _gpu_reference(h, w, target, dloss, rows):
+    """Loss, dh of the first and last rows and dw in float64 on the GPU, a block of rows at a time."""
+    T, V = h.shape[0], w.shape[0]
+    w64, dw, loss, dh = w.double(), torch.zeros(w.shape, dtype=torch.float64, device=DEV), [], []
+    for t0 in range(0, T, rows):
+        hb, tb = h[t0:t0 + rows].double(), target[t0:t0 + rows].long()
+        l = hb @ w64.t()
+        lse = torch.logsumexp(l, 1)
+        at = torch.arange(len(tb), device=DEV)
+        loss.append(lse - l[at, tb])
+        p = torch.exp(l - lse[:, None])
+        p[at, tb] -= 1.0
+        p *= dloss[t0:t0 + rows, None].double()
+        dw += p.t().contiguous() @ hb
+        if t0 == 0 or t0 + rows >= T:
+            dh.append((p @ w64)[:1] if t0 == 0 else (p @ w64)[-1:])
+    return torch.cat(loss), torch.cat(dh), dw
+
+
+@pytest.mark.parametrize("T,d,V", [(530_000, 64, 4096), (24, 4096, 600_000)])
+def test_vocab_loss_offsets_beyond_32_bits(T, d, V):
+    """P of 2.2e9 elements; w and dw of 2.5e9.  The layer's tolerance: the sums are far longer than the
+    terms that matter, and the bound by terms would say nothing."""
+    log(f"vocab loss bf16 T={T} d={d} V={V}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    h = torch.randn(T, d, device=DEV, generator=g).to(torch.bfloat16)
+    w = (0.1 * torch.randn(V, d, device=DEV, generator=g)).to(torch.bfloat16)
+    target = torch.randint(0, V, (T,), device=DEV, generator=g).to(torch.int32)
+    target[-1] = V - 1
+    dloss = torch.rand(T, device=DEV, generator=g)
+    loss, lse, dh, dw = empty(T), empty(T), torch.empty_like(h), torch.empty_like(w)
+    ws = torch.empty(L.moe_vocab_loss_workspace_size(T, d, V, 1), dtype=torch.uint8, device=DEV)
+    L.moe_vocab_loss(h, w, target, T, d, V, L.MOE_BF16, loss, lse, ws, ws.numel())
+    ws = torch.empty(L.moe_vocab_loss_bwd_workspace_size(T, d, V, 1), dtype=torch.uint8, device=DEV)
+    L.moe_vocab_loss_bwd(h, w, target, lse, dloss, T, d, V, L.MOE_BF16, dh, dw, ws, ws.numel())
+    ref_loss, ref_dh, ref_dw = _gpu_reference(h, w, target, dloss, 65536)
+    if T == 24:
+        ref_dh = torch.cat([ref_dh[:1], ref_dh[:1]])   # one block: its first row
+    err = lambda a, b: float((a.double() - b).abs().max() / b.abs().max())
+    assert err(loss, ref_loss) < 1e-5
+    assert err(dh[:1], ref_dh[:1]) < 2e-2 and (T == 24 or err(dh[-1:], ref_dh[1:]) < 2e-2)
+    assert err(dw, ref_dw) < 2e-2 and err(dw[-1], ref_dw[-1]) < 2e-2
 
 
 def test_vocab_loss_with_no_target_at_all_and_confident_rows():
@@ -424,6 +504,70 @@ def test_clip_of_a_norm_summed_over_ranks():
     got = lists[0].tensors[0] + lists[1].tensors[0]
     for a, b, t in zip(got, whole, types):   # the two sums of squares may differ in their last bits
         assert torch.allclose(a.float(), b.float(), rtol=2 * HALF[t] + 1e-7, atol=0)
+
+
+# ------------------------------------------------------------------------------------------- guards
+
+class Guarded:
+    """Tensors and workspaces with a run of known bytes behind each, which no call may change."""
+
+    def __init__(self):
+        self.all = []
+
+    def __call__(self, *shape, dtype=torch.float32, fill=0):
+        n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+        raw = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        t = raw[:n].view(dtype).view(*shape)
+        t.fill_(fill)
+        self.all.append((raw, n))
+        return t
+
+    def copy(self, t):
+        g = self(*t.shape, dtype=t.dtype)
+        g.copy_(t)
+        return g
+
+    def check(self):
+        torch.cuda.synchronize()
+        for i, (raw, n) in enumerate(self.all):
+            assert bool((raw[n:] == 0x5A).all()), f"bytes behind buffer {i} changed"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,V,k,gate_rows", [(1, 8, 1, 1, 1), (65, 264, 333, 3, 7), (300, 1032, 12345, 4, 300),
+                                                (1029, 2056, 2047, 2, 100), (4097, 520, 9001, 1, 0)])
+def test_nothing_is_written_behind_outputs_and_workspaces(dtype, T, d, V, k, gate_rows):
+    log(f"guards {dtype} T={T} d={d} V={V}")
+    G, dt, td = Guarded(), DT[dtype], torch.bfloat16 if dtype == "bf16" else torch.float32
+    rnd = lambda *s: G.copy(torch.randn(*s, device=DEV).to(td))
+    x, y, dout, w, gate = rnd(T, d), rnd(T, d), rnd(T, d), rnd(d), rnd(-(-T // gate_rows), d) if gate_rows else None
+    xn, out, dy, dx, yc = (G(T, d, dtype=td) for _ in range(5))
+    r1, r2, dw1, dw2 = G(T), G(T), G(d), G(d)
+    dgate = G(*gate.shape) if gate_rows else None
+    n = L.moe_norm_bwd_workspace_size(T, d)
+    ws = G(n, dtype=torch.uint8)
+    L.moe_norm_in(x, w, T, d, EPS, dt, xn, r1)
+    L.moe_norm_out(y, x, w, gate, gate_rows, 1.0, EPS, T, d, dt, out, r2)
+    L.moe_norm_out_bwd(dout, y, w, gate, gate_rows, r2, T, d, dt, dy, dw1, dgate, ws, n)
+    L.moe_norm_in_bwd(dout, x, w, r1, dout, 1.0, T, d, dt, dx, dw2, ws, n)
+    yp, tg = rnd(T * k, d), G.copy(torch.rand(T, k, device=DEV))
+    pos = G.copy(torch.randperm(T * k, device=DEV).to(torch.int32))
+    L.moe_combine_norm_out(yp, tg, pos, y, x, w, gate, gate_rows, 1.0, EPS, T, d, k, dt, yc, out, r2)
+    words, target = rnd(V, d), G.copy(torch.randint(0, V, (T,), device=DEV).to(torch.int32))
+    loss, lse, dl = G(T), G(T), G(T, fill=1.0)
+    nf, nb = L.moe_vocab_loss_workspace_size(T, d, V, dt), L.moe_vocab_loss_bwd_workspace_size(T, d, V, dt)
+    wf, wb, dh, dw = G(nf, dtype=torch.uint8), G(nb, dtype=torch.uint8), G(T, d, dtype=td), G(V, d, dtype=td)
+    L.moe_vocab_loss(x, words, target, T, d, V, dt, loss, lse, wf, nf)
+    L.moe_vocab_loss_bwd(x, words, target, lse, dl, T, d, V, dt, dh, dw, wb, nb)
+    grads = [dh, dw, dw1, dw2, G(1, dtype=td, fill=3.0)]
+    lst = L.grad_list(grads, [G(*g.shape, dtype=g.dtype) for g in grads])
+    ng, norm, sq = L.moe_grad_workspace_size(lst), G(1), G(1, dtype=torch.float64)
+    wg = G(ng, dtype=torch.uint8)
+    L.moe_grad_clip(lst, 0.1, norm, wg, ng)
+    L.moe_grad_norm(lst, sq, norm, wg, ng)
+    L.moe_grad_scale(lst, sq, 0.1, norm)
+    G.check()
+    assert all(bool(torch.isfinite(t).all()) for t in (xn, out, dy, dx, dw1, dw2, loss, dh, dw))
 
 
 # --------------------------------------------------------------------------------- the run of them
