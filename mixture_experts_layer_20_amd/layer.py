@@ -166,9 +166,13 @@ class MoELayer:
         self.gate_rows = cfg.T if gate_rows is None else int(gate_rows)
         self.res_scale = float(res_scale)
         self.norm_eps = float(norm_eps)
-        self._grads: L.GradList | None = None   # clip_gradients
         if self.norm:
             self._allocate_norm()
+        if cfg.backward:   # clip_gradients
+            dev = params["x"].device
+            self.bufs.t.setdefault("grad_norm", torch.empty(1, dtype=torch.float32, device=dev))
+            self._ws_grad = torch.empty(L.moe_grad_workspace_size(L.grad_list(self.gradients())), dtype=torch.uint8,
+                                        device=dev)
         self.renorm = renormalize
         self.merge = merge_shared
         self.recompute = recompute
@@ -221,13 +225,23 @@ class MoELayer:
         for w in (p["norm_in"], p["norm_out"], gate):
             if w is not None and w.dtype != p["x"].dtype:
                 raise ValueError("the norms' weights and gate must have x's dtype")
-        t["xn"] = torch.empty_like(p["x"])
-        t["rstd_in"], t["rstd_out"] = f32(c.T), f32(c.T)
+        # Layers that share their buffers share these too, as far as the shapes agree: what one of them
+        # was captured with stays.  The gate's gradient and its shape are the layer's own.
+        def keep(name, *shape, dtype=torch.float32):
+            if name not in t or tuple(t[name].shape) != shape or t[name].dtype != dtype:
+                t[name] = torch.empty(*shape, dtype=dtype, device=dev)
+        rows = tuple(p["x"].shape)
+        keep("xn", *rows, dtype=p["x"].dtype)
+        keep("rstd_in", c.T)
+        keep("rstd_out", c.T)
         if c.backward:
-            t["y_block"], t["dblock"], t["dxn"] = (torch.empty_like(p["x"]) for _ in range(3))
-            t["dnorm_in"], t["dnorm_out"] = f32(c.d), f32(c.d)
-            t["dnorm_gate"] = None if gate is None else f32(*gate.shape)
-            t["ws_norm"] = torch.empty(max(256, L.moe_norm_bwd_workspace_size(c.T, c.d)), dtype=torch.uint8, device=dev)
+            for name in ("y_block", "dblock", "dxn"):
+                keep(name, *rows, dtype=p["x"].dtype)
+            keep("dnorm_in", c.d)
+            keep("dnorm_out", c.d)
+            keep("ws_norm", max(256, L.moe_norm_bwd_workspace_size(c.T, c.d)), dtype=torch.uint8)
+            self._dnorm_gate = None if gate is None else f32(*gate.shape)
+            t["dnorm_gate"] = self._dnorm_gate
 
     def _sets(self, dout=None, stash=True):
         """The routed experts and (if any) the shared expert as expert sets; stash=False leaves out
@@ -308,6 +322,7 @@ class MoELayer:
         learned = c.routing == "learned"
         if not self.norm:
             return self._block_backward(dout, b["dx"])
+        b["dnorm_gate"] = self._dnorm_gate
         self._stage("norm_out_bwd", L.moe_norm_out_bwd, dout, b["y_block"], p["norm_out"], p.get("norm_gate"),
                     self.gate_rows, b["rstd_out"], T, d, dt, b["dblock"], b["dnorm_out"], b["dnorm_gate"], b["ws_norm"],
                     b["ws_norm"].numel())
@@ -452,22 +467,19 @@ class MoELayer:
         if c.routing == "learned":
             names.append("dwr")
         if self.norm:
-            names += ["dnorm_in", "dnorm_out", "dnorm_gate"]
-        return [t[n] for n in names if t.get(n) is not None]
+            names += ["dnorm_in", "dnorm_out"]
+        grads = [t[n] for n in names]
+        if self.norm and self._dnorm_gate is not None:
+            grads.append(self._dnorm_gate)
+        return grads
 
     def clip_gradients(self, max_norm: float) -> torch.Tensor:
         """Scale the gradients in place to a global norm of at most max_norm; returns the norm before
         that ([1] float, on the device)."""
         if not self.cfg.backward:
             raise ValueError("the layer has no backward")
-        b, grads = self.bufs.t, self.gradients()
-        if self._grads is None or any(g is not h for g, h in zip(grads, self._grads.tensors[0])):
-            self._grads = L.grad_list(grads)
-            dev = self.p["x"].device
-            b["grad_norm"] = torch.empty(1, dtype=torch.float32, device=dev)
-            b["ws_grad"] = torch.empty(L.moe_grad_workspace_size(self._grads), dtype=torch.uint8, device=dev)
-        self._stage("grad_clip", L.moe_grad_clip, self._grads, max_norm, b["grad_norm"], b["ws_grad"],
-                    b["ws_grad"].numel())
+        b, grads = self.bufs.t, L.grad_list(self.gradients())
+        self._stage("grad_clip", L.moe_grad_clip, grads, max_norm, b["grad_norm"], self._ws_grad, self._ws_grad.numel())
         return b["grad_norm"]
 
     def step(self):

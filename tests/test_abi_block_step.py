@@ -162,3 +162,20 @@ def test_layer_refuses_norm_weights_of_another_shape_or_type():
             make(**bad)
     with pytest.raises(ValueError):
         make().clip_gradients(1.0)   # no backward
+
+
+def test_layers_that_share_buffers_keep_their_own_gate_gradient():
+    """A second layer over the same buffers, with fewer gate rows or none, must not take away or shrink
+    what the first one's backward writes; tensors of equal shapes stay the same ones."""
+    cfg = MoEConfig("t", 6, 256, 4, 2, 128, 0, "f32", "random", 0.0, True)
+    z = torch.zeros
+    p = dict(x=z(6, 256), logits=z(6, 4), norm_in=z(256), norm_out=z(256), dout=z(6, 256))
+    first = LY.MoELayer(cfg, dict(p, norm_gate=z(6, 256)), block_norm=True, gate_rows=1)
+    held = {n: first.bufs[n] for n in ("xn", "rstd_in", "rstd_out", "y_block", "dblock", "dxn", "dnorm_in", "dnorm_out",
+                                       "ws_norm", "grad_norm")}
+    second = LY.MoELayer(cfg, dict(p, norm_gate=z(1, 256)), bufs=first.bufs, block_norm=True)
+    third = LY.MoELayer(cfg, p, bufs=first.bufs, block_norm=True)
+    LY.MoELayer(cfg, p, bufs=first.bufs)
+    assert first.gradients()[-1].shape == (6, 256) and second.gradients()[-1].shape == (1, 256)
+    assert len(third.gradients()) == len(first.gradients()) - 1
+    assert all(first.bufs[n] is t for n, t in held.items())

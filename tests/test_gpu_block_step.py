@@ -730,3 +730,32 @@ def test_train_step_in_a_graph_and_on_another_stream():
         s.run()
         torch.cuda.synchronize()
         assert same(), f"eager run {i}"
+
+
+def test_layers_that_share_buffers():
+    """Blocks run one after the other over the same buffers, their gates of different shapes, give the
+    gradients that each gives over buffers of its own."""
+    log("layers over shared buffers")
+    cfg, vals, extra, params, head, target = block_case(gate_rows=1)
+    rows = [1, 64, cfg.T, 0]   # the fewest gate rows, and none, after the most
+    cases = []
+    for r in rows:
+        p = dict(params)
+        gate = p.pop("norm_gate")
+        if r:
+            p["norm_gate"] = gate[:-(-cfg.T // r)].contiguous()
+        cases.append((p, r or None))
+    dout = torch.randn(cfg.T, cfg.d, device=DEV).to(torch.bfloat16)
+    own = [LY.MoELayer(cfg, p, block_norm=True, gate_rows=r) for p, r in cases]
+    bufs = LY.Buffers.allocate(cfg, params["x"].device)
+    shared = [LY.MoELayer(cfg, p, bufs=bufs, block_norm=True, gate_rows=r) for p, r in cases]
+    for a, b in zip(own, shared):
+        for lay in (a, b):
+            lay.forward()
+            lay.backward(dout)
+            lay.clip_gradients(0.01)
+        torch.cuda.synchronize()
+        assert torch.equal(a.bufs["dx"], b.bufs["dx"]) and torch.equal(a.bufs["grad_norm"], b.bufs["grad_norm"])
+        assert all(torch.equal(g, h) for g, h in zip(a.gradients(), b.gradients()))
+        gate = b.bufs["dnorm_gate"]
+        assert gate is None if "norm_gate" not in b.p else torch.equal(gate, a.bufs["dnorm_gate"])
