@@ -316,13 +316,11 @@ class MoELayer:
 
     def backward(self, dout=None):
         c, p, b, dt = self.cfg, self.p, self.bufs, self.dt
-        T, d, E, k, f, fs = c.T, c.d, c.E, c.k, c.f, c.fs
-        Tk = T * k
+        T, d = c.T, c.d
         dout = p["dout"] if dout is None else dout
-        learned = c.routing == "learned"
         if not self.norm:
             return self._block_backward(dout, b["dx"])
-        b["dnorm_gate"] = self._dnorm_gate
+        b.t["dnorm_gate"] = self._dnorm_gate
         self._stage("norm_out_bwd", L.moe_norm_out_bwd, dout, b["y_block"], p["norm_out"], p.get("norm_gate"),
                     self.gate_rows, b["rstd_out"], T, d, dt, b["dblock"], b["dnorm_out"], b["dnorm_gate"], b["ws_norm"],
                     b["ws_norm"].numel())
