@@ -178,11 +178,16 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, lead=None) -> int | None:
+    """The stream's handle, by default the current device's current one; ``lead``: a tensor of the call,
+    which must then be on that device (a kernel that got host memory or another device's would fault)."""
     if stream is None:
         if torch.cuda.is_initialized():
             # the handle alone: a Stream object costs 3 us a call, as much as a launch
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            dev = torch._C._cuda_getDevice()
+            if lead is not None and not isinstance(lead, int) and lead.get_device() != dev:
+                raise ValueError(f"a tensor on {lead.device}, but the current device is cuda:{dev}")
+            return torch._C._cuda_getCurrentRawStream(dev)
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -354,18 +359,18 @@ def moe_router_aux_bwd(logits, load_frac, x, w_router, T, d, E, weight, dt, dw_r
 
 
 def moe_norm_in(x, w, T, d, eps, dt, xn, rstd, stream=None):
-    _call("moe_norm_in", _ptr(x), _ptr(w), T, d, eps, dt, _ptr(xn), _ptr(rstd), _stream(stream))
+    _call("moe_norm_in", _ptr(x), _ptr(w), T, d, eps, dt, _ptr(xn), _ptr(rstd), _stream(stream, x))
 
 
 def moe_norm_out(y, x, w, gate, gate_rows, res_scale, eps, T, d, dt, out, rstd, stream=None):
     _call("moe_norm_out", _ptr(y), _ptr(x), _ptr(w), _ptr(gate), gate_rows, res_scale, eps, T, d, dt, _ptr(out),
-          _ptr(rstd), _stream(stream))
+          _ptr(rstd), _stream(stream, y))
 
 
 def moe_combine_norm_out(y_perm, topk_gate, dest_pos, shared_out, x, w, gate, gate_rows, res_scale, eps, T, d, k, dt,
                          y, out, rstd, stream=None):
     _call("moe_combine_norm_out", _ptr(y_perm), _ptr(topk_gate), _ptr(dest_pos), _ptr(shared_out), _ptr(x), _ptr(w),
-          _ptr(gate), gate_rows, res_scale, eps, T, d, k, dt, _ptr(y), _ptr(out), _ptr(rstd), _stream(stream))
+          _ptr(gate), gate_rows, res_scale, eps, T, d, k, dt, _ptr(y), _ptr(out), _ptr(rstd), _stream(stream, y_perm))
 
 
 def moe_norm_bwd_workspace_size(T, d) -> int:
@@ -374,12 +379,12 @@ def moe_norm_bwd_workspace_size(T, d) -> int:
 
 def moe_norm_out_bwd(dout, y, w, gate, gate_rows, rstd, T, d, dt, dy, dw, dgate, ws, ws_bytes, stream=None):
     _call("moe_norm_out_bwd", _ptr(dout), _ptr(y), _ptr(w), _ptr(gate), gate_rows, _ptr(rstd), T, d, dt, _ptr(dy),
-          _ptr(dw), _ptr(dgate), _ptr(ws), ws_bytes, _stream(stream))
+          _ptr(dw), _ptr(dgate), _ptr(ws), ws_bytes, _stream(stream, dout))
 
 
 def moe_norm_in_bwd(dxn, x, w, rstd, dres, res_scale, T, d, dt, dx, dw, ws, ws_bytes, stream=None):
     _call("moe_norm_in_bwd", _ptr(dxn), _ptr(x), _ptr(w), _ptr(rstd), _ptr(dres), res_scale, T, d, dt, _ptr(dx),
-          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream))
+          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream, dxn))
 
 
 def moe_vocab_loss_workspace_size(T, d, V, dt) -> int:
@@ -388,7 +393,7 @@ def moe_vocab_loss_workspace_size(T, d, V, dt) -> int:
 
 def moe_vocab_loss(h, w, target, T, d, V, dt, loss, lse, ws, ws_bytes, stream=None):
     _call("moe_vocab_loss", _ptr(h), _ptr(w), _ptr(target), T, d, V, dt, _ptr(loss), _ptr(lse), _ptr(ws), ws_bytes,
-          _stream(stream))
+          _stream(stream, h))
 
 
 def moe_vocab_loss_bwd_workspace_size(T, d, V, dt) -> int:
@@ -397,7 +402,7 @@ def moe_vocab_loss_bwd_workspace_size(T, d, V, dt) -> int:
 
 def moe_vocab_loss_bwd(h, w, target, lse, dloss, T, d, V, dt, dh, dw, ws, ws_bytes, stream=None):
     _call("moe_vocab_loss_bwd", _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), T, d, V, dt, _ptr(dh),
-          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream))
+          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream, h))
 
 
 class GradList:
@@ -415,6 +420,8 @@ class GradList:
                 raise ValueError("an out must have its gradient's dtype and size")
             e.grad, e.out, e.n, e.dt = _ptr(g), _ptr(o), g.numel(), dtype_code(g)
         self.ptr = ctypes.cast(self.array, _P)
+        if len({t.device for s in self.tensors for t in s if t is not None}) > 1:
+            raise ValueError("the tensors are on different devices")
 
 
 def grad_list(grads, outs=None) -> GradList:
@@ -423,20 +430,26 @@ def grad_list(grads, outs=None) -> GradList:
     return GradList(grads, grads if outs is None else outs)
 
 
+def _lead(grads):
+    return grads.tensors[0][0] if grads.count and isinstance(grads, GradList) else None
+
+
 def moe_grad_workspace_size(grads: GradList) -> int:
     return lib().moe_grad_workspace_size(grads.ptr, grads.count)
 
 
 def moe_grad_norm(grads: GradList, sumsq, norm, ws, ws_bytes, stream=None):
-    _call("moe_grad_norm", grads.ptr, grads.count, _ptr(sumsq), _ptr(norm), _ptr(ws), ws_bytes, _stream(stream))
+    _call("moe_grad_norm", grads.ptr, grads.count, _ptr(sumsq), _ptr(norm), _ptr(ws), ws_bytes,
+          _stream(stream, _lead(grads)))
 
 
 def moe_grad_scale(grads: GradList, sumsq, max_norm, norm, stream=None):
-    _call("moe_grad_scale", grads.ptr, grads.count, _ptr(sumsq), max_norm, _ptr(norm), _stream(stream))
+    _call("moe_grad_scale", grads.ptr, grads.count, _ptr(sumsq), max_norm, _ptr(norm), _stream(stream, _lead(grads)))
 
 
 def moe_grad_clip(grads: GradList, max_norm, norm, ws, ws_bytes, stream=None):
-    _call("moe_grad_clip", grads.ptr, grads.count, max_norm, _ptr(norm), _ptr(ws), ws_bytes, _stream(stream))
+    _call("moe_grad_clip", grads.ptr, grads.count, max_norm, _ptr(norm), _ptr(ws), ws_bytes,
+          _stream(stream, _lead(grads)))
 
 
 def moe_mx_quantize_rows(x, R, K, ldx, codes, scales, stream=None):

@@ -179,3 +179,25 @@ def test_layers_that_share_buffers_keep_their_own_gate_gradient():
     assert first.gradients()[-1].shape == (6, 256) and second.gradients()[-1].shape == (1, 256)
     assert len(third.gradients()) == len(first.gradients()) - 1
     assert all(first.bufs[n] is t for n, t in held.items())
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    """With the device in use (here only said to be), host tensors and another device's are turned away."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    t = torch.zeros(64)
+    target, grads = torch.zeros(8, dtype=torch.int32), L.grad_list([t])
+    calls = [lambda: L.moe_norm_in(t, t, 8, 8, 0.0, F32, t, None),
+             lambda: L.moe_norm_out(t, t, t, None, 1, 1.0, 0.0, 8, 8, F32, t, None),
+             lambda: L.moe_combine_norm_out(t, t, target, None, t, t, None, 1, 1.0, 0.0, 8, 8, 1, F32, None, t, None),
+             lambda: L.moe_norm_out_bwd(t, t, t, None, 1, t, 8, 8, F32, t, t, None, t, 256),
+             lambda: L.moe_norm_in_bwd(t, t, t, t, None, 1.0, 8, 8, F32, t, t, t, 256),
+             lambda: L.moe_vocab_loss(t, t, target, 8, 8, 8, F32, t, t, t, 256),
+             lambda: L.moe_vocab_loss_bwd(t, t, target, t, t, 8, 8, 8, F32, t, t, t, 256),
+             lambda: L.moe_grad_norm(grads, t, None, t, 256), lambda: L.moe_grad_scale(grads, t, 1.0, None),
+             lambda: L.moe_grad_clip(grads, 1.0, None, t, 256)]
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    with pytest.raises(ValueError, match="different devices"):
+        L.grad_list([t, torch.zeros(8, device="meta")])
