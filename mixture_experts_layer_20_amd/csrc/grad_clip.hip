@@ -12,7 +12,7 @@
 // copy to the device and can be captured.
 //
 // Bound by memory: the sum reads the list once, the scaling reads it again and writes it.  409 M bf16
-// values (818 MB): the sum 142 us (5.75 TB/s), the scaling 305 us (5.4 TB/s), against 5.1 TB/s of a
+// values (818 MB): the sum 140 us (5.8 TB/s), the scaling 312 us (5.2 TB/s), against 5.1 TB/s of a
 // device copy.  The scaling starts where the sum ended, whose last quarter of a GB is still in the
 // last-level cache, and its own loads and stores are nontemporal so that they do not displace it:
 // 365 us in the order of the sum with ordinary loads.

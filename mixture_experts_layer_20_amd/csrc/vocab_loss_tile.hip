@@ -3,11 +3,15 @@
 //
 // A workgroup of 4 waves takes one tile, 32x32 per wave, two or four workgroups per CU.  K goes through
 // two LDS stages of 256 or 128 bytes per row and operand (64 bf16 or 32 fp32 values in 128 bytes),
-// filled by direct-to-LDS loads two steps ahead.  An operand contiguous along K is kept [64 rows][256
-// or 128 bytes], 16-byte chunks XOR-swizzled by the row; one contiguous along its rows is kept [k][64 rows] and read transposed
-// (bf16) or value by value (fp32).  fp32 products run on v_mfma_f32_32x32x2_f32, which multiplies and
+// filled by direct-to-LDS loads two steps ahead (four stages are no faster).  An operand contiguous
+// along K is kept [64 rows][256 or 128 bytes], 16-byte chunks XOR-swizzled by the row; one contiguous
+// along its rows is kept [k][64 rows] and read transposed (bf16) or value by value (fp32).  fp32 products run on v_mfma_f32_32x32x2_f32, which multiplies and
 // adds in fp32; the two k of an instruction are 4 apart, so one 16-byte read feeds four of them.
 // Rows past the end are read clamped and not stored, K and columns past the end read zeros.
+//
+// Large fp32 products run at 101-104 TFLOP/s (a library product: 139), the matrix cores busy for
+// 75-81% of the time at 4096 x 512 x 32768; few rows at the rate of the words' stream: 7 tokens x 50021 words x
+// d 2048 in 43 us (205 MB, 4.8 TB/s).  Small products are bound by the latency of their few steps.
 #include "vocab_loss.h"
 
 #include <algorithm>
