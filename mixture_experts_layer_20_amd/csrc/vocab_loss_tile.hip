@@ -23,6 +23,7 @@ namespace {
 
 constexpr int TS = 64;                  // tile rows and columns
 constexpr int NT = 256;
+constexpr int JOIN_FEW = 32768;         // vectors of a join whose splits are dealt to 16 slices
 // NF: fragment groups of a stage, 16 bf16 or 8 fp32 k each, so 32 NF bytes of a row.
 constexpr int row_bytes(int nf) { return 32 * nf; }
 constexpr int loads(int nf) { return nf / 2; }           // direct loads per wave, stage and operand
@@ -352,7 +353,7 @@ __global__ __launch_bounds__(NT, 4) void vocab_tile_pair_kernel(VocabArgs p, Cut
   else run_tile<T, VL_DW, 4, false>(p, dw, blockIdx.x - dh_blocks, lds);
 }
 
-// out = the scaled sum of ks partial products of n elements in split order, rounded; two such sums in
+// out = the scaled sum of ks partial products of n elements in a fixed order, rounded; two such sums in
 // one launch (n = 0: none).
 template <typename T>
 struct Join {
@@ -361,28 +362,57 @@ struct Join {
   size_t n;   // a multiple of 8
   int ks;
 };
-template <typename T>
+// SL slices of the splits are summed side by side, then joined in order: 16 where the outputs are few
+// and the splits many, whose loads then overlap (forward and backward, us): 1 x 100000 words x d 128,
+// 256 splits, 68.6 -> 57.4; 6 x 18673 x 376 41.0 -> 36.7; 100 x 60000 x 256 63.7 -> 61.1.
+template <typename T, int SL>
 __global__ __launch_bounds__(NT) void vocab_tile_join_kernel(Join<T> a, Join<T> b, const float* scale) {
-  const size_t step = (size_t)gridDim.x * NT * 4;
-  for (size_t i = ((size_t)blockIdx.x * NT + threadIdx.x) * 4; i < a.n + b.n; i += step) {
+  constexpr int VPB = NT / SL;   // vectors of 4 of a workgroup at a time
+  __shared__ float4 red[SL > 1 ? SL - 1 : 1][VPB];
+  const int slice = threadIdx.x / VPB, x = threadIdx.x % VPB;
+  const size_t vectors = (a.n + b.n) / 4;
+  for (size_t v0 = (size_t)blockIdx.x * VPB; v0 < vectors; v0 += (size_t)gridDim.x * VPB) {
+    const size_t i = (v0 + x) * 4;
+    const bool in = v0 + x < vectors;
     const Join<T>& j = i < a.n ? a : b;
     const size_t at = i < a.n ? i : i - a.n;
     float v[4] = {0, 0, 0, 0};
+    if (in) {
+      const int per = SL == 1 ? j.ks : (j.ks + SL - 1) / SL, s1 = min(j.ks, (slice + 1) * per);
 #pragma unroll 4
-    for (int s = 0; s < j.ks; ++s) {
-      const float4 o = *reinterpret_cast<const float4*>(j.parts + s * j.n + at);
-      v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+      for (int s = slice * per; s < s1; ++s) {
+        const float4 o = *reinterpret_cast<const float4*>(j.parts + s * j.n + at);
+        v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+      }
     }
+    if constexpr (SL > 1) {
+      if (slice > 0) red[slice - 1][x] = make_float4(v[0], v[1], v[2], v[3]);
+      __syncthreads();
+      if (slice == 0) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] *= *scale;
-    store4(j.out + at, v);
+        for (int s = 0; s < SL - 1; ++s) {
+          const float4 o = red[s][x];
+          v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+        }
+      }
+      __syncthreads();
+    }
+    if (in && slice == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= *scale;
+      store4(j.out + at, v);
+    }
   }
 }
 template <typename T>
 hipError_t launch_join(const Join<T>& a, const Join<T>& b, const float* scale, hipStream_t s) {
   if (a.n + b.n == 0) return hipSuccess;
-  vocab_tile_join_kernel<T><<<dim3((unsigned)std::min<size_t>(((a.n + b.n) / 4 + NT - 1) / NT, 1 << 20)), dim3(NT), 0, s>>>(a, b, scale);
-  return hipGetLastError();
+  auto run = [&](auto kernel, int vpb) {
+    kernel<<<dim3((unsigned)std::min<size_t>(((a.n + b.n) / 4 + vpb - 1) / vpb, 1 << 20)), dim3(NT), 0, s>>>(a, b, scale);
+    return hipGetLastError();
+  };
+  if ((a.n + b.n) / 4 <= JOIN_FEW && std::max(a.n ? a.ks : 0, b.n ? b.ks : 0) >= 16) return run(vocab_tile_join_kernel<T, 16>, NT / 16);
+  return run(vocab_tile_join_kernel<T, 1>, NT);
 }
 
 // K per split of dh or dw, a multiple of a stage; dh's is the same for every piece of a call.
