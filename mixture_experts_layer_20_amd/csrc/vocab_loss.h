@@ -24,6 +24,7 @@ struct VocabArgs {
   void* dh;
   void* dw;
   bool first, last;   // the piece is the first / the last one
+  bool large;         // launch_tile, launch_tile_pair, launch_tile_join: 128x128 tiles
 };
 
 enum VocabMode { VL_STATS = 0, VL_GRAD = 1, VL_DH = 2, VL_DW = 3 };
@@ -50,9 +51,11 @@ size_t pipe_dw_bytes(int T, int d, int words);
 hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s);
 hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s);
 
-// 64x64 tiles, both types.  dh_acc and dw_acc hold tile_splits() partial products of all outputs.
-int tile_splits(int M, int N, int K);
-size_t tile_acc_bytes(int M, int N, int K);
+// 64x64 or (p.large) 128x128 tiles, both types.  dh_acc and dw_acc hold tile_splits() partial products
+// of all outputs.
+long long tile_count(int M, int N, bool large);
+int tile_splits(int M, int N, int K, bool large);
+size_t tile_acc_bytes(int M, int N, int K, bool large);
 hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s);
 // VL_DH and VL_DW in one launch, and the joins that they need (dh's after the last piece).
 hipError_t launch_tile_pair(const VocabArgs& p, bool bf16, hipStream_t s);

@@ -17,6 +17,7 @@
 #include "vocab_loss.h"
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 namespace moe {
@@ -144,29 +145,93 @@ int piece_words(long long T, long long V) {
   return (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
 }
 
-// Which tiles a bf16 product takes, by an estimate of each (us): rounds of the workgroups that run at
-// once, times a tile's K steps and its ends.  Forward pass with the 64x64 tiles against the 256x256
-// ones (us): 64 tokens x 12485 words x d 3472: 24.7, 68.7; 500 x 4000 x 2048: 21.7, 46.3;
-// 1 x 50021 x 2048: 38.7, 43.5; 4000 x 1000 x 2048: 47.5, 49.1; 257 x 20000 x 512: 24.1, 20.3;
-// 500 x 32000 x 2048: 116, 63.9; 2048 x 8000 x 1024: 76.3, 38.0.  fp32 always takes the small tiles.
-bool use_pipe(int M, int N, int K, int pipe_ks, int tile_ks, bool bf16) {
-  if (!bf16) return false;
-  const long long big = (long long)ceil_div(M, 256) * ceil_div(N, 256) * pipe_ks;
-  const long long small = (long long)ceil_div(M, 64) * ceil_div(N, 64) * tile_ks;
-  const double pipe_us = ceil_div(big, NUM_CUS) * (4.0 + 1.4 * ceil_div(ceil_div(K, pipe_ks), 64));
-  const double tile_us = ceil_div(small, 2 * NUM_CUS) * (2.0 + 0.85 * ceil_div(ceil_div(K, tile_ks), 128));
-  return pipe_us < tile_us;
+// Which tiles a product takes: 64x64, 128x128 (vocab_loss_tile.hip) or, bf16 only, 256x256
+// (vocab_loss_pipe.hip), by an estimate of each in us, straight lines through the times of some 20 shapes
+// that they meet within 6-16%: of the tile kernels the work per CU, n tiles of s steps of K, of the
+// pipelined kernel the rounds of its workgroups, one per CU.  Measured forward kernels, 64, 128 and 256 (us):
+// 100 tokens x 8000 words x d 4096: 20.8, 36.7, 54.3; 1000 x 4000 x 1000: 22.3, 17.0, 28.6;
+// 2000 x 4000 x 1000: 41.3, 27.8, 29.0; 3000 x 20000 x 128: 56, 54, 28; 184 x 30594 x 3784: 137, 100, 102.
+enum Tiles { SMALL, LARGE, PIPE };
+
+// n: tiles per CU; K of a tile.
+struct Load {
+  double n;
+  int k;
+};
+Load tile_load(int M, int N, int K, int splits, bool large) {
+  return Load{(double)tile_count(M, N, large) * splits / NUM_CUS, ceil_div(K, splits)};
 }
-bool logits_pipe(int T, int d, int words, bool bf16) { return use_pipe(T, words, d, 1, 1, bf16); }
-bool dw_pipe(int T, int d, int words, bool bf16) {
-  return use_pipe(words, d, T, pipe_dw_splits(T, d, words), tile_splits(words, d, T), bf16);
-}
-bool dh_pipe(int T, int d, int words, bool bf16) {
-  return use_pipe(T, d, words, pipe_dh_splits(T, d, words), tile_splits(T, d, words), bf16);
+// fp32 is bound by the matrix cores: 0.0198 us of a CU for each k of a 64x64 tile, 0.069 of a 128x128
+// one, of which two run together and end together.
+double f32_us(Load a, Load b, bool large) {
+  const double n = a.n + b.n, k = (a.n * a.k + b.n * b.k) / n;
+  if (!large) return 4.0 + 0.0198 * std::min(std::ceil(n), n + 0.5) * k;
+  return 6.0 + 0.069 * (n <= 1 ? 1 : 2 * std::ceil(n / 2)) * k;
 }
 
-hipError_t launch_product(bool pipe, int mode, const VocabArgs& p, bool bf16, hipStream_t s) {
-  return pipe ? launch_pipe(mode, p, s) : launch_tile(mode, p, bf16, s);
+Tiles logits_tiles(int T, int d, int words, bool bf16) {
+  const Load s = tile_load(T, words, d, 1, false), l = tile_load(T, words, d, 1, true);
+  const bool one_row = T <= 64;   // of 64x64 tiles: large ones would be half empty
+  if (!bf16) return !one_row && f32_us(l, Load{0, 0}, true) < f32_us(s, Load{0, 0}, false) ? LARGE : SMALL;
+  double best = 3.3 + 0.6 * std::max(s.n, 0.9) * (ceil_div(d, 128) + 0.35);
+  Tiles tiles = SMALL;
+  const double large = 5.4 + 0.65 * std::max(l.n, 0.75) * (ceil_div(d, 64) + 3.1);
+  if (!one_row && large < best) best = large, tiles = LARGE;
+  const int rounds = ceil_div((long long)ceil_div(T, 256) * ceil_div(words, 256), NUM_CUS);
+  return 3.2 + rounds * (3.7 + 1.3 * ceil_div(d, 64)) < best ? PIPE : tiles;
+}
+
+// dh and dw: both in tiles of one size run as one launch.
+struct GradTiles {
+  Tiles dh, dw;
+};
+GradTiles grad_tiles(int T, int d, int words, bool bf16) {
+  const auto join_us = [](double partials) { return partials > 0 ? 3.0 + partials * 4 / 6.4e6 : 0.0; };
+  GradTiles plan{SMALL, SMALL};
+  double best = 0;
+  for (Tiles dh : {SMALL, LARGE, PIPE})
+    for (Tiles dw : {SMALL, LARGE, PIPE}) {
+      if (dh != PIPE && dw != PIPE ? dh != dw : !bf16) continue;
+      double us = 0, sums = 0;   // sums: elements of the partial products that the tiles' join reads
+      Load tile[2] = {};
+      bool large = false;
+      const auto add = [&](Load& to, int M, int N, int K, Tiles t) {
+        large = t == LARGE;
+        const int splits = tile_splits(M, N, K, large);
+        to = tile_load(M, N, K, splits, large);
+        if (splits > 1) sums += (double)splits * M * N;
+      };
+      if (dh == PIPE) {
+        const int splits = pipe_dh_splits(T, d, words);
+        const int rounds = ceil_div((long long)ceil_div(T, 256) * ceil_div(d, 256) * splits, NUM_CUS);
+        us += 1.1 + rounds * (2.9 + 1.87 * ceil_div(ceil_div(words, splits), 64)) + join_us((double)splits * T * d);
+      } else {
+        add(tile[0], T, d, words, dh);
+      }
+      if (dw == PIPE) {
+        const int splits = pipe_dw_splits(T, d, words);
+        const int rounds = ceil_div((long long)ceil_div(words, 256) * ceil_div(d, 256) * splits, NUM_CUS);
+        us += rounds * (9.7 + 1.47 * ceil_div(ceil_div(T, splits), 64)) + (splits > 1 ? join_us((double)splits * words * d) : 0.0);
+      } else {
+        add(tile[1], words, d, T, dw);
+      }
+      if (dh != PIPE || dw != PIPE) {
+        if (!bf16) {
+          us += f32_us(tile[0], tile[1], large);
+        } else {
+          us += large ? 6.2 : 4.5;
+          for (const Load& t : tile) us += large ? 0.55 * t.n * (ceil_div(t.k, 64) + 6) : 0.565 * t.n * (ceil_div(t.k, 128) + 0.6);
+        }
+        us += join_us(sums);
+      }
+      if (best == 0 || us < best) best = us, plan = GradTiles{dh, dw};
+    }
+  return plan;
+}
+
+hipError_t launch_product(Tiles tiles, int mode, VocabArgs p, bool bf16, hipStream_t s) {
+  p.large = tiles == LARGE;
+  return tiles == PIPE ? launch_pipe(mode, p, s) : launch_tile(mode, p, bf16, s);
 }
 
 template <typename T>
@@ -175,10 +240,10 @@ hipError_t loss_fwd(VocabArgs p, float* loss, float* lse, void* ws, hipStream_t 
   p.part = reinterpret_cast<float2*>(ws);
   p.v0 = 0;
   p.vn = p.V;
-  const bool pipe = logits_pipe(p.T, p.d, p.V, bf16);
-  const hipError_t e = launch_product(pipe, VL_STATS, p, bf16, s);
+  const Tiles tiles = logits_tiles(p.T, p.d, p.V, bf16);
+  const hipError_t e = launch_product(tiles, VL_STATS, p, bf16, s);
   if (e != hipSuccess) return e;
-  return launch_lse<T>(p, ceil_div(p.V, pipe ? PIPE_PART : TILE_PART), loss, lse, s);
+  return launch_lse<T>(p, ceil_div(p.V, tiles == PIPE ? PIPE_PART : TILE_PART), loss, lse, s);
 }
 
 // The workspace of the backward: the scale, dh's accumulators, dw's partial products (where its rows
@@ -189,12 +254,14 @@ struct BwdSpace {
 };
 BwdSpace bwd_space(int T, int d, int V, bool bf16) {
   const int words = piece_words(T, V), wide = std::min(words, V), last = V - (V - 1) / words * words;
+  const GradTiles tiles = grad_tiles(T, d, words, bf16);
   BwdSpace s;
-  s.dh = align256(dh_pipe(T, d, words, bf16) ? pipe_dh_bytes(T, d, words) : tile_acc_bytes(T, d, words));
+  s.dh = align256(tiles.dh == PIPE ? pipe_dh_bytes(T, d, words) : tile_acc_bytes(T, d, words, tiles.dh == LARGE));
   s.dw = 0;
   for (int vn : {wide, last}) {
-    const size_t tile = tile_splits(vn, d, T) > 1 ? tile_acc_bytes(vn, d, T) : 0;
-    s.dw = std::max(s.dw, align256(dw_pipe(T, d, vn, bf16) ? pipe_dw_bytes(T, d, vn) : tile));
+    const bool large = tiles.dw == LARGE;
+    const size_t tile = tile_splits(vn, d, T, large) > 1 ? tile_acc_bytes(vn, d, T, large) : 0;
+    s.dw = std::max(s.dw, align256(tiles.dw == PIPE ? pipe_dw_bytes(T, d, vn) : tile));
   }
   s.p = (size_t)T * words * (bf16 ? 2 : 4);
   return s;
@@ -209,7 +276,7 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
   }
   constexpr bool bf16 = sizeof(T) == 2;
   const int words = piece_words(p.T, p.V);
-  const bool dhp = dh_pipe(p.T, p.d, words, bf16);
+  const GradTiles tiles = grad_tiles(p.T, p.d, words, bf16);
   const BwdSpace space = bwd_space(p.T, p.d, p.V, bf16);
   p.ldp = words;
   char* at = reinterpret_cast<char*>(ws);
@@ -219,7 +286,7 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
   p.dw_acc = reinterpret_cast<float*>(at += space.dh);
   p.p = at += space.dw;
   hipError_t e = hipSuccess;
-  if (p.T <= SCALE_ROWS && !logits_pipe(p.T, p.d, std::min(words, p.V), bf16)) {
+  if (p.T <= SCALE_ROWS && logits_tiles(p.T, p.d, std::min(words, p.V), bf16) != PIPE) {
     p.scale_out = scale;   // the first piece's tiles find it
   } else {
     vocab_scale_kernel<<<dim3(1), dim3(1024), 0, s>>>(p, scale);
@@ -230,17 +297,18 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
     p.vn = std::min(words, p.V - v0);
     p.first = v0 == 0;
     p.last = v0 + words >= p.V;
-    e = launch_product(logits_pipe(p.T, p.d, p.vn, bf16), VL_GRAD, p, bf16, s);
+    e = launch_product(logits_tiles(p.T, p.d, p.vn, bf16), VL_GRAD, p, bf16, s);
+    if (e != hipSuccess) return e;
     p.scale_out = nullptr;
-    const bool dwp = dw_pipe(p.T, p.d, p.vn, bf16);
-    if (!dhp && !dwp) {
-      if (e == hipSuccess) e = launch_tile_pair(p, bf16, s);
-      if (e != hipSuccess) return e;
-      continue;
+    if (tiles.dh != PIPE && tiles.dw != PIPE) {
+      p.large = tiles.dh == LARGE;
+      e = launch_tile_pair(p, bf16, s);
+    } else {
+      e = launch_product(tiles.dh, VL_DH, p, bf16, s);
+      if (e == hipSuccess) e = launch_product(tiles.dw, VL_DW, p, bf16, s);
+      p.large = tiles.dh == LARGE;
+      if (e == hipSuccess && p.last) e = tiles.dh == PIPE ? launch_pipe_join(p, s) : launch_tile_join(p, bf16, s);
     }
-    if (e == hipSuccess) e = launch_product(dhp, VL_DH, p, bf16, s);
-    if (e == hipSuccess) e = launch_product(dwp, VL_DW, p, bf16, s);
-    if (e == hipSuccess && p.last) e = dhp ? launch_pipe_join(p, s) : launch_tile_join(p, bf16, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -249,7 +317,7 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
 }  // namespace
 
 size_t vocab_loss_ws_bytes(long long T, long long d, long long V, bool bf16) {
-  return (size_t)T * ceil_div(V, logits_pipe((int)T, (int)d, (int)V, bf16) ? PIPE_PART : TILE_PART) * sizeof(float2);
+  return (size_t)T * ceil_div(V, logits_tiles((int)T, (int)d, (int)V, bf16) == PIPE ? PIPE_PART : TILE_PART) * sizeof(float2);
 }
 
 hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target, int T, int d, int V, bool bf16,

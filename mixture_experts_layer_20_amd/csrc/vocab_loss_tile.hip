@@ -1,17 +1,20 @@
-// The products of the vocabulary loss (vocab_loss.hip has the formulas) in 64x64 tiles, both types:
-// fp32, and bf16 where the 256x256 tiles of vocab_loss_pipe.hip are too few to fill the CUs.
+// The products of the vocabulary loss (vocab_loss.hip has the formulas) in tiles of 64x64 or 128x128,
+// both types: fp32, and bf16 where the 256x256 tiles of vocab_loss_pipe.hip fill the CUs badly.
 //
-// A workgroup of 4 waves takes one tile, 32x32 per wave, two or four workgroups per CU.  K goes through
-// two LDS stages of 256 or 128 bytes per row and operand (64 bf16 or 32 fp32 values in 128 bytes),
-// filled by direct-to-LDS loads two steps ahead (four stages are no faster).  An operand contiguous
-// along K is kept [64 rows][256 or 128 bytes], 16-byte chunks XOR-swizzled by the row; one contiguous
-// along its rows is kept [k][64 rows] and read transposed (bf16) or value by value (fp32).  fp32 products run on v_mfma_f32_32x32x2_f32, which multiplies and
-// adds in fp32; the two k of an instruction are 4 apart, so one 16-byte read feeds four of them.
+// A workgroup of 4 waves takes one tile, RB x RB blocks of 32x32 per wave; two or four workgroups share
+// a CU.  K goes through two LDS stages of 256 or 128 bytes per row and operand (64 bf16 or 32 fp32
+// values in 128 bytes), filled by direct-to-LDS loads two steps ahead (four stages are no faster).  An
+// operand contiguous along K is kept [64 rows][256 or 128 bytes], 16-byte chunks XOR-swizzled by the
+// row; one contiguous along its rows is kept [k][64 rows] and read transposed (bf16) or value by value
+// (fp32).  fp32 products run on v_mfma_f32_32x32x2_f32, which multiplies and adds in fp32; the two k of
+// an instruction are 4 apart, so one 16-byte read feeds four of them.
 // Rows past the end are read clamped and not stored, K and columns past the end read zeros.
 //
-// Large fp32 products run at 101-104 TFLOP/s (a library product: 139), the matrix cores busy for
-// 75-81% of the time at 4096 x 512 x 32768; few rows at the rate of the words' stream: 7 tokens x 50021 words x
-// d 2048 in 43 us (205 MB, 4.8 TB/s).  Small products are bound by the latency of their few steps.
+// Large fp32 products run at 122-125 TFLOP/s in 128x128 tiles and 101-111 in 64x64 ones (a library
+// product: 139), bound by the matrix cores.  A bf16 tile of 128x128 reads half as much LDS for each
+// matrix instruction: 1500 tokens x 5000 words x d 3000 forward 64.5 us (700 TFLOP/s) against 126.  Few
+// rows run at the rate of the words' stream: 7 tokens x 50021 words x d 2048 in 43 us (205 MB, 4.8
+// TB/s).  Small products are bound by the latency of their few steps.
 #include "vocab_loss.h"
 
 #include <algorithm>
@@ -21,7 +24,7 @@ namespace moe {
 namespace vocab {
 namespace {
 
-constexpr int TS = 64;                  // tile rows and columns
+constexpr int TS = 64;                  // tile rows and columns of RB = 1
 constexpr int NT = 256;
 constexpr int JOIN_FEW = 32768;         // vectors of a join whose splits are dealt to 16 slices
 // NF: fragment groups of a stage, 16 bf16 or 8 fp32 k each, so 32 NF bytes of a row.
@@ -197,10 +200,11 @@ __device__ __forceinline__ float scale_of_rows(const VocabArgs& p) {
 
 // One tile.  Workgroup `block` of the product runs on XCD block % 8: each XCD walks one run of the tile
 // order, rows first, so the tiles that read one panel of the large operand run together.
-template <typename T, int MODE, int NF, bool ONCE>
+template <typename T, int MODE, int NF, bool ONCE, int RB>
 __device__ __forceinline__ void run_tile(const VocabArgs& p, const Cut& cut, int block, char* lds) {
   constexpr bool AK = Tr<MODE>::a_kc, BKC = Tr<MODE>::b_kc;
-  constexpr int BK = row_bytes(NF) / sizeof(T), LP = loads(NF), OPB = op_bytes(NF), STAGE = 2 * OPB;
+  constexpr int BK = row_bytes(NF) / sizeof(T), LP = loads(NF), OPB = op_bytes(NF), STAGE = 2 * RB * OPB;
+  constexpr int TR = TS * RB;   // the tile's rows and columns
   const int ks = cut.ks, kchunk = cut.kchunk;
   const bool direct = cut.direct;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -216,75 +220,84 @@ __device__ __forceinline__ void run_tile(const VocabArgs& p, const Cut& cut, int
   const T* bbase = MODE == VL_DW ? h : w;
   const size_t lda = LOGITS ? p.d : p.ldp, ldb = p.d;
 
-  const int MT = (M + TS - 1) / TS, NTL = (N + TS - 1) / TS, total = MT * NTL * ks;
+  const int MT = (M + TR - 1) / TR, NTL = (N + TR - 1) / TR, total = MT * NTL * ks;
   const int per = (total + 7) >> 3;
   const int L = (block & 7) * per + (block >> 3);
   if ((block >> 3) >= per || L >= total) return;
   const int split = L / (MT * NTL), l = L - split * (MT * NTL);
   const int nt = l / MT, mt = l - nt * MT;
-  const int m0 = mt * TS, n0 = nt * TS;
+  const int m0 = mt * TR, n0 = nt * TR;
   const int k0 = split * kchunk, k_end = min(K - k0, kchunk);
   const int nk = (k_end + BK - 1) / BK;
 
-  Operand<T, AK, NF, false> oa;
-  Operand<T, BKC, NF, ONCE> ob;
-  oa.init(abase, lda, m0, M, k0, wave, lane);
-  ob.init(bbase, ldb, n0, N, k0, wave, lane);
+  // An operand is RB blocks of 64 rows; a wave reads one of them whole (RB = 2) or half of it.
+  Operand<T, AK, NF, false> oa[RB];
+  Operand<T, BKC, NF, ONCE> ob[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) {
+    oa[b].init(abase, lda, m0 + TS * b, M, k0, wave, lane);
+    ob[b].init(bbase, ldb, n0 + TS * b, N, k0, wave, lane);
+  }
+  auto issue = [&](char* slot, int at) {
+#pragma unroll
+    for (int b = 0; b < RB; ++b) oa[b].issue(slot + b * OPB, at, k_end, lda, wave);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) ob[b].issue(slot + (RB + b) * OPB, at, k_end, ldb, wave);
+  };
   // Past the last stage the loads read zeros into slots that nobody reads.
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    oa.issue(lds + s * STAGE, s * BK, k_end, lda, wave);
-    ob.issue(lds + s * STAGE + OPB, s * BK, k_end, ldb, wave);
-  }
-  f32x16_t acc;
+  for (int s = 0; s < 2; ++s) issue(lds + s * STAGE, s * BK);
+  f32x16_t acc[RB][RB];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
+  for (int a = 0; a < RB; ++a)
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[a][b][e] = 0.0f;
   const uint32_t lds0 = lds_addr_of(lds);
   for (int j = 0; j < nk; ++j) {
     char* slot = lds + (j & 1) * STAGE;
     const uint32_t sb = lds0 + (j & 1) * STAGE;
-    wait_vm<2 * LP>();   // stage j has landed, stage j + 1 may be in flight
+    wait_vm<2 * LP * RB>();   // stage j has landed, stage j + 1 may be in flight
     barrier();
-    Frags<T, AK, NF> fa;
-    Frags<T, BKC, NF> fb;
-    fa.read(sb, wm * 32, lane);
-    fb.read(sb + OPB, wn * 32, lane);
+    Frags<T, AK, NF> fa[RB];
+    Frags<T, BKC, NF> fb[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      fa[b].read(sb + (RB == 1 ? 0 : wm * OPB), RB == 1 ? wm * 32 : b * 32, lane);
+      fb[b].read(sb + (RB == 1 ? OPB : (RB + wn) * OPB), RB == 1 ? wn * 32 : b * 32, lane);
+    }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    fa.landed();
-    fb.landed();
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      fa[b].landed();
+      fb[b].landed();
+    }
     barrier();           // every wave has read stage j
-    oa.issue(slot, (j + 2) * BK, k_end, lda, wave);
-    ob.issue(slot + OPB, (j + 2) * BK, k_end, ldb, wave);
+    issue(slot, (j + 2) * BK);
 #pragma unroll
     for (int s = 0; s < NF; ++s) {
       if constexpr (sizeof(T) == 2) {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb.get16(s), fa.get16(s), acc, 0, 0, 0);
+#pragma unroll
+        for (int a = 0; a < RB; ++a)
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[b].get16(s), fa[a].get16(s), acc[a][b], 0, 0, 0);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fb.get32(s, e), fa.get32(s, e), acc, 0, 0, 0);
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int a = 0; a < RB; ++a)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+              acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[b].get32(s, e), fa[a].get32(s, e), acc[a][b], 0, 0, 0);
       }
     }
   }
   wait_vm<0>();   // no direct load may still be writing when the workgroup's LDS is released
 
-  // Lane l holds row l % 32 and, in element e, column 8 (e / 4) + 4 (l / 32) + e % 4 of the block.
-  const int row = m0 + wm * 32 + (lane & 31), c0 = n0 + wn * 32, half = lane >> 5;
-  if constexpr (MODE == VL_STATS) {
-    if (c0 >= N) return;
-    float mx = -__builtin_inff();
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (c0 + 8 * (e >> 2) + 4 * half + (e & 3) >= N) acc[e] = -__builtin_inff();
-      mx = fmaxf(mx, acc[e]);
-    }
-    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-    float sm = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sm += expf(acc[e] - mx);
-    sm += __shfl_xor(sm, 32, 64);
-    if (half == 0 && row < M) p.part[(size_t)((p.v0 + c0) / TILE_PART) * p.T + row] = make_float2(mx, sm);
-    return;
-  }
+  // Lane l holds row l % 32 of a block and, in element e, column 8 (e / 4) + 4 (l / 32) + e % 4.
+  const int half = lane >> 5;
   float scale = 1.0f;
   if constexpr (MODE == VL_GRAD) {
     if (p.scale_out) {   // few rows: every tile finds the scale itself, one writes it for the kernels after
@@ -294,63 +307,90 @@ __device__ __forceinline__ void run_tile(const VocabArgs& p, const Cut& cut, int
       scale = *p.scale;
     }
   }
-  if (row >= M) return;
-  const float out_scale = MODE != VL_GRAD && direct ? *p.scale : 1.0f;   // else the join scales
-  float lse = 0.0f, dl = 0.0f;
-  int tgt = -1;
-  if constexpr (MODE == VL_GRAD) {
-    lse = p.lse[row];
-    tgt = p.target[row];
-    dl = tgt >= 0 && tgt < p.V ? p.dloss[row] / scale : 0.0f;
-    tgt -= p.v0;
-  }
+  const float out_scale = (MODE == VL_DH || MODE == VL_DW) && direct ? *p.scale : 1.0f;   // else the join scales
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int n = c0 + 8 * g + 4 * half;
-    float v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = acc[4 * g + e] * out_scale;
-    if constexpr (MODE == VL_GRAD) {   // columns up to the tile's end, inside P's row of a multiple of 256
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float q = expf(v[e] - lse) - (n + e == tgt ? 1.0f : 0.0f);
-        v[e] = dl == 0.0f || n + e >= N ? 0.0f : dl * q;
+  for (int a = 0; a < RB; ++a) {
+    const int row = m0 + wm * 32 * RB + a * 32 + (lane & 31);
+    float lse = 0.0f, dl = 0.0f;
+    int tgt = -1;
+    if constexpr (MODE == VL_GRAD) {
+      if (row < M) {
+        lse = p.lse[row];
+        tgt = p.target[row];
+        dl = tgt >= 0 && tgt < p.V ? p.dloss[row] / scale : 0.0f;
+        tgt -= p.v0;
       }
-      store4(reinterpret_cast<T*>(p.p) + (size_t)row * p.ldp + n, v);
-    } else if (n < N) {   // N = d, a multiple of 8
-      if constexpr (MODE == VL_DH) {
-        if (direct) {
-          store4(reinterpret_cast<T*>(p.dh) + (size_t)row * p.d + n, v);
-        } else {   // dh: partial product `split` of the pieces so far
-          float* to = p.dh_acc + ((size_t)split * p.T + row) * p.d + n;
-          if (!p.first) {
-            const float4 o = *reinterpret_cast<const float4*>(to);
-            v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
-          }
-          store4(to, v);
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+      const int c0 = n0 + wn * 32 * RB + b * 32;
+      f32x16_t& x = acc[a][b];
+      if constexpr (MODE == VL_STATS) {
+        if (c0 >= N) continue;
+        float mx = -__builtin_inff();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          if (c0 + 8 * (e >> 2) + 4 * half + (e & 3) >= N) x[e] = -__builtin_inff();
+          mx = fmaxf(mx, x[e]);
         }
-      } else if (direct) {
-        store4(reinterpret_cast<T*>(p.dw) + (size_t)(p.v0 + row) * p.d + n, v);
-      } else {
-        store4(p.dw_acc + ((size_t)split * M + row) * p.d + n, v);
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        float sm = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sm += expf(x[e] - mx);
+        sm += __shfl_xor(sm, 32, 64);
+        if (half == 0 && row < M) p.part[(size_t)((p.v0 + c0) / TILE_PART) * p.T + row] = make_float2(mx, sm);
+        continue;
+      }
+      if (row >= M) continue;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int n = c0 + 8 * g + 4 * half;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = x[4 * g + e] * out_scale;
+        if constexpr (MODE == VL_GRAD) {   // columns up to the tile's end, inside P's row of a multiple of 256
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float q = expf(v[e] - lse) - (n + e == tgt ? 1.0f : 0.0f);
+            v[e] = dl == 0.0f || n + e >= N ? 0.0f : dl * q;
+          }
+          store4(reinterpret_cast<T*>(p.p) + (size_t)row * p.ldp + n, v);
+        } else if (n < N) {   // N = d, a multiple of 8
+          if constexpr (MODE == VL_DH) {
+            if (direct) {
+              store4(reinterpret_cast<T*>(p.dh) + (size_t)row * p.d + n, v);
+            } else {   // dh: partial product `split` of the pieces so far
+              float* to = p.dh_acc + ((size_t)split * p.T + row) * p.d + n;
+              if (!p.first) {
+                const float4 o = *reinterpret_cast<const float4*>(to);
+                v[0] += o.x; v[1] += o.y; v[2] += o.z; v[3] += o.w;
+              }
+              store4(to, v);
+            }
+          } else if (direct) {
+            store4(reinterpret_cast<T*>(p.dw) + (size_t)(p.v0 + row) * p.d + n, v);
+          } else {
+            store4(p.dw_acc + ((size_t)split * M + row) * p.d + n, v);
+          }
+        }
       }
     }
   }
 }
 
-template <typename T, int MODE, int NF, bool ONCE>
-__global__ __launch_bounds__(NT, NF == 8 ? 2 : 4) void vocab_tile_kernel(VocabArgs p, Cut cut) {
-  __shared__ __attribute__((aligned(1024))) char lds[4 * op_bytes(NF)];
-  run_tile<T, MODE, NF, ONCE>(p, cut, blockIdx.x, lds);
+template <typename T, int MODE, int NF, bool ONCE, int RB>
+__global__ __launch_bounds__(NT, NF * RB == 8 ? 2 : 4) void vocab_tile_kernel(VocabArgs p, Cut cut) {
+  __shared__ __attribute__((aligned(1024))) char lds[4 * RB * op_bytes(NF)];
+  run_tile<T, MODE, NF, ONCE, RB>(p, cut, blockIdx.x, lds);
 }
 
 // dh's and dw's products side by side: neither needs the other, and of few rows and words neither
 // fills the CUs alone (257 x 256 against 1000 words in fp32: 10 us together, 10 us each apart).
-template <typename T>
-__global__ __launch_bounds__(NT, 4) void vocab_tile_pair_kernel(VocabArgs p, Cut dh, Cut dw, int dh_blocks) {
-  __shared__ __attribute__((aligned(1024))) char lds[4 * op_bytes(4)];
-  if ((int)blockIdx.x < dh_blocks) run_tile<T, VL_DH, 4, false>(p, dh, blockIdx.x, lds);
-  else run_tile<T, VL_DW, 4, false>(p, dw, blockIdx.x - dh_blocks, lds);
+template <typename T, int RB>
+__global__ __launch_bounds__(NT, RB == 2 ? 2 : 4) void vocab_tile_pair_kernel(VocabArgs p, Cut dh, Cut dw, int dh_blocks) {
+  __shared__ __attribute__((aligned(1024))) char lds[4 * RB * op_bytes(4)];
+  if ((int)blockIdx.x < dh_blocks) run_tile<T, VL_DH, 4, false, RB>(p, dh, blockIdx.x, lds);
+  else run_tile<T, VL_DW, 4, false, RB>(p, dw, blockIdx.x - dh_blocks, lds);
 }
 
 // out = the scaled sum of ks partial products of n elements in a fixed order, rounded; two such sums in
@@ -417,20 +457,20 @@ hipError_t launch_join(const Join<T>& a, const Join<T>& b, const float* scale, h
 
 // K per split of dh or dw, a multiple of a stage; dh's is the same for every piece of a call.
 template <typename T>
-int split_chunk(int M, int N, int K) {
+int split_chunk(int M, int N, int K, bool large) {
   constexpr int BK = 256 / sizeof(T);
-  return ceil_div(ceil_div(K, tile_splits(M, N, K)), BK) * BK;
+  return ceil_div(ceil_div(K, tile_splits(M, N, K, large)), BK) * BK;
 }
 
 template <typename T>
 Cut cut_of(int mode, const VocabArgs& p) {
-  Cut c{1, mode == VL_DW ? p.T : p.d, true};
+  Cut c{1, p.d, true};
   if (mode == VL_DH) {
-    c.kchunk = split_chunk<T>(p.T, p.d, p.ldp);
+    c.kchunk = split_chunk<T>(p.T, p.d, p.ldp, p.large);
     c.ks = ceil_div(p.vn, c.kchunk);
     c.direct = c.ks == 1 && p.first && p.last;   // dh of several pieces is accumulated in fp32
   } else if (mode == VL_DW) {
-    c.kchunk = split_chunk<T>(p.vn, p.d, p.T);
+    c.kchunk = split_chunk<T>(p.vn, p.d, p.T, p.large);
     c.ks = ceil_div(p.T, c.kchunk);
     c.direct = c.ks == 1;
   }
@@ -440,7 +480,7 @@ Cut cut_of(int mode, const VocabArgs& p) {
 // Workgroups of a product, a multiple of the XCDs.
 unsigned blocks_of(int mode, const VocabArgs& p, const Cut& c) {
   const int M = mode == VL_DW ? p.vn : p.T, N = mode == VL_DW || mode == VL_DH ? p.d : p.vn;
-  return (unsigned)(((long long)ceil_div(M, TS) * ceil_div(N, TS) * c.ks + 7) / 8 * 8);
+  return (unsigned)((tile_count(M, N, p.large) * c.ks + 7) / 8 * 8);
 }
 
 template <typename T>
@@ -450,7 +490,7 @@ Join<T> join_dw(const VocabArgs& p, const Cut& c) {
 // The sum over all pieces: the first one, the widest, used every split.
 template <typename T>
 Join<T> join_dh(const VocabArgs& p) {
-  const int wide = std::min(p.V, p.ldp), ks = ceil_div(wide, split_chunk<T>(p.T, p.d, p.ldp));
+  const int wide = std::min(p.V, p.ldp), ks = ceil_div(wide, split_chunk<T>(p.T, p.d, p.ldp, p.large));
   return Join<T>{p.dh_acc, reinterpret_cast<T*>(p.dh), ks == 1 && p.V <= p.ldp ? 0 : (size_t)p.T * p.d, ks};
 }
 
@@ -465,14 +505,18 @@ hipError_t launch(const VocabArgs& p, hipStream_t s) {
   // 7 tokens against 205 MB of words 45.5 us instead of 52.5; 87 MB, which the backward then finds in
   // the cache, would take 12 us longer there.
   constexpr bool LOGITS = MODE == VL_STATS || MODE == VL_GRAD;
-  auto run = [&](auto nf, auto once) {
-    hipLaunchKernelGGL((vocab_tile_kernel<T, MODE, decltype(nf)::value, decltype(once)::value>), grid, dim3(NT), 0, s, p, c);
+  auto run = [&](auto nf, auto once, auto rb) {
+    hipLaunchKernelGGL((vocab_tile_kernel<T, MODE, decltype(nf)::value, decltype(once)::value, decltype(rb)::value>), grid,
+                       dim3(NT), 0, s, p, c);
   };
+  typedef std::integral_constant<int, 1> One;
+  typedef std::integral_constant<int, 4> Short;
   typedef std::integral_constant<int, LOGITS ? 8 : 4> Stream;
   typedef std::integral_constant<bool, MODE == VL_STATS> Once;
-  if (LOGITS && p.T <= TS && (size_t)p.vn * p.d * sizeof(T) >= size_t(128) << 20) run(Stream{}, Once{});
-  else if (LOGITS && p.T <= TS) run(Stream{}, std::false_type{});
-  else run(std::integral_constant<int, 4>{}, std::false_type{});
+  if (LOGITS && p.T <= TS && (size_t)p.vn * p.d * sizeof(T) >= size_t(128) << 20) run(Stream{}, Once{}, One{});
+  else if (LOGITS && p.T <= TS) run(Stream{}, std::false_type{}, One{});
+  else if (p.large) run(Short{}, std::false_type{}, std::integral_constant<int, 2>{});
+  else run(Short{}, std::false_type{}, One{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || MODE != VL_DW) return e;
   return launch_join(join_dw<T>(p, c), Join<T>{}, p.scale, s);
@@ -493,7 +537,8 @@ template <typename T>
 hipError_t launch_both(const VocabArgs& p, hipStream_t s) {
   const Cut dh = cut_of<T>(VL_DH, p), dw = cut_of<T>(VL_DW, p);
   const unsigned nh = blocks_of(VL_DH, p, dh), nw = blocks_of(VL_DW, p, dw);
-  hipLaunchKernelGGL(vocab_tile_pair_kernel<T>, dim3(nh + nw), dim3(NT), 0, s, p, dh, dw, (int)nh);
+  auto kernel = p.large ? vocab_tile_pair_kernel<T, 2> : vocab_tile_pair_kernel<T, 1>;
+  hipLaunchKernelGGL(kernel, dim3(nh + nw), dim3(NT), 0, s, p, dh, dw, (int)nh);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   return launch_join(join_dw<T>(p, dw), p.last ? join_dh<T>(p) : Join<T>{}, p.scale, s);
@@ -501,13 +546,17 @@ hipError_t launch_both(const VocabArgs& p, hipStream_t s) {
 
 }  // namespace
 
-// Splits of the K of an M x N product: as many as fill two workgroups per CU, at least 256 k each.
-int tile_splits(int M, int N, int K) {
-  const long long tiles = (long long)ceil_div(M, TS) * ceil_div(N, TS);
-  return (int)std::max<long long>(1, std::min<long long>(2 * NUM_CUS / tiles, K / 256));
+long long tile_count(int M, int N, bool large) {
+  const int ts = large ? 2 * TS : TS;
+  return (long long)ceil_div(M, ts) * ceil_div(N, ts);
 }
 
-size_t tile_acc_bytes(int M, int N, int K) { return (size_t)tile_splits(M, N, K) * M * N * sizeof(float); }
+// Splits of the K of an M x N product: as many as fill two workgroups per CU, at least 256 k each.
+int tile_splits(int M, int N, int K, bool large) {
+  return (int)std::max<long long>(1, std::min<long long>(2 * NUM_CUS / tile_count(M, N, large), K / 256));
+}
+
+size_t tile_acc_bytes(int M, int N, int K, bool large) { return (size_t)tile_splits(M, N, K, large) * M * N * sizeof(float); }
 
 hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s) {
   return bf16 ? launch_mode<bf16_t>(mode, p, s) : launch_mode<float>(mode, p, s);

@@ -759,3 +759,13 @@ def test_layers_that_share_buffers():
         assert all(torch.equal(g, h) for g, h in zip(a.gradients(), b.gradients()))
         gate = b.bufs["dnorm_gate"]
         assert gate is None if "norm_gate" not in b.p else torch.equal(gate, a.bufs["dnorm_gate"])
+
+
+@pytest.mark.parametrize("dtype,T,d,V", [("bf16", 1990, 1000, 3990), ("f32", 1990, 512, 3990), ("bf16", 190, 2000, 20000),
+                                         ("bf16", 16400, 136, 4500), ("f32", 16400, 136, 4500)])
+def test_vocab_loss_in_larger_tiles(dtype, T, d, V):
+    """Products of some hundred tiles of 128x128, whose last rows and columns are ragged; the last two
+    go through two pieces of the vocabulary."""
+    log(f"vocab loss {dtype} larger tiles T={T} d={d} V={V}")
+    data = loss_data(T, d, V, dtype, 0.1, 9)
+    check_loss(*data, dtype, run_loss(*data, dtype))
