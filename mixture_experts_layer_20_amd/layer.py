@@ -170,7 +170,7 @@ class MoELayer:
             self._allocate_norm()
         if cfg.backward:   # clip_gradients
             dev = params["x"].device
-            self.bufs.t.setdefault("grad_norm", torch.empty(1, dtype=torch.float32, device=dev))
+            self.grad_norm = torch.empty(1, dtype=torch.float32, device=dev)
             self._ws_grad = torch.empty(L.moe_grad_workspace_size(L.grad_list(self.gradients())), dtype=torch.uint8,
                                         device=dev)
         self.renorm = renormalize
@@ -476,9 +476,9 @@ class MoELayer:
         that ([1] float, on the device)."""
         if not self.cfg.backward:
             raise ValueError("the layer has no backward")
-        b, grads = self.bufs.t, L.grad_list(self.gradients())
-        self._stage("grad_clip", L.moe_grad_clip, grads, max_norm, b["grad_norm"], self._ws_grad, self._ws_grad.numel())
-        return b["grad_norm"]
+        grads = L.grad_list(self.gradients())
+        self._stage("grad_clip", L.moe_grad_clip, grads, max_norm, self.grad_norm, self._ws_grad, self._ws_grad.numel())
+        return self.grad_norm
 
     def step(self):
         """One pass of the whole path: forward, then backward when the workload has one."""

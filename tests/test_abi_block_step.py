@@ -172,7 +172,7 @@ def test_layers_that_share_buffers_keep_their_own_gate_gradient():
     p = dict(x=z(6, 256), logits=z(6, 4), norm_in=z(256), norm_out=z(256), dout=z(6, 256))
     first = LY.MoELayer(cfg, dict(p, norm_gate=z(6, 256)), block_norm=True, gate_rows=1)
     held = {n: first.bufs[n] for n in ("xn", "rstd_in", "rstd_out", "y_block", "dblock", "dxn", "dnorm_in", "dnorm_out",
-                                       "ws_norm", "grad_norm")}
+                                       "ws_norm")}
     second = LY.MoELayer(cfg, dict(p, norm_gate=z(1, 256)), bufs=first.bufs, block_norm=True)
     third = LY.MoELayer(cfg, p, bufs=first.bufs, block_norm=True)
     LY.MoELayer(cfg, p, bufs=first.bufs)
