@@ -15,6 +15,8 @@
  *               no pointer after a call returns and allocates no device memory: scratch space is
  *               the caller's workspace, sized by the matching *_workspace_size function (or, for
  *               moe_permute_noalloc, a fixed device array the library holds per GPU).
+ *               A workspace serves one call at a time: calls that may run at once, on two streams or
+ *               in two graphs, need one each.
  *               Every device pointer (tensors, index arrays, workspaces) must be 16-byte
  *               aligned: the kernels use 16-byte vector and direct-to-LDS accesses from each base
  *               (hipMalloc and PyTorch allocations are 256-byte aligned); a misaligned pointer
@@ -374,7 +376,8 @@ moe_status_t moe_norm_in_bwd(const void* dxn, const void* x, const void* w, cons
  *     marks a token without loss: loss 0 and no gradient.  Its row of h is still read and must be finite.
  *   loss, lse [T] float                              OUTPUT
  * Products of bf16 data accumulate in fp32, exponentials and sums are fp32.  d must be a multiple of
- * 8, at most 65536; T and V at most 2^22, T V, V d and T d at most 2^35; T may be 0.
+ * 8, at most 65536; T and V at most 2^22, T V, V d and T d at most 2^35; T may be 0.  Outputs must not
+ * overlap inputs.
  * Source: "Olmo-core DDP MoE examples", "Production throughput runs" (language-model training runs;
  * the pages do not print the loss). */
 size_t moe_vocab_loss_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt);
