@@ -73,6 +73,16 @@ template <> struct Seg8<float> {
   }
 };
 
+__device__ __forceinline__ void load4(const bf16_t* p, float (&v)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 w = *reinterpret_cast<const float4*>(p);
+  v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
+}
+
 constexpr int NT = 256;   // threads of a workgroup, or L where a row takes more
 template <int L>
 constexpr int threads() { return L < NT ? NT : L; }
@@ -276,7 +286,65 @@ struct BwdArgs {
   float* part;   // [3][blocks][d]: dw partials (MULTI), head (the only ones otherwise), tail
   float* dw;
   float* dgate;
+  int row_blocks;   // workgroups behind these take the column sums, if there are any
 };
+
+// Few rows: the column sums need each row's rstd alone, which is given, so workgroups beside those of
+// the rows form them, 16 columns each, from a second reading of the rows, and no join follows.
+template <typename T, int TH>
+__device__ __forceinline__ void column_sums(const T* dout, const T* y, const T* w, const T* gate, const float* rstd,
+                                            const BwdArgs& p) {
+  constexpr int SL = TH / 4;
+  __shared__ float red[SL][16 + 1];
+  const int d = p.d, slice = threadIdx.x / 4, x = threadIdx.x % 4 * 4;
+  const int c = ((int)blockIdx.x - p.row_blocks) * 16 + x;
+  const bool in = c < d;   // d is a multiple of 8
+  float dw[4] = {0, 0, 0, 0};
+  for (int t0 = 0, seg = 0; t0 < p.rows; ++seg) {
+    const int t1 = gate ? (int)min((long long)p.rows, (long long)t0 + p.gate_rows) : p.rows;
+    float S[4] = {0, 0, 0, 0};
+    if (in) {
+#pragma unroll 4
+      for (int t = t0 + slice; t < t1; t += SL) {
+        float n[4], g[4];
+        load4(y + (size_t)t * d + c, n);
+        load4(dout + (size_t)t * d + c, g);
+        const float r = rstd[t];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[e] += g[e] * (n[e] * r);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[slice][x + e] = S[e];
+#pragma unroll
+    for (int off = SL / 2; off >= 1; off >>= 1) {
+      __syncthreads();
+      if (slice < off) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) red[slice][x + e] += red[slice + off][x + e];
+      }
+    }
+    if (slice == 0 && in) {
+      float wv[4], gv[4];
+      if (gate) {
+        load4(w + c, wv);
+        load4(gate + (size_t)seg * d + c, gv);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = red[0][x + e];
+        dw[e] += gate ? gv[e] * v : v;
+        if (gate) p.dgate[(size_t)seg * d + c + e] = wv[e] * v;
+      }
+    }
+    __syncthreads();
+    t0 = t1;
+  }
+  if (slice == 0 && in) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p.dw[c + e] = dw[e];
+  }
+}
 
 // IN: dxn (as dout), x (as y), dres.  Otherwise: dout, y, gate.  The next row is loaded while the
 // current one is reduced: without it the loads of a row waited for the statistic of the row before.
@@ -289,8 +357,10 @@ __global__ __launch_bounds__(threads<L>()) void norm_bwd_kernel(const T* dout, c
   extern __shared__ float sums[];   // [NS - 1][8 NV L] column sums of the other waves (L = 64)
   const int lane = threadIdx.x % L, me = threadIdx.x / L;
   const int d = p.d;
+  if ((int)blockIdx.x >= p.row_blocks) return column_sums<T, threads<L>()>(dout, y, w, gate, rstd, p);
   const int r0 = blockIdx.x * p.R, r1 = min(p.rows, r0 + p.R);
-  const int blocks = gridDim.x;
+  const int blocks = p.row_blocks;
+  const bool sums_here = (int)gridDim.x == blocks;
   const float inv_d = 1.0f / (float)d;
   int slot = 0;
   struct Row {
@@ -379,6 +449,8 @@ __global__ __launch_bounds__(threads<L>()) void norm_bwd_kernel(const T* dout, c
         Seg8<T>::put(dy + (size_t)t * d + q.c, g);
       }
     }
+    p0 = p1;
+    if (!sums_here) continue;
     // S over the workgroup's waves, into wave 0 (L = 64)
     if constexpr (NS > 1) {
       if (me > 0) {
@@ -430,10 +502,9 @@ __global__ __launch_bounds__(threads<L>()) void norm_bwd_kernel(const T* dout, c
         }
       }
     }
-    p0 = p1;
   }
   if constexpr (MULTI) {
-    if (me == 0) {
+    if (me == 0 && sums_here) {
       float* to = blocks == 1 ? p.dw : p.part + (size_t)blockIdx.x * d;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -525,19 +596,28 @@ int bwd_rows(long long T, int d) {
   return (int)std::max<long long>(ns, (r + ns - 1) / ns * ns);
 }
 
+// Few rows: column sums beside the rows instead of partials and their join.  Forward and backward, a
+// call after the other (us): 61 rows x 2048 30.3 -> 26.3, 512 x 4096 32.7 -> 26.3, 1024 x 1024 29.7 ->
+// 27.0; but 1024 x 4096 44.9 -> 46.4, 2048 x 1000 in fp32 29.7 -> 36.4, 200 x 16384 40.7 -> 46.8.  Gate
+// rows are walked one after the other: 512 x 1000 with 4 of them 26.2 -> 23.9, 1000 x 1000 with 8 26.1 ->
+// 33.2.
+bool few_rows(long long T, int d) { return T <= 1024 && T * d <= 1 << 21; }
+
 template <typename T, bool IN, bool MULTI>
 hipError_t norm_bwd_rows(const T* dout, const T* y, const T* w, const T* gate, const T* dres, const float* rstd, T* dy,
-                         const BwdArgs& p, hipStream_t s) {
+                         BwdArgs p, hipStream_t s) {
   const int blocks = ceil_div(p.rows, p.R);
+  const int gate_rows = MULTI ? ceil_div(p.rows, p.gate_rows) : 0;
+  const int columns = blocks > 1 && gate_rows <= 4 && few_rows(p.rows, p.d) ? ceil_div(p.d, 16) : 0;
+  p.row_blocks = blocks;
   hipError_t e = by_width(p.d, [&](auto L, auto NV) {
     constexpr int th = threads<decltype(L)::value>(), ns = th / decltype(L)::value;
     const size_t lds = (size_t)(ns - 1) * 8 * decltype(NV)::value * decltype(L)::value * sizeof(float);
-    hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(L)::value, decltype(NV)::value, IN, MULTI>), dim3(blocks), dim3(th),
+    hipLaunchKernelGGL((norm_bwd_kernel<T, decltype(L)::value, decltype(NV)::value, IN, MULTI>), dim3(blocks + columns), dim3(th),
                        lds, s, dout, y, w, gate, dres, rstd, dy, p);
     return hipGetLastError();
   });
-  if (e != hipSuccess || blocks == 1) return e;
-  const int gate_rows = MULTI ? ceil_div(p.rows, p.gate_rows) : 0;
+  if (e != hipSuccess || blocks == 1 || columns > 0) return e;
   const bool by_row = gate_rows < blocks;
   norm_bwd_join_kernel<T, MULTI><<<dim3(ceil_div(p.d, 16), 1 + (MULTI ? (by_row ? gate_rows : blocks - 1) : 0)), dim3(NT), 0,
                                    s>>>(w, gate, p, blocks, by_row);

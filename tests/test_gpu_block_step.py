@@ -769,3 +769,11 @@ def test_vocab_loss_in_larger_tiles(dtype, T, d, V):
     log(f"vocab loss {dtype} larger tiles T={T} d={d} V={V}")
     data = loss_data(T, d, V, dtype, 0.1, 9)
     check_loss(*data, dtype, run_loss(*data, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,gate_rows", [(300, 200, 300), (1000, 1000, 0), (65, 72, 33), (5, 8, 0), (300, 5000, 299),
+                                           (1024, 2048, 128), (77, 24, 11), (70, 3000, 8), (1023, 104, 1), (33, 16384, 20)])
+def test_norms_of_few_rows(dtype, T, d, gate_rows):
+    """Where the column sums are formed beside the rows, and (4 gate rows are the most) where not."""
+    test_norms_match_oracle(dtype, T, d, gate_rows)
