@@ -168,11 +168,9 @@ class MoELayer:
         self.norm_eps = float(norm_eps)
         if self.norm:
             self._allocate_norm()
-        if cfg.backward:   # clip_gradients
-            dev = params["x"].device
-            self.grad_norm = torch.empty(1, dtype=torch.float32, device=dev)
-            self._ws_grad = torch.empty(L.moe_grad_workspace_size(L.grad_list(self.gradients())), dtype=torch.uint8,
-                                        device=dev)
+        if cfg.backward:   # clip_gradients, whose workspace is made when it is first called
+            self.grad_norm = torch.empty(1, dtype=torch.float32, device=params["x"].device)
+            self._ws_grad = None
         self.renorm = renormalize
         self.merge = merge_shared
         self.recompute = recompute
@@ -473,10 +471,12 @@ class MoELayer:
 
     def clip_gradients(self, max_norm: float) -> torch.Tensor:
         """Scale the gradients in place to a global norm of at most max_norm; returns the norm before
-        that ([1] float, on the device)."""
+        that ([1] float, on the device).  The first call allocates the workspace that later ones use."""
         if not self.cfg.backward:
             raise ValueError("the layer has no backward")
         grads = L.grad_list(self.gradients())
+        if self._ws_grad is None:
+            self._ws_grad = torch.empty(L.moe_grad_workspace_size(grads), dtype=torch.uint8, device=self.grad_norm.device)
         self._stage("grad_clip", L.moe_grad_clip, grads, max_norm, self.grad_norm, self._ws_grad, self._ws_grad.numel())
         return self.grad_norm
 

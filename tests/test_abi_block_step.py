@@ -201,3 +201,28 @@ def test_tensors_off_the_current_device_are_refused(monkeypatch):
             call()
     with pytest.raises(ValueError, match="different devices"):
         L.grad_list([t, torch.zeros(8, device="meta")])
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_layer_with_a_backward_over_forward_buffers(norm):
+    """Buffers without the backward's tensors serve a forward, whatever the configuration says."""
+    cfg = MoEConfig("t", 6, 256, 4, 2, 128, 0, "f32", "random", 0.0, True)
+    z = torch.zeros
+    p = dict(x=z(6, 256), logits=z(6, 4), norm_in=z(256), norm_out=z(256), dout=z(6, 256))
+    bufs = LY.Buffers.allocate(cfg.with_(backward=False), torch.device("cpu"))
+    assert "dw1" not in bufs.t
+    LY.MoELayer(cfg, p, bufs=bufs, block_norm=norm)
+
+
+def test_clipping_workspace_is_made_once_when_it_is_needed(monkeypatch):
+    cfg = MoEConfig("t", 6, 256, 4, 2, 128, 0, "f32", "random", 0.0, True)
+    z = torch.zeros
+    lay = LY.MoELayer(cfg, dict(x=z(6, 256), logits=z(6, 4), dout=z(6, 256)))
+    before = set(lay.bufs.t)
+    calls = []
+    monkeypatch.setattr(L, "moe_grad_clip", lambda *a: calls.append(a))
+    lay.clip_gradients(1.0)
+    lay.clip_gradients(2.0)
+    (grads, _, norm, ws, n), second = calls[0], calls[1]
+    assert ws.numel() == n >= L.moe_grad_workspace_size(grads) and norm is lay.grad_norm
+    assert second[3] is ws and set(lay.bufs.t) == before
