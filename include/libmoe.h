@@ -393,6 +393,15 @@ size_t moe_vocab_loss_bwd_workspace_size(int64_t T, int64_t d, int64_t V, moe_dt
 moe_status_t moe_vocab_loss_bwd(const void* h, const void* w, const int32_t* target, const float* lse,
                                 const float* dloss, int64_t T, int64_t d, int64_t V, moe_dtype_t dt, void* dh,
                                 void* dw, void* ws, size_t ws_bytes, moe_stream_t stream);
+/* How the two calls cut their products at a size (a host query; all zero where T is 0). */
+typedef struct {
+  int32_t piece_words, pieces; /* the backward's pieces of the vocabulary; the last may hold fewer words */
+  int32_t fwd_tile;            /* rows and columns of an output tile: the forward's logits, */
+  int32_t logits_tile;         /* the backward's logits of its first piece, */
+  int32_t dh_tile, dw_tile;    /* dh and dw */
+  int32_t dh_splits, dw_splits; /* partial products of the first piece that dh and dw are joined from */
+} moe_vocab_loss_plan_t;
+moe_status_t moe_vocab_loss_plan(int64_t T, int64_t d, int64_t V, moe_dtype_t dt, moe_vocab_loss_plan_t* plan);
 
 /* ------------------------------------------------------------------------------------------ */
 /* Global gradient norm and clipping                                                            */

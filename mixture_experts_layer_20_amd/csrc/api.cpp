@@ -745,6 +745,16 @@ moe_status_t moe_vocab_loss(const void* h, const void* w, const int32_t* target,
                    "vocabulary loss");
 }
 
+moe_status_t moe_vocab_loss_plan(int64_t T, int64_t d, int64_t V, moe_dtype_t dt, moe_vocab_loss_plan_t* plan) {
+  g_err.clear();
+  moe_status_t st = check_vocab(T, d, V, dt);
+  if (st != MOE_OK) return st;
+  CHECK(plan, MOE_ERR_INVALID_VALUE, "plan is NULL");
+  const moe::VocabPlan p = moe::vocab_loss_plan((int)T, (int)d, (int)V, dt == MOE_BF16);
+  *plan = moe_vocab_loss_plan_t{p.piece_words, p.pieces, p.fwd_tile, p.logits_tile, p.dh_tile, p.dw_tile, p.dh_splits, p.dw_splits};
+  return MOE_OK;
+}
+
 size_t moe_vocab_loss_bwd_workspace_size(int64_t T, int64_t d, int64_t V, moe_dtype_t dt) {
   if (check_vocab(T, d, V, dt) != MOE_OK) return 0;
   return align256(moe::vocab_loss_bwd_ws_bytes(T, d, V, dt == MOE_BF16));

@@ -45,6 +45,10 @@ hipError_t launch_grad_scale(const GradItem* g, int count, double* sums, int nsu
                              hipStream_t s);
 
 // Softmax cross entropy over a vocabulary
+struct VocabPlan {   // moe_vocab_loss_plan_t
+  int piece_words, pieces, fwd_tile, logits_tile, dh_tile, dw_tile, dh_splits, dw_splits;
+};
+VocabPlan vocab_loss_plan(int T, int d, int V, bool bf16);
 size_t vocab_loss_ws_bytes(long long T, long long d, long long V, bool bf16);
 hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target, int T, int d, int V, bool bf16,
                              float* loss, float* lse, void* ws, hipStream_t s);

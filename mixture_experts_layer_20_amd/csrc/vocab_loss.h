@@ -48,6 +48,7 @@ int pipe_dh_splits(int T, int d, int words);
 int pipe_dw_splits(int T, int d, int words);
 size_t pipe_dh_bytes(int T, int d, int words);
 size_t pipe_dw_bytes(int T, int d, int words);
+int pipe_ks(int mode, const VocabArgs& p);   // partial products that a launch sums K in
 hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s);
 hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s);
 
@@ -56,6 +57,7 @@ hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s);
 long long tile_count(int M, int N, bool large);
 int tile_splits(int M, int N, int K, bool large);
 size_t tile_acc_bytes(int M, int N, int K, bool large);
+int tile_ks(int mode, const VocabArgs& p, bool bf16);
 hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s);
 // VL_DH and VL_DW in one launch, and the joins that they need (dh's after the last piece).
 hipError_t launch_tile_pair(const VocabArgs& p, bool bf16, hipStream_t s);

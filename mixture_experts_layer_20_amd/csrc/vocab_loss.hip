@@ -327,6 +327,32 @@ hipError_t launch_vocab_loss(const void* h, const void* w, const int32_t* target
   return bf16 ? loss_fwd<bf16_t>(p, loss, lse, ws, s) : loss_fwd<float>(p, loss, lse, ws, s);
 }
 
+VocabPlan vocab_loss_plan(int T, int d, int V, bool bf16) {
+  VocabPlan plan{};
+  if (T == 0) return plan;
+  const auto side = [](Tiles t) { return t == PIPE ? 256 : t == LARGE ? 128 : 64; };
+  VocabArgs p{};
+  p.T = T; p.d = d; p.V = V;
+  p.ldp = piece_words(T, V);
+  p.vn = std::min(p.ldp, V);
+  p.first = true;
+  p.last = p.vn == V;
+  plan.piece_words = p.ldp;
+  plan.pieces = ceil_div(V, p.ldp);
+  plan.fwd_tile = side(logits_tiles(T, d, V, bf16));
+  plan.logits_tile = side(logits_tiles(T, d, p.vn, bf16));
+  const GradTiles tiles = grad_tiles(T, d, p.ldp, bf16);
+  plan.dh_tile = side(tiles.dh);
+  plan.dw_tile = side(tiles.dw);
+  const auto ks = [&](Tiles t, int mode) {
+    p.large = t == LARGE;
+    return t == PIPE ? pipe_ks(mode, p) : tile_ks(mode, p, bf16);
+  };
+  plan.dh_splits = ks(tiles.dh, VL_DH);
+  plan.dw_splits = ks(tiles.dw, VL_DW);
+  return plan;
+}
+
 size_t vocab_loss_bwd_ws_bytes(long long T, long long d, long long V, bool bf16) {
   if (T <= 0) return 0;
   return bwd_space((int)T, (int)d, (int)V, bf16).total();

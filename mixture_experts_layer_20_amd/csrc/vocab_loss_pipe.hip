@@ -733,13 +733,21 @@ size_t pipe_dw_bytes(int T, int d, int words) {
   return ks > 1 ? acc_bytes(words, d, ks) : 0;
 }
 
+// K of a product, and K per split of it.
+static int pipe_k(int mode, const VocabArgs& p) { return mode == VL_DH ? p.vn : mode == VL_DW ? p.T : p.d; }
+static int pipe_chunk(int mode, const VocabArgs& p) {
+  if (mode == VL_DH) return split_chunk(p.ldp, pipe_dh_splits(p.T, p.d, p.ldp));
+  return mode == VL_DW ? split_chunk(p.T, pipe_dw_splits(p.T, p.d, p.vn)) : p.d;
+}
+int pipe_ks(int mode, const VocabArgs& p) { return ceil_div(pipe_k(mode, p), pipe_chunk(mode, p)); }
+
 hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s) {
+  const int kchunk = pipe_chunk(mode, p), ks = pipe_ks(mode, p);
   switch (mode) {
-    case VL_STATS: return launch<VL_STATS>(p, p.T, p.vn, p.d, p.d, s);
-    case VL_GRAD: return launch<VL_GRAD>(p, p.T, p.vn, p.d, p.d, s);
-    case VL_DH: return launch<VL_DH>(p, p.T, p.d, p.vn, split_chunk(p.ldp, pipe_dh_splits(p.T, p.d, p.ldp)), s);
+    case VL_STATS: return launch<VL_STATS>(p, p.T, p.vn, p.d, kchunk, s);
+    case VL_GRAD: return launch<VL_GRAD>(p, p.T, p.vn, p.d, kchunk, s);
+    case VL_DH: return launch<VL_DH>(p, p.T, p.d, p.vn, kchunk, s);
     case VL_DW: {
-      const int kchunk = split_chunk(p.T, pipe_dw_splits(p.T, p.d, p.vn)), ks = ceil_div(p.T, kchunk);
       if (ks == 1) return launch<VL_DW>(p, p.vn, p.d, p.T, kchunk, s);
       const hipError_t e = launch<VL_DW_SPLIT>(p, p.vn, p.d, p.T, kchunk, s);
       if (e != hipSuccess) return e;
@@ -750,9 +758,9 @@ hipError_t launch_pipe(int mode, const VocabArgs& p, hipStream_t s) {
 }
 
 hipError_t launch_pipe_join(const VocabArgs& p, hipStream_t s) {
-  // the first piece, the widest, used every split
-  const int ks = ceil_div(std::min(p.V, p.ldp), split_chunk(p.ldp, pipe_dh_splits(p.T, p.d, p.ldp)));
-  return launch_join(p.dh_acc, reinterpret_cast<bf16_t*>(p.dh), p.T, p.d, ks, p.scale, s);
+  VocabArgs first = p;   // the first piece, the widest, used every split
+  first.vn = std::min(p.V, p.ldp);
+  return launch_join(p.dh_acc, reinterpret_cast<bf16_t*>(p.dh), p.T, p.d, pipe_ks(VL_DH, first), p.scale, s);
 }
 
 }  // namespace vocab

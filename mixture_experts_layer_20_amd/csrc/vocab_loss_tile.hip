@@ -558,6 +558,10 @@ int tile_splits(int M, int N, int K, bool large) {
 
 size_t tile_acc_bytes(int M, int N, int K, bool large) { return (size_t)tile_splits(M, N, K, large) * M * N * sizeof(float); }
 
+int tile_ks(int mode, const VocabArgs& p, bool bf16) {
+  return bf16 ? cut_of<bf16_t>(mode, p).ks : cut_of<float>(mode, p).ks;
+}
+
 hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s) {
   return bf16 ? launch_mode<bf16_t>(mode, p, s) : launch_mode<float>(mode, p, s);
 }

@@ -70,6 +70,12 @@ class Grad(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64), ("dt", ctypes.c_int32)]
 
 
+class VocabLossPlan(ctypes.Structure):
+    """moe_vocab_loss_plan_t: how the vocabulary loss cuts its products."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("piece_words", "pieces", "fwd_tile", "logits_tile", "dh_tile", "dw_tile",
+                                              "dh_splits", "dw_splits")]
+
+
 # name -> (restype, argtypes); mirrors include/libmoe.h
 _SIGS = {
     "moe_route": (_I32, [_P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _P]),
@@ -111,6 +117,7 @@ _SIGS = {
     "moe_norm_in_bwd": (_I32, [_P, _P, _P, _P, _P, _F, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
     "moe_vocab_loss_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
     "moe_vocab_loss": (_I32, [_P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
+    "moe_vocab_loss_plan": (_I32, [_I64, _I64, _I64, _I32, _P]),
     "moe_vocab_loss_bwd_workspace_size": (_SZ, [_I64, _I64, _I64, _I32]),
     "moe_vocab_loss_bwd": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, _SZ, _P]),
     "moe_grad_workspace_size": (_SZ, [_P, _I32]),
@@ -394,6 +401,12 @@ def moe_vocab_loss_workspace_size(T, d, V, dt) -> int:
 def moe_vocab_loss(h, w, target, T, d, V, dt, loss, lse, ws, ws_bytes, stream=None):
     _call("moe_vocab_loss", _ptr(h), _ptr(w), _ptr(target), T, d, V, dt, _ptr(loss), _ptr(lse), _ptr(ws), ws_bytes,
           _stream(stream, h))
+
+
+def moe_vocab_loss_plan(T, d, V, dt) -> VocabLossPlan:
+    plan = VocabLossPlan()
+    _call("moe_vocab_loss_plan", T, d, V, dt, ctypes.addressof(plan))
+    return plan
 
 
 def moe_vocab_loss_bwd_workspace_size(T, d, V, dt) -> int:
