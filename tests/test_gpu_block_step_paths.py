@@ -1,0 +1,149 @@
+"""Paths of the block norms, the vocabulary loss and gradient clipping that sizes, lists and values choose:
+wide rows with partial column sums, lists of long chunks, NaN, and the block norms with each of the layer's
+options."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_20_amd import layer as LY
+from mixture_experts_layer_20_amd import libmoe as L
+from oracle import block_step as S
+from tests import test_gpu_block_step as B
+from tests.gpu_helpers import DEV, log, tnp
+
+pytestmark = pytest.mark.gpu
+
+U, HALF, EPS = B.U, B.HALF, B.EPS
+
+
+# ------------------------------------------------------------------------------------------- norms
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,gate_rows", [(140, 16384, 0), (140, 16384, 30), (40, 16384, 4), (1100, 16384, 300),
+                                           (300, 8192, 50), (600, 8192, 0), (1500, 2056, 400), (1500, 2048, 70),
+                                           (1100, 1000, 0), (1100, 1024, 20)])
+def test_norms_that_join_partial_column_sums(dtype, T, d, gate_rows):
+    """Every width of the backward where its workgroups write partial sums: too many rows or values for
+    column sums beside the rows, or more than four gate rows."""
+    B.test_norms_match_oracle(dtype, T, d, gate_rows)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_norms_keep_a_bad_row_to_itself(dtype):
+    """NaN or an infinity makes its own row what the formula makes of it; the others keep their bits."""
+    log(f"norms {dtype}: NaN and infinity in a row")
+    T, d, dt = 70, 520, B.DT[dtype]
+    c, t = B.norm_data(T, d, dtype, 0, 3)
+
+    def run(x, y):
+        xn, out, r1, r2 = B.empty(T, d, dtype=dtype), B.empty(T, d, dtype=dtype), B.empty(T), B.empty(T)
+        L.moe_norm_in(x, t["w_in"], T, d, EPS, dt, xn, r1)
+        L.moe_norm_out(y, t["x"], t["w_out"], None, 1, 1.0, EPS, T, d, dt, out, r2)
+        dy, dx, dw = B.empty(T, d, dtype=dtype), B.empty(T, d, dtype=dtype), B.empty(d)
+        ws = B.ws_of(L.moe_norm_bwd_workspace_size(T, d))
+        L.moe_norm_out_bwd(t["dout"], y, t["w_out"], None, 1, r2, T, d, dt, dy, dw, None, ws, ws.numel())
+        L.moe_norm_in_bwd(t["dxn"], x, t["w_in"], r1, None, 1.0, T, d, dt, dx, dw, ws, ws.numel())
+        return [xn, out, dy, dx]
+
+    good = run(t["x"], t["y"])
+    x, y = t["x"].clone(), t["y"].clone()
+    x[1, 3], y[1, 3] = float("nan"), float("nan")
+    x[69, 519], y[69, 519] = float("inf"), float("-inf")
+    bad = run(x, y)
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[1] = rest[69] = False
+    for g, b in zip(good, bad):
+        assert torch.equal(g[rest], b[rest]) and bool(torch.isnan(b[1]).all())
+    # infinity / infinity is NaN, everything else over infinity is zero
+    assert torch.isnan(bad[0][69, 519]) and not bad[0][69, :519].any()
+    assert torch.isnan(bad[1][69, 519]) and torch.equal(bad[1][69, :519], t["x"][69, :519])
+
+
+# -------------------------------------------------------------------------------------------- loss
+
+@pytest.mark.parametrize("T,d,V,dtype", [(300, 64, 700, "f32"), (300, 64, 700, "bf16"), (1500, 256, 16421, "bf16")])
+def test_gradient_of_a_nan_row_stays_in_the_row(T, d, V, dtype):
+    log(f"vocab loss {dtype}: NaN row T={T} d={d} V={V}")
+    h, w, target, dloss = B.loss_data(T, d, V, dtype, 0.0, 6)
+    _, _, dh, _ = B.run_loss(h, w, target, dloss, dtype)
+    hn = h.copy()
+    hn[4, 2] = np.nan
+    _, _, bad, dw = B.run_loss(hn, w, target, dloss, dtype)
+    rest = torch.arange(T, device=DEV) != 4
+    assert torch.equal(dh[rest], bad[rest]) and bool(torch.isnan(bad[4]).all()) and bool(torch.isnan(dw).all())
+
+
+# ---------------------------------------------------------------------------------------- clipping
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+def test_clip_of_long_chunks(max_norm):
+    """More than 63 M values, so chunks of at least 32768, scaled in eighths, with tensors that end inside
+    an eighth, at its end and at a chunk's end."""
+    log(f"clip: 75 M values max_norm={max_norm}")
+    sizes = [40_000_003, 30_000_001, 7, 100_003, 3 * 36864, 4608, 4609, 5_000_000, 1]
+    types = [torch.bfloat16 if i % 2 == 0 else torch.float32 for i in range(len(sizes))]
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    grads = [((1 + i) * torch.randn(n, device=DEV, generator=gen)).to(t) for i, (n, t) in enumerate(zip(sizes, types))]
+    outs = [torch.full_like(g, float("nan")) for g in grads]
+    lst = L.grad_list(grads, outs)
+    ws, norm = B.ws_of(L.moe_grad_workspace_size(lst)), B.empty(1)
+    L.moe_grad_clip(lst, max_norm, norm, ws, ws.numel())
+    ref = float(sum(g.double().square().sum() for g in grads).sqrt())
+    B.within("norm", tnp(norm), [ref], 2 * U * ref)
+    c = min(1.0, max_norm / (ref + 1e-6))
+    for g, o in zip(grads, outs):
+        half = HALF["bf16" if g.dtype == torch.bfloat16 else "f32"]
+        r = g.double() * c
+        bound = (3 * U + half) * r.abs() + (2.0 ** -133 if g.dtype == torch.bfloat16 else 2.0 ** -149)
+        assert bool(((o.double() - r).abs() <= bound).all())
+        assert c < 1 or torch.equal(o, g)
+    inplace = [g.clone() for g in grads]
+    lst2 = L.grad_list(inplace)
+    sumsq, norm2 = torch.zeros(1, dtype=torch.float64, device=DEV), B.empty(1)
+    L.moe_grad_norm(lst2, sumsq, norm2, ws, ws.numel())
+    L.moe_grad_scale(lst2, sumsq, max_norm, None)
+    assert torch.equal(norm, norm2) and abs(float(sumsq) - ref ** 2) <= 1e-11 * ref ** 2
+    assert all(torch.equal(a, b) for a, b in zip(inplace, outs))
+    once = [g.clone() for g in grads]
+    lst3 = L.grad_list(once)
+    L.moe_grad_clip(lst3, max_norm, None, ws, ws.numel())
+    assert all(torch.equal(a, b) for a, b in zip(once, outs))
+
+
+# ------------------------------------------------------------------------------------------- layer
+
+@pytest.mark.parametrize("kw", [dict(recompute=True), dict(lbl_weight=0.3), dict(precision="mxfp8"),
+                                dict(recompute=True, lbl_weight=0.3), dict(precision="mxfp8", lbl_weight=0.3)])
+def test_block_norm_with_the_layers_options(kw):
+    """With each option, the block computes what the plain layer with the same option computes of the
+    normalised input and of the gradient behind the norm, bit for bit, and the norms' own part is that of
+    a block without options."""
+    log(f"block norm with {kw}")
+    cfg, vals, extra, params, head, target = B.block_case(gate_rows=64)
+    normed = LY.MoELayer(cfg, params, block_norm=True, gate_rows=64, res_scale=0.8, **kw)
+    out = normed.forward()
+    b = normed.bufs
+    plain = LY.MoELayer(cfg, dict(params, x=b["xn"].clone()), **kw)
+    assert torch.equal(plain.forward(), b["y_block"])
+    ref, _ = S.norm_out(tnp(b["y_block"]).astype(np.float64), vals["x"], extra["norm_out"], extra["norm_gate"], 64, 0.8, EPS)
+    # the block normalises the combined row before it is rounded: one rounding of y more in the reference
+    normed_part = np.abs(ref - 0.8 * vals["x"])
+    B.within("out", tnp(out), ref, 3 * HALF["bf16"] * normed_part + HALF["bf16"] * 1.001 * np.abs(ref) + 3 * U * np.abs(vals["x"]))
+    dout = torch.randn(cfg.T, cfg.d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3)).to(torch.bfloat16)
+    dx = normed.backward(dout)
+    plain.backward(b["dblock"])
+    assert torch.equal(b["dxn"], plain.bufs["dx"])
+    assert all(torch.equal(b[n], plain.bufs[n]) for n in ("dw1", "dw3", "dw2", "dws1", "dws3", "dws2", "dwr"))
+    if "lbl_weight" in kw:
+        assert torch.equal(b["lbl_loss"], plain.bufs["lbl_loss"])
+    _, r_in = S.norm_in(vals["x"], extra["norm_in"], EPS)
+    ref_dx, ref_dw = S.norm_in_bwd(tnp(b["dxn"]).astype(np.float64), vals["x"], extra["norm_in"], r_in, tnp(dout), 0.8)
+    B.assert_close("dx", tnp(dx), ref_dx, 1e-2)
+    B.assert_close("dnorm_in", tnp(b["dnorm_in"]), ref_dw, 1e-4)
+    norm = float(torch.stack([g.double().square().sum() for g in normed.gradients()]).sum().sqrt())
+    before = [g.clone() for g in normed.gradients()]
+    got = normed.clip_gradients(norm / 2)
+    assert abs(float(got) / norm - 1) < 2 * U + 1e-9
+    for g, o in zip(normed.gradients(), before):
+        half = HALF["bf16" if g.dtype == torch.bfloat16 else "f32"]
+        assert bool(((g.double() - o.double() / 2).abs() <= (half + 4 * U + 1e-6 / norm) * o.double().abs() / 2 + 2.0 ** -133).all())
