@@ -375,6 +375,7 @@ moe_status_t moe_norm_in_bwd(const void* dxn, const void* x, const void* w, cons
  *   h [T, d] (dt), w [V, d] (dt), target [T] int32   INPUT.  A target outside [0, V) (such as -100)
  *     marks a token without loss: loss 0 and no gradient.  Its row of h is still read and must be finite.
  *   loss, lse [T] float                              OUTPUT
+ * A word whose logit is -inf adds nothing to the sum, one of +inf makes lse infinite, and NaN stays NaN.
  * Products of bf16 data accumulate in fp32, exponentials and sums are fp32.  d must be a multiple of
  * 8, at most 65536; T and V at most 2^22, T V, V d and T d at most 2^35; T may be 0.  Outputs must not
  * overlap inputs.

@@ -402,7 +402,9 @@ __device__ __forceinline__ void stats_epilogue(const VocabArgs& p, const Geo& g,
         mx = fmaxf(mx, acc[i][j][e]);
       }
     mx = other_half_max(mx);
-    const float m2 = mx * LOG2E;
+    // of an infinite maximum: words that are all -inf add nothing, one of +inf makes the sum infinite
+    float m2 = mx * LOG2E;
+    if (!(fabsf(m2) < __builtin_inff())) m2 = 0.0f;
     float s = 0.0f;
 #pragma unroll
     for (int j = 0; j < NI; ++j)

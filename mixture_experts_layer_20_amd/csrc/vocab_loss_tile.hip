@@ -334,9 +334,11 @@ __device__ __forceinline__ void run_tile(const VocabArgs& p, const Cut& cut, int
           mx = fmaxf(mx, x[e]);
         }
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        // of an infinite maximum: words that are all -inf add nothing, one of +inf makes the sum infinite
+        const float m = fabsf(mx) < __builtin_inff() ? mx : 0.0f;
         float sm = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sm += expf(x[e] - mx);
+        for (int e = 0; e < 16; ++e) sm += expf(x[e] - m);
         sm += __shfl_xor(sm, 32, 64);
         if (half == 0 && row < M) p.part[(size_t)((p.v0 + c0) / TILE_PART) * p.T + row] = make_float2(mx, sm);
         continue;

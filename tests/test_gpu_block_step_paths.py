@@ -1,5 +1,5 @@
 """Paths of the block norms, the vocabulary loss and gradient clipping that sizes, lists and values choose:
-wide rows with partial column sums, lists of long chunks, NaN, and the block norms with each of the layer's
+wide rows with partial column sums, lists of long chunks, infinities and NaN, and the block norms with each of the layer's
 options."""
 import numpy as np
 import pytest
@@ -9,7 +9,8 @@ from mixture_experts_layer_20_amd import layer as LY
 from mixture_experts_layer_20_amd import libmoe as L
 from oracle import block_step as S
 from tests import test_gpu_block_step as B
-from tests.gpu_helpers import DEV, log, tnp
+from tests.gpu_helpers import DEV, dev_tensor, log, tnp
+from tests.vocab_loss_sizes import FORWARD
 
 pytestmark = pytest.mark.gpu
 
@@ -60,6 +61,78 @@ def test_norms_keep_a_bad_row_to_itself(dtype):
 
 
 # -------------------------------------------------------------------------------------------- loss
+
+def _infinite_case(T, d, V, dtype, seed):
+    """Hidden states whose first value is 1, so that a word's first weight is added to its logit."""
+    h, w, target, dloss = B.loss_data(T, d, V, dtype, 0.0, seed, scale=2.0 / d ** 0.5)
+    h[:, 0] = 1.0
+    return h, w, np.random.default_rng(seed).integers(0, V, T).astype(np.int32), dloss
+
+
+def _forward(h, w, target, dtype):
+    (T, d), V = h.shape, w.shape[0]
+    loss, lse = B.empty(T), B.empty(T)
+    ws = B.ws_of(L.moe_vocab_loss_workspace_size(T, d, V, B.DT[dtype]))
+    L.moe_vocab_loss(dev_tensor(h, dtype), dev_tensor(w, dtype), torch.from_numpy(target).to(DEV), T, d, V, B.DT[dtype], loss,
+                     lse, ws, ws.numel())
+    return tnp(loss).astype(np.float64), tnp(lse).astype(np.float64)
+
+
+@pytest.mark.parametrize("T,d,V,dtype,tile", FORWARD)
+def test_words_of_minus_infinity_add_nothing(T, d, V, dtype, tile):
+    """Words masked by a logit of -inf, whole groups of them among them: the sums are those of the others."""
+    log(f"vocab loss {dtype}: words of -inf T={T} d={d} V={V}")
+    h, w, target, _ = _infinite_case(T, d, V, dtype, 3)
+    masked = np.zeros(V, bool)
+    masked[[0, 1, 77]] = masked[128:384] = masked[V - 150:] = True
+    target[masked[target]] = 6
+    target[:3] = [5, 0, -100]   # the second: a masked target has an infinite loss
+    wm = w.copy()
+    wm[masked, 0] = -np.inf
+    loss, lse = _forward(h, wm, target, dtype)
+    keep = np.nonzero(~masked)[0]
+    to = np.full(V, -100)
+    to[keep] = np.arange(len(keep))
+    ref_target = np.where(target >= 0, to[np.clip(target, 0, V - 1)], -100)
+    ref, ref_lse = S.vocab_loss(h, w[keep], ref_target)
+    e_l = 2 * d * U * (np.abs(h.astype(np.float64)) @ np.abs(w[keep].astype(np.float64)).T).max(axis=1)
+    e_lse = e_l + 2.0 ** -20 + 4 * U * np.abs(ref_lse)
+    B.within("lse", lse, ref_lse, e_lse)
+    assert loss[1] == np.inf and loss[2] == 0
+    rows = np.arange(T) != 1
+    B.within("loss", loss[rows], ref[rows], (2 * e_lse + 4 * U * np.abs(ref))[rows])
+
+
+@pytest.mark.parametrize("T,d,V,dtype,tile", FORWARD)
+def test_infinite_and_nan_logits(T, d, V, dtype, tile):
+    """A logit of +inf makes the row's sum infinite, words that are all -inf make it -inf, NaN stays NaN:
+    in the rows that have them alone, and never where there is no loss."""
+    log(f"vocab loss {dtype}: infinite logits T={T} d={d} V={V}")
+    h, w, target, _ = _infinite_case(T, d, V, dtype, 4)
+    target[:3] = [5, 6, -100]
+    target[3:][target[3:] == 5] = 6
+    good, good_lse = _forward(h, w, target, dtype)
+    up = w.copy()
+    up[5, 0] = np.inf
+    loss, lse = _forward(h, up, target, dtype)
+    assert np.all(lse == np.inf) and np.isnan(loss[0]) and loss[2] == 0
+    rest = np.arange(T) > 2
+    assert np.all(loss[rest & (target >= 0)] == np.inf)
+    down = w.copy()
+    down[:, 0] = -np.inf
+    loss, lse = _forward(h, down, target, dtype)
+    assert np.all(lse == -np.inf) and np.isnan(loss[0]) and loss[2] == 0
+    hn = h.copy()
+    hn[4, 2] = np.nan
+    loss, lse = _forward(hn, w, target, dtype)
+    assert np.isnan(lse[4]) and np.isnan(loss[4])
+    rest = np.arange(T) != 4
+    assert np.array_equal(lse[rest], good_lse[rest]) and np.array_equal(loss[rest], good[rest])
+    wn = w.copy()
+    wn[7, 1] = np.nan
+    loss, lse = _forward(h, wn, target, dtype)
+    assert np.isnan(lse).all() and loss[2] == 0
+
 
 @pytest.mark.parametrize("T,d,V,dtype", [(300, 64, 700, "f32"), (300, 64, 700, "bf16"), (1500, 256, 16421, "bf16")])
 def test_gradient_of_a_nan_row_stays_in_the_row(T, d, V, dtype):
