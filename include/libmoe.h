@@ -423,9 +423,10 @@ moe_status_t moe_grad_norm(const moe_grad_t* grads, int32_t count, double* sumsq
                            size_t ws_bytes, moe_stream_t stream);
 /* out = c grad with c = min(1, max_norm / (sqrt(sumsq) + 1e-6)) in fp32, rounded once; sumsq [1]
  * double INPUT: from moe_grad_norm, after a sum over ranks where the gradients are sharded.  When c
- * is 1, out is a copy (nothing is written in place).  An infinite or NaN norm scales nothing (c = 1):
- * read the norm and skip the step.  norm [1] float OUTPUT or NULL.  max_norm > 0.  An out may overlap
- * no other tensor of the list (MOE_ERR_INVALID_VALUE), so no tensor is scaled twice. */
+ * is 1, out is a copy (nothing is written in place).  A norm that is infinite or NaN as the float that
+ * is reported (of finite gradients, from 3.4e38 on) scales nothing (c = 1): read the norm and skip the
+ * step.  norm [1] float OUTPUT or NULL.  max_norm > 0.  An out may overlap no other tensor of the list
+ * (MOE_ERR_INVALID_VALUE), so no tensor is scaled twice. */
 moe_status_t moe_grad_scale(const moe_grad_t* grads, int32_t count, const double* sumsq, float max_norm,
                             float* norm, moe_stream_t stream);
 /* Both: clip to a global norm of max_norm.  norm [1] float OUTPUT or NULL (the norm before clipping). */

@@ -146,8 +146,8 @@ __global__ __launch_bounds__(NT) void grad_scale_kernel(GradTable t, long long c
   const double norm = sqrt(sum_partials(sums, count, red));
   if (norm_out && t.base == 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   const double q = (double)max_norm / (norm + 1e-6);
-  // a norm that is infinite or NaN scales nothing
-  const float c = q < 1.0 && norm <= 1.7976931348623157e308 ? (float)q : 1.0f;
+  // A norm that is infinite or NaN as it is reported, in fp32, scales nothing: 3.4e38 < norm < 1e308 too
+  const float c = q < 1.0 && (float)norm <= 3.4028234664e38f ? (float)q : 1.0f;
   const Chunk k = find_chunk(t, blockIdx.x, chunk);
   if (c == 1.0f && t.out[k.tensor] == t.grad[k.tensor]) return;
   const long long part = chunk / gridDim.y, at = (long long)(gridDim.y - 1 - blockIdx.y) * part;

@@ -92,5 +92,6 @@ def grad_norm(grads):
 
 def clip(grads, max_norm):
     norm = grad_norm(grads)
-    c = min(1.0, max_norm / (norm + 1e-6)) if np.isfinite(norm) else 1.0
+    with np.errstate(over="ignore"):
+        c = min(1.0, max_norm / (norm + 1e-6)) if np.isfinite(np.float32(norm)) else 1.0   # as the norm is reported
     return [np.asarray(g, D) * c for g in grads], norm

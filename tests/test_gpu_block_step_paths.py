@@ -148,6 +148,24 @@ def test_gradient_of_a_nan_row_stays_in_the_row(T, d, V, dtype):
 
 # ---------------------------------------------------------------------------------------- clipping
 
+def test_clip_scales_nothing_where_the_reported_norm_is_infinite():
+    """Finite gradients whose norm is beyond fp32: reported as infinite, so nothing is scaled; one just
+    inside is scaled."""
+    log("clip: norms about fp32's range")
+    for vals, infinite in (([3e38, -3e38], True), ([2e38, 2e38], False)):
+        v = B.f32(vals)
+        outs, norm = B._clip_once([v], 1e30)
+        lst = L.grad_list([v.clone()])
+        sumsq, norm2, ws = torch.zeros(1, dtype=torch.float64, device=DEV), B.empty(1), B.ws_of(L.moe_grad_workspace_size(lst))
+        L.moe_grad_norm(lst, sumsq, norm2, ws, ws.numel())
+        L.moe_grad_scale(lst, sumsq, 1e30, None)
+        assert np.isinf(norm) == np.isinf(float(norm2)) == infinite
+        assert torch.equal(outs[0], lst.tensors[0][0])
+        ref, _ = S.clip([tnp(v)], float(np.float32(1e30)))
+        B.within("out", tnp(outs[0]), ref[0], 4 * U * np.abs(ref[0]))
+        assert torch.equal(outs[0], v) == infinite
+
+
 @pytest.mark.parametrize("max_norm", [0.5, 1e9])
 def test_clip_of_long_chunks(max_norm):
     """More than 63 M values, so chunks of at least 32768, scaled in eighths, with tensors that end inside

@@ -113,3 +113,10 @@ def test_clip_hand_values():
     assert norm == 5.0 and np.allclose([got[0][0], got[1][0]], [0.6, 0.8], atol=1e-6)
     got, norm = S.clip([[np.inf], [4.0]], 1.0)   # nothing is scaled
     assert np.isinf(norm) and got[1][0] == 4.0
+
+
+def test_clip_of_a_norm_beyond_fp32():
+    got, norm = S.clip([[3e38, -3e38]], 1.0)   # reported in fp32 as infinite: nothing is scaled
+    assert norm > 4e38 and got[0].tolist() == [3e38, -3e38]
+    got, norm = S.clip([[2e38, 2e38]], 1e30)
+    assert np.allclose(got[0], 1e30 / np.sqrt(2), rtol=1e-12)
