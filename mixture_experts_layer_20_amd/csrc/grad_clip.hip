@@ -202,10 +202,14 @@ long long chunk_size(long long total) {
   return std::max<long long>(4096, (c + 2047) / 2048 * 2048);
 }
 
-// A list whose chunks are this long (64 M elements) is scaled in eighths of chunks, after a launch of
-// its own has added the partial sums; in a shorter one every workgroup adds them itself (16 KB from
-// the L2 cache), which a launch would take longer to do.
+// A list whose chunks are this long (64 M elements) is scaled in eighths of chunks.
 constexpr long long LONG_CHUNK = 32768;
+// The partial sums of such a list, or more than this many (a tensor has one at least), are added by a
+// launch of their own; otherwise every scaling workgroup adds them itself, at most 18 KB from the L2
+// cache.  Whole calls with and without that launch (us): 300 tensors of 1500 values 21 and 20, 1500 of
+// 4000 99 and 101, 2500 of 1500 110 and 125, 10000 of 1500 579 and 814, 40000 of 1500 3280 and 6617:
+// what the workgroups read grows with the square of the number of tensors.
+constexpr int MOST_SUMS = 2304;
 constexpr int PARTS = 8;   // a chunk is a multiple of 2048 elements: a part starts at 16 bytes
 
 }  // namespace
@@ -270,7 +274,7 @@ hipError_t launch_grad_scale(const GradItem* g, int count, double* sums, int nsu
                              hipStream_t s) {
   const long long chunk = chunk_size(total_elements(g, count));
   const bool parts = chunk >= LONG_CHUNK;
-  if (parts && nsums > 1) {
+  if (nsums > 1 && (parts || nsums > MOST_SUMS)) {
     const hipError_t e = launch_grad_total(sums, nsums, sums + nsums, nullptr, s);
     if (e != hipSuccess) return e;
     sums += nsums;

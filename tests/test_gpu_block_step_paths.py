@@ -1,6 +1,6 @@
 """Paths of the block norms, the vocabulary loss and gradient clipping that sizes, lists and values choose:
-wide rows with partial column sums, lists of long chunks, infinities and NaN, and the block norms with each of the layer's
-options."""
+wide rows with partial column sums, lists of long chunks and of many tensors, infinities and NaN, and the
+block norms with each of the layer's options."""
 import numpy as np
 import pytest
 import torch
@@ -164,6 +164,34 @@ def test_clip_scales_nothing_where_the_reported_norm_is_infinite():
         ref, _ = S.clip([tnp(v)], float(np.float32(1e30)))
         B.within("out", tnp(outs[0]), ref[0], 4 * U * np.abs(ref[0]))
         assert torch.equal(outs[0], v) == infinite
+
+
+def test_clip_of_thousands_of_tensors_adds_the_sums_once():
+    """A partial sum for each tensor: where there are thousands, a launch of its own adds them (its total
+    lies behind them in the workspace) instead of every scaling workgroup."""
+    log("clip: 5000 tensors")
+    n = 5000
+    flat = torch.randn(4 * n, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    out = torch.full_like(flat, float("nan"))
+    views = lambda f: [f[4 * i:4 * i + 3] for i in range(n)]
+    lst = L.grad_list(views(flat), views(out))
+    size = L.moe_grad_workspace_size(lst)
+    assert size >= 8 * (n + 1)
+    ws, norm = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV), B.empty(1)
+    L.moe_grad_clip(lst, 0.5, norm, ws, size)
+    v = flat.view(n, 4)[:, :3].double()
+    ref = float(v.square().sum().sqrt())
+    B.within("norm", tnp(norm), [ref], 2 * U * ref)
+    B.within("out", tnp(out.view(n, 4)[:, :3]), (v * (0.5 / (ref + 1e-6))).cpu().numpy(), 4 * U * np.abs(v.cpu().numpy()) * 0.5 / ref)
+    assert bool(torch.isnan(out.view(n, 4)[:, 3]).all())
+    total = float(ws[8 * n:8 * n + 8].view(torch.float64))
+    assert abs(total - ref ** 2) <= 1e-12 * ref ** 2
+    sumsq, norm2 = torch.zeros(1, dtype=torch.float64, device=DEV), B.empty(1)
+    again = torch.full_like(flat, float("nan"))
+    lst2 = L.grad_list(views(flat), views(again))
+    L.moe_grad_norm(lst2, sumsq, norm2, ws, size)
+    L.moe_grad_scale(lst2, sumsq, 0.5, None)
+    assert torch.equal(norm, norm2) and torch.equal(out.nan_to_num(7.0), again.nan_to_num(7.0))
 
 
 @pytest.mark.parametrize("max_norm", [0.5, 1e9])
