@@ -185,22 +185,58 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _stream(stream, lead=None) -> int | None:
-    """The stream's handle, by default the current device's current one; ``lead``: a tensor of the call,
-    which must then be on that device (a kernel that got host memory or another device's would fault)."""
+class _Public:
+    """torch's public functions for what _device has."""
+    _cuda_getDevice = staticmethod(torch.cuda.current_device)
+    _cuda_getCurrentRawStream = staticmethod(lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+# The current device and its current stream's handle alone: the public functions cost 0.3 and 3 us a call,
+# against 3 us for a launch.  A torch that has no such functions is served by the public ones.
+_device = torch._C if hasattr(torch._C, "_cuda_getCurrentRawStream") else _Public
+
+
+def _stream(stream) -> int | None:
+    """The stream's handle, by default the current device's current one."""
     if stream is None:
         if torch.cuda.is_initialized():
-            # the handle alone: a Stream object costs 3 us a call, as much as a launch
-            dev = torch._C._cuda_getDevice()
-            if lead is not None and not isinstance(lead, int) and lead.get_device() != dev:
-                raise ValueError(f"a tensor on {lead.device}, but the current device is cuda:{dev}")
-            return torch._C._cuda_getCurrentRawStream(dev)
+            return _device._cuda_getCurrentRawStream(_device._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _place(stream, tensors, grads=None):
+    """The stream's handle and the tensors' addresses.  Every tensor, and the list of gradients, must be on
+    the stream's device: by default the current device and its current stream; for a handle, whose device
+    is not known, the one that the first of them is on.  (A kernel that got host memory or another
+    device's would fault.)"""
+    dev, what = None, "call"   # None: no device to check for
+    if stream is None:
+        if torch.cuda.is_initialized() or torch.cuda.is_available():
+            dev, what = _device._cuda_getDevice(), "current device"
+    elif not isinstance(stream, int):
+        dev, stream = getattr(stream, "device_index", None), stream.cuda_stream
+    elif torch.cuda.is_initialized():
+        held = [getattr(grads, "device", None)] + [t.get_device() for t in tensors if isinstance(t, torch.Tensor)]
+        dev = next((on for on in held if on is not None), None)
+        if dev is not None and dev < 0:
+            raise ValueError("libmoe takes device memory, got a tensor on the host")
+    if grads is not None and dev is not None and getattr(grads, "device", None) not in (None, dev):
+        raise ValueError(f"gradients on {grads.tensors[0][0].device}, but the {what} is cuda:{dev}")
+    out = []
+    for t in tensors:
+        if t is not None and t.__class__ is not int:
+            if t.get_device() != dev and dev is not None:
+                raise ValueError(f"a tensor on {t.device}, but the {what} is cuda:{dev}")
+            if not t.is_contiguous():
+                raise ValueError("libmoe takes contiguous tensors only")
+            t = t.data_ptr()
+        out.append(t)
+    return stream if what == "call" else _device._cuda_getCurrentRawStream(dev), out
+
+
 def _call(name: str, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_LIB or lib(), name)(*args)
     if st != MOE_OK:
         raise MoEError(st, name, last_error())
 
@@ -366,18 +402,21 @@ def moe_router_aux_bwd(logits, load_frac, x, w_router, T, d, E, weight, dt, dw_r
 
 
 def moe_norm_in(x, w, T, d, eps, dt, xn, rstd, stream=None):
-    _call("moe_norm_in", _ptr(x), _ptr(w), T, d, eps, dt, _ptr(xn), _ptr(rstd), _stream(stream, x))
+    s, (x, w, xn, rstd) = _place(stream, (x, w, xn, rstd))
+    _call("moe_norm_in", x, w, T, d, eps, dt, xn, rstd, s)
 
 
 def moe_norm_out(y, x, w, gate, gate_rows, res_scale, eps, T, d, dt, out, rstd, stream=None):
-    _call("moe_norm_out", _ptr(y), _ptr(x), _ptr(w), _ptr(gate), gate_rows, res_scale, eps, T, d, dt, _ptr(out),
-          _ptr(rstd), _stream(stream, y))
+    s, (y, x, w, gate, out, rstd) = _place(stream, (y, x, w, gate, out, rstd))
+    _call("moe_norm_out", y, x, w, gate, gate_rows, res_scale, eps, T, d, dt, out, rstd, s)
 
 
 def moe_combine_norm_out(y_perm, topk_gate, dest_pos, shared_out, x, w, gate, gate_rows, res_scale, eps, T, d, k, dt,
                          y, out, rstd, stream=None):
-    _call("moe_combine_norm_out", _ptr(y_perm), _ptr(topk_gate), _ptr(dest_pos), _ptr(shared_out), _ptr(x), _ptr(w),
-          _ptr(gate), gate_rows, res_scale, eps, T, d, k, dt, _ptr(y), _ptr(out), _ptr(rstd), _stream(stream, y_perm))
+    s, (y_perm, topk_gate, dest_pos, shared_out, x, w, gate, y, out, rstd) = _place(
+        stream, (y_perm, topk_gate, dest_pos, shared_out, x, w, gate, y, out, rstd))
+    _call("moe_combine_norm_out", y_perm, topk_gate, dest_pos, shared_out, x, w, gate, gate_rows, res_scale, eps, T, d, k,
+          dt, y, out, rstd, s)
 
 
 def moe_norm_bwd_workspace_size(T, d) -> int:
@@ -385,13 +424,13 @@ def moe_norm_bwd_workspace_size(T, d) -> int:
 
 
 def moe_norm_out_bwd(dout, y, w, gate, gate_rows, rstd, T, d, dt, dy, dw, dgate, ws, ws_bytes, stream=None):
-    _call("moe_norm_out_bwd", _ptr(dout), _ptr(y), _ptr(w), _ptr(gate), gate_rows, _ptr(rstd), T, d, dt, _ptr(dy),
-          _ptr(dw), _ptr(dgate), _ptr(ws), ws_bytes, _stream(stream, dout))
+    s, (dout, y, w, gate, rstd, dy, dw, dgate, ws) = _place(stream, (dout, y, w, gate, rstd, dy, dw, dgate, ws))
+    _call("moe_norm_out_bwd", dout, y, w, gate, gate_rows, rstd, T, d, dt, dy, dw, dgate, ws, ws_bytes, s)
 
 
 def moe_norm_in_bwd(dxn, x, w, rstd, dres, res_scale, T, d, dt, dx, dw, ws, ws_bytes, stream=None):
-    _call("moe_norm_in_bwd", _ptr(dxn), _ptr(x), _ptr(w), _ptr(rstd), _ptr(dres), res_scale, T, d, dt, _ptr(dx),
-          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream, dxn))
+    s, (dxn, x, w, rstd, dres, dx, dw, ws) = _place(stream, (dxn, x, w, rstd, dres, dx, dw, ws))
+    _call("moe_norm_in_bwd", dxn, x, w, rstd, dres, res_scale, T, d, dt, dx, dw, ws, ws_bytes, s)
 
 
 def moe_vocab_loss_workspace_size(T, d, V, dt) -> int:
@@ -399,8 +438,8 @@ def moe_vocab_loss_workspace_size(T, d, V, dt) -> int:
 
 
 def moe_vocab_loss(h, w, target, T, d, V, dt, loss, lse, ws, ws_bytes, stream=None):
-    _call("moe_vocab_loss", _ptr(h), _ptr(w), _ptr(target), T, d, V, dt, _ptr(loss), _ptr(lse), _ptr(ws), ws_bytes,
-          _stream(stream, h))
+    s, (h, w, target, loss, lse, ws) = _place(stream, (h, w, target, loss, lse, ws))
+    _call("moe_vocab_loss", h, w, target, T, d, V, dt, loss, lse, ws, ws_bytes, s)
 
 
 def moe_vocab_loss_plan(T, d, V, dt) -> VocabLossPlan:
@@ -414,8 +453,8 @@ def moe_vocab_loss_bwd_workspace_size(T, d, V, dt) -> int:
 
 
 def moe_vocab_loss_bwd(h, w, target, lse, dloss, T, d, V, dt, dh, dw, ws, ws_bytes, stream=None):
-    _call("moe_vocab_loss_bwd", _ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), T, d, V, dt, _ptr(dh),
-          _ptr(dw), _ptr(ws), ws_bytes, _stream(stream, h))
+    s, (h, w, target, lse, dloss, dh, dw, ws) = _place(stream, (h, w, target, lse, dloss, dh, dw, ws))
+    _call("moe_vocab_loss_bwd", h, w, target, lse, dloss, T, d, V, dt, dh, dw, ws, ws_bytes, s)
 
 
 class GradList:
@@ -435,6 +474,7 @@ class GradList:
         self.ptr = ctypes.cast(self.array, _P)
         if len({t.device for s in self.tensors for t in s if t is not None}) > 1:
             raise ValueError("the tensors are on different devices")
+        self.device = self.tensors[0][0].get_device() if self.count else None   # -1: the host
 
 
 def grad_list(grads, outs=None) -> GradList:
@@ -443,26 +483,23 @@ def grad_list(grads, outs=None) -> GradList:
     return GradList(grads, grads if outs is None else outs)
 
 
-def _lead(grads):
-    return grads.tensors[0][0] if grads.count and isinstance(grads, GradList) else None
-
-
 def moe_grad_workspace_size(grads: GradList) -> int:
     return lib().moe_grad_workspace_size(grads.ptr, grads.count)
 
 
 def moe_grad_norm(grads: GradList, sumsq, norm, ws, ws_bytes, stream=None):
-    _call("moe_grad_norm", grads.ptr, grads.count, _ptr(sumsq), _ptr(norm), _ptr(ws), ws_bytes,
-          _stream(stream, _lead(grads)))
+    s, (sumsq, norm, ws) = _place(stream, (sumsq, norm, ws), grads)
+    _call("moe_grad_norm", grads.ptr, grads.count, sumsq, norm, ws, ws_bytes, s)
 
 
 def moe_grad_scale(grads: GradList, sumsq, max_norm, norm, stream=None):
-    _call("moe_grad_scale", grads.ptr, grads.count, _ptr(sumsq), max_norm, _ptr(norm), _stream(stream, _lead(grads)))
+    s, (sumsq, norm) = _place(stream, (sumsq, norm), grads)
+    _call("moe_grad_scale", grads.ptr, grads.count, sumsq, max_norm, norm, s)
 
 
 def moe_grad_clip(grads: GradList, max_norm, norm, ws, ws_bytes, stream=None):
-    _call("moe_grad_clip", grads.ptr, grads.count, max_norm, _ptr(norm), _ptr(ws), ws_bytes,
-          _stream(stream, _lead(grads)))
+    s, (norm, ws) = _place(stream, (norm, ws), grads)
+    _call("moe_grad_clip", grads.ptr, grads.count, max_norm, norm, ws, ws_bytes, s)
 
 
 def moe_mx_quantize_rows(x, R, K, ldx, codes, scales, stream=None):

@@ -226,3 +226,66 @@ def test_clipping_workspace_is_made_once_when_it_is_needed(monkeypatch):
     (grads, _, norm, ws, n), second = calls[0], calls[1]
     assert ws.numel() == n >= L.moe_grad_workspace_size(grads) and norm is lay.grad_norm
     assert second[3] is ws and set(lay.bufs.t) == before
+
+
+class OnDevice(torch.Tensor):
+    """A tensor that says it is on device 1, with an address that nothing reads."""
+
+    @staticmethod
+    def __new__(cls):
+        return torch.Tensor._make_subclass(cls, torch.zeros(64))
+
+    def get_device(self):
+        return 1
+
+    def data_ptr(self):
+        return FAKE
+
+
+def _calls(t, grads):
+    """Each call over the tensors ``t`` (a function of a tensor's place in the call), and how many it takes."""
+    return [(4, lambda s: L.moe_norm_in(t(0), t(1), 8, 8, 0.0, F32, t(2), t(3), s)),
+            (6, lambda s: L.moe_norm_out(t(0), t(1), t(2), t(3), 1, 1.0, 0.0, 8, 8, F32, t(4), t(5), s)),
+            (10, lambda s: L.moe_combine_norm_out(t(0), t(1), t(2), t(3), t(4), t(5), t(6), 1, 1.0, 0.0, 8, 8, 1, F32, t(7),
+                                                  t(8), t(9), s)),
+            (9, lambda s: L.moe_norm_out_bwd(t(0), t(1), t(2), t(3), 1, t(4), 8, 8, F32, t(5), t(6), t(7), t(8), 1 << 20, s)),
+            (8, lambda s: L.moe_norm_in_bwd(t(0), t(1), t(2), t(3), t(4), 1.0, 8, 8, F32, t(5), t(6), t(7), 1 << 20, s)),
+            (6, lambda s: L.moe_vocab_loss(t(0), t(1), t(2), 8, 8, 8, F32, t(3), t(4), t(5), 1 << 20, s)),
+            (8, lambda s: L.moe_vocab_loss_bwd(t(0), t(1), t(2), t(3), t(4), 8, 8, 8, F32, t(5), t(6), t(7), 1 << 20, s)),
+            (3, lambda s: L.moe_grad_norm(grads, t(0), t(1), t(2), 1 << 20, s)),
+            (2, lambda s: L.moe_grad_scale(grads, t(0), 1.0, t(1), s)),
+            (2, lambda s: L.moe_grad_clip(grads, 1.0, t(0), t(1), 1 << 20, s))]
+
+
+class FakeStream:
+    device_index, cuda_stream = 1, 0
+
+
+@pytest.mark.parametrize("stream,initialized", [(None, True), (None, False), (FakeStream(), True), (FakeStream(), False),
+                                                (64, True)])
+def test_every_tensor_of_a_call_must_be_on_its_device(monkeypatch, stream, initialized):
+    """One tensor of the call on the host, each in turn, with the stream by default (also before anything
+    used the device), given, or given as a handle: refused before libmoe is called."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: initialized)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    reached = []
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(L, "_call", lambda name, *a: reached.append(name))
+    host, device, grads = torch.zeros(64), OnDevice(), L.grad_list([OnDevice()])
+    off = [None]
+    t = lambda i: host if i == off[0] else device
+    for n, call in _calls(t, grads):
+        off[0] = None
+        call(stream)
+        assert reached.pop()
+        for off[0] in range(n):
+            with pytest.raises(ValueError):
+                call(stream)
+            assert not reached
+    off[0] = None
+    for n, call in _calls(t, L.grad_list([torch.zeros(64)]))[-3:]:
+        with pytest.raises(ValueError):
+            call(stream)
+        assert not reached
