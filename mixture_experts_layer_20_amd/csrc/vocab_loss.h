@@ -58,10 +58,10 @@ long long tile_count(int M, int N, bool large);
 int tile_splits(int M, int N, int K, bool large);
 size_t tile_acc_bytes(int M, int N, int K, bool large);
 int tile_ks(int mode, const VocabArgs& p, bool bf16);
-hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s);
+hipError_t launch_tile(int mode, const VocabArgs& p, bool bf16, hipStream_t s);   // VL_DH, VL_DW: bf16
 // VL_DH and VL_DW in one launch, and the joins that they need (dh's after the last piece).
 hipError_t launch_tile_pair(const VocabArgs& p, bool bf16, hipStream_t s);
-hipError_t launch_tile_join(const VocabArgs& p, bool bf16, hipStream_t s);   // dh's
+hipError_t launch_tile_join(const VocabArgs& p, hipStream_t s);   // dh's, of a bf16 VL_DH launched alone
 
 }  // namespace vocab
 }  // namespace moe

@@ -307,7 +307,7 @@ hipError_t loss_bwd(VocabArgs p, void* ws, hipStream_t s) {
       e = launch_product(tiles.dh, VL_DH, p, bf16, s);
       if (e == hipSuccess) e = launch_product(tiles.dw, VL_DW, p, bf16, s);
       p.large = tiles.dh == LARGE;
-      if (e == hipSuccess && p.last) e = tiles.dh == PIPE ? launch_pipe_join(p, s) : launch_tile_join(p, bf16, s);
+      if (e == hipSuccess && p.last) e = tiles.dh == PIPE ? launch_pipe_join(p, s) : launch_tile_join(p, s);
     }
     if (e != hipSuccess) return e;
   }

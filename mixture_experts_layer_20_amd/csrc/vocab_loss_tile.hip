@@ -524,13 +524,14 @@ hipError_t launch(const VocabArgs& p, hipStream_t s) {
   return launch_join(join_dw<T>(p, c), Join<T>{}, p.scale, s);
 }
 
+// dh or dw alone: bf16, where the other one takes the 256x256 tiles.
 template <typename T>
 hipError_t launch_mode(int mode, const VocabArgs& p, hipStream_t s) {
-  switch (mode) {
-    case VL_STATS: return launch<T, VL_STATS>(p, s);
-    case VL_GRAD: return launch<T, VL_GRAD>(p, s);
-    case VL_DH: return launch<T, VL_DH>(p, s);
-    case VL_DW: return launch<T, VL_DW>(p, s);
+  if (mode == VL_STATS) return launch<T, VL_STATS>(p, s);
+  if (mode == VL_GRAD) return launch<T, VL_GRAD>(p, s);
+  if constexpr (sizeof(T) == 2) {
+    if (mode == VL_DH) return launch<T, VL_DH>(p, s);
+    if (mode == VL_DW) return launch<T, VL_DW>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -572,8 +573,8 @@ hipError_t launch_tile_pair(const VocabArgs& p, bool bf16, hipStream_t s) {
   return bf16 ? launch_both<bf16_t>(p, s) : launch_both<float>(p, s);
 }
 
-hipError_t launch_tile_join(const VocabArgs& p, bool bf16, hipStream_t s) {
-  return bf16 ? launch_join(join_dh<bf16_t>(p), Join<bf16_t>{}, p.scale, s) : launch_join(join_dh<float>(p), Join<float>{}, p.scale, s);
+hipError_t launch_tile_join(const VocabArgs& p, hipStream_t s) {
+  return launch_join(join_dh<bf16_t>(p), Join<bf16_t>{}, p.scale, s);
 }
 
 }  // namespace vocab
