@@ -34,6 +34,7 @@ PLANS = [
     (4827, 80, 15695, "f32", 128, 128, 128, True, True, True),
 ]
 
-# T, d, V, dtype and the forward's tiles.
+# T, d, V, dtype and the forward's tiles.  The last two: at most 64 tokens against 128 MB of words, read
+# past the caches.
 FORWARD = [(40, 64, 1000, "bf16", 64), (40, 64, 1000, "f32", 64), (200, 72, 700, "bf16", 64), (1010, 1000, 3990, "bf16", 128),
-           (1990, 512, 3990, "f32", 128), (700, 200, 16421, "bf16", 256)]
+           (1990, 512, 3990, "f32", 128), (700, 200, 16421, "bf16", 256), (7, 2048, 33001, "bf16", 64), (50, 2048, 16421, "f32", 64)]
