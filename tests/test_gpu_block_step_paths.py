@@ -266,3 +266,31 @@ def test_block_norm_with_the_layers_options(kw):
     for g, o in zip(normed.gradients(), before):
         half = HALF["bf16" if g.dtype == torch.bfloat16 else "f32"]
         assert bool(((g.double() - o.double() / 2).abs() <= (half + 4 * U + 1e-6 / norm) * o.double().abs() / 2 + 2.0 ** -133).all())
+
+
+def test_clipping_first_called_inside_a_graph():
+    """The workspace of clip_gradients made while a graph is captured serves the replays and eager calls."""
+    log("clip_gradients first called in a capture")
+    cfg, vals, extra, params, head, target = B.block_case(gate_rows=64)
+    eager, lay = (LY.MoELayer(cfg, params, block_norm=True, gate_rows=64) for _ in range(2))
+    dout = torch.randn(cfg.T, cfg.d, device=DEV, generator=torch.Generator(device=DEV).manual_seed(4)).to(torch.bfloat16)
+
+    def step(l):
+        l.forward()
+        l.backward(dout)
+        l.clip_gradients(0.01)
+
+    step(eager)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(lay)
+    for i in range(3):
+        for run in (graph.replay, lambda: step(lay)):
+            for g in lay.gradients() + [lay.grad_norm]:
+                g.fill_(float("nan"))
+            torch.cuda.synchronize()
+            run()
+            torch.cuda.synchronize()
+            assert torch.equal(lay.grad_norm, eager.grad_norm)
+            assert all(torch.equal(a, b) for a, b in zip(lay.gradients(), eager.gradients())), i
