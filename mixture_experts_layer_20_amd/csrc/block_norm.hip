@@ -14,7 +14,8 @@
 //
 // Bound by memory.  A row lies in the registers of a wave (d <= 1024), else of a workgroup of up to
 // 1024 lanes, from its loads to its stores, so each tensor passes once.  8192 x 4096 bf16, top-4 and a
-// shared expert: before 21 us (134 MB, 6.3 TB/s), combine and after 72 us (470 MB, 6.5 TB/s).
+// shared expert: before 21 us (134 MB, 6.3 TB/s), combine and after 73 us (470 MB, 6.4 TB/s), with the
+// combined rows kept for the backward 89 us (537 MB, 6.0 TB/s; 97 us for as many bytes at 16384 x 2048).
 // 16384 x 2048 bf16: before 24 us, after 35 us (201 MB, 5.7 TB/s), their backward 44 us (268 MB, 6.1
 // TB/s) and 33 us (201 MB, 6.1 TB/s) and 6.4 us each for the join of the column sums.  A device copy
 // moves 5.1 TB/s; what is above it comes from the last-level cache.

@@ -18,8 +18,8 @@
 // normal data take 3.38 ms (1300 TFLOP/s, the matrix cores busy for 74%), of all-zero data 2.61 ms; a
 // library product of the same operands, which writes the logits instead of reading them off, takes
 // 3.04 and 2.32 ms.  Of the 3.38 ms some 0.10 are outside the K loop.  P, dh and dw of a piece of 8192
-// words: 0.446, 0.451 and 0.424 ms (1230, 1220 and 1300 TFLOP/s).  At 1031 x 1000 x 50021 a quarter of
-// the tiles' rows is empty and the four products take 114-152 us each (680-910 TFLOP/s).
+// words: 0.446, 0.451 and 0.424 ms (1230, 1220 and 1300 TFLOP/s).  At 1031 x 1000 x 50021 a fifth of
+// the tiles' rows is empty and the four products take 133-169 us each (610-780 TFLOP/s).
 #include "vocab_loss.h"
 
 #include <algorithm>

@@ -294,3 +294,16 @@ def test_clipping_first_called_inside_a_graph():
             torch.cuda.synchronize()
             assert torch.equal(lay.grad_norm, eager.grad_norm)
             assert all(torch.equal(a, b) for a, b in zip(lay.gradients(), eager.gradients())), i
+
+
+def test_norms_of_the_largest_values_at_the_widest():
+    """Squares of 1e17 add up inside fp32's range at the largest width."""
+    log("norms: 16384 values of 1e17")
+    T, d = 3, 16384
+    x = (1e17 * np.sign(np.random.default_rng(2).standard_normal((T, d)))).astype(np.float32)
+    w = np.linspace(0.5, 2.0, d).astype(np.float32)
+    xn, r = B.empty(T, d), B.empty(T)
+    L.moe_norm_in(B.f32(x), B.f32(w), T, d, EPS, L.MOE_F32, xn, r)
+    ref, ref_r = S.norm_in(x, w, EPS)
+    B.within("rstd", tnp(r), ref_r, B.STAT * ref_r)
+    B.within("xn", tnp(xn), ref, (B.STAT + 4 * U) * np.abs(ref))
