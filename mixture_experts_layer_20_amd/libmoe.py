@@ -212,8 +212,10 @@ def _place(stream, tensors, grads=None):
     device's would fault.)"""
     dev, what = None, "call"   # None: no device to check for
     if stream is None:
-        if torch.cuda.is_initialized() or torch.cuda.is_available():
+        if torch.cuda.is_initialized():
             dev, what = _device._cuda_getDevice(), "current device"
+        elif torch.cuda.is_available():   # nothing has used the device yet: this does
+            dev, what = torch.cuda.current_device(), "current device"
     elif not isinstance(stream, int):
         dev, stream = getattr(stream, "device_index", None), stream.cuda_stream
     elif torch.cuda.is_initialized():
