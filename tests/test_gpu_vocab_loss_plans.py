@@ -109,3 +109,12 @@ def test_the_bound_shows_what_is_left_out():
     P[:, top] = 0
     with pytest.raises(AssertionError, match="dh"):
         check_loss(h, w, target, dloss, "bf16", (got[0], got[1], (P @ y).to(h.dtype), got[3]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,d,V", [(300, 65536, 700), (5, 65536, 9), (3, 8, 1 << 22), (1 << 22, 8, 64)])
+def test_vocab_loss_at_its_limits(T, d, V, dtype):
+    """The widest rows, the most words and the most tokens that the calls take."""
+    log(f"vocab loss limits {dtype} T={T} d={d} V={V}")
+    data = make_data(T, d, V, dtype, 11)
+    check_loss(*data, dtype, run_loss(*data, dtype))
