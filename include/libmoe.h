@@ -527,6 +527,145 @@ moe_status_t moe_mx_gemm_k(const uint8_t* a_codes, const uint8_t* a_scales, int6
                            moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------ */
+/* Routing by scores                                                                            */
+/* A router whose choice and gates are apart: the choice goes by scores plus a bias that keeps the
+ * experts' loads balanced and is moved by counts, not by a gradient; the gates go by the scores alone.
+ *   s = sigmoid(l) (MOE_SCORE_SIGMOID) or the softmax of the token's E logits (MOE_SCORE_SOFTMAX)
+ *   c = s + select_bias
+ *   Experts form `groups` runs of E / groups neighbours.  A group's score is the sum of its two largest c
+ *   (its only c where a group is one expert); the topk_groups best groups are open to the token.
+ *   topk_idx: the k largest c of the open groups, largest first.
+ *   gate_j = scale * s_j, or with renormalize = 1 scale * s_j / sum of the chosen s.
+ * The order is that of the exact values: without a bias c orders as the logits do, with one, and for the
+ * groups, it is decided in double wherever fp32 does not tell.  Of equal values the lower index comes
+ * first.  A NaN ranks after every number; whatever logits and bias hold, topk_idx has k different values
+ * in [0, E), and the gates of a token with a NaN or +inf are unspecified.  A logit of -inf is a score of
+ * 0; where every chosen score is 0 the gates are 0.  Scores of -inf from the bias shut an expert as long
+ * as k others are open.
+ * Source: "Olmo-core DDP MoE examples", "Other experiments in the report" (load-balancing experiments); the
+ * pages do not print the router: the formulas above are the reading. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/* x, w_router, logits, E <= 256, k <= 8, dt as for moe_route (w_router NULL: logits [T, E] float are an
+ * input, x is not read); select_bias [E] float or NULL; 1 <= topk_groups <= groups, groups divides E,
+ * k <= topk_groups * E / groups; scale finite.  topk_idx [T, k] int32, topk_gate [T, k] float OUTPUT. */
+moe_status_t moe_route_balanced(const void* x, const void* w_router, float* logits, const float* select_bias,
+                                int64_t T, int64_t d, int32_t E, int32_t k, int32_t groups, int32_t topk_groups,
+                                int32_t score, int32_t renormalize, float scale, moe_dtype_t dt, int32_t* topk_idx,
+                                float* topk_gate, moe_stream_t stream);
+
+/* Backward of the gates with respect to the logits, and through them to the router and its input.  dgate
+ * [T, k] float, logits [T, E] float and topk_idx [T, k] (of the forward call), offsets [E+1] and src_row
+ * [T*k] from moe_permute, x [T, d], w_router [E, d] (dt) INPUT:
+ *   dw_router = dL^T x  [E, d] float OUTPUT;   dx_router = dL w_router  [T, d] (dt) OUTPUT
+ * The choice carries no gradient, nor does the bias.  dL is zero outside the chosen experts, but for
+ * softmax scores with renormalize = 0, whose every logit has a gradient: that form needs d to be a
+ * multiple of 8.  Logits must be free of NaN and +inf.  Outputs must not overlap inputs. */
+size_t moe_route_balanced_bwd_workspace_size(int64_t T, int64_t d, int32_t E, int32_t k, int32_t score,
+                                             int32_t renormalize);
+moe_status_t moe_route_balanced_bwd(const float* dgate, const float* logits, const int32_t* topk_idx,
+                                    const int32_t* offsets, const int32_t* src_row, const void* x,
+                                    const void* w_router, int64_t T, int64_t d, int32_t E, int32_t k, int32_t score,
+                                    int32_t renormalize, float scale, moe_dtype_t dt, float* dw_router,
+                                    void* dx_router, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* After a step: bias_out[e] = bias[e] + rate * sign(mean count - counts[e]) (0 where they are equal).
+ * counts [E] int32 (from moe_permute, or summed over ranks and micro-batches), bias, bias_out [E] float;
+ * bias_out may be bias.  rate finite. */
+moe_status_t moe_route_bias_update(const int32_t* counts, int32_t E, float rate, const float* bias, float* bias_out,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Grouped products in 8-bit floating point with a float scale for each block of 128            */
+/* Next to MXFP8, whose scales are powers of two for 32 elements: E4M3 codes and one float scale for 128
+ * elements of a row (activations) or for 128 x 128 (weights).
+ *   scale = max(largest magnitude of the block, 2^-100) / 448
+ *   code  = E4M3(448 v / max(largest magnitude, 2^-100)), rounded to nearest, ties to even (exactly)
+ * A block that holds an infinity or a NaN gets a scale of NaN, and what is multiplied with it is NaN.
+ * A product is that of the matrices which codes and scales stand for: each block's 128 products are summed
+ * in fp32, scaled, and the blocks are added in fp32; outputs are bf16, rounded once.
+ * Source: the pages' 8-bit recipe ("Olmo-core DDP MoE examples", "Other experiments in the report") in the
+ * form with longer blocks. */
+
+/* x [R, K] bf16, row stride ldx (a multiple of 8, >= K), K a multiple of 128:
+ *   codes [R, K] uint8 OUTPUT;  scales [K / 128, R] float OUTPUT (the rows' scales of one block column lie
+ *   next to each other). */
+moe_status_t moe_fp8_quantize_rows(const void* x, int64_t R, int64_t K, int64_t ldx, uint8_t* codes, float* scales,
+                                   moe_stream_t stream);
+/* w [G, N, K] bf16, N and K multiples of 128: codes [G, N, K], scales [G, N / 128, K / 128] OUTPUT;
+ * codes_t [G, K, N], scales_t [G, K / 128, N / 128] OUTPUT or both NULL: the same transposed. */
+moe_status_t moe_fp8_quantize_weights(const void* w, int32_t G, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                                      uint8_t* codes_t, float* scales_t, moe_stream_t stream);
+
+/* Grouped product over ragged row ranges: C[m, n] = sum_k A[m, k] B_g[n, k] for rows m of group g =
+ * offsets[g] .. offsets[g+1]-1 (offsets [G+1] int32 device, non-decreasing, clamped to [0, M]; rows outside
+ * every group are not written).
+ *   a_codes [M, K], a_scales [K / 128, M] (moe_fp8_quantize_rows);
+ *   b_codes [G, N, K], b_scales [G, N / 128, K / 128] (moe_fp8_quantize_weights);
+ *   b2_codes, b2_scales: NULL, or with MOE_MX_EPI_SWIGLU the up-projection, as b; otherwise the columns
+ *   k >= b2_k of B ([G, N, K - b2_k], b then is [G, N, b2_k], b2_k a multiple of 128 in (0, K)): the
+ *   gate/up data gradient contracts [dA | dB] with W1 and W3;
+ *   epilogue, out0, out1, out2, aux0, aux1: as for moe_mx_gemm_rows.
+ * K and N must be multiples of 128.  Outputs must not overlap inputs.  ws: moe_fp8_gemm_workspace_size
+ * bytes (NULL allowed where that is 0; the size depends on the compute units of the current device). */
+size_t moe_fp8_gemm_workspace_size(int32_t G, int64_t M, int64_t N, int64_t K);
+moe_status_t moe_fp8_gemm_rows(const uint8_t* a_codes, const float* a_scales, const uint8_t* b_codes,
+                               const float* b_scales, const uint8_t* b2_codes, const float* b2_scales, int64_t b2_k,
+                               const int32_t* offsets, int32_t G, int64_t M, int64_t N, int64_t K, int32_t epilogue,
+                               void* out0, void* out1, void* out2, const void* aux0, const void* aux1, void* ws,
+                               size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* AdamW over a list of tensors                                                                 */
+/* The step that follows the gradients' norm, with the clipping in the same pass over the gradients:
+ *   g = c grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = (1 - lr weight_decay) p - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ * all in fp32.  c = 1 without sumsq; with it (moe_grad_norm) c = min(1, max_norm / (sqrt(sumsq) + 1e-6)),
+ * and a norm that is infinite as a float or NaN makes no step: every output is its input.
+ *   state_bits 32: m, v [n] float, scale NULL.
+ *   state_bits 8:  m, v [n] uint8, E4M3 codes of m and of sqrt(v); scale [2, ceil(n / 128)] float, m's and
+ *     then those of sqrt(v): a code stands for itself times its block's scale (largest magnitude / 448).
+ *     Rounded up or down at random with the right mean, a positive v not to zero.  The step uses m and v
+ *     before that.  A block that gets an infinity or a NaN gets a scale of NaN.
+ *   A bf16 parameter with a master copy is that copy, rounded to nearest, and not read; without one it is
+ *     rounded at random like the 8-bit states.  fp32 parameters have no master copy (NULL).
+ * Random bits are a function of seed, the tensor's place in the list and the element's place in it.
+ * Every out is the same tensor as its input (in place) or overlaps nothing else of the list: two tensors of
+ * the list must not share memory either, which moe_adamw_check finds and moe_adamw does not look for.
+ * Tensors are contiguous and 16-byte aligned; n may be 0.  Zeros are the state before the first step.
+ * Source: "Olmo-core DDP MoE examples" (training runs; the pages name an optimizer without printing it). */
+typedef struct {
+  const void* param;     /* [n] (dt); may be NULL with a master copy */
+  const void* grad;      /* [n] (grad_dt) */
+  const void* m;
+  const void* v;
+  const float* scale;
+  const float* master;   /* [n] or NULL */
+  void* param_out;
+  void* m_out;
+  void* v_out;
+  float* scale_out;
+  float* master_out;
+  int64_t n;
+  double weight_decay;
+  moe_dtype_t dt, grad_dt;
+} moe_adamw_t;
+typedef struct {
+  double lr, beta1, beta2, eps;   /* lr >= 0, betas in [0, 1), eps > 0 */
+  int64_t step;                   /* 1 for the first */
+  uint32_t seed;
+  int32_t state_bits;             /* 32 or 8 */
+} moe_adamw_step_t;
+
+/* tensors: a HOST array, read before the call returns; sumsq [1] double, device, or NULL; max_norm > 0
+ * where it is given. */
+moe_status_t moe_adamw(const moe_adamw_t* tensors, int32_t count, const moe_adamw_step_t* step, const double* sumsq,
+                       float max_norm, moe_stream_t stream);
+/* The list's pointers, sizes and types as moe_adamw checks them, and that no out overlaps another tensor of
+ * the list (a host query: once for a list that is used again and again). */
+moe_status_t moe_adamw_check(const moe_adamw_t* tensors, int32_t count, int32_t state_bits);
+
+/* ------------------------------------------------------------------------------------------ */
 /* Utilities                                                                                   */
 
 /* The calls that take a workspace, for moe_workspace_bytes. */
@@ -545,7 +684,10 @@ typedef enum {
   MOE_OP_ROUTER_AUX_BWD = 10, /* moe_router_aux_bwd */
   MOE_OP_MX_GEMM_ROWS = 11,   /* moe_mx_gemm_rows over the routed experts (and the shared expert) */
   MOE_OP_MX_GEMM_K = 12,      /* moe_mx_gemm_k, both weight-gradient products of each set */
-  MOE_OP_NORM_BWD = 13        /* moe_norm_out_bwd, moe_norm_in_bwd */
+  MOE_OP_NORM_BWD = 13,       /* moe_norm_out_bwd, moe_norm_in_bwd */
+  MOE_OP_ROUTE_BALANCED_BWD = 14, /* moe_route_balanced_bwd, any scores */
+  MOE_OP_FP8_GEMM_ROWS = 15   /* moe_fp8_gemm_rows, every product of the routed experts (and the shared
+                                 expert) */
 } moe_op_t;
 
 /* Device workspace bytes that call `op` needs in a layer of T tokens of width d, each routed to

@@ -4,6 +4,7 @@
 #include "libmoe.h"
 
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -16,6 +17,7 @@
 #include "block_step.h"
 #include "common.h"
 #include "mxfp8.h"
+#include "train_step.h"
 
 namespace {
 
@@ -1081,6 +1083,344 @@ moe_status_t moe_mx_gemm_k(const uint8_t* a_codes, const uint8_t* a_scales, int6
 }
 
 // ---------------------------------------------------------------------------------------------
+// Routing by scores
+
+namespace {
+
+moe_status_t check_scores(int32_t score, int32_t renormalize, float scale) {
+  CHECK(score == MOE_SCORE_SOFTMAX || score == MOE_SCORE_SIGMOID, MOE_ERR_INVALID_VALUE,
+        "score must be MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID (got %d)", score);
+  CHECK(renormalize == 0 || renormalize == 1, MOE_ERR_INVALID_VALUE, "renormalize must be 0 or 1");
+  CHECK(std::isfinite(scale), MOE_ERR_INVALID_VALUE, "scale must be finite");
+  return MOE_OK;
+}
+
+bool dense_scores(int32_t score, int32_t renormalize) {
+  return moe::route_scores_dense(score == MOE_SCORE_SIGMOID, renormalize != 0);
+}
+
+moe::RouteScores route_scores(const float* logits, const float* bias, int64_t T, int32_t E, int32_t k, int32_t groups,
+                              int32_t topk_groups, int32_t score, int32_t renormalize, float scale) {
+  moe::RouteScores r{};
+  r.logits = logits;
+  r.bias = bias;
+  r.T = (int)T;
+  r.E = E;
+  r.k = k;
+  r.groups = groups;
+  r.topk_groups = topk_groups;
+  r.sigmoid = score == MOE_SCORE_SIGMOID;
+  r.renormalize = renormalize != 0;
+  r.scale = scale;
+  return r;
+}
+
+}  // namespace
+
+moe_status_t moe_route_balanced(const void* x, const void* w_router, float* logits, const float* select_bias,
+                                int64_t T, int64_t d, int32_t E, int32_t k, int32_t groups, int32_t topk_groups,
+                                int32_t score, int32_t renormalize, float scale, moe_dtype_t dt, int32_t* topk_idx,
+                                float* topk_gate, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_dtype(dt);
+  if (st != MOE_OK) return st;
+  if ((st = check_tokens(T, d, E, k)) != MOE_OK) return st;
+  if ((st = check_scores(score, renormalize, scale)) != MOE_OK) return st;
+  CHECK(groups >= 1 && E % groups == 0, MOE_ERR_INVALID_VALUE, "groups must divide E (got groups=%d, E=%d)", groups, E);
+  CHECK(topk_groups >= 1 && topk_groups <= groups, MOE_ERR_INVALID_VALUE,
+        "topk_groups must be in [1, groups] (got %d of %d)", topk_groups, groups);
+  CHECK(k <= topk_groups * (E / groups), MOE_ERR_INVALID_VALUE, "k = %d, but %d open groups have %d experts", k,
+        topk_groups, topk_groups * (E / groups));
+  CHECK(!w_router || x, MOE_ERR_INVALID_VALUE, "x is NULL with a learned router");
+  if (T == 0) return MOE_OK;
+  CHECK(logits && topk_idx && topk_gate, MOE_ERR_INVALID_VALUE, "logits/topk_idx/topk_gate is NULL");
+  CHECK_ALIGN16(x, w_router, logits, select_bias, topk_idx, topk_gate);
+  if (w_router) {
+    st = hip_check(moe::launch_router_logits(x, w_router, nullptr, logits, (int)T, (int)d, E, dt == MOE_BF16, S(stream)),
+                   "router logits");
+    if (st != MOE_OK) return st;
+  }
+  return hip_check(moe::launch_route_scores(route_scores(logits, select_bias, T, E, k, groups, topk_groups, score,
+                                                         renormalize, scale),
+                                            topk_idx, topk_gate, S(stream)),
+                   "routing by scores");
+}
+
+size_t moe_route_balanced_bwd_workspace_size(int64_t T, int64_t d, int32_t E, int32_t k, int32_t score,
+                                             int32_t renormalize) {
+  if (check_tokens(T, d, E, k) != MOE_OK || check_scores(score, renormalize, 1.0f) != MOE_OK) return 0;
+  return moe::route_scores_bwd_ws_bytes(T, d, E, k, dense_scores(score, renormalize));
+}
+
+moe_status_t moe_route_balanced_bwd(const float* dgate, const float* logits, const int32_t* topk_idx,
+                                    const int32_t* offsets, const int32_t* src_row, const void* x,
+                                    const void* w_router, int64_t T, int64_t d, int32_t E, int32_t k, int32_t score,
+                                    int32_t renormalize, float scale, moe_dtype_t dt, float* dw_router,
+                                    void* dx_router, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  moe_status_t st = check_dtype(dt);
+  if (st != MOE_OK) return st;
+  if ((st = check_tokens(T, d, E, k)) != MOE_OK) return st;
+  if ((st = check_scores(score, renormalize, scale)) != MOE_OK) return st;
+  const bool dense = dense_scores(score, renormalize);
+  CHECK(!dense || d % 8 == 0, MOE_ERR_UNSUPPORTED,
+        "softmax scores without renormalization need d %% 8 == 0 (got %lld)", (long long)d);
+  CHECK(dw_router && offsets && w_router, MOE_ERR_INVALID_VALUE, "dw_router/offsets/w_router is NULL");
+  CHECK(T == 0 || (dgate && logits && topk_idx && src_row && x && dx_router), MOE_ERR_INVALID_VALUE,
+        "dgate/logits/topk_idx/src_row/x/dx_router is NULL");
+  const size_t need = moe::route_scores_bwd_ws_bytes(T, d, E, k, dense);
+  CHECK(ws && ws_bytes >= need, MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  CHECK_ALIGN16(dgate, logits, topk_idx, offsets, src_row, x, w_router, dw_router, dx_router, ws);
+  return hip_check(moe::launch_route_scores_bwd(route_scores(logits, nullptr, T, E, k, 1, 1, score, renormalize, scale),
+                                                dgate, topk_idx, offsets, src_row, x, w_router, (int)d, dt == MOE_BF16,
+                                                dw_router, dx_router, ws, S(stream)),
+                   "backward of routing by scores");
+}
+
+moe_status_t moe_route_bias_update(const int32_t* counts, int32_t E, float rate, const float* bias, float* bias_out,
+                                   moe_stream_t stream) {
+  g_err.clear();
+  CHECK(E > 0, MOE_ERR_INVALID_VALUE, "E must be > 0 (got %d)", E);
+  CHECK(E <= 256, MOE_ERR_UNSUPPORTED, "E > 256 is not supported (got %d)", E);
+  CHECK(std::isfinite(rate), MOE_ERR_INVALID_VALUE, "rate must be finite");
+  CHECK(counts && bias && bias_out, MOE_ERR_INVALID_VALUE, "counts/bias/bias_out is NULL");
+  CHECK_ALIGN16(counts, bias, bias_out);
+  return hip_check(moe::launch_route_bias(counts, E, rate, bias, bias_out, S(stream)), "bias update");
+}
+
+// ---------------------------------------------------------------------------------------------
+// Products in 8-bit floating point, a scale for each block of 128
+
+moe_status_t moe_fp8_quantize_rows(const void* x, int64_t R, int64_t K, int64_t ldx, uint8_t* codes, float* scales,
+                                   moe_stream_t stream) {
+  g_err.clear();
+  CHECK(R >= 0 && K > 0, MOE_ERR_INVALID_VALUE, "R must be >= 0 and K > 0 (got R=%lld, K=%lld)", (long long)R,
+        (long long)K);
+  CHECK(K % 128 == 0, MOE_ERR_UNSUPPORTED, "K must be a multiple of 128 (got %lld)", (long long)K);
+  CHECK(ldx >= K && ldx % 8 == 0, MOE_ERR_INVALID_VALUE, "ldx must be >= K and a multiple of 8 (got %lld)",
+        (long long)ldx);
+  CHECK(K <= kMaxInt && R <= kMaxInt && ldx <= kMaxInt, MOE_ERR_UNSUPPORTED, "R, K and ldx must fit in int32");
+  if (R == 0) return MOE_OK;
+  CHECK(x && codes && scales, MOE_ERR_INVALID_VALUE, "x/codes/scales is NULL");
+  CHECK_ALIGN16(x, codes, scales);
+  return hip_check(moe::launch_fp8_quant_rows(x, R, (int)K, ldx, codes, scales, S(stream)), "8-bit row quantization");
+}
+
+moe_status_t moe_fp8_quantize_weights(const void* w, int32_t G, int64_t N, int64_t K, uint8_t* codes, float* scales,
+                                      uint8_t* codes_t, float* scales_t, moe_stream_t stream) {
+  g_err.clear();
+  CHECK(G > 0 && N > 0 && K > 0, MOE_ERR_INVALID_VALUE, "G, N and K must be > 0");
+  CHECK(N % 128 == 0 && K % 128 == 0, MOE_ERR_UNSUPPORTED, "N and K must be multiples of 128 (got N=%lld, K=%lld)",
+        (long long)N, (long long)K);
+  CHECK(N <= kMaxInt && K <= kMaxInt && (N / 128) * (K / 128) <= (1 << 23) / G, MOE_ERR_UNSUPPORTED,
+        "more than 2^23 blocks");
+  CHECK(w && codes && scales, MOE_ERR_INVALID_VALUE, "w/codes/scales is NULL");
+  CHECK((codes_t == nullptr) == (scales_t == nullptr), MOE_ERR_INVALID_VALUE,
+        "codes_t and scales_t must both be given or both be NULL");
+  CHECK_ALIGN16(w, codes, scales, codes_t, scales_t);
+  return hip_check(moe::launch_fp8_quant_weights(w, G, (int)N, (int)K, codes, scales, codes_t, scales_t, S(stream)),
+                   "8-bit weight quantization");
+}
+
+namespace {
+
+moe_status_t check_fp8_sizes(int32_t G, int64_t M, int64_t N, int64_t K) {
+  CHECK(G > 0 && G <= 1024, MOE_ERR_INVALID_VALUE, "G must be in [1, 1024] (got %d)", G);
+  CHECK(M >= 0 && N > 0 && K > 0, MOE_ERR_INVALID_VALUE, "M must be >= 0, N and K > 0");
+  CHECK(N % 128 == 0 && K % 128 == 0, MOE_ERR_UNSUPPORTED, "N and K must be multiples of 128 (got N=%lld, K=%lld)",
+        (long long)N, (long long)K);
+  CHECK(M <= kMaxInt / 2 && N <= 1 << 20 && K <= 1 << 20, MOE_ERR_UNSUPPORTED, "sizes out of the supported range");
+  CHECK(((M + 15) / 16 + G) * (N / 32) < (1 << 23), MOE_ERR_UNSUPPORTED, "grid too large");
+  return MOE_OK;
+}
+
+}  // namespace
+
+size_t moe_fp8_gemm_workspace_size(int32_t G, int64_t M, int64_t N, int64_t K) {
+  if (check_fp8_sizes(G, M, N, K) != MOE_OK) return 0;
+  return moe::fp8_gemm_ws_bytes(G, M, N, K);
+}
+
+moe_status_t moe_fp8_gemm_rows(const uint8_t* a_codes, const float* a_scales, const uint8_t* b_codes,
+                               const float* b_scales, const uint8_t* b2_codes, const float* b2_scales, int64_t b2_k,
+                               const int32_t* offsets, int32_t G, int64_t M, int64_t N, int64_t K, int32_t epilogue,
+                               void* out0, void* out1, void* out2, const void* aux0, const void* aux1, void* ws,
+                               size_t ws_bytes, moe_stream_t stream) {
+  g_err.clear();
+  CHECK(epilogue >= MOE_MX_EPI_STORE && epilogue <= MOE_MX_EPI_SWIGLU_BWD, MOE_ERR_INVALID_VALUE,
+        "unknown epilogue %d", epilogue);
+  moe_status_t st = check_fp8_sizes(G, M, N, K);
+  if (st != MOE_OK) return st;
+  CHECK((b2_codes == nullptr) == (b2_scales == nullptr), MOE_ERR_INVALID_VALUE,
+        "b2_codes and b2_scales must both be given or both be NULL");
+  if (epilogue == MOE_MX_EPI_SWIGLU) {
+    CHECK(b2_codes, MOE_ERR_INVALID_VALUE, "the SwiGLU epilogue needs the up-projection rows in b2");
+  } else if (b2_codes) {
+    CHECK(b2_k > 0 && b2_k < K && b2_k % 128 == 0, MOE_ERR_INVALID_VALUE,
+          "b2_k must be a multiple of 128 in (0, K) (got %lld)", (long long)b2_k);
+  }
+  const size_t need = moe::fp8_gemm_ws_bytes(G, M, N, K);
+  CHECK(need == 0 || (ws && ws_bytes >= need), MOE_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need,
+        ws ? ws_bytes : (size_t)0);
+  if (M == 0) return MOE_OK;
+  CHECK(a_codes && a_scales && b_codes && b_scales && offsets, MOE_ERR_INVALID_VALUE, "an operand pointer is NULL");
+  if (epilogue == MOE_MX_EPI_STORE) CHECK(out0, MOE_ERR_INVALID_VALUE, "out0 is NULL");
+  if (epilogue == MOE_MX_EPI_SWIGLU) CHECK(out2, MOE_ERR_INVALID_VALUE, "out2 is NULL");
+  if (epilogue == MOE_MX_EPI_SWIGLU_BWD)
+    CHECK(out0 && aux0 && aux1, MOE_ERR_INVALID_VALUE, "out0/aux0/aux1 is NULL");
+  CHECK_ALIGN16(a_codes, a_scales, b_codes, b_scales, b2_codes, b2_scales, offsets, out0, out1, out2, aux0, aux1, ws);
+  moe::Fp8GemmArgs a{};
+  a.a = a_codes;
+  a.as = a_scales;
+  a.b = b_codes;
+  a.bs = b_scales;
+  a.b2 = b2_codes;
+  a.bs2 = b2_scales;
+  a.ksplit = (epilogue != MOE_MX_EPI_SWIGLU && b2_codes) ? (int)b2_k : 0;
+  a.offsets = offsets;
+  a.G = G;
+  a.M = (int)M;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.out0 = out0;
+  a.out1 = out1;
+  a.out2 = out2;
+  a.aux0 = aux0;
+  a.aux1 = aux1;
+  a.ws = ws;
+  return hip_check(moe::launch_fp8_gemm(epilogue, a, S(stream)), "8-bit grouped GEMM");
+}
+
+// ---------------------------------------------------------------------------------------------
+// AdamW
+
+namespace {
+
+// One bijective round of the hash that the kernel's random bits come from.
+uint32_t mix32(uint32_t h) {
+  h ^= h >> 16;
+  h *= 0x9D2B4F35u;
+  h ^= h >> 15;
+  h *= 0xC5A1E6B7u;
+  return h ^ (h >> 16);
+}
+
+constexpr int64_t kAdamWMost = int64_t(1) << 34;   // elements of a tensor: runs of 8 are counted in 32 bits
+
+moe_status_t check_adamw(const moe_adamw_t* t, int32_t count, int32_t state_bits) {
+  CHECK(count >= 0, MOE_ERR_INVALID_VALUE, "count must be >= 0 (got %d)", count);
+  CHECK(count == 0 || t, MOE_ERR_INVALID_VALUE, "tensors is NULL");
+  CHECK(count <= 1 << 20, MOE_ERR_UNSUPPORTED, "count must be at most 2^20 (got %d)", count);
+  CHECK(state_bits == 32 || state_bits == 8, MOE_ERR_INVALID_VALUE, "state_bits must be 32 or 8 (got %d)", state_bits);
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_t& a = t[i];
+    moe_status_t st = check_dtype(a.dt);
+    if (st == MOE_OK) st = check_dtype(a.grad_dt);
+    if (st != MOE_OK) return st;
+    CHECK(a.n >= 0, MOE_ERR_INVALID_VALUE, "tensor %d has n = %lld", i, (long long)a.n);
+    CHECK(a.n <= kAdamWMost, MOE_ERR_UNSUPPORTED, "tensor %d has more than 2^34 elements", i);
+    CHECK(a.n <= kGradMaxElements - total, MOE_ERR_UNSUPPORTED, "more than 2^41 elements");
+    total += a.n;
+    CHECK(a.weight_decay >= 0 && std::isfinite(a.weight_decay), MOE_ERR_INVALID_VALUE,
+          "tensor %d: weight_decay must be finite and >= 0", i);
+    if (a.n == 0) continue;
+    CHECK((a.param || a.master) && a.grad && a.m && a.v && a.param_out && a.m_out && a.v_out, MOE_ERR_INVALID_VALUE,
+          "tensor %d: param/grad/m/v or an out is NULL", i);
+    const bool scaled = state_bits == 8;
+    CHECK((a.scale != nullptr) == scaled && (a.scale_out != nullptr) == scaled, MOE_ERR_INVALID_VALUE,
+          "tensor %d: scale and scale_out go with 8-bit states, and only with them", i);
+    CHECK((a.master == nullptr) == (a.master_out == nullptr), MOE_ERR_INVALID_VALUE,
+          "tensor %d: master and master_out must both be given or both be NULL", i);
+    CHECK(!a.master || a.dt == MOE_BF16, MOE_ERR_INVALID_VALUE, "tensor %d: a float parameter has no master copy", i);
+    CHECK(aligned16({a.param, a.grad, a.m, a.v, a.scale, a.master, a.param_out, a.m_out, a.v_out, a.scale_out,
+                     a.master_out}),
+          MOE_ERR_INVALID_VALUE, "device pointers must be 16-byte aligned (tensor %d)", i);
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status_t moe_adamw_check(const moe_adamw_t* tensors, int32_t count, int32_t state_bits) {
+  g_err.clear();
+  moe_status_t st = check_adamw(tensors, count, state_bits);
+  if (st != MOE_OK) return st;
+  // Address ranges in order of their starts, with the furthest end of an output and of any range so far;
+  // an output in the place of its input is one range.
+  struct Range {
+    uintptr_t begin, end;
+    bool out;
+  };
+  std::unique_ptr<Range[]> r(new (std::nothrow) Range[11 * (size_t)std::max(count, 1)]);
+  CHECK(r, MOE_ERR_UNSUPPORTED, "no host memory for a list of %d tensors", count);
+  size_t n = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_t& a = tensors[i];
+    if (a.n == 0) continue;
+    const size_t state = (size_t)a.n * (state_bits / 8), blocks = 2 * (((size_t)a.n + 127) / 128) * sizeof(float);
+    auto add = [&](const void* in, const void* out, size_t bytes) {
+      const uintptr_t o = reinterpret_cast<uintptr_t>(out), p = reinterpret_cast<uintptr_t>(in);
+      if (out) r[n++] = Range{o, o + bytes, true};
+      if (in && in != out) r[n++] = Range{p, p + bytes, false};
+    };
+    add(a.param, a.param_out, (size_t)a.n * esize(a.dt));
+    add(a.grad, nullptr, (size_t)a.n * esize(a.grad_dt));
+    add(a.m, a.m_out, state);
+    add(a.v, a.v_out, state);
+    add(a.scale, a.scale_out, blocks);
+    add(a.master, a.master_out, (size_t)a.n * sizeof(float));
+  }
+  std::sort(r.get(), r.get() + n, [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t end_out = 0, end_any = 0;
+  for (size_t i = 0; i < n; ++i) {
+    CHECK(r[i].begin >= end_out && (!r[i].out || r[i].begin >= end_any), MOE_ERR_INVALID_VALUE,
+          "an out overlaps another tensor of the list");
+    end_any = std::max(end_any, r[i].end);
+    if (r[i].out) end_out = std::max(end_out, r[i].end);
+  }
+  return MOE_OK;
+}
+
+moe_status_t moe_adamw(const moe_adamw_t* tensors, int32_t count, const moe_adamw_step_t* step, const double* sumsq,
+                       float max_norm, moe_stream_t stream) {
+  g_err.clear();
+  CHECK(step, MOE_ERR_INVALID_VALUE, "step is NULL");
+  moe_status_t st = check_adamw(tensors, count, step->state_bits);
+  if (st != MOE_OK) return st;
+  CHECK(step->lr >= 0 && std::isfinite(step->lr), MOE_ERR_INVALID_VALUE, "lr must be finite and >= 0");
+  CHECK(step->beta1 >= 0 && step->beta1 < 1 && step->beta2 >= 0 && step->beta2 < 1, MOE_ERR_INVALID_VALUE,
+        "beta1 and beta2 must be in [0, 1)");
+  CHECK((float)step->eps > 0 && std::isfinite((float)step->eps), MOE_ERR_INVALID_VALUE, "eps must be finite and > 0");
+  CHECK(step->step >= 1, MOE_ERR_INVALID_VALUE, "step must be >= 1 (got %lld)", (long long)step->step);
+  if (sumsq && (st = check_max_norm(max_norm)) != MOE_OK) return st;
+  CHECK_ALIGN16(sumsq);
+  if (count == 0) return MOE_OK;
+  std::unique_ptr<moe::AdamWItem[]> items(new (std::nothrow) moe::AdamWItem[count]);
+  CHECK(items, MOE_ERR_UNSUPPORTED, "no host memory for a list of %d tensors", count);
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_t& a = tensors[i];
+    items[i] = moe::AdamWItem{a.param,     a.grad,       a.m,          a.v,
+                              a.scale,     a.master,     a.param_out,  a.m_out,
+                              a.v_out,     a.scale_out,  a.master_out, (long long)a.n,
+                              a.dt == MOE_BF16, a.grad_dt == MOE_BF16, (float)(1.0 - step->lr * a.weight_decay),
+                              mix32(step->seed + 0x9E3779B9u * (uint32_t)(i + 1))};
+  }
+  moe::AdamWStep s{};
+  s.beta1 = (float)step->beta1;
+  s.one_minus_beta1 = (float)(1.0 - step->beta1);
+  s.beta2 = (float)step->beta2;
+  s.one_minus_beta2 = (float)(1.0 - step->beta2);
+  s.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(step->beta2, (double)step->step)));
+  s.step_size = (float)(step->lr / (1.0 - std::pow(step->beta1, (double)step->step)));
+  s.eps = (float)step->eps;
+  s.sumsq = sumsq;
+  s.max_norm = max_norm;
+  return hip_check(moe::launch_adamw(items.get(), count, s, step->state_bits == 8, S(stream)), "AdamW");
+}
+
+// ---------------------------------------------------------------------------------------------
 
 size_t moe_workspace_bytes(int32_t op, int64_t T, int64_t d, int32_t E, int32_t k, int64_t f, int64_t fs) {
   g_err.clear();
@@ -1120,6 +1460,18 @@ size_t moe_workspace_bytes(int32_t op, int64_t T, int64_t d, int32_t E, int32_t 
       return need;
     }
     case MOE_OP_NORM_BWD: return moe_norm_bwd_workspace_size(T, d);
+    case MOE_OP_ROUTE_BALANCED_BWD:
+      return std::max(moe_route_balanced_bwd_workspace_size(T, d, E, k, MOE_SCORE_SIGMOID, 1),
+                      moe_route_balanced_bwd_workspace_size(T, d, E, k, MOE_SCORE_SOFTMAX, 0));
+    case MOE_OP_FP8_GEMM_ROWS: {
+      size_t need = 0;
+      for (int q = 0; q < nsets; ++q) {
+        const moe_expert_set_t& e = sets[q];
+        need = std::max({need, moe_fp8_gemm_workspace_size(e.G, e.M, e.f, d), moe_fp8_gemm_workspace_size(e.G, e.M, d, e.f),
+                         moe_fp8_gemm_workspace_size(e.G, e.M, d, 2 * e.f)});
+      }
+      return need;
+    }
     default:
       fail(MOE_ERR_INVALID_VALUE, "unknown op %d", op);
       return 0;

@@ -412,9 +412,18 @@ __global__ __launch_bounds__(256) void topk_gate_kernel(const float* logits, int
 // evaluated as g_j * sum_i g_i (dg_j - dg_i), equal because the gates sum to one; this form has no
 // cancellation between large terms when one gate is close to 1 and the others are tiny.  Entries
 // j >= k are 0.  Every kernel below takes its dl from here, so all of them see the same values.
+// Without gates (NULL) dgate holds the logit gradients themselves.
 template <int K>
 __device__ __forceinline__ void token_logit_grads(const float* gate, const float* dgate, size_t t, int k,
                                                   float (&dl)[K]) {
+  if (gate == nullptr) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const float v = dgate[t * k + (i < k ? i : k - 1)];
+      dl[i] = i < k ? v : 0.0f;
+    }
+    return;
+  }
   float g[K], dg[K];
 #pragma unroll
   for (int i = 0; i < K; ++i) {   // loads at a clamped index, never under a condition
@@ -433,6 +442,7 @@ __device__ __forceinline__ void token_logit_grads(const float* gate, const float
 }
 // The logit gradient of assignment a = t*k + j.
 __device__ __forceinline__ float assignment_logit_grad(const float* gate, const float* dgate, int a, int k) {
+  if (gate == nullptr) return dgate[a];
   float dl[8];
   token_logit_grads<8>(gate, dgate, (size_t)(a / k), k, dl);
   const int j = a % k;

@@ -41,6 +41,11 @@ MOE_OP_ROUTER_AUX_BWD = 10
 MOE_OP_MX_GEMM_ROWS = 11
 MOE_OP_MX_GEMM_K = 12
 MOE_OP_NORM_BWD = 13
+MOE_OP_ROUTE_BALANCED_BWD = 14
+MOE_OP_FP8_GEMM_ROWS = 15
+
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 MOE_MX_EPI_STORE = 0
 MOE_MX_EPI_SWIGLU = 1
@@ -74,6 +79,19 @@ class VocabLossPlan(ctypes.Structure):
     """moe_vocab_loss_plan_t: how the vocabulary loss cuts its products."""
     _fields_ = [(n, ctypes.c_int32) for n in ("piece_words", "pieces", "fwd_tile", "logits_tile", "dh_tile", "dw_tile",
                                               "dh_splits", "dw_splits")]
+
+
+class AdamW(ctypes.Structure):
+    """moe_adamw_t: one tensor of an optimizer step."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "scale", "master", "param_out", "m_out", "v_out",
+                                               "scale_out", "master_out")] + [
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_double), ("dt", ctypes.c_int32), ("grad_dt", ctypes.c_int32)]
+
+
+class AdamWStep(ctypes.Structure):
+    """moe_adamw_step_t: what all tensors of a step share."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint32), ("state_bits", ctypes.c_int32)]
 
 
 # name -> (restype, argtypes); mirrors include/libmoe.h
@@ -132,6 +150,18 @@ _SIGS = {
                                 _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_mx_gemm_k_workspace_size": (_SZ, [_I32, _I64, _I64]),
     "moe_mx_gemm_k": (_I32, [_P, _P, _I64, _P, _P, _I64, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _SZ, _P]),
+    "moe_route_balanced": (_I32, [_P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _I32, _I32, _F, _I32, _P, _P, _P]),
+    "moe_route_balanced_bwd_workspace_size": (_SZ, [_I64, _I64, _I32, _I32, _I32, _I32]),
+    "moe_route_balanced_bwd": (_I32, [_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I32, _I32, _I32, _I32, _F, _I32, _P, _P,
+                                      _P, _SZ, _P]),
+    "moe_route_bias_update": (_I32, [_P, _I32, _F, _P, _P, _P]),
+    "moe_fp8_quantize_rows": (_I32, [_P, _I64, _I64, _I64, _P, _P, _P]),
+    "moe_fp8_quantize_weights": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P, _P, _P]),
+    "moe_fp8_gemm_workspace_size": (_SZ, [_I32, _I64, _I64, _I64]),
+    "moe_fp8_gemm_rows": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _P, _I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P,
+                                 _SZ, _P]),
+    "moe_adamw": (_I32, [_P, _I32, _P, _P, _F, _P]),
+    "moe_adamw_check": (_I32, [_P, _I32, _I32]),
     "moe_workspace_bytes": (_SZ, [_I32, _I64, _I64, _I32, _I32, _I64, _I64]),
     "moe_status_string": (_c.c_char_p, [_I32]),
     "moe_last_error": (_c.c_char_p, []),
@@ -538,3 +568,121 @@ def moe_mx_gemm_k(a_codes, a_scales, lda, b_codes, b_scales, ldb, kbase, G, M, N
                   stream=None):
     _call("moe_mx_gemm_k", _ptr(a_codes), _ptr(a_scales), lda, _ptr(b_codes), _ptr(b_scales), ldb, _ptr(kbase),
           G, M, N, split, _ptr(out0), _ptr(out1), _ptr(ws), ws_bytes, _stream(stream))
+
+
+def moe_route_balanced(x, w_router, logits, select_bias, T, d, E, k, groups, topk_groups, score, renormalize, scale, dt,
+                       topk_idx, topk_gate, stream=None):
+    s, (x, w_router, logits, select_bias, topk_idx, topk_gate) = _place(
+        stream, (x, w_router, logits, select_bias, topk_idx, topk_gate))
+    _call("moe_route_balanced", x, w_router, logits, select_bias, T, d, E, k, groups, topk_groups, score, renormalize,
+          scale, dt, topk_idx, topk_gate, s)
+
+
+def moe_route_balanced_bwd_workspace_size(T, d, E, k, score, renormalize) -> int:
+    return lib().moe_route_balanced_bwd_workspace_size(T, d, E, k, score, renormalize)
+
+
+def moe_route_balanced_bwd(dgate, logits, topk_idx, offsets, src_row, x, w_router, T, d, E, k, score, renormalize, scale,
+                           dt, dw_router, dx_router, ws, ws_bytes, stream=None):
+    s, (dgate, logits, topk_idx, offsets, src_row, x, w_router, dw_router, dx_router, ws) = _place(
+        stream, (dgate, logits, topk_idx, offsets, src_row, x, w_router, dw_router, dx_router, ws))
+    _call("moe_route_balanced_bwd", dgate, logits, topk_idx, offsets, src_row, x, w_router, T, d, E, k, score, renormalize,
+          scale, dt, dw_router, dx_router, ws, ws_bytes, s)
+
+
+def moe_route_bias_update(counts, E, rate, bias, bias_out, stream=None):
+    s, (counts, bias, bias_out) = _place(stream, (counts, bias, bias_out))
+    _call("moe_route_bias_update", counts, E, rate, bias, bias_out, s)
+
+
+def moe_fp8_quantize_rows(x, R, K, ldx, codes, scales, stream=None):
+    s, (x, codes, scales) = _place(stream, (x, codes, scales))
+    _call("moe_fp8_quantize_rows", x, R, K, ldx, codes, scales, s)
+
+
+def moe_fp8_quantize_weights(w, G, N, K, codes, scales, codes_t, scales_t, stream=None):
+    s, (w, codes, scales, codes_t, scales_t) = _place(stream, (w, codes, scales, codes_t, scales_t))
+    _call("moe_fp8_quantize_weights", w, G, N, K, codes, scales, codes_t, scales_t, s)
+
+
+def moe_fp8_gemm_workspace_size(G, M, N, K) -> int:
+    return lib().moe_fp8_gemm_workspace_size(G, M, N, K)
+
+
+def moe_fp8_gemm_rows(a_codes, a_scales, b_codes, b_scales, b2_codes, b2_scales, b2_k, offsets, G, M, N, K, epilogue, out0,
+                      out1, out2, aux0, aux1, ws, ws_bytes, stream=None):
+    s, (a_codes, a_scales, b_codes, b_scales, b2_codes, b2_scales, offsets, out0, out1, out2, aux0, aux1, ws) = _place(
+        stream, (a_codes, a_scales, b_codes, b_scales, b2_codes, b2_scales, offsets, out0, out1, out2, aux0, aux1, ws))
+    _call("moe_fp8_gemm_rows", a_codes, a_scales, b_codes, b_scales, b2_codes, b2_scales, b2_k, offsets, G, M, N, K,
+          epilogue, out0, out1, out2, aux0, aux1, ws, ws_bytes, s)
+
+
+STATE_BLOCK = 128   # elements of an 8-bit optimizer state that share a scale
+
+
+def adamw_states(params, bits=32, master=False):
+    """The states before the first step, for adamw_list: m, v, scales (None each with 32 bits) and masters
+    (float copies of the bf16 parameters, or None each)."""
+    kind = {32: torch.float32, 8: torch.uint8}[bits]
+    params = list(params)
+    m = [torch.zeros(p.numel(), dtype=kind, device=p.device) for p in params]
+    v = [torch.zeros(p.numel(), dtype=kind, device=p.device) for p in params]
+    scales = [torch.zeros(2 * -(-p.numel() // STATE_BLOCK), device=p.device) if bits == 8 else None for p in params]
+    masters = [p.detach().float().reshape(-1).clone() if master and p.dtype == torch.bfloat16 else None for p in params]
+    return m, v, scales, masters
+
+
+class AdamWList:
+    """A list of parameters with their gradients and states in the form moe_adamw takes, checked once.  It
+    holds the tensors, so their memory lives as long as the list; values are read when a call's kernels run."""
+
+    def __init__(self, params, grads, m, v, scales, masters, weight_decay, out):
+        n = len(params)
+        none = [None] * n
+        scales, masters = scales or none, masters or none
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+        po, mo, vo, so, wo = out if out is not None else (params, m, v, scales, masters)
+        so, wo = so or none, wo or none
+        rows = [params, grads, m, v, scales, masters, po, mo, vo, so, wo]
+        rows = [list(r) for r in rows]
+        if any(len(r) != n for r in rows + [decay]):
+            raise ValueError("the lists differ in length")
+        self.count = n
+        self.bits = 8 if n and m[0].element_size() == 1 else 32
+        kinds = (torch.uint8, torch.float8_e4m3fn) if self.bits == 8 else (torch.float32,)
+        self.tensors = rows
+        self.array = (AdamW * max(1, n))()
+        for i, e in enumerate(self.array[:n]):
+            p, g, a, b, sc, w, p2, a2, b2, sc2, w2 = (r[i] for r in rows)
+            size = p.numel()
+            blocks = 2 * -(-size // STATE_BLOCK)
+            if any(t.numel() != size for t in (g, a, b, p2, a2, b2)) or p2.dtype != p.dtype:
+                raise ValueError(f"tensor {i}: a gradient, state or out must have its parameter's size, an out its type")
+            if any(t.dtype not in kinds for t in (a, b, a2, b2)):
+                raise ValueError(f"tensor {i}: states must be float32, or all uint8 or float8_e4m3fn")
+            if any((t is not None) != (self.bits == 8) or t is not None and (t.numel() != blocks or t.dtype != torch.float32)
+                   for t in (sc, sc2)):
+                raise ValueError(f"tensor {i}: 8-bit states, and only they, need a float scale of 2 ceil(n / 128) elements")
+            if any(t is not None and (t.numel() != size or t.dtype != torch.float32) for t in (w, w2)):
+                raise ValueError(f"tensor {i}: a master copy must be float32 of the parameter's size")
+            (e.param, e.grad, e.m, e.v, e.scale, e.master, e.param_out, e.m_out, e.v_out, e.scale_out, e.master_out) = (
+                _ptr(t) for t in (p, g, a, b, sc, w, p2, a2, b2, sc2, w2))
+            e.n, e.weight_decay, e.dt, e.grad_dt = size, decay[i], dtype_code(p), dtype_code(g)
+        self.ptr = ctypes.cast(self.array, _P)
+        if len({t.device for r in rows for t in r if t is not None}) > 1:
+            raise ValueError("the tensors are on different devices")
+        self.device = params[0].get_device() if n else None   # -1: the host
+        _call("moe_adamw_check", self.ptr, n, self.bits)
+
+
+def adamw_list(params, grads, m, v, scales=None, masters=None, weight_decay=0.0, out=None) -> AdamWList:
+    """Parameters, gradients and states for moe_adamw.  weight_decay: one for all or a list; out: the lists
+    that params, m, v, scales and masters go to (default: in place)."""
+    return AdamWList(list(params), list(grads), list(m), list(v), scales and list(scales), masters and list(masters),
+                     weight_decay, out)
+
+
+def moe_adamw(tensors: AdamWList, lr, beta1, beta2, eps, step, seed=0, sumsq=None, max_norm=1.0, stream=None):
+    s, (sumsq,) = _place(stream, (sumsq,), tensors)
+    cfg = AdamWStep(lr, beta1, beta2, eps, step, seed & 0xFFFFFFFF, tensors.bits)
+    _call("moe_adamw", tensors.ptr, tensors.count, ctypes.addressof(cfg), sumsq, max_norm, s)
