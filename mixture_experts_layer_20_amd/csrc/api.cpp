@@ -1392,7 +1392,8 @@ moe_status_t moe_adamw(const moe_adamw_t* tensors, int32_t count, const moe_adam
   CHECK(step->lr >= 0 && std::isfinite(step->lr), MOE_ERR_INVALID_VALUE, "lr must be finite and >= 0");
   CHECK(step->beta1 >= 0 && step->beta1 < 1 && step->beta2 >= 0 && step->beta2 < 1, MOE_ERR_INVALID_VALUE,
         "beta1 and beta2 must be in [0, 1)");
-  CHECK((float)step->eps > 0 && std::isfinite((float)step->eps), MOE_ERR_INVALID_VALUE, "eps must be finite and > 0");
+  CHECK((float)step->eps >= 1.17549435e-38f && std::isfinite((float)step->eps), MOE_ERR_INVALID_VALUE,
+        "eps must be a normal float > 0");
   CHECK(step->step >= 1, MOE_ERR_INVALID_VALUE, "step must be >= 1 (got %lld)", (long long)step->step);
   if (sumsq && (st = check_max_norm(max_norm)) != MOE_OK) return st;
   CHECK_ALIGN16(sumsq);

@@ -74,27 +74,6 @@ struct AdamWStep {
   const double* sumsq;   // NULL: gradients as they are
   double max_norm;
 };
-constexpr int kAdamWTable = 36;   // tensors per launch: the table stays within 4 KiB of kernel arguments
-struct AdamWTable {
-  AdamWStep step;
-  const void* param[kAdamWTable];
-  const void* grad[kAdamWTable];
-  const void* m[kAdamWTable];
-  const void* v[kAdamWTable];
-  const float* scale[kAdamWTable];
-  const float* master[kAdamWTable];
-  void* param_out[kAdamWTable];
-  void* m_out[kAdamWTable];
-  void* v_out[kAdamWTable];
-  float* scale_out[kAdamWTable];
-  float* master_out[kAdamWTable];
-  int first[kAdamWTable + 1];      // first chunk of each tensor, among this launch's chunks
-  uint32_t tail[kAdamWTable];      // elements of its last chunk; bit 31: bf16 gradient, bit 30: bf16 parameter
-  float decay[kAdamWTable];
-  uint32_t seed[kAdamWTable];
-  int count;
-  uint32_t chunk;
-};
 hipError_t launch_adamw(const AdamWItem* items, int count, const AdamWStep& step, bool bits8, hipStream_t s);
 
 }  // namespace moe
