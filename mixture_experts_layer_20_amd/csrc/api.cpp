@@ -1231,7 +1231,7 @@ moe_status_t check_fp8_sizes(int32_t G, int64_t M, int64_t N, int64_t K) {
   CHECK(N % 128 == 0 && K % 128 == 0, MOE_ERR_UNSUPPORTED, "N and K must be multiples of 128 (got N=%lld, K=%lld)",
         (long long)N, (long long)K);
   CHECK(M <= kMaxInt / 2 && N <= 1 << 20 && K <= 1 << 20, MOE_ERR_UNSUPPORTED, "sizes out of the supported range");
-  CHECK(((M + 15) / 16 + G) * (N / 32) < (1 << 23), MOE_ERR_UNSUPPORTED, "grid too large");
+  CHECK(((M + 127) / 128 + G) * (N / 64) < (1 << 24), MOE_ERR_UNSUPPORTED, "more than 2^24 output tiles");
   return MOE_OK;
 }
 

@@ -1,0 +1,880 @@
+// Grouped products in 8-bit floating point (E4M3) with a float scale for each block of 128.
+//
+//   C[m, n] = sum_b sa[m, b] sb[n / 128, b] sum_{k in block b} a[m, k] w[n, k]
+//
+// The matrix instruction multiplies E4M3 codes exactly and adds in fp32; a block's 128 products per output
+// start from a zero accumulator, whose result is scaled and added.  The weights are the instruction's first
+// operand, so a lane's accumulators are output columns of one row: its row's scale is one register, and the
+// weights' scale is the same for all of them.
+#include "train_step.h"
+
+#include "block_store.h"
+#include "mxfp8.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace moe {
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int BLK = 128;
+constexpr int ONE = 0x7f7f7f7f;   // scale bytes of the matrix instruction: 2^0
+
+// ---- Products: 128 x 128 tiles ------------------------------------------------------------------
+// Four waves, 64 x 64 each; K goes in blocks of 128 through a double-buffered LDS tile, 16-byte chunks
+// XOR-swizzled by (row >> 1) & 7.  The weights are the instruction's first operand, so a lane's
+// accumulators hold 4 consecutive output columns of one row: its row's scale is one register.
+constexpr int TB = 128;
+constexpr int OPBYTES = TB * TB;
+
+__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+
+// The group of row tile mt and its rows, from the group offsets: rows of a group in tiles of TM, groups in
+// order; false past the last.  A wave's lanes count 64 groups at a time.
+template <int TM>
+__device__ __forceinline__ bool find_rows(const int32_t* offsets, int G, int M, int mt, int& g, int& m0, int& m_end) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int g0 = 0; g0 < G; g0 += 64) {
+    const int q = g0 + lane;
+    int r0 = 0, r1 = 0;
+    if (q < G) {
+      r0 = min(max(offsets[q], 0), M);
+      r1 = min(max(offsets[q + 1], r0), M);
+    }
+    const int n = (r1 - r0 + TM - 1) / TM;
+    int sum = n;   // tiles of the lanes up to this one
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += o;
+    }
+    const int all = __shfl(sum, 63, 64);
+    if (mt < before + all) {
+      const unsigned long long later = __ballot(before + sum > mt);
+      const int at = __ffsll((long long)later) - 1;
+      g = g0 + at;
+      m0 = __shfl(r0, at, 64) + (mt - before - __shfl(sum - n, at, 64)) * TM;
+      m_end = __shfl(r1, at, 64);
+      return true;
+    }
+    before += all;
+  }
+  return false;
+}
+
+__device__ __forceinline__ i32x8_t read_frag(const uint8_t* tile, int row, int s, int h) {
+  const uint8_t* base = tile + row * TB;
+  const int sw = swz(row);
+  const u32x4_t p = *reinterpret_cast<const u32x4_t*>(base + 16 * ((4 * s + h) ^ sw));
+  const u32x4_t q = *reinterpret_cast<const u32x4_t*>(base + 16 * ((4 * s + 2 + h) ^ sw));
+  i32x8_t r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = (int)p[j];
+    r[4 + j] = (int)q[j];
+  }
+  return r;
+}
+
+template <int EPI>
+__global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][OPBYTES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave >> 1, wn = wave & 1, li = lane & 31, h = lane >> 5;
+  constexpr int OC = EPI == MX_EPI_SWIGLU ? 64 : 128;   // the SwiGLU tile: 64 gate and 64 up columns
+  const int NT = p.N / OC;
+  const int nt = blockIdx.x % NT;
+  int g, m0, m_end;
+  if (!find_rows<TB>(p.offsets, p.G, p.M, blockIdx.x / NT, g, m0, m_end)) return;
+  const int nk = p.K / TB;
+  const bool split = EPI != MX_EPI_SWIGLU && p.b2 != nullptr;
+  const int K1 = split ? p.ksplit : p.K, K2 = EPI == MX_EPI_SWIGLU ? p.K : p.K - K1;
+
+  // Loads: rows (tid >> 3) + 32 j, 16-byte chunk tid & 7, of both operands.
+  const int lrow = tid >> 3, lch = tid & 7;
+  const uint8_t* ga[4];
+  const uint8_t* gb[4];
+  const uint8_t* gb2[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = lrow + 32 * j;
+    ga[j] = p.a + (long long)min(m0 + r, m_end - 1) * p.K + 16 * lch;
+    if constexpr (EPI == MX_EPI_SWIGLU) {
+      const long long br = (long long)g * p.N + nt * 64 + (r >> 6) * 32 + (r & 31);
+      gb[j] = (((r >> 5) & 1) ? p.b2 : p.b) + br * p.K + 16 * lch;
+      gb2[j] = gb[j];
+    } else {
+      const long long br = (long long)g * p.N + nt * TB + r;
+      gb[j] = p.b + br * K1 + 16 * lch;
+      gb2[j] = split ? p.b2 + br * K2 + 16 * lch - K1 : gb[j];
+    }
+  }
+  const int lofs = lrow * TB + 16 * (lch ^ swz(lrow));
+  // Scales: one of each of the lane's two rows, one of each of the wave's column blocks of 128.
+  const float* sa_p[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) sa_p[i] = p.as + min(m0 + wm * 64 + i * 32 + li, m_end - 1);
+  const long long nblk = (long long)g * (p.N / BLK) + (EPI == MX_EPI_SWIGLU ? nt / 2 : nt);
+  const float* sb_p = p.bs + nblk * (K1 / BLK);
+  const float* sb2_p = p.bs2 ? p.bs2 + nblk * (K2 / BLK) : nullptr;
+
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  u32x4_t ra[4], rb[4];
+  auto fetch = [&](int kt) {
+    const int off = kt * TB;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      ra[j] = *reinterpret_cast<const u32x4_t*>(ga[j] + off);
+      rb[j] = *reinterpret_cast<const u32x4_t*>((off >= K1 ? gb2[j] : gb[j]) + off);
+    }
+  };
+  auto store = [&](int buf) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      *reinterpret_cast<u32x4_t*>(&lds[buf][0][lofs + 32 * TB * j]) = ra[j];
+      *reinterpret_cast<u32x4_t*>(&lds[buf][1][lofs + 32 * TB * j]) = rb[j];
+    }
+  };
+  fetch(0);
+  store(0);
+  __syncthreads();
+  for (int kt = 0; kt < nk; ++kt) {
+    const int cur = kt & 1;
+    if (kt + 1 < nk) fetch(kt + 1);
+    float sa[2], sb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sa[i] = sa_p[i][(long long)kt * p.M];
+    if constexpr (EPI == MX_EPI_SWIGLU) {
+      sb[0] = sb_p[kt];
+      sb[1] = sb2_p[kt];
+    } else {
+      sb[0] = sb[1] = kt * TB >= K1 ? sb2_p[kt - K1 / TB] : sb_p[kt];
+    }
+    f32x16_t part[2][2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      i32x8_t fa[2], fb[2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        fa[q] = read_frag(lds[cur][0], wm * 64 + q * 32 + li, s, h);
+        fb[q] = read_frag(lds[cur][1], wn * 64 + q * 32 + li, s, h);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (s == 0) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) part[i][j][r] = 0.f;
+          }
+          part[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[j], fa[i], part[i][j], 0, 0, 0, ONE, 0, ONE);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float f = sa[i] * sb[j];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] += f * part[i][j][r];
+      }
+    if (kt + 1 < nk) store(cur ^ 1);
+    __syncthreads();
+  }
+
+  // Epilogue: lane holds row li of each 32-row block, columns 8 (r / 4) + 4 h + r % 4.
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int row = m0 + wm * 64 + i * 32 + li;
+    if (row >= m_end) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if constexpr (EPI == MX_EPI_SWIGLU) {
+        const long long o = (long long)row * p.N + nt * 64 + wn * 32 + 8 * q + 4 * h;
+        float hv[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float a = acc[i][0][4 * q + r];
+          hv[r] = a * sigmoid_f32(a) * acc[i][1][4 * q + r];
+        }
+        auto put = [&](void* out, float v0, float v1, float v2, float v3) {
+          *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + o) = make_uint2(bf16pack(v0, v1), bf16pack(v2, v3));
+        };
+        if (p.out0) put(p.out0, acc[i][0][4 * q], acc[i][0][4 * q + 1], acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]);
+        if (p.out1) put(p.out1, acc[i][1][4 * q], acc[i][1][4 * q + 1], acc[i][1][4 * q + 2], acc[i][1][4 * q + 3]);
+        put(p.out2, hv[0], hv[1], hv[2], hv[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int col = nt * TB + wn * 64 + j * 32 + 8 * q + 4 * h;
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r];
+          if constexpr (EPI == MX_EPI_SWIGLU_BWD) {
+            const long long o = (long long)row * p.N + col;
+            const uint2 av = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux0) + o);
+            const uint2 bv = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux1) + o);
+            const uint32_t aw[2] = {av.x, av.y}, bw[2] = {bv.x, bv.y};
+            float da[4], db[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float a = bf16_to_f32((bf16_t)(aw[r >> 1] >> (16 * (r & 1))));
+              const float bb = bf16_to_f32((bf16_t)(bw[r >> 1] >> (16 * (r & 1))));
+              const float sg = sigmoid_f32(a);
+              da[r] = v[r] * bb * sg * (1.0f + a * (1.0f - sg));
+              db[r] = v[r] * a * sg;
+            }
+            bf16_t* dab = reinterpret_cast<bf16_t*>(p.out0) + (long long)row * (2 * p.N);
+            *reinterpret_cast<uint2*>(dab + col) = make_uint2(bf16pack(da[0], da[1]), bf16pack(da[2], da[3]));
+            *reinterpret_cast<uint2*>(dab + p.N + col) = make_uint2(bf16pack(db[0], db[1]), bf16pack(db[2], db[3]));
+          } else {
+            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(p.out0) + (long long)row * p.N + col) =
+                make_uint2(bf16pack(v[0], v[1]), bf16pack(v[2], v[3]));
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int EPI>
+hipError_t launch_tiles(const Fp8GemmArgs& a, hipStream_t s) {
+  const long long rows = (a.M + TB - 1) / TB + std::min(a.G, a.M);
+  const long long tiles = rows * (a.N / (EPI == MX_EPI_SWIGLU ? 64 : 128));
+  fp8_gemm_kernel<EPI><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// ---- Products of few rows ---------------------------------------------------------------------------
+// 16 rows by 16 output columns (16 of the gate and 16 of the up-projection for SwiGLU) a workgroup: the
+// weights' rows are read once, straight into registers, K dealt to four waves, whose sums are added in
+// order through LDS.  A lane takes 16 bytes at 16 q and at 64 + 16 q of a block's 128 of its row, q = lane /
+// 16, of both operands: products are added in an order of the instruction's own, the same for both.
+__device__ __forceinline__ i32x8_t load32(const uint8_t* p) {
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p), b = *reinterpret_cast<const u32x4_t*>(p + 64);
+  i32x8_t r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = (int)a[j];
+    r[4 + j] = (int)b[j];
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint2 pack4(const f32x4_t& v) { return make_uint2(bf16pack(v[0], v[1]), bf16pack(v[2], v[3])); }
+
+constexpr int W = 4;
+
+template <int EPI>
+__global__ __launch_bounds__(64 * W) void fp8_few_kernel(Fp8GemmArgs p) {
+  constexpr int B = EPI == MX_EPI_SWIGLU ? 2 : 1;   // weight streams
+  constexpr int AHEAD = 4 / B;                      // blocks of 128 in flight
+  __shared__ __attribute__((aligned(16))) float red[W][B][16][20];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, q = lane >> 4;
+  const int NT = p.N / 16, nt = blockIdx.x % NT;
+  int g, m0, m_end;
+  if (!find_rows<16>(p.offsets, p.G, p.M, blockIdx.x / NT, g, m0, m_end)) return;
+  const bool split = EPI != MX_EPI_SWIGLU && p.b2 != nullptr;
+  const int K1 = split ? p.ksplit : p.K, K2 = EPI == MX_EPI_SWIGLU ? p.K : p.K - K1;
+  const int nk = p.K / BLK, k0 = wave * nk / W, k1 = (wave + 1) * nk / W;
+  const int arow = min(m0 + li, m_end - 1);
+  const uint8_t* pa = p.a + (long long)arow * p.K + 16 * q;
+  const float* ps = p.as + arow;
+  const long long wrow = (long long)g * p.N + nt * 16 + li, wblk = (long long)g * (p.N / BLK) + nt / 8;
+  // first source, second source: for SwiGLU two streams, otherwise two runs of columns
+  const uint8_t* pb[2] = {p.b + wrow * K1 + 16 * q, p.b2 ? p.b2 + wrow * K2 + 16 * q : nullptr};
+  const float* psb[2] = {p.bs + wblk * (K1 / BLK), p.bs2 ? p.bs2 + wblk * (K2 / BLK) : nullptr};
+
+  f32x4_t acc[B];
+#pragma unroll
+  for (int s = 0; s < B; ++s) acc[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int kb = k0; kb < k1; kb += AHEAD) {
+    i32x8_t fa[AHEAD], fb[AHEAD][B];
+    float sa[AHEAD], sb[AHEAD][B];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int k = min(kb + u, k1 - 1);   // one block more than once rather than a load under a condition
+#pragma unroll
+      for (int s = 0; s < B; ++s) {
+        const bool second = EPI == MX_EPI_SWIGLU ? s == 1 : k * BLK >= K1;
+        const int at = EPI != MX_EPI_SWIGLU && second ? k - K1 / BLK : k;
+        fb[u][s] = load32((second ? pb[1] : pb[0]) + (long long)at * BLK);
+        sb[u][s] = (second ? psb[1] : psb[0])[at];
+      }
+      fa[u] = load32(pa + (long long)k * BLK);
+      sa[u] = ps[(long long)k * p.M];
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+      for (int s = 0; s < B; ++s) {
+        const f32x4_t part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            fb[u][s], fa[u], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, ONE, 0, ONE);
+        const float f = kb + u < k1 ? sa[u] * sb[u][s] : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[s][e] = __builtin_fmaf(f, part[e], acc[s][e]);
+      }
+  }
+  // lane: row li of each 16, columns 4 q .. 4 q + 3
+#pragma unroll
+  for (int s = 0; s < B; ++s) *reinterpret_cast<f32x4_t*>(&red[wave][s][li][4 * q]) = acc[s];
+  __syncthreads();
+  if (wave == 0) {
+    const int m = lane >> 2, c = 4 * (lane & 3), row = m0 + m;
+    if (row >= m_end) return;
+    f32x4_t v[B];
+#pragma unroll
+    for (int s = 0; s < B; ++s) {
+      v[s] = *reinterpret_cast<const f32x4_t*>(&red[0][s][m][c]);
+#pragma unroll
+      for (int w = 1; w < W; ++w) {
+        const f32x4_t o = *reinterpret_cast<const f32x4_t*>(&red[w][s][m][c]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[s][e] += o[e];
+      }
+    }
+    const int col = nt * 16 + c;
+    const long long o = (long long)row * p.N + col;
+    auto at = [&](void* base, long long off) { return reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(base) + off); };
+    if constexpr (EPI == MX_EPI_SWIGLU) {
+      f32x4_t hv;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) hv[e] = v[0][e] * sigmoid_f32(v[0][e]) * v[B - 1][e];
+      if (p.out0) *at(p.out0, o) = pack4(v[0]);
+      if (p.out1) *at(p.out1, o) = pack4(v[B - 1]);
+      *at(p.out2, o) = pack4(hv);
+    } else if constexpr (EPI == MX_EPI_SWIGLU_BWD) {
+      const uint2 aw = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux0) + o);
+      const uint2 bw = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux1) + o);
+      f32x4_t da, db;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t ua = e < 2 ? aw.x : aw.y, ub = e < 2 ? bw.x : bw.y;
+        const float a = bf16_to_f32((bf16_t)(ua >> (16 * (e & 1)))), b = bf16_to_f32((bf16_t)(ub >> (16 * (e & 1))));
+        const float sg = sigmoid_f32(a);
+        da[e] = v[0][e] * b * sg * (1.0f + a * (1.0f - sg));
+        db[e] = v[0][e] * a * sg;
+      }
+      const long long o2 = (long long)row * (2 * p.N) + col;
+      *at(p.out0, o2) = pack4(da);
+      *at(p.out0, o2 + p.N) = pack4(db);
+    } else {
+      *at(p.out0, o) = pack4(v[0]);
+    }
+  }
+}
+
+template <int EPI>
+hipError_t launch_few(const Fp8GemmArgs& a, hipStream_t s) {
+  const long long rows = (a.M + 15) / 16 + std::min(a.G, a.M);
+  fp8_few_kernel<EPI><<<dim3((unsigned)(rows * (a.N / 16))), dim3(64 * W), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+// ---- Pipelined products: 256 x 256 tiles ------------------------------------------------------------
+// Persistent, one workgroup per CU, 8 waves (two per SIMD).  A stage is a block of 128 of K: 32 KiB of
+// activations, 32 KiB of weights and their scales, brought into LDS by direct loads (lane l's 16 bytes land at
+// M0 + 16 l); two stages, one of them in flight while the other is multiplied, and the stream of stages runs
+// on across tiles, so the next tile's first one loads during an epilogue.  Rows are whole 128-byte lines,
+// their 16-byte chunk c at c ^ ((row >> 1) & 7).
+//
+// Wave (wm, wn) multiplies 64 columns at 64 wn and the rows 64 i + 32 wm .. + 31 of every quarter i of the
+// tile: a group's last tile leaves out the quarters that it does not fill, loads, products and stores, and
+// all waves leave out the same.  (128 x 256 tiles in three stages, whose waves of 64 x 64 read a third more of
+// LDS for a product and meet at twice as many barriers: 1002 us for 950, 32768 x 3584 by 64 weights of 3584 x
+// 2560 with SwiGLU.)
+constexpr int PM = 256, PN = 256;
+constexpr int PSCALE = (PM + PN) * BLK;   // a stage's scales: 8 runs of 64 floats, one for each wave's load
+constexpr int PSTAGE = PSCALE + 8 * 256;
+constexpr int PNST = 2;
+constexpr int PSTART = PNST * PSTAGE;     // first row of each group (clamped), G + 1 <= 1025 ints
+constexpr int PPREF = PSTART + 4 * 1028;  // row tiles of the groups before each, G + 1 ints
+constexpr int PLDS = PPREF + 4 * 1028;
+static_assert(PLDS <= 160 * 1024, "LDS of a CU");
+
+// A direct load of 16 (4) bytes a lane from base + offset to LDS, lane l's at lds + 16 l (4 l), where live > FROM
+// (by the execution mask: a branch would part the code that stands around it).  It writes no register, so
+// nothing but the ring's own waits has to know of it; the compiler, which would let every LDS read wait for
+// its builtin form, counts reads on their own.  All lanes of the wave are active.
+template <int FROM>
+__device__ __forceinline__ void direct16(int live, const void* base, uint32_t offset, uint32_t lds) {
+  uint32_t m0;   // as it was: the compiler does not know that it is used here
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_cmp_gt_i32 %1, %5\n\ts_cselect_b64 exec, -1, 0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+      "global_load_lds_dwordx4 %3, %4\n\ts_mov_b64 exec, -1\n\ts_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(__builtin_amdgcn_readfirstlane(live)), "s"(lds), "v"(offset), "s"(base), "n"(FROM)
+      : "scc");
+}
+template <int FROM>
+__device__ __forceinline__ void direct4(int live, const void* base, uint32_t offset, uint32_t lds) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_cmp_gt_i32 %1, %5\n\ts_cselect_b64 exec, -1, 0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+      "global_load_lds_dword %3, %4\n\ts_mov_b64 exec, -1\n\ts_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(__builtin_amdgcn_readfirstlane(live)), "s"(lds), "v"(offset), "s"(base), "n"(FROM)
+      : "scc");
+}
+__device__ __forceinline__ uint32_t lds_off(const void* ptr) {
+  return (uint32_t)(uintptr_t)((const __attribute__((address_space(3))) char*)ptr);
+}
+__device__ __forceinline__ int lds_i32(uint32_t addr) {   // a value all lanes share
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(addr) : "memory");
+  return __builtin_amdgcn_readfirstlane(v);
+}
+struct PTile {
+  int g, m0, m_end, nt, quarters;   // quarters: of 64 rows, that the group fills, 1 to 4
+};
+// Tile Lt of the launch.  Groups in order; in a group the row tiles run fastest, up to 4 of them, then the
+// column tiles: the 32 workgroups of an XCD then share a weight tile among up to 4 and a row tile among at
+// least 8.
+constexpr int PROWS = 4;
+__device__ __forceinline__ bool pipe_tile(const Fp8GemmArgs& p, int Lt, int NT, uint32_t lds, PTile& t) {
+  const uint32_t pref = lds + PPREF, start = lds + PSTART;
+  const int row = Lt / NT;
+  if (row >= lds_i32(pref + 4 * p.G)) return false;
+  int lo = 0, hi = p.G;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (lds_i32(pref + 4 * mid) <= row) lo = mid; else hi = mid;
+  }
+  t.g = lo;
+  const int before = lds_i32(pref + 4 * lo), rows = lds_i32(pref + 4 * lo + 4) - before;
+  const int q = Lt - before * NT, band = q / (PROWS * NT), in_band = q - band * PROWS * NT;
+  const int high = min(PROWS, rows - band * PROWS);
+  t.nt = in_band / high;
+  const int mt = band * PROWS + in_band - t.nt * high;
+  const int r0 = lds_i32(start + 4 * lo), r1 = lds_i32(start + 4 * lo + 4);
+  t.m0 = r0 + mt * PM;
+  t.m_end = max(r1, r0);
+  t.quarters = min(4, (t.m_end - t.m0 + 63) >> 6);
+  return true;
+}
+
+// The sources of a tile's stages: instruction j of a wave fills rows 64 j + 8 wave + lane / 8 of both operands,
+// physical chunk lane % 8, and one loads a scale for each lane.  Bases and steps are the wave's (scalar), offsets
+// the lane's; the weights' rows of one instruction are 64 (32 of a source for SwiGLU) below the last one's.
+struct PLoad {
+  const uint8_t* a;
+  const uint8_t* b;
+  const char* s;
+  uint32_t oa[4], ob, os;
+  long long b_step;   // bytes from an instruction's rows to the next one's
+  long long s_step;   // bytes from one block of K to the next
+};
+template <int EPI>
+__device__ __forceinline__ void weight_sources(const Fp8GemmArgs& p, const PTile& t, bool second, int K1, int wave,
+                                               int lane, PLoad& L) {
+  const int K = second ? p.K - K1 : K1;   // columns of the source
+  const int row = 8 * wave + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+  const long long gn = (long long)t.g * p.N;
+  if constexpr (EPI == MX_EPI_SWIGLU) {   // 16 gate rows and 16 up rows in turn
+    L.b = ((wave >> 1 & 1) ? p.b2 : p.b) + (gn + t.nt * 128 + 16 * (wave >> 2)) * K;
+    L.ob = (uint32_t)((row & 15) * K + 16 * c);
+    L.b_step = 32LL * K;
+  } else {
+    L.b = (second ? p.b2 : p.b) + (gn + t.nt * PN) * K;
+    L.ob = (uint32_t)(row * K + 16 * c);
+    L.b_step = 64LL * K;
+  }
+  if (wave == 4 || wave == 5) {   // the weights' scales: gate and up, or of the tile's two column blocks
+    const int kb = K / BLK;
+    const bool up = EPI == MX_EPI_SWIGLU ? wave == 5 : second;
+    const long long blk = gn / BLK + (EPI == MX_EPI_SWIGLU ? t.nt : 2 * t.nt + wave - 4);
+    L.s = reinterpret_cast<const char*>((up ? p.bs2 : p.bs) + blk * kb);
+    L.os = 0;
+    L.s_step = 4;
+  }
+}
+template <int EPI>
+__device__ __forceinline__ void tile_sources(const Fp8GemmArgs& p, const PTile& t, int K1, int wave, int lane, PLoad& L) {
+  const int most = t.m_end - 1 - t.m0;
+  L.a = p.a + (long long)t.m0 * p.K;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = 64 * j + 8 * wave + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+    L.oa[j] = (uint32_t)(min(row, most) * p.K + 16 * c);
+  }
+  // waves 0 to 3: the rows' scales; 4 and 5: the weights'; 6 and 7 fill what nothing reads
+  L.s = reinterpret_cast<const char*>(p.as + t.m0);
+  L.os = (uint32_t)(min(64 * min(wave, 3) + lane, most) * 4);
+  L.s_step = 4LL * p.M;
+  weight_sources<EPI>(p, t, false, K1, wave, lane, L);
+}
+
+// Fragments of a block of 128 for the 16 x 16 x 128 instruction: lane (li, q) takes chunks q and 4 + q of its
+// row, of both operands.  x: the address of a row's chunk q; its chunk 4 + q is there with bit 6 flipped.
+struct BFrag {
+  u32x4_t v[4][2];   // 16 columns, chunk
+  float scale[2];
+};
+struct AFrag {
+  u32x4_t v[2][2];   // 16 rows, chunk
+  float scale[2];
+};
+__device__ __forceinline__ u32x4_t lds16(const char* plds, uint32_t at) { return *reinterpret_cast<const u32x4_t*>(plds + at); }
+__device__ __forceinline__ float lds4(const char* plds, uint32_t at) { return *reinterpret_cast<const float*>(plds + at); }
+__device__ __forceinline__ void read_b(BFrag& f, const char* plds, uint32_t x, uint32_t s) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    f.v[c][0] = lds16(plds, x + c * 16 * BLK);
+    f.v[c][1] = lds16(plds, (x ^ 64u) + c * 16 * BLK);
+  }
+  f.scale[0] = lds4(plds, s);
+  f.scale[1] = lds4(plds, s + 256);
+}
+template <int I, int U>
+__device__ __forceinline__ u32x4_t read_rows(const char* plds, uint32_t x, int chunk) {   // of quarter I
+  return lds16(plds, (chunk ? x ^ 64u : x) + (I * 64 + U * 16) * BLK);
+}
+__device__ __forceinline__ i32x8_t frag8(const u32x4_t& lo, const u32x4_t& hi) {
+  i32x8_t r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = (int)lo[j];
+    r[4 + j] = (int)hi[j];
+  }
+  return r;
+}
+
+// Two 16 x 16 blocks side by side, lane (li, q) with columns 4 q .. 4 q + 3 of row li in each, to 8 columns a
+// lane: after the swaps lane (li, 2 h + e) holds columns 8 e .. 8 e + 7 of block h.
+__device__ __forceinline__ void side_by_side(const f32x4_t& l, const f32x4_t& r, float (&x)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(l[e]), __float_as_uint(r[e]), false, false);
+    const auto v = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+    x[e] = __uint_as_float(v[0]);
+    x[4 + e] = __uint_as_float(v[1]);
+  }
+}
+
+// acc[2 i + u][c]: rows 64 i + 32 wm + 16 u + li, columns 16 c + 4 q of the wave's 64 (for SwiGLU gate, up, gate,
+// up).
+template <int EPI>
+__device__ __forceinline__ void pipe_epilogue(const Fp8GemmArgs& p, const PTile& t, const f32x4_t (&acc)[8][4], int wm,
+                                              int wn, int lane) {
+  const int cl = 8 * (lane >> 4), li = lane & 15;   // 16 h + 8 e, q = 2 h + e
+  auto at = [](void* base, long long off) { return reinterpret_cast<u32x4_t*>(reinterpret_cast<bf16_t*>(base) + off); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= t.quarters) break;
+    const int r0 = t.m0 + i * 64 + wm * 32 + li;
+    if constexpr (EPI == MX_EPI_SWIGLU) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x4_t(&c)[4] = acc[2 * i + u];
+        f32x4_t hv[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) hv[b][e] = c[2 * b][e] * sigmoid_f32(c[2 * b][e]) * c[2 * b + 1][e];
+        float g[8], up[8], x[8];
+        side_by_side(c[0], c[2], g);
+        side_by_side(c[1], c[3], up);
+        side_by_side(hv[0], hv[1], x);
+        const int row = r0 + 16 * u;
+        if (row >= t.m_end) continue;
+        const long long o = (long long)row * p.N + t.nt * 128 + wn * 32 + cl;
+        if (p.out0) *at(p.out0, o) = pack8(g);
+        if (p.out1) *at(p.out1, o) = pack8(up);
+        *at(p.out2, o) = pack8(x);
+      }
+    } else {
+      // the stash of 32 rows is loaded before their first store, which it may alias as far as the compiler
+      // knows; rows past the group are clamped on load and dropped on store
+      u32x4_t sa[2][2], sb[2][2];
+      if constexpr (EPI == MX_EPI_SWIGLU_BWD) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const long long o = (long long)min(r0 + 16 * u, t.m_end - 1) * p.N + t.nt * PN + wn * 64 + 32 * b + cl;
+            sa[u][b] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const bf16_t*>(p.aux0) + o);
+            sb[u][b] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const bf16_t*>(p.aux1) + o);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float x[8];
+          side_by_side(acc[2 * i + u][2 * b], acc[2 * i + u][2 * b + 1], x);
+          const int row = r0 + 16 * u, col = t.nt * PN + wn * 64 + 32 * b + cl;
+          if (row >= t.m_end) continue;
+          if constexpr (EPI == MX_EPI_SWIGLU_BWD) {
+            float a[8], bb[8], da[8], db[8];
+            unpack8(sa[u][b], a);
+            unpack8(sb[u][b], bb);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float sg = sigmoid_f32(a[e]);
+              da[e] = x[e] * bb[e] * sg * (1.0f + a[e] * (1.0f - sg));
+              db[e] = x[e] * a[e] * sg;
+            }
+            const long long o = (long long)row * (2 * p.N) + col;
+            *at(p.out0, o) = pack8(da);
+            *at(p.out0, o + p.N) = pack8(db);
+          } else {
+            *at(p.out0, (long long)row * p.N + col) = pack8(x);
+          }
+        }
+    }
+  }
+}
+
+template <int EPI>
+__global__ __launch_bounds__(512, 2) void fp8_pipe_kernel(Fp8GemmArgs p) {
+  extern __shared__ __attribute__((aligned(128))) char plds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave & 1, wn = wave >> 1, li = lane & 15, q = lane >> 4;
+  const int NT = p.N / (EPI == MX_EPI_SWIGLU ? 128 : PN), nk = p.K / BLK;
+  const uint32_t lds0 = lds_off(plds);
+  if (wave == 0) {   // the groups' first rows and row tiles, 64 groups at a time
+    int* start = reinterpret_cast<int*>(plds + PSTART);
+    int* pref = reinterpret_cast<int*>(plds + PPREF);
+    int tiles = 0;
+    for (int g0 = 0; g0 <= p.G; g0 += 64) {
+      const int g = g0 + lane;
+      const int r0 = min(max(p.offsets[min(g, p.G)], 0), p.M);
+      const int r1 = min(max(p.offsets[min(g + 1, p.G)], 0), p.M);
+      const int rows = g < p.G ? max(r1, r0) - r0 : 0;
+      const int n = (rows + PM - 1) / PM;
+      int sum = n;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const int o = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += o;
+      }
+      if (g <= p.G) {
+        start[g] = r0;
+        pref[g] = tiles + sum - n;
+      }
+      tiles += __shfl(sum, 63, 64);
+    }
+  }
+  __syncthreads();
+  // Each XCD (workgroup b runs on XCD b % 8) takes a run of an eighth of the tiles, its workgroups in turn: the
+  // column tiles of a row tile, which share its rows, run side by side there, and so do the row tiles of a
+  // group, which share its weights.  A group's last tile may have a quarter of another's work, but shares by an
+  // estimated time, with the next tile taken from a counter, gained and lost as much: 287 us for 294 on 32768
+  // rows of 64 groups, K 2048, N 2816, 380 for 371 on N 4096.  What a lighter CU leaves, the others' clock takes.
+  const int U = lds_i32(lds0 + PPREF + 4 * p.G) * NT;
+  const int nb = gridDim.x, xcd = (int)blockIdx.x & 7;
+  const int first = (int)((long long)xcd * U / 8), last = (int)((long long)(xcd + 1) * U / 8);
+  const int mates = nb / 8 + (xcd < nb % 8 ? 1 : 0);   // workgroups of the XCD
+  const bool split = EPI != MX_EPI_SWIGLU && p.b2 != nullptr;
+  const int K1 = split ? p.ksplit : p.K;
+
+  // Producer: the next stage to load (tile pl, block pj), its slot; live: the tile's quarters, 0 past the last.
+  int pl = first + (int)(blockIdx.x >> 3), pj = 0, pslot = 0, live = 0;
+  PTile pt;
+  PLoad L;
+  auto pseek = [&]() {
+    live = 0;
+    if (pl < last && pipe_tile(p, pl, NT, lds0, pt)) {
+      live = pt.quarters;
+      tile_sources<EPI>(p, pt, K1, wave, lane, L);
+    }
+  };
+  // Load k of a stage's nine: the scales, the weights' four, the rows' four (those of the tile's quarters).
+  auto load = [&](auto index) {
+    constexpr int k = decltype(index)::value;
+    const uint32_t st = lds0 + pslot * PSTAGE;
+    if constexpr (k == 0) direct4<0>(live, L.s, L.os, st + PSCALE + wave * 256);
+    else if constexpr (k < 5) direct16<0>(live, L.b + (k - 1) * L.b_step, L.ob, st + PM * BLK + (8 * (k - 1) + wave) * 1024);
+    else direct16<k - 5>(live, L.a, L.oa[k < 5 ? 0 : k - 5], st + (8 * (k - 5) + wave) * 1024);
+  };
+  auto advance = [&]() {   // to the next stage
+    if (live == 0) return;
+    L.s += L.s_step;
+    L.b += BLK;
+    L.a += BLK;
+    pslot ^= 1;
+    ++pj;
+    if (pj == nk) {
+      pj = 0;
+      pl += mates;
+      pseek();
+    } else if (split && pj == K1 / BLK) {
+      weight_sources<EPI>(p, pt, true, K1, wave, lane, L);
+    }
+  };
+  auto each = [](auto&& f) {
+    f(std::integral_constant<int, 0>());
+    f(std::integral_constant<int, 1>());
+    f(std::integral_constant<int, 2>());
+    f(std::integral_constant<int, 3>());
+    f(std::integral_constant<int, 4>());
+    f(std::integral_constant<int, 5>());
+    f(std::integral_constant<int, 6>());
+    f(std::integral_constant<int, 7>());
+  };
+  pseek();
+  each(load);
+  load(std::integral_constant<int, 8>());
+
+  // LDS addresses of this lane in a stage: chunk q of its rows, and their scales.
+  const uint32_t chunk = (uint32_t)(16 * (q ^ ((li >> 1) & 7)));
+  const uint32_t oa = (uint32_t)((wm * 32 + li) * BLK) + chunk, ob = (uint32_t)(PM * BLK + (wn * 64 + li) * BLK) + chunk;
+  const uint32_t osa = (uint32_t)(PSCALE + 4 * (wm * 32 + li));
+  const uint32_t osb = (uint32_t)(PSCALE + 4 * 256 + (EPI == MX_EPI_SWIGLU ? 0 : 256 * (wn >> 1)));
+
+  int slot = 0;   // of the next stage to multiply
+  while (live != 0) {   // the tile whose first stage was loaded last
+    const PTile t = pt;
+    f32x4_t acc[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // Q quarters, 2 Q runs of 16 rows.  Between the matrix instructions of one run stand the scaling and
+    // adding of the run before, the last run's beside the next stage's first.
+    auto multiply = [&](auto count) {
+      constexpr int Q = decltype(count)::value;
+      f32x4_t part[2][4];
+      float f[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f[u][0] = f[u][1] = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) part[u][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
+      auto add = [&](auto index, int c) {   // run `index`
+        constexpr int i = decltype(index)::value;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][c][e] = __builtin_fmaf(f[i & 1][c & 1], part[i & 1][c][e], acc[i][c][e]);
+      };
+      for (int kb = 0; kb < nk; ++kb) {
+        advance();
+        // this wave's part of the stage (and an epilogue's stores), then everybody's
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        const uint32_t st = (uint32_t)(slot * PSTAGE);
+        slot ^= 1;
+        BFrag fb;
+        AFrag fa[2];
+        fa[0].v[0][0] = read_rows<0, 0>(plds, st + oa, 0);
+        fa[0].v[0][1] = read_rows<0, 0>(plds, st + oa, 1);
+        read_b(fb, plds, st + ob, st + osb);
+        fa[0].v[1][0] = read_rows<0, 1>(plds, st + oa, 0);
+        fa[0].v[1][1] = read_rows<0, 1>(plds, st + oa, 1);
+        fa[0].scale[0] = lds4(plds, st + osa);
+        fa[0].scale[1] = lds4(plds, st + osa + 64);
+        __builtin_amdgcn_sched_barrier(0);
+        each(load);   // the next stage into the other slot: every wave is past its reads
+        load(std::integral_constant<int, 8>());
+        __builtin_amdgcn_sched_barrier(0);
+        // Between two matrix instructions of a run stand one read of the next quarter and the scaling of a block
+        // of the run before.  (The nine loads between them too, one each: 1039 us for 1003, the prompt's step.)
+        auto run = [&](auto index) {
+          constexpr int i = decltype(index)::value, u = i & 1;
+          if constexpr (i < 2 * Q) {
+            const AFrag& a = fa[(i >> 1) & 1];
+            AFrag& ahead = fa[((i >> 1) + 1) & 1];
+            const i32x8_t rows = frag8(a.v[u][0], a.v[u][1]);
+            auto block = [&](auto column) {
+              constexpr int c = decltype(column)::value;
+              part[u][c] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                  frag8(fb.v[c][0], fb.v[c][1]), rows, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, ONE, 0, ONE);
+              if constexpr (i / 2 + 1 < Q) {
+                if constexpr (u == 0) ahead.v[c >> 1][c & 1] = read_rows<i / 2 + 1, (c >> 1)>(plds, st + oa, c & 1);
+                else if constexpr (c < 2) ahead.scale[c] = lds4(plds, st + osa + ((i / 2 + 1) * 64 + c * 16) * 4);
+              }
+              add(std::integral_constant<int, (i + 2 * Q - 1) % (2 * Q)>(), c);
+              __builtin_amdgcn_sched_barrier(0);
+            };
+            block(std::integral_constant<int, 0>());
+            block(std::integral_constant<int, 1>());
+            block(std::integral_constant<int, 2>());
+            block(std::integral_constant<int, 3>());
+#pragma unroll
+            for (int j = 0; j < 2; ++j) f[u][j] = a.scale[u] * (EPI == MX_EPI_SWIGLU ? fb.scale[j] : fb.scale[0]);
+          }
+        };
+        each(run);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) add(std::integral_constant<int, 2 * Q - 1>(), c);
+    };
+    switch (t.quarters) {
+      case 1: multiply(std::integral_constant<int, 1>()); break;
+      case 2: multiply(std::integral_constant<int, 2>()); break;
+      case 3: multiply(std::integral_constant<int, 3>()); break;
+      default: multiply(std::integral_constant<int, 4>());
+    }
+    pipe_epilogue<EPI>(p, t, acc, wm, wn, lane);
+  }
+}
+
+int device_cus() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+template <int EPI>
+hipError_t launch_pipe(const Fp8GemmArgs& a, hipStream_t s) {
+  // the dynamic LDS limit above 64 KiB is an attribute of the kernel on each device: set once (bit d of the
+  // mask; devices past 63 set it on every launch)
+  static unsigned long long attr_set = 0;
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) dev = 0;
+  if (dev >= 64 || !((attr_set >> dev) & 1ull)) {
+    const hipError_t e = hipFuncSetAttribute((const void*)fp8_pipe_kernel<EPI>, hipFuncAttributeMaxDynamicSharedMemorySize, PLDS);
+    if (e != hipSuccess) return e;
+    if (dev < 64) attr_set |= 1ull << dev;
+  }
+  const long long tiles = ((a.M + PM - 1) / PM + std::min(a.G, a.M)) * (a.N / (EPI == MX_EPI_SWIGLU ? 128 : PN));
+  fp8_pipe_kernel<EPI><<<dim3((unsigned)std::min<long long>(tiles, device_cus())), dim3(512), PLDS, s>>>(a);
+  return hipGetLastError();
+}
+
+template <int EPI>
+hipError_t launch_epi(const Fp8GemmArgs& a, hipStream_t s) {
+  // A wave's 16 rows read a group's weights at the rate of memory, but each further 16 read them again: 64
+  // groups of 2048 x 2048, microseconds of few rows / of 256-row tiles, at 1, 4, 8, 16 rows a group 46 / 51,
+  // 50 / 50, 55 / 52, 68 / 52; with SwiGLU (N 1024) 28 / 46, 40 / 52, 48 / 54, 66 / 60.  And a tile's workgroup
+  // reads its weights alone: one group, K 7168, N 2048, at 16 and 64 rows 10 / 46 and 18 / 47.
+  const bool fits = ((a.M + 15) / 16 + a.G) * (long long)(a.N / 16) <= 1 << 22;   // below 2^31 threads
+  if ((a.M <= 64 || a.M <= 8LL * a.G) && fits) return launch_few<EPI>(a, s);
+  // a tile's columns: 256 of N, or 128 gate and 128 up columns
+  if (a.N % (EPI == MX_EPI_SWIGLU ? 128 : PN) == 0) return launch_pipe<EPI>(a, s);
+  return launch_tiles<EPI>(a, s);
+}
+
+}  // namespace
+
+size_t fp8_gemm_ws_bytes(int G, long long M, long long N, long long K) {
+  (void)G; (void)M; (void)N; (void)K;
+  return 0;
+}
+
+hipError_t launch_fp8_gemm(int epi, const Fp8GemmArgs& a, hipStream_t s) {
+  if (a.M == 0) return hipSuccess;
+  switch (epi) {
+    case MX_EPI_SWIGLU: return launch_epi<MX_EPI_SWIGLU>(a, s);
+    case MX_EPI_SWIGLU_BWD: return launch_epi<MX_EPI_SWIGLU_BWD>(a, s);
+    default: return launch_epi<MX_EPI_STORE>(a, s);
+  }
+}
+
+}  // namespace moe

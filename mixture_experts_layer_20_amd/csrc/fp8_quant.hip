@@ -1,0 +1,152 @@
+// Quantizers to 8-bit floating point (E4M3) with a float scale for each block of 128.
+//
+//   scale = max(|v|, 2^-100) / 448 over a block;  code = E4M3(448 v / max |v|), to nearest, ties to even
+//
+// Activations have a block for 128 elements of a row, weights for 128 x 128: the weights' blocks lie
+// square, so the transposed weights that the data gradient multiplies with are the same codes and scales
+// in another order, not a second rounding.
+//
+// A bf16 v times 448 is exact in fp32 (8 + 3 bits), and the quotient of an 11-bit by an 8-bit number is
+// either a number of at most 5 bits, where two codes meet, or further than 2^-14 of itself from every such
+// number: rounding the quotient to fp32 first changes no code.
+#include "train_step.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int BLK = 128;
+constexpr float TOP = 448.0f;
+constexpr float TINY = 0x1p-100f;
+
+__device__ __forceinline__ uint32_t row16_max(uint32_t b) {   // of a row of 16 lanes
+  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0xB1, 0xf, 0xf, false));    // quad_perm 1,0,3,2
+  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x4E, 0xf, 0xf, false));    // quad_perm 2,3,0,1
+  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x124, 0xf, 0xf, false));   // row_ror 4
+  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x128, 0xf, 0xf, false));   // row_ror 8
+  return b;
+}
+
+// Bits of the largest magnitude of 8 bf16 values (as fp32 bits; a NaN is above all).
+__device__ __forceinline__ uint32_t max8(const u32x4_t& w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) m = max(m, max((w[q] & 0x7fffu) << 16, w[q] & 0x7fff0000u));
+  return m;
+}
+
+// A block's largest magnitude as it is divided by, and its scale: NaN where the block has a NaN or an
+// infinity, so that every product with it is NaN.
+__device__ __forceinline__ float block_top(uint32_t bits) { return fmaxf(__uint_as_float(bits), TINY); }
+__device__ __forceinline__ float block_scale(uint32_t bits) {
+  return bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : block_top(bits) / TOP;
+}
+
+__device__ __forceinline__ float quotient(uint32_t bits, float top) {
+  return fminf(fmaxf(__uint_as_float(bits) * TOP / top, -TOP), TOP);
+}
+__device__ __forceinline__ u32x2_t codes8(const u32x4_t& w, float top) {
+  u32x2_t c;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(w[2 * q] << 16, top), quotient(w[2 * q] & 0xffff0000u, top), 0, false);
+    c[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(w[2 * q + 1] << 16, top),
+                                                     quotient(w[2 * q + 1] & 0xffff0000u, top), lo, true);
+  }
+  return c;
+}
+
+// Rows: 8 elements a lane, 16 lanes a block.
+__global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const bf16_t* __restrict__ x, long long R, int K,
+                                                             long long ldx, uint8_t* __restrict__ codes,
+                                                             float* __restrict__ scales) {
+  const int nch = K >> 3;   // a multiple of 16
+  const long long total = R * nch, stride = (long long)gridDim.x * 256;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += stride) {
+    const long long r = i / nch;
+    const int c = (int)(i - r * nch);
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + r * ldx + (long long)c * 8);
+    const uint32_t bits = row16_max(max8(v));
+    *reinterpret_cast<u32x2_t*>(codes + r * K + (long long)c * 8) = codes8(v, block_top(bits));
+    if ((c & 15) == 0) scales[(long long)(c >> 4) * R + r] = block_scale(bits);
+  }
+}
+
+// Weights: one 128 x 128 block a workgroup; the codes also transposed, through LDS.
+__global__ __launch_bounds__(256) void fp8_quant_weights_kernel(const bf16_t* __restrict__ w, int N, int K,
+                                                                uint8_t* __restrict__ codes, float* __restrict__ scales,
+                                                                uint8_t* __restrict__ codes_t, float* __restrict__ scales_t) {
+  __shared__ uint32_t top_s[4];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[BLK][BLK + 16];
+  const int nb = N / BLK, kb = K / BLK;
+  const long long blk = blockIdx.x;
+  const int g = (int)(blk / ((long long)nb * kb)), rem = (int)(blk - (long long)g * nb * kb);
+  const int bn = rem / kb, bk = rem - bn * kb;
+  const int row = threadIdx.x >> 4, c = threadIdx.x & 15;   // rows row + 16 i, 8 elements at 8 c
+  const bf16_t* src = w + ((long long)g * N + (long long)bn * BLK) * K + (long long)bk * BLK + 8 * c;
+  u32x4_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4_t*>(src + (long long)(row + 16 * i) * K);
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bits = max(bits, max8(v[i]));
+  bits = row16_max(bits);
+  bits = max(bits, (uint32_t)__shfl_xor((int)bits, 16, 64));
+  bits = max(bits, (uint32_t)__shfl_xor((int)bits, 32, 64));
+  if ((threadIdx.x & 63) == 0) top_s[threadIdx.x >> 6] = bits;
+  __syncthreads();
+  bits = max(max(top_s[0], top_s[1]), max(top_s[2], top_s[3]));
+  const float top = block_top(bits);
+  uint8_t* dst = codes + ((long long)g * N + (long long)bn * BLK) * K + (long long)bk * BLK + 8 * c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const u32x2_t q = codes8(v[i], top);
+    *reinterpret_cast<u32x2_t*>(dst + (long long)(row + 16 * i) * K) = q;
+    if (codes_t) *reinterpret_cast<u32x2_t*>(&tile[row + 16 * i][8 * c]) = q;
+  }
+  if (threadIdx.x == 0) {
+    scales[((long long)g * nb + bn) * kb + bk] = block_scale(bits);
+    if (codes_t) scales_t[((long long)g * kb + bk) * nb + bn] = block_scale(bits);
+  }
+  if (!codes_t) return;
+  __syncthreads();
+  // transposed: column `col` of the block, rows 64 half .. + 63
+  const int col = threadIdx.x >> 1, half = threadIdx.x & 1;
+  uint8_t* to = codes_t + ((long long)g * K + (long long)bk * BLK + col) * N + (long long)bn * BLK + 64 * half;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    u32x4_t o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 64 * half + 16 * q + 4 * e;
+      o[e] = tile[r][col] | ((uint32_t)tile[r + 1][col] << 8) | ((uint32_t)tile[r + 2][col] << 16) |
+             ((uint32_t)tile[r + 3][col] << 24);
+    }
+    *reinterpret_cast<u32x4_t*>(to + 16 * q) = o;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quant_rows(const void* x, long long R, int K, long long ldx, uint8_t* codes, float* scales,
+                                 hipStream_t s) {
+  const long long total = R * (K / 8);
+  if (total == 0) return hipSuccess;
+  const int blocks = (int)std::min<long long>((total + 255) / 256, 256LL * 16);
+  fp8_quant_rows_kernel<<<dim3(blocks), dim3(256), 0, s>>>(reinterpret_cast<const bf16_t*>(x), R, K, ldx, codes, scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_quant_weights(const void* w, int G, int N, int K, uint8_t* codes, float* scales, uint8_t* codes_t,
+                                    float* scales_t, hipStream_t s) {
+  const long long blocks = (long long)G * (N / BLK) * (K / BLK);
+  fp8_quant_weights_kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(reinterpret_cast<const bf16_t*>(w), N, K, codes,
+                                                                        scales, codes_t, scales_t);
+  return hipGetLastError();
+}
+
+}  // namespace moe
