@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libmoe.so")
 
 SOURCES = ["api.cpp", "route.hip", "router_aux.hip", "dispatch.hip", "combine.hip", "grouped_gemm.hip",
            "grouped_gemm_pipe.hip", "mxfp8.hip", "block_norm.hip", "vocab_loss.hip",
-           "vocab_loss_pipe.hip", "vocab_loss_tile.hip", "grad_clip.hip", "route_scores.hip", "fp8_quant.hip", "fp8_gemm.hip",
+           "vocab_loss_pipe.hip", "vocab_loss_tile.hip", "grad_clip.hip", "route_scores.hip", "route_dense.hip", "fp8_quant.hip", "fp8_gemm.hip",
            "adamw.hip"]
 
 ARCH = "gfx950"

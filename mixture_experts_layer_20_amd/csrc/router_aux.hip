@@ -169,9 +169,9 @@ __device__ __forceinline__ void st8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// dx[t, :] += sum_e G[t, e] w[e, :], or = without ADD  (DX_TPB tokens per block, 8 columns per thread,
-// experts in order; the sum is rounded once to the element type on the way back).
-template <typename T, bool ADD>
+// dx[t, :] += sum_e G[t, e] w[e, :]  (DX_TPB tokens per block, 8 columns per thread, experts in
+// order; the sum is rounded once to the element type on the way back).
+template <typename T>
 __global__ __launch_bounds__(256) void aux_dx_kernel(const float* G, const T* w, int ntok, int d, int E, T* dx) {
   __shared__ float gs[DX_TPB][256];
   const int t0 = blockIdx.x * DX_TPB;
@@ -203,14 +203,9 @@ __global__ __launch_bounds__(256) void aux_dx_kernel(const float* G, const T* w,
       if (i >= nt) break;
       float v[8];
       T* out = dx + (size_t)(t0 + i) * d + c;
-      if constexpr (ADD) {
-        ld8(out, v);
+      ld8(out, v);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += acc[i][q];
-      } else {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = acc[i][q];
-      }
+      for (int q = 0; q < 8; ++q) v[q] += acc[i][q];
       st8(out, v);
     }
   }
@@ -252,16 +247,14 @@ __global__ __launch_bounds__(256) void aux_dw_partial_kernel(const float* G, con
     if (e0 + i < E) partial[((size_t)s * E + e0 + i) * d + col] = acc[i];
 }
 
-// dw[e, col] += sum over the splits in order, or = without ADD.
-template <bool ADD>
+// dw[e, col] += sum over the splits in order.
 __global__ __launch_bounds__(256) void aux_dw_reduce_kernel(const float* partial, int nsplit, int E, int d, float* dw) {
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x, n = (size_t)E * d;
   if (i >= n) return;
   float s = 0.0f;
 #pragma unroll 16
   for (int q = 0; q < nsplit; ++q) s += partial[(size_t)q * n + i];   // in order; loads overlap
-  if constexpr (ADD) dw[i] += s;
-  else dw[i] = s;
+  dw[i] += s;
 }
 
 inline size_t align256(size_t b) { return (b + 255) / 256 * 256; }
@@ -289,25 +282,6 @@ size_t router_aux_bwd_ws_bytes(long long T, long long d, int E) {
   return align256((size_t)T * E * sizeof(float)) + align256((size_t)nsplit * E * d * sizeof(float));
 }
 
-namespace {
-
-// dw and dx of a dense logit gradient G, added to what is there or not.
-template <typename T, bool ADD>
-hipError_t launch_dense_products(const float* G, const T* x, const T* w, int ntok, int d, int E, float* dw, T* dx,
-                                 float* partial, hipStream_t s) {
-  const int nsplit = ceil_div(ntok, DW_TSPLIT);
-  if (ntok > 0) {
-    const dim3 gdw(ceil_div(d, 256), ceil_div(E, DW_ET), nsplit);
-    hipLaunchKernelGGL((aux_dx_kernel<T, ADD>), dim3(ceil_div(ntok, DX_TPB)), dim3(256), 0, s, G, w, ntok, d, E, dx);
-    hipLaunchKernelGGL(aux_dw_partial_kernel<T>, gdw, dim3(256), 0, s, G, x, ntok, d, E, partial);
-  }
-  hipLaunchKernelGGL(aux_dw_reduce_kernel<ADD>, dim3(ceil_div((long long)E * d, 256)), dim3(256), 0, s, partial, nsplit,
-                     E, d, dw);
-  return hipGetLastError();
-}
-
-}  // namespace
-
 hipError_t launch_router_aux_bwd(const float* logits, const float* load_frac, const void* x, const void* w,
                                  int T, int d, int E, float weight, bool bf16, float* dw, void* dx, void* ws,
                                  hipStream_t s) {
@@ -316,28 +290,24 @@ hipError_t launch_router_aux_bwd(const float* logits, const float* load_frac, co
   float* G = reinterpret_cast<float*>(p);
   p += align256((size_t)T * E * sizeof(float));
   float* partial = reinterpret_cast<float*>(p);
+  const int nsplit = ceil_div(T, DW_TSPLIT);
   const float c = weight * (float)E / (float)T;
   hipLaunchKernelGGL(aux_grad_kernel, dim3(ceil_div(T, 4)), dim3(256), 0, s, logits, load_frac, T, E, c, G);
-  if (bf16)
-    return launch_dense_products<bf16_t, true>(G, reinterpret_cast<const bf16_t*>(x), reinterpret_cast<const bf16_t*>(w),
-                                               T, d, E, dw, reinterpret_cast<bf16_t*>(dx), partial, s);
-  return launch_dense_products<float, true>(G, reinterpret_cast<const float*>(x), reinterpret_cast<const float*>(w), T,
-                                            d, E, dw, reinterpret_cast<float*>(dx), partial, s);
-}
-
-size_t router_dense_bwd_ws_bytes(long long T, long long d, int E) {
-  const long long nsplit = (T + DW_TSPLIT - 1) / DW_TSPLIT;
-  return align256((size_t)nsplit * E * d * sizeof(float));
-}
-
-hipError_t launch_router_dense_bwd(const float* G, const void* x, const void* w, int T, int d, int E, bool bf16,
-                                   float* dw, void* dx, void* ws, hipStream_t s) {
-  float* partial = reinterpret_cast<float*>(ws);
-  if (bf16)
-    return launch_dense_products<bf16_t, false>(G, reinterpret_cast<const bf16_t*>(x), reinterpret_cast<const bf16_t*>(w),
-                                                T, d, E, dw, reinterpret_cast<bf16_t*>(dx), partial, s);
-  return launch_dense_products<float, false>(G, reinterpret_cast<const float*>(x), reinterpret_cast<const float*>(w), T,
-                                             d, E, dw, reinterpret_cast<float*>(dx), partial, s);
+  const dim3 gdw(ceil_div(d, 256), ceil_div(E, DW_ET), nsplit);
+  if (bf16) {
+    hipLaunchKernelGGL(aux_dx_kernel<bf16_t>, dim3(ceil_div(T, DX_TPB)), dim3(256), 0, s, G,
+                       reinterpret_cast<const bf16_t*>(w), T, d, E, reinterpret_cast<bf16_t*>(dx));
+    hipLaunchKernelGGL(aux_dw_partial_kernel<bf16_t>, gdw, dim3(256), 0, s, G, reinterpret_cast<const bf16_t*>(x),
+                       T, d, E, partial);
+  } else {
+    hipLaunchKernelGGL(aux_dx_kernel<float>, dim3(ceil_div(T, DX_TPB)), dim3(256), 0, s, G,
+                       reinterpret_cast<const float*>(w), T, d, E, reinterpret_cast<float*>(dx));
+    hipLaunchKernelGGL(aux_dw_partial_kernel<float>, gdw, dim3(256), 0, s, G, reinterpret_cast<const float*>(x),
+                       T, d, E, partial);
+  }
+  hipLaunchKernelGGL(aux_dw_reduce_kernel, dim3(ceil_div((long long)E * d, 256)), dim3(256), 0, s, partial, nsplit,
+                     E, d, dw);
+  return hipGetLastError();
 }
 
 }  // namespace moe

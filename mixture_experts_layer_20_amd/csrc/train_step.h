@@ -12,6 +12,7 @@ struct RouteScores {
   const float* bias;     // [E] or NULL
   int T, E, k, groups, topk_groups;
   bool sigmoid, renormalize;
+  bool whole;            // set by the launcher
   float scale;
 };
 hipError_t launch_route_scores(const RouteScores& r, int32_t* topk_idx, float* topk_gate, hipStream_t s);
