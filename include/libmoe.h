@@ -583,7 +583,8 @@ moe_status_t moe_route_bias_update(const int32_t* counts, int32_t E, float rate,
  *   code  = E4M3(448 v / max(largest magnitude, 2^-100)), rounded to nearest, ties to even (exactly)
  * A block that holds an infinity or a NaN gets a scale of NaN, and what is multiplied with it is NaN.
  * A product is that of the matrices which codes and scales stand for: each block's 128 products are summed
- * in fp32, scaled, and the blocks are added in fp32; outputs are bf16, rounded once.
+ * by the matrix instruction (8 neighbours at a time with 13 bits below the largest of them, those sums in
+ * fp32), scaled, and the blocks are added in fp32; outputs are bf16, rounded once.
  * Source: the pages' 8-bit recipe ("Olmo-core DDP MoE examples", "Other experiments in the report") in the
  * form with longer blocks. */
 
@@ -607,7 +608,7 @@ moe_status_t moe_fp8_quantize_weights(const void* w, int32_t G, int64_t N, int64
  *   gate/up data gradient contracts [dA | dB] with W1 and W3;
  *   epilogue, out0, out1, out2, aux0, aux1: as for moe_mx_gemm_rows.
  * K and N must be multiples of 128.  Outputs must not overlap inputs.  ws: moe_fp8_gemm_workspace_size
- * bytes (NULL allowed where that is 0; the size depends on the compute units of the current device). */
+ * bytes (NULL allowed where that is 0, as it is now for every size). */
 size_t moe_fp8_gemm_workspace_size(int32_t G, int64_t M, int64_t N, int64_t K);
 moe_status_t moe_fp8_gemm_rows(const uint8_t* a_codes, const float* a_scales, const uint8_t* b_codes,
                                const float* b_scales, const uint8_t* b2_codes, const float* b2_scales, int64_t b2_k,
