@@ -46,16 +46,24 @@ __device__ __forceinline__ float block_scale(uint32_t bits) {
   return bits >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : block_top(bits) / TOP;
 }
 
-__device__ __forceinline__ float quotient(uint32_t bits, float top) {
-  return fminf(fmaxf(__uint_as_float(bits) * TOP / top, -TOP), TOP);
+// 448 / top as a product and a division; both are made smaller where 448 v could pass the largest float.
+struct Ratio {
+  float mul, div;
+};
+__device__ __forceinline__ Ratio block_ratio(uint32_t bits) {
+  const float top = block_top(bits), less = top >= 0x1p64f ? 0x1p-32f : 1.0f;
+  return {TOP * less, top * less};
 }
-__device__ __forceinline__ u32x2_t codes8(const u32x4_t& w, float top) {
+__device__ __forceinline__ float quotient(uint32_t bits, const Ratio& by) {
+  return fminf(fmaxf(__uint_as_float(bits) * by.mul / by.div, -TOP), TOP);
+}
+__device__ __forceinline__ u32x2_t codes8(const u32x4_t& w, const Ratio& by) {
   u32x2_t c;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(w[2 * q] << 16, top), quotient(w[2 * q] & 0xffff0000u, top), 0, false);
-    c[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(w[2 * q + 1] << 16, top),
-                                                     quotient(w[2 * q + 1] & 0xffff0000u, top), lo, true);
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(w[2 * q] << 16, by), quotient(w[2 * q] & 0xffff0000u, by), 0, false);
+    c[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(w[2 * q + 1] << 16, by),
+                                                     quotient(w[2 * q + 1] & 0xffff0000u, by), lo, true);
   }
   return c;
 }
@@ -71,7 +79,7 @@ __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const bf16_t* __res
     const int c = (int)(i - r * nch);
     const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + r * ldx + (long long)c * 8);
     const uint32_t bits = row16_max(max8(v));
-    *reinterpret_cast<u32x2_t*>(codes + r * K + (long long)c * 8) = codes8(v, block_top(bits));
+    *reinterpret_cast<u32x2_t*>(codes + r * K + (long long)c * 8) = codes8(v, block_ratio(bits));
     if ((c & 15) == 0) scales[(long long)(c >> 4) * R + r] = block_scale(bits);
   }
 }
@@ -100,11 +108,11 @@ __global__ __launch_bounds__(256) void fp8_quant_weights_kernel(const bf16_t* __
   if ((threadIdx.x & 63) == 0) top_s[threadIdx.x >> 6] = bits;
   __syncthreads();
   bits = max(max(top_s[0], top_s[1]), max(top_s[2], top_s[3]));
-  const float top = block_top(bits);
+  const Ratio by = block_ratio(bits);
   uint8_t* dst = codes + ((long long)g * N + (long long)bn * BLK) * K + (long long)bk * BLK + 8 * c;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const u32x2_t q = codes8(v[i], top);
+    const u32x2_t q = codes8(v[i], by);
     *reinterpret_cast<u32x2_t*>(dst + (long long)(row + 16 * i) * K) = q;
     if (codes_t) *reinterpret_cast<u32x2_t*>(&tile[row + 16 * i][8 * c]) = q;
   }
