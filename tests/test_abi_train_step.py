@@ -1,0 +1,205 @@
+"""Refusals of routing by scores, of the block-scaled 8-bit products and of AdamW: every bad argument is
+turned away on the host, before anything is enqueued (CPU)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from mixture_experts_layer_20_amd import libmoe as L
+
+FAKE = 1 << 20   # a non-null pointer value; never dereferenced, the checks fail first
+BF, F32 = L.MOE_BF16, L.MOE_F32
+INVALID, UNSUPPORTED, WORKSPACE = L.MOE_ERR_INVALID_VALUE, L.MOE_ERR_UNSUPPORTED, L.MOE_ERR_WORKSPACE
+SOFT, SIG = L.MOE_SCORE_SOFTMAX, L.MOE_SCORE_SIGMOID
+
+
+def expect(status, fn, *args):
+    with pytest.raises(L.MoEError) as ei:
+        fn(*args)
+    assert ei.value.status == status, str(ei.value)
+    assert L.last_error() != ""
+
+
+def test_route_balanced_refusals():
+    f = L.moe_route_balanced
+    args = lambda x=FAKE, w=FAKE, lg=FAKE, b=FAKE, T=4, d=16, E=8, k=2, g=1, tg=1, sc=SIG, rn=1, s=1.0, dt=BF, i=FAKE, o=FAKE: (
+        x, w, lg, b, T, d, E, k, g, tg, sc, rn, s, dt, i, o)
+    expect(INVALID, f, *args(dt=7))
+    expect(INVALID, f, *args(T=-1))
+    expect(INVALID, f, *args(k=0))
+    expect(INVALID, f, *args(k=9, E=8))
+    expect(UNSUPPORTED, f, *args(k=9, E=16))
+    expect(UNSUPPORTED, f, *args(E=257))
+    expect(INVALID, f, *args(sc=2))
+    expect(INVALID, f, *args(rn=2))
+    expect(INVALID, f, *args(s=math.inf))
+    expect(INVALID, f, *args(s=math.nan))
+    expect(INVALID, f, *args(g=0))
+    expect(INVALID, f, *args(g=3))
+    expect(INVALID, f, *args(g=4, tg=0))
+    expect(INVALID, f, *args(g=4, tg=5))
+    expect(INVALID, f, *args(k=3, g=8, tg=2))
+    expect(INVALID, f, *args(x=None))
+    expect(INVALID, f, *args(lg=None))
+    expect(INVALID, f, *args(i=None))
+    expect(INVALID, f, *args(o=None))
+    expect(INVALID, f, *args(b=FAKE + 4))
+    expect(INVALID, f, *args(x=None, w=None, lg=FAKE + 4))
+    f(*args(x=None, w=None, lg=None, b=None, T=0, i=None, o=None))   # no token: nothing to do
+
+
+def test_route_balanced_bwd_refusals():
+    need = L.moe_route_balanced_bwd_workspace_size(100, 64, 8, 2, SIG, 1)
+    dense = L.moe_route_balanced_bwd_workspace_size(100, 64, 8, 2, SOFT, 0)
+    assert need > 0 and dense > 0
+    assert L.moe_route_balanced_bwd_workspace_size(100, 64, 8, 9, SIG, 1) == 0
+    assert L.moe_route_balanced_bwd_workspace_size(100, 64, 8, 2, 5, 1) == 0
+    f = L.moe_route_balanced_bwd
+    args = lambda dg=FAKE, lg=FAKE, i=FAKE, of=FAKE, sr=FAKE, x=FAKE, w=FAKE, T=100, d=64, sc=SIG, rn=1, s=1.0, dw=FAKE, dx=FAKE, ws=FAKE, n=need: (
+        dg, lg, i, of, sr, x, w, T, d, 8, 2, sc, rn, s, BF, dw, dx, ws, n)
+    expect(WORKSPACE, f, *args(n=need - 1))
+    expect(WORKSPACE, f, *args(ws=None))
+    expect(WORKSPACE, f, *args(sc=SOFT, rn=0, n=dense - 1))
+    expect(UNSUPPORTED, f, *args(d=63, sc=SOFT, rn=0, n=1 << 40))
+    for name in ("dg", "lg", "i", "of", "sr", "x", "w", "dw", "dx"):
+        expect(INVALID, f, *args(**{name: None}))
+        expect(INVALID, f, *args(**{name: FAKE + 4}))
+    expect(INVALID, f, *args(s=math.nan))
+
+
+def test_bias_update_refusals():
+    f = L.moe_route_bias_update
+    expect(INVALID, f, FAKE, 0, 0.1, FAKE, FAKE)
+    expect(UNSUPPORTED, f, FAKE, 257, 0.1, FAKE, FAKE)
+    expect(INVALID, f, FAKE, 8, math.nan, FAKE, FAKE)
+    expect(INVALID, f, None, 8, 0.1, FAKE, FAKE)
+    expect(INVALID, f, FAKE, 8, 0.1, None, FAKE)
+    expect(INVALID, f, FAKE, 8, 0.1, FAKE, FAKE + 4)
+
+
+def test_fp8_quantize_refusals():
+    f = L.moe_fp8_quantize_rows
+    expect(INVALID, f, FAKE, -1, 128, 128, FAKE, FAKE)
+    expect(INVALID, f, FAKE, 4, 0, 128, FAKE, FAKE)
+    expect(UNSUPPORTED, f, FAKE, 4, 192, 192, FAKE, FAKE)
+    expect(INVALID, f, FAKE, 4, 256, 128, FAKE, FAKE)
+    expect(INVALID, f, FAKE, 4, 128, 132, FAKE, FAKE)
+    expect(UNSUPPORTED, f, FAKE, 1 << 31, 128, 128, FAKE, FAKE)
+    expect(INVALID, f, None, 4, 128, 128, FAKE, FAKE)
+    expect(INVALID, f, FAKE, 4, 128, 128, FAKE + 8, FAKE)
+    f(None, 0, 128, 128, None, None)
+    g = L.moe_fp8_quantize_weights
+    expect(INVALID, g, FAKE, 0, 128, 128, FAKE, FAKE, None, None)
+    expect(UNSUPPORTED, g, FAKE, 1, 64, 128, FAKE, FAKE, None, None)
+    expect(UNSUPPORTED, g, FAKE, 1, 128, 64, FAKE, FAKE, None, None)
+    expect(INVALID, g, FAKE, 1, 128, 128, FAKE, FAKE, FAKE, None)
+    expect(INVALID, g, FAKE, 1, 128, 128, None, FAKE, None, None)
+    expect(INVALID, g, FAKE, 1, 128, 128, FAKE, FAKE + 4, None, None)
+
+
+def test_fp8_gemm_refusals():
+    f = L.moe_fp8_gemm_rows
+    STORE, SWIGLU, BWD = L.MOE_MX_EPI_STORE, L.MOE_MX_EPI_SWIGLU, L.MOE_MX_EPI_SWIGLU_BWD
+    args = lambda a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, b2=None, s2=None, k2=0, off=FAKE, G=2, M=8, N=128, K=256, epi=STORE, o0=FAKE, o1=None, o2=None, x0=None, x1=None: (
+        a, sa, b, sb, b2, s2, k2, off, G, M, N, K, epi, o0, o1, o2, x0, x1, FAKE, 1 << 30)
+    expect(INVALID, f, *args(epi=3))
+    expect(INVALID, f, *args(epi=-1))
+    expect(INVALID, f, *args(G=0))
+    expect(INVALID, f, *args(G=1025))
+    expect(INVALID, f, *args(M=-1))
+    expect(UNSUPPORTED, f, *args(N=192))
+    expect(UNSUPPORTED, f, *args(K=64))
+    expect(UNSUPPORTED, f, *args(M=1 << 31))
+    expect(UNSUPPORTED, f, *args(N=1 << 20, M=1 << 20))
+    for name in ("a", "sa", "b", "sb", "off", "o0"):
+        expect(INVALID, f, *args(**{name: None}))
+        expect(INVALID, f, *args(**{name: FAKE + 4}))
+    expect(INVALID, f, *args(b2=FAKE))
+    expect(INVALID, f, *args(b2=FAKE, s2=FAKE, k2=0))
+    expect(INVALID, f, *args(b2=FAKE, s2=FAKE, k2=256))
+    expect(INVALID, f, *args(b2=FAKE, s2=FAKE, k2=64))
+    expect(INVALID, f, *args(epi=SWIGLU, o2=FAKE))
+    expect(INVALID, f, *args(epi=SWIGLU, b2=FAKE, s2=FAKE))
+    expect(INVALID, f, *args(epi=BWD, x0=FAKE))
+    f(*args(M=0, a=None, o0=None))
+
+
+def host_list(n=300, bits=32, master=False, dt=torch.float32, **kw):
+    p, g = torch.zeros(n, dtype=dt), torch.zeros(n, dtype=dt)
+    m, v, sc, w = L.adamw_states([p], bits, master)
+    return L.adamw_list([p], [g], m, v, sc, w, **kw)
+
+
+def test_adamw_list_refusals():
+    p, g = torch.zeros(300), torch.zeros(300)
+    m, v, sc, _ = L.adamw_states([p], 8)
+    assert m[0].dtype == torch.uint8 and sc[0].numel() == 6
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g, g], m, v, sc)
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g[:200]], m, v, sc)
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g], m, v)
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g], m, v, [sc[0][:4]])
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g], [p], [p.clone()], sc)
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g], m, [v[0].float()], sc)
+    with pytest.raises(ValueError):
+        L.adamw_list([p], [g], m, v, sc, weight_decay=[0.1, 0.1])
+    expect(INVALID, L.adamw_list, [p], [g], m, v, sc, None, -0.1)
+    expect(INVALID, L.adamw_list, [p], [g], m, v, sc, None, math.nan)
+    expect(INVALID, L.adamw_list, [p], [g], m, v, sc, [p.clone()])        # a float parameter with a master copy
+    expect(INVALID, L.adamw_list, [p], [g], m, m, sc)                      # m and v are one tensor
+    q = torch.zeros(304)
+    expect(INVALID, L.adamw_list, [p], [g], m, v, sc, None, 0.0, ([g], m, v, sc, None))
+    expect(INVALID, L.adamw_list, [q[:300]], [g], m, v, sc, None, 0.0, ([q[4:]], m, v, sc, None))
+    n = L.adamw_states([p, p])
+    expect(INVALID, L.adamw_list, [p, p], [g, g], n[0], n[1])              # one parameter twice
+    expect(INVALID, L.adamw_list, [q[1:301]], [g], *L.adamw_states([p])[:2])
+
+
+def test_adamw_step_refusals():
+    t = host_list()
+    f = lambda lr=1e-3, b1=0.9, b2=0.95, eps=1e-8, step=1: L.moe_adamw(t, lr, b1, b2, eps, step)
+    for bad in (dict(lr=-1.0), dict(lr=math.nan), dict(lr=math.inf), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0), dict(b2=math.nan),
+                dict(eps=0.0), dict(eps=1e-39), dict(eps=math.nan), dict(step=0), dict(step=-3)):
+        with pytest.raises(L.MoEError) as ei:
+            f(**bad)
+        assert ei.value.status == INVALID, bad
+    cfg = L.AdamWStep(1e-3, 0.9, 0.95, 1e-8, 1, 0, 16)
+    expect(INVALID, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), None, 1.0, None)     # state_bits
+    cfg.state_bits = 32
+    expect(INVALID, L._call, "moe_adamw", t.ptr, -1, ctypes.addressof(cfg), None, 1.0, None)
+    expect(INVALID, L._call, "moe_adamw", None, 1, ctypes.addressof(cfg), None, 1.0, None)
+    expect(INVALID, L._call, "moe_adamw", t.ptr, 1, None, None, 1.0, None)
+    expect(INVALID, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), FAKE, 0.0, None)     # max_norm
+    expect(INVALID, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), FAKE + 8, 1.0, None)
+    e = t.array[0]
+    for name in ("grad", "m", "v", "param_out", "m_out", "v_out"):
+        kept = getattr(e, name)
+        for bad in (None, kept + 4):
+            setattr(e, name, bad)
+            expect(INVALID, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), None, 1.0, None)
+        setattr(e, name, kept)
+    e.n = -1
+    expect(INVALID, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), None, 1.0, None)
+    e.n = (1 << 34) + 1
+    expect(UNSUPPORTED, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), None, 1.0, None)
+    e.n, e.grad_dt = 300, 5
+    expect(INVALID, L._call, "moe_adamw", t.ptr, 1, ctypes.addressof(cfg), None, 1.0, None)
+    empty = L.adamw_list([], [], [], [])
+    L.moe_adamw(empty, 1e-3, 0.9, 0.95, 1e-8, 1)   # nothing to do
+
+
+def test_workspace_query():
+    T, d, E, k, f, fs = 1000, 256, 16, 4, 384, 128
+    need = max(L.moe_route_balanced_bwd_workspace_size(T, d, E, k, SIG, 1),
+               L.moe_route_balanced_bwd_workspace_size(T, d, E, k, SOFT, 0))
+    assert L.moe_workspace_bytes(L.MOE_OP_ROUTE_BALANCED_BWD, T, d, E, k, f, fs) == need > 0
+    sizes = [L.moe_fp8_gemm_workspace_size(G, M, N, K) for G, M, w in ((E, T * k, f), (1, T, fs))
+             for N, K in ((w, d), (d, w), (d, 2 * w))]
+    assert L.moe_workspace_bytes(L.MOE_OP_FP8_GEMM_ROWS, T, d, E, k, f, fs) == max(sizes)
+    assert L.moe_fp8_gemm_workspace_size(0, 8, 128, 128) == 0 and L.last_error() != ""

@@ -1,0 +1,778 @@
+"""Routing by scores, products in block-scaled 8-bit floating point and AdamW on the GPU against the float64
+oracle.  Tolerances count roundings: half a step is 2^-24 of the value in fp32, 2^-8 in bf16, 2^-4 in E4M3."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_20_amd import libmoe as L
+from oracle import train_step as S
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F = 2.0 ** -24
+BF = 2.0 ** -8
+SOFT, SIG = L.MOE_SCORE_SOFTMAX, L.MOE_SCORE_SIGMOID
+DT = {torch.float32: L.MOE_F32, torch.bfloat16: L.MOE_BF16}
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def put(a, dt=torch.float32):
+    return torch.as_tensor(np.ascontiguousarray(a)).to(dt).to(DEV)
+
+
+def workspace(n):
+    return torch.empty(max(16, n), dtype=torch.uint8, device=DEV)
+
+
+# ---- routing by scores --------------------------------------------------------------------------------
+
+def route(logits, bias, k, groups=1, topk_groups=1, score=SIG, renorm=1, scale=1.0):
+    T, E = logits.shape
+    idx = torch.full((T + 1, k), -7, dtype=torch.int32, device=DEV)
+    gate = torch.full((T + 1, k), -7.0, device=DEV)
+    L.moe_route_balanced(None, None, logits, bias, T, 8, E, k, groups, topk_groups, score, renorm, scale, L.MOE_F32, idx, gate)
+    assert (idx[T] == -7).all() and (gate[T] == -7.0).all()   # rows behind the last token
+    return idx[:T], gate[:T]
+
+
+def check_route(l, b, k, groups, topk_groups, score, renorm, scale):
+    logits, bias = put(l), None if b is None else put(b)
+    idx, gate = route(logits, bias, k, groups, topk_groups, score, renorm, scale)
+    want = S.choose(np64(logits), None if b is None else np64(bias), k, groups, topk_groups, score == SIG)
+    np.testing.assert_array_equal(idx.cpu().numpy(), want)
+    g = S.gates(np64(logits), want, score == SIG, renorm, scale)
+    # an exponential of an argument that is rounded once (|argument| half steps) and a few units of its own,
+    # a sum of at most 256 of them in a tree, a division
+    # (at most the value itself: gates are not negative, and a largest argument of 3e38 would bound nothing)
+    finite = np.abs(np64(logits)[np.isfinite(l)])
+    tol = min((4 * (finite.max() if finite.size else 0.0) + 40) * F, 1.0)
+    assert np.all(np.abs(np64(gate) - g) <= tol * np.abs(g) + 2.0 ** -120), np.abs(np64(gate) - g).max()
+
+
+ROUTES = [  # T, E, k, groups, topk_groups
+    (1, 8, 2, 1, 1), (17, 60, 3, 4, 2), (33, 64, 8, 1, 1), (65, 128, 4, 8, 3), (130, 256, 8, 8, 4), (31, 200, 6, 1, 1),
+    (20, 1, 1, 1, 1), (20, 3, 3, 1, 1), (40, 255, 5, 3, 2), (9, 150, 8, 5, 5), (64, 256, 8, 64, 10), (50, 256, 2, 256, 7),
+    (40, 16, 2, 16, 5), (23, 96, 8, 32, 8), (70, 240, 7, 16, 16), (12, 12, 8, 4, 3),
+]
+
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("T,E,k,groups,topk_groups", ROUTES)
+def test_route(T, E, k, groups, topk_groups, score):
+    r = np.random.default_rng(T * 1000 + E)
+    for biased in (False, True):
+        for renorm, scale in ((1, 1.0), (0, 2.5)):
+            l = (r.standard_normal((T, E)) * r.uniform(0.2, 3.0)).astype(np.float32)
+            b = (0.1 * r.standard_normal(E)).astype(np.float32) if biased else None
+            check_route(l, b, k, groups, topk_groups, score, renorm, scale)
+
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (4, 2), (8, 8), (12, 5)])
+def test_route_near_and_equal(groups, topk_groups, score):
+    """Scores that fp32 does not tell apart, equal ones, and whole rows of them."""
+    r = np.random.default_rng(11)
+    T, E, k = 48, 96, 6
+    l = np.repeat(r.standard_normal((T, E // 8)), 8, axis=1) + r.integers(-2, 3, (T, E)) * 2.0 ** -22
+    l[5], l[6], l[7] = 0.25, 0.0, np.arange(E) % 3
+    l = l[:, r.permutation(E)].astype(np.float32)
+    check_route(l, None, k, groups, topk_groups, score, 1, 1.0)
+    b = (np.round(r.standard_normal(E) * 4) / 4 + r.integers(-1, 2, E) * 2.0 ** -23).astype(np.float32)
+    check_route(l, b, k, groups, topk_groups, score, 1, 1.0)
+    check_route(l, np.zeros(E, np.float32), k, groups, topk_groups, score, 0, 1.0)
+
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("groups,topk_groups", [(1, 1), (4, 2), (6, 3)])
+def test_route_infinities(groups, topk_groups, score):
+    r = np.random.default_rng(12)
+    T, E, k = 40, 48, 4
+    l = r.standard_normal((T, E)).astype(np.float32)
+    l[r.random((T, E)) < 0.5] = -np.inf
+    l[3] = -np.inf                       # nothing to choose from: k different experts, gates of 0
+    l[4] = -3.0e38
+    l[5, :] = -np.inf
+    l[5, 7] = 1.0
+    check_route(l, None, k, groups, topk_groups, score, 1, 1.0)
+    b = (0.1 * r.standard_normal(E)).astype(np.float32)
+    b[::5] = -np.inf                     # shut experts
+    l = r.standard_normal((T, E)).astype(np.float32)
+    check_route(l, b, k, groups, topk_groups, score, 1, 2.0)
+    idx, _ = route(put(l), put(b), k, groups, topk_groups, score)
+    assert not np.isin(idx.cpu().numpy(), np.arange(0, E, 5)).any()
+    l[:, ::3] = np.nan                   # whatever there is, k different experts
+    l[8] = np.nan
+    idx, _ = route(put(l), put(b), k, groups, topk_groups, score)
+    rows = np.sort(idx.cpu().numpy(), axis=1)
+    assert rows.min() >= 0 and rows.max() < E and (np.diff(rows, axis=1) > 0).all()
+
+
+def test_route_underflow_and_no_tokens():
+    l = np.array([[-90.0, -95.0, -200.0, -300.0], [-1000.0, -1000.5, -3e4, -2e4]], np.float32)
+    check_route(l, None, 3, 1, 1, SIG, 1, 1.0)
+    idx, gate = route(torch.empty(0, 8, device=DEV), None, 2)
+    assert idx.shape == (0, 2)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_route_from_activations(dt):
+    """The learned router's logits are those of moe_route, and the choice follows them."""
+    T, d, E, k = 67, 96, 40, 4
+    g = torch.Generator().manual_seed(2)
+    x, w = torch.randn(T, d, generator=g).to(dt).to(DEV), (0.2 * torch.randn(E, d, generator=g)).to(dt).to(DEV)
+    logits, idx, gate = torch.empty(T, E, device=DEV), torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    L.moe_route_balanced(x, w, logits, None, T, d, E, k, 4, 2, SIG, 1, 1.0, DT[dt], idx, gate)
+    other, i2, g2 = torch.empty_like(logits), torch.empty_like(idx), torch.empty_like(gate)
+    L.moe_route(x, w, None, other, T, d, E, k, 1, DT[dt], i2, g2)
+    assert torch.equal(logits, other)
+    np.testing.assert_array_equal(idx.cpu().numpy(), S.choose(np64(logits), None, k, 4, 2, True))
+
+
+def plan(idx, E):
+    flat = idx.reshape(-1).long()
+    offsets = torch.cat([torch.zeros(1, dtype=torch.long, device=DEV), torch.bincount(flat, minlength=E).cumsum(0)])
+    return offsets.to(torch.int32), torch.sort(flat, stable=True).indices.to(torch.int32)
+
+
+def route_bwd(dgate, logits, idx, x, w, score, renorm, scale):
+    T, E = logits.shape
+    d, k, dt = w.shape[1], idx.shape[1], DT[w.dtype]
+    offsets, src = plan(idx, E) if T else (torch.zeros(E + 1, dtype=torch.int32, device=DEV), idx)
+    n = L.moe_route_balanced_bwd_workspace_size(T, d, E, k, score, renorm)
+    dw = torch.full((E + 1, d), 9.0, device=DEV)
+    dx = torch.full((T + 1, d), 9.0, dtype=w.dtype, device=DEV)
+    L.moe_route_balanced_bwd(dgate, logits, idx, offsets, src, x, w, T, d, E, k, score, renorm, scale, dt, dw, dx, workspace(n), n)
+    assert (dw[E] == 9).all() and (dx[T] == 9).all()
+    return dw[:E], dx[:T]
+
+
+@pytest.mark.parametrize("score,renorm", [(SIG, 1), (SIG, 0), (SOFT, 1), (SOFT, 0)])
+@pytest.mark.parametrize("T,d,E,k,dt", [
+    (1, 8, 4, 2, torch.float32), (50, 72, 60, 3, torch.float32), (130, 264, 128, 8, torch.bfloat16),
+    (333, 64, 7, 1, torch.bfloat16), (65, 1000, 66, 4, torch.float32), (700, 136, 256, 4, torch.bfloat16)])
+def test_route_backward(T, d, E, k, dt, score, renorm):
+    r = np.random.default_rng(T + E)
+    scale = 1.5
+    logits = put(r.standard_normal((T, E)) * 2)
+    x, w, dgate = put(r.standard_normal((T, d)), dt), put(r.standard_normal((E, d)) * 0.3, dt), put(r.standard_normal((T, k)))
+    idx, _ = route(logits, None, k, 1, 1, score, renorm, scale)
+    dw, dx = route_bwd(dgate, logits, idx, x, w, score, renorm, scale)
+    l, dg, i = np64(logits), np64(dgate), idx.cpu().numpy().astype(np.int64)
+    dl = S.gates_bwd(dg, l, i, score == SIG, renorm, scale)
+    # terms of a logit's gradient, and their roundings: the gates' own, k differences and products
+    g = S.gates(l, i, score == SIG, renorm, 1.0)
+    size = np.zeros_like(dl)
+    if score == SOFT and not renorm:
+        size += scale * S.scores(l, False) * (g * np.abs(dg)).sum(1, keepdims=True)
+    inner = np.abs(dg) + ((g * np.abs(dg)).sum(1, keepdims=True) if renorm else 0.0)
+    np.add.at(size, (np.arange(T)[:, None], i), scale * g * inner)
+    e_dl = (12 * np.abs(l).max() + 100) * F * size
+    x64, w64 = np64(x), np64(w)
+    want_dw, want_dx = dl.T @ x64, dl @ w64
+    tol_dw = e_dl.T @ np.abs(x64) + (T + 8) * F * (np.abs(dl).T @ np.abs(x64))
+    out = 0.0 if dt == torch.float32 else BF
+    tol_dx = e_dl @ np.abs(w64) + (E + 8) * F * (np.abs(dl) @ np.abs(w64)) + out * np.abs(want_dx)
+    assert np.all(np.abs(np64(dw) - want_dw) <= tol_dw * 1.01 + 1e-30)
+    assert np.all(np.abs(np64(dx) - want_dx) <= tol_dx * 1.01 + 1e-30)
+
+
+@pytest.mark.parametrize("score,renorm", [(SIG, 1), (SIG, 0), (SOFT, 1), (SOFT, 0)])
+def test_route_backward_against_differences(score, renorm):
+    """The gates of the GPU moved by a step in the router: differences of fp32 values, so a coarse bound."""
+    r = np.random.default_rng(4)
+    T, d, E, k = 24, 16, 8, 2
+    x, w0, dg = r.standard_normal((T, d)), r.standard_normal((E, d)) * 0.3, r.standard_normal((T, k))
+    lg = put(x @ w0.T)
+    idx, _ = route(lg, None, k, 1, 1, score, renorm)
+    dw, _ = route_bwd(put(dg), lg, idx, put(x), put(w0), score, renorm, 1.0)
+    v = r.standard_normal((E, d))
+    h = 2.0 ** -8
+    i = idx.cpu().numpy().astype(np.int64)
+
+    def value(t):   # with the choice held
+        return (S.gates(x @ (w0 + t * v).T, i, score == SIG, renorm, 1.0) * dg).sum()
+    diff, mine = (value(h) - value(-h)) / (2 * h), (np64(dw) * v).sum()
+    # third derivatives: h^2 / 6 times the cube of the logits' steps, summed over the gates
+    third = h * h * np.abs(dg).sum() * np.abs(x @ v.T).max() ** 3
+    assert abs(diff - mine) <= third + 1e-5 * (np.abs(np64(dw)) * np.abs(v)).sum()
+
+
+def test_route_backward_without_tokens():
+    w = torch.randn(4, 16, device=DEV)
+    e = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device=DEV)
+    for score, renorm in ((SIG, 1), (SOFT, 0)):
+        dw, _ = route_bwd(e(0, 2), e(0, 4), e(0, 2, dt=torch.int32), e(0, 16), w, score, renorm, 1.0)
+        assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("E", [1, 7, 64, 256])
+def test_bias_update(E):
+    r = np.random.default_rng(E)
+    counts = r.integers(0, 5, E)
+    counts[r.integers(E)] += 2 ** 30
+    bias = r.standard_normal(E).astype(np.float32)
+    for n in (counts, np.full(E, 3)):
+        b, out = put(bias), torch.empty(E + 1, device=DEV).fill_(5.0)
+        L.moe_route_bias_update(put(n, torch.int32), E, 1e-3, b, out[:E])
+        want = (bias + np.float32(1e-3) * np.sign(n.sum() - n * E).astype(np.float32)).astype(np.float32)
+        np.testing.assert_array_equal(out[:E].cpu().numpy(), want)
+        assert out[E] == 5.0
+        L.moe_route_bias_update(put(n, torch.int32), E, 1e-3, b, b)   # in place
+        np.testing.assert_array_equal(b.cpu().numpy(), want)
+
+
+# ---- products in 8-bit floating point -------------------------------------------------------------------
+
+def quantize_rows(x, K=None):
+    R, ldx = x.shape
+    K = K or ldx
+    codes = torch.full((R + 1, K), 0x55, dtype=torch.uint8, device=DEV)
+    scales = torch.empty(K // 128, R, device=DEV)
+    L.moe_fp8_quantize_rows(x, R, K, ldx, codes, scales)
+    assert (codes[R] == 0x55).all()
+    return codes[:R], scales
+
+
+def quantize_weights(w, both=False):
+    G, N, K = w.shape
+    codes, scales = torch.empty(G, N, K, dtype=torch.uint8, device=DEV), torch.empty(G, N // 128, K // 128, device=DEV)
+    ct = torch.empty(G, K, N, dtype=torch.uint8, device=DEV) if both else None
+    st = torch.empty(G, K // 128, N // 128, device=DEV) if both else None
+    L.moe_fp8_quantize_weights(w, G, N, K, codes, scales, ct, st)
+    return (codes, scales, ct, st) if both else (codes, scales)
+
+
+@pytest.mark.parametrize("R,K,ldx", [(1, 128, 128), (3, 256, 264), (257, 384, 384), (64, 1024, 2048)])
+def test_quantize_rows(R, K, ldx):
+    r = np.random.default_rng(R)
+    base = put(r.standard_normal((R, ldx)) * np.exp(3 * r.standard_normal((R, 1))), torch.bfloat16)
+    x = base[:, :K]
+    if R > 2:
+        x[1, :128] = 0.0
+        x[2, :128] = 1e-38
+        x[2, 128:256] *= 2.0 ** 110
+    codes, scales = quantize_rows(base, K)
+    want, s = S.quantize_rows(np64(x))
+    assert np.array_equal(S.E4M3[codes.cpu().numpy()], S.E4M3[want])   # of -0 and 0 either
+    assert np.all(np.abs(np64(scales) - s) <= F * s)
+
+
+@pytest.mark.parametrize("exponent", [-95, -60, 0, 64, 100, 119])
+def test_quantize_rows_ties_and_ends(exponent):
+    """Values on the borders of codes, at both ends of bf16's range; subnormals of the code."""
+    mid = (S.E4M3[:0x7E] + S.E4M3[1:0x7F]) / 2                 # 4 or 5 bits: bf16 values
+    v = np.concatenate([mid, S.E4M3[:0x7F], -mid, [448.0, 2.0 ** -10, 3 * 2.0 ** -10]])
+    v = np.resize(v, 512)
+    v[::128] = 448.0
+    x = put(np.ldexp(v, exponent), torch.bfloat16).reshape(1, 512)
+    assert np.array_equal(np64(x)[0], np.ldexp(v, exponent))
+    codes, _ = quantize_rows(x)
+    want, _ = S.quantize_rows(np64(x))
+    assert np.array_equal(S.E4M3[codes.cpu().numpy()], S.E4M3[want])
+
+
+def test_quantize_infinities():
+    x = torch.randn(4, 256, device=DEV).to(torch.bfloat16)
+    x[1, 3], x[2, 200] = float("inf"), float("nan")
+    _, s = quantize_rows(x)
+    bad = torch.isnan(s)
+    assert bad[0, 1] and bad[1, 2] and bad.sum() == 2
+    w = torch.randn(2, 256, 128, device=DEV).to(torch.bfloat16)
+    w[1, 200, 5] = float("-inf")
+    _, s = quantize_weights(w)
+    assert torch.isnan(s[1, 1, 0]) and torch.isnan(s).sum() == 1
+
+
+@pytest.mark.parametrize("G,N,K", [(1, 128, 128), (3, 256, 384)])
+def test_quantize_weights(G, N, K):
+    r = np.random.default_rng(G)
+    w = put(r.standard_normal((G, N, K)) * np.exp(r.standard_normal((G, N, 1))), torch.bfloat16)
+    w[0, :128, :128] = 0.0
+    codes, scales, ct, st = quantize_weights(w, True)
+    want, s = S.quantize_weights(np64(w))
+    assert np.array_equal(S.E4M3[codes.cpu().numpy()], S.E4M3[want])
+    assert np.all(np.abs(np64(scales) - s) <= F * s)
+    assert torch.equal(ct, codes.transpose(1, 2)) and torch.equal(st, scales.transpose(1, 2))
+    alone = quantize_weights(w)
+    assert torch.equal(alone[0], codes) and torch.equal(alone[1], scales)
+
+
+def random_codes(r, shape):
+    c = r.integers(0, 256, shape).astype(np.uint8)
+    c[(c & 0x7F) == 0x7F] = 0x7E          # no NaN
+    return c
+
+
+def sums_bound(size, tops, K):
+    """Of a product.  The matrix instruction shifts 8 neighbouring products to the exponents of the largest, 2^e, and
+    cuts each below 2^(e-13): seven of them lose less than 2^-13 of that one each (seen with 448 * 448 - 448 * 448
+    and one more product of the same eight, which comes back in multiples of 8; beside other eights it is exact).
+    The rest are 128 additions in fp32 a block (which may cut off: a whole step each), a scaling by two factors and
+    an addition a block."""
+    return 7 * 2.0 ** -13 * tops + (128 + K // 128 + 6) * 2 * F * size
+
+
+def silu(a):
+    return a / (1.0 + np.exp(-a))
+
+
+SIZES = [  # M, offsets, N, K: one row, few, tiles and their quarters, ragged groups, empty ones, rows outside
+    (1, [0, 1], 128, 128),
+    (5, [0, 5], 256, 1152),
+    (40, [0, 0, 16, 17, 17, 40], 384, 256),
+    (70, [3, 30, 30, 61], 256, 640),
+    (64, [0, 64], 256, 128),
+    (65, [0, 65], 256, 128),
+    (300, [0, 300], 256, 256),
+    (700, [0, 256, 257, 257, 512, 690], 512, 384),
+    (700, [10, 330, 331, 512, 700], 128, 256),
+    (1500, [0, 1, 400, 1100, 1101, 1500], 768, 128),
+    (2100, [0, 700, 1400, 2100], 384, 512),
+]
+
+
+@pytest.mark.parametrize("M,offsets,N,K", SIZES)
+def test_product(M, offsets, N, K):
+    r = np.random.default_rng(M + N)
+    G = len(offsets) - 1
+    a, b = random_codes(r, (M, K)), random_codes(r, (G, N, K))
+    sa, sb = np.exp(r.standard_normal((K // 128, M))), np.exp(r.standard_normal((G, N // 128, K // 128)))
+    args = [put(t, torch.uint8) if t.dtype == np.uint8 else put(t) for t in (a, sa, b, sb)]
+    out = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    n = L.moe_fp8_gemm_workspace_size(G, M, N, K)
+    off = put(np.array(offsets), torch.int32)
+    L.moe_fp8_gemm_rows(*args, None, None, 0, off, G, M, N, K, L.MOE_MX_EPI_STORE, out, None, None, None, None, workspace(n), n)
+    A, B = S.rows_of(a, np64(args[1])), S.weights_of(b, np64(args[3]))
+    want, size, tops = S.grouped_product(A, B, offsets)
+    inside = ~np.isnan(want[:, 0])
+    got = np64(out)
+    assert np.all(got[:M][~inside] == 7.0) and np.all(got[M] == 7.0)   # rows of no group stay as they were
+    err, tol = np.abs(got[:M] - want)[inside], (sums_bound(size, tops, K) * (1 + BF) + BF * np.abs(want))[inside]
+    assert np.all(err <= tol), (err / tol).max()
+    # the same again
+    again = torch.full_like(out, 7.0)
+    L.moe_fp8_gemm_rows(*args, None, None, 0, off, G, M, N, K, L.MOE_MX_EPI_STORE, again, None, None, None, None, workspace(n), n)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("M,offsets,N,K", SIZES)
+def test_product_of_two_sources(M, offsets, N, K):
+    """b and b2 hold K-columns below and from b2_k on: the same numbers as one b."""
+    r = np.random.default_rng(M + K)
+    G, K2 = len(offsets) - 1, 128 if K == 128 else 256
+    Ks = K + K2
+    a, b = random_codes(r, (M, Ks)), random_codes(r, (G, N, Ks))
+    sa, sb = np.exp(r.standard_normal((Ks // 128, M))), np.exp(r.standard_normal((G, N // 128, Ks // 128)))
+    ta, tsa, tb, tsb = put(a, torch.uint8), put(sa), put(b, torch.uint8), put(sb)
+    off, n = put(np.array(offsets), torch.int32), L.moe_fp8_gemm_workspace_size(G, M, N, Ks)
+    one, two = (torch.zeros(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    tail = (off, G, M, N, Ks, L.MOE_MX_EPI_STORE)
+    L.moe_fp8_gemm_rows(ta, tsa, tb, tsb, None, None, 0, *tail, one, None, None, None, None, workspace(n), n)
+    kb = K // 128
+    part = lambda v, lo, hi: v[:, :, lo:hi].clone(memory_format=torch.contiguous_format)
+    L.moe_fp8_gemm_rows(ta, tsa, part(tb, 0, K), part(tsb, 0, kb), part(tb, K, Ks), part(tsb, kb, Ks // 128), K, *tail, two, None,
+                        None, None, None, workspace(n), n)
+    assert torch.equal(one, two)
+
+
+@pytest.mark.parametrize("M,offsets,N,K", SIZES)
+def test_product_swiglu(M, offsets, N, K):
+    r = np.random.default_rng(M + N + 1)
+    G = len(offsets) - 1
+    a, b, b2 = random_codes(r, (M, K)), random_codes(r, (G, N, K)), random_codes(r, (G, N, K))
+    sc = 2.0 / (np.sqrt(K) * 90.0)   # E4M3's codes have a root mean square of 90: gates of a few units
+    sa = sc * np.exp(0.5 * r.standard_normal((K // 128, M)))
+    sb, sb2 = (np.exp(0.5 * r.standard_normal((G, N // 128, K // 128))) / 90.0 for _ in range(2))
+    t = [put(v, torch.uint8) if v.dtype == np.uint8 else put(v) for v in (a, sa, b, sb, b2, sb2)]
+    off, n = put(np.array(offsets), torch.int32), L.moe_fp8_gemm_workspace_size(G, M, N, K)
+    o = [torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    call = lambda o0, o1, o2: L.moe_fp8_gemm_rows(*t, 0, off, G, M, N, K, L.MOE_MX_EPI_SWIGLU, o0, o1, o2, None, None, workspace(n), n)
+    call(*o)
+    A = S.rows_of(a, np64(t[1]))
+    (ga, size_a, top_a), (up, size_u, top_u) = (S.grouped_product(A, S.weights_of(c, np64(s)), offsets) for c, s in ((b, t[3]), (b2, t[5])))
+    inside = ~np.isnan(ga[:, 0])
+    ea, eu = sums_bound(size_a, top_a, K), sums_bound(size_u, top_u, K)
+    h = silu(ga) * up
+    # silu's slope is below 1.1; an exponential of an argument rounded |a| half steps, a division, two products
+    eh = 1.1 * ea * (np.abs(up) + eu) + np.abs(silu(ga)) * eu + (8 * np.abs(ga) + 24) * F * np.abs(h)
+    for got, want, e in zip(o, (ga, up, h), (ea, eu, eh)):
+        got = np64(got)
+        assert np.all(got[:M][~inside] == 7.0) and np.all(got[M] == 7.0)
+        err, tol = np.abs(got[:M] - want)[inside], (e * (1 + BF) + BF * np.abs(want))[inside]
+        assert np.all(err <= tol), (err / tol).max()
+    alone = torch.full_like(o[2], 7.0)
+    call(None, None, alone)
+    assert torch.equal(alone, o[2])
+
+
+@pytest.mark.parametrize("M,offsets,N,K", SIZES)
+def test_product_swiglu_backward(M, offsets, N, K):
+    r = np.random.default_rng(M + N + 2)
+    G = len(offsets) - 1
+    a, b = random_codes(r, (M, K)), random_codes(r, (G, N, K))
+    sa, sb = np.exp(0.5 * r.standard_normal((K // 128, M))) / 90.0, np.exp(0.5 * r.standard_normal((G, N // 128, K // 128))) / 90.0
+    t = [put(v, torch.uint8) if v.dtype == np.uint8 else put(v) for v in (a, sa, b, sb)]
+    ga, up = (put(r.standard_normal((M, N)) * 2, torch.bfloat16) for _ in range(2))
+    off, n = put(np.array(offsets), torch.int32), L.moe_fp8_gemm_workspace_size(G, M, N, K)
+    out = torch.full((M + 1, 2 * N), 7.0, dtype=torch.bfloat16, device=DEV)
+    L.moe_fp8_gemm_rows(*t, None, None, 0, off, G, M, N, K, L.MOE_MX_EPI_SWIGLU_BWD, out, None, None, ga, up, workspace(n), n)
+    dh, size, tops = S.grouped_product(S.rows_of(a, np64(t[1])), S.weights_of(b, np64(t[3])), offsets)
+    inside = ~np.isnan(dh[:, 0])
+    e, A, U = sums_bound(size, tops, K), np64(ga), np64(up)
+    sg = 1.0 / (1.0 + np.exp(-A))
+    fa, fb = U * sg * (1.0 + A * (1.0 - sg)), A * sg
+    # 1 + a (1 - sg) cancels where it is near zero: its terms are counted by themselves
+    slack_a = (8 * np.abs(A) + 24) * F * np.abs(dh) * np.abs(U) * sg * (1.0 + np.abs(A))
+    slack_b = (8 * np.abs(A) + 24) * F * np.abs(dh * fb)
+    got = np64(out)
+    assert np.all(got[:M][~inside] == 7.0) and np.all(got[M] == 7.0)
+    for got_, f, slack in ((got[:M, :N], fa, slack_a), (got[:M, N:], fb, slack_b)):
+        want = dh * f
+        err, tol = np.abs(got_ - want)[inside], (e * np.abs(f) + slack)[inside] * (1 + BF) + BF * np.abs(want)[inside]
+        assert np.all(err <= tol + 1e-30), (err / (tol + 1e-30)).max()
+
+
+def test_product_offsets_out_of_range():
+    """Offsets past M are cut to it: no row behind the last is read or written."""
+    r = np.random.default_rng(1)
+    M, N, K = 100, 256, 128
+    for offsets in ([0, 60, 4000], [-5, 50, 100], [100, 100, 100]):
+        a, b = random_codes(r, (M, K)), random_codes(r, (2, N, K))
+        one = np.ones((1, M)), np.ones((2, 2, 1))
+        out = torch.full((M + 64, N), 7.0, dtype=torch.bfloat16, device=DEV)
+        L.moe_fp8_gemm_rows(put(a, torch.uint8), put(one[0]), put(b, torch.uint8), put(one[1]), None, None, 0,
+                            put(np.array(offsets), torch.int32), 2, M, N, K, L.MOE_MX_EPI_STORE, out, None, None, None, None, None, 0)
+        want, size, tops = S.grouped_product(S.E4M3[a], S.E4M3[b], offsets)
+        got, inside = np64(out), ~np.isnan(want[:, 0])
+        assert np.all(got[M:] == 7.0) and np.all(got[:M][~inside] == 7.0)
+        assert np.all(np.abs(got[:M] - want)[inside] <= (sums_bound(size, tops, K) * 1.01 + BF * np.abs(want))[inside])
+
+
+def test_product_of_a_lost_block():
+    """A block with a NaN scale makes its row NaN, and nothing else."""
+    for M in (8, 200):
+        x = torch.randn(M, 256, device=DEV).to(torch.bfloat16)
+        x[3, 200] = float("inf")
+        w = torch.randn(1, 256, 256, device=DEV).to(torch.bfloat16)
+        out = torch.empty(M, 256, dtype=torch.bfloat16, device=DEV)
+        L.moe_fp8_gemm_rows(*quantize_rows(x), *quantize_weights(w), None, None, 0, put(np.array([0, M]), torch.int32), 1, M,
+                            256, 256, L.MOE_MX_EPI_STORE, out, None, None, None, None, None, 0)
+        bad = torch.isnan(out)
+        assert bad[3].all() and bad.sum() == 256
+
+
+# ---- AdamW --------------------------------------------------------------------------------------------
+
+HYPER = dict(lr=0.01, beta1=0.9, beta2=0.95, eps=1e-8, step=7)
+
+
+def fill(t, v):
+    t.copy_(put(v, t.dtype) if t.dtype != torch.uint8 else put(v, torch.uint8))
+
+
+def guarded(n, dt):
+    """n elements with 32 known ones behind them."""
+    b = torch.full((n + 32,), 77, dtype=dt, device=DEV)
+    return b, b[:n]
+
+
+class Case:
+    """Tensors of AdamW with random contents; out in other tensors, guarded."""
+
+    def __init__(self, sizes, types, grads, bits, master, seed=0):
+        r = np.random.default_rng(seed)
+        self.bits, self.n = bits, len(sizes)
+        self.p = [put(0.1 * r.standard_normal(n), t) for n, t in zip(sizes, types)]
+        self.g = [put(r.standard_normal(n) * 10.0 ** r.uniform(-3, 0), t) for n, t in zip(sizes, grads)]
+        self.m, self.v, self.sc, self.w = L.adamw_states(self.p, bits, master)
+        for i, n in enumerate(sizes):
+            blocks = -(-n // 128)
+            if bits == 8:
+                c = random_codes(r, 2 * n)
+                fill(self.m[i], c[:n])
+                fill(self.v[i], c[n:] & 0x7F)
+                fill(self.sc[i], np.exp(r.standard_normal(2 * blocks)) * 1e-4)
+            else:
+                fill(self.m[i], r.standard_normal(n) * 0.01)
+                fill(self.v[i], r.standard_normal(n) ** 2 * 1e-3)
+            if self.w[i] is not None:
+                fill(self.w[i], np64(self.p[i]) * (1 + 0.001 * r.uniform(-1, 1, n)))
+        like = lambda ts: [None if t is None else guarded(t.numel(), t.dtype) for t in ts]
+        self.out = [like(ts) for ts in (self.p, self.m, self.v, self.sc, self.w)]
+
+    def list(self, decay, in_place=False):
+        out = None if in_place else [[None if o is None else o[1] for o in os] for os in self.out]
+        return L.adamw_list(self.p, self.g, self.m, self.v, self.sc, self.w, decay, out)
+
+    def results(self, i):
+        return [None if os[i] is None else os[i][1] for os in self.out]
+
+    def check_guards(self):
+        for os in self.out:
+            for o in os:
+                assert o is None or (o[0][-32:] == 77).all()
+
+
+def states_before(c, i):
+    if c.bits == 32:
+        return np64(c.m[i]), np64(c.v[i])
+    s = np64(c.sc[i]).reshape(2, -1)
+    return S.state_of(c.m[i].cpu().numpy(), s[0]), S.state_of(c.v[i].cpu().numpy(), s[1]) ** 2
+
+
+def code_step(y):
+    """The distance of E4M3's values around |y|."""
+    return np.maximum(2.0 ** -9, 2.0 ** (np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -9))) - 3))
+
+
+def check_adamw(c, i, decay, clip, hyper=HYPER):
+    p, m, v, sc, w = c.results(i)
+    start = np64(c.w[i]) if c.w[i] is not None else np64(c.p[i])
+    m0, v0 = states_before(c, i)
+    g = clip * np64(c.g[i])
+    P, M, V = S.adamw(start, np64(c.g[i]), m0, v0, decay=decay, c=clip, **hyper)
+    b1, b2, t = hyper["beta1"], hyper["beta2"], hyper["step"]
+    # coefficients and terms are rounded a few times each; a dequantized code is a product, rounded once
+    e_m = 10 * F * (b1 * np.abs(m0) + (1 - b1) * np.abs(g))
+    e_v = 16 * F * V
+    den = np.sqrt(V / (1 - b2 ** t)) + hyper["eps"]
+    size = hyper["lr"] / (1 - b1 ** t) / den
+    u = size * np.abs(M)
+    e_p = size * e_m + 24 * F * u + 4 * F * (np.abs(start) + u)
+    if c.w[i] is not None:
+        assert np.all(np.abs(np64(w) - P) <= e_p)
+        assert torch.equal(p, w.to(torch.bfloat16))
+    elif c.p[i].dtype == torch.float32:
+        assert np.all(np.abs(np64(p) - P) <= e_p)
+    else:   # up or down at random: less than a step, 2^-7 of the value
+        assert np.all(np.abs(np64(p) - P) <= e_p * 1.01 + 2 * BF * np.abs(P) * (1 + BF))
+    if c.bits == 32:
+        assert np.all(np.abs(np64(m) - M) <= e_m) and np.all(np.abs(np64(v) - V) <= e_v)
+        return
+    s = np64(sc).reshape(2, -1)
+    for codes, scale, want, e in ((m, s[0], M, e_m), (v, s[1], np.sqrt(V), 10 * F * np.sqrt(V))):
+        tops = S.block_tops(want)
+        e_tops = np.array([e[j:j + 128].max() for j in range(0, len(e), 128)])
+        assert np.all(np.abs(scale * 448 - tops) <= e_tops + 8 * F * tops)
+        per = np.repeat(scale, 128)[:len(want)]
+        y = want / per
+        # the rest of a step at most, of the value that the kernel has
+        slack = (e + np.repeat(e_tops, 128)[:len(e)]) / per + 16 * F * np.abs(y)
+        got = S.E4M3[codes.cpu().numpy()]
+        assert np.all(np.abs(got - y) <= np.maximum(code_step(np.abs(y) + slack), code_step(y)) + slack)
+    # a positive v keeps a code above zero (v is fp32: below its normal numbers there is nothing to keep)
+    assert np.all(S.E4M3[v.cpu().numpy()][V >= 2.0 ** -126] > 0)
+
+
+BF16, F32 = torch.bfloat16, torch.float32
+LISTS = {
+    "one": ([1], [F32], [F32]),
+    "odd": ([127, 128, 129, 2047, 2049, 4096, 5], [F32, BF16] * 3 + [F32], [F32, BF16] * 3 + [F32]),
+    "types": ([1000, 1001, 3, 9000], [BF16, F32, BF16, BF16], [F32, BF16, F32, BF16]),
+    "empty": ([0, 300, 0, 4, 0], [F32, BF16, BF16, F32, F32], [F32, BF16, BF16, F32, F32]),
+    "long": (list(range(1, 78)), [BF16 if i % 3 else F32 for i in range(77)], [BF16 if i % 2 else F32 for i in range(77)]),
+    "longer": ([1 + 7 * (i % 50) for i in range(600)], [BF16] * 600, [BF16] * 600),
+}
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("master", [False, True])
+@pytest.mark.parametrize("name", list(LISTS))
+def test_adamw(name, master, bits):
+    c = Case(*LISTS[name], bits, master, seed=len(name))
+    decay = [0.1 * (i % 3) for i in range(c.n)]
+    L.moe_adamw(c.list(decay), seed=5, **HYPER)
+    c.check_guards()
+    for i in range(c.n):
+        if c.p[i].numel():
+            check_adamw(c, i, decay[i], 1.0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("norm,max_norm", [(0.5, 1.0), (40.0, 1.0), (0.0, 1.0), (3e19, 2.0)])
+def test_adamw_clips(norm, max_norm, bits):
+    c = Case(*LISTS["odd"], bits, False, seed=2)
+    sumsq = put(np.array([norm * norm]), torch.float64)
+    L.moe_adamw(c.list(0.1), seed=5, sumsq=sumsq, max_norm=max_norm, **HYPER)
+    for i in range(c.n):
+        check_adamw(c, i, 0.1, S.clip(norm * norm, max_norm))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan"), 1e78])
+def test_adamw_makes_no_step_without_a_norm(bad, bits):
+    for master in (False, True):
+        c = Case(*LISTS["types"], bits, master, seed=3)
+        L.moe_adamw(c.list(0.1), seed=5, sumsq=put(np.array([bad]), torch.float64), **HYPER)
+        for i in range(c.n):
+            for a, b in zip((c.p[i], c.m[i], c.v[i], c.sc[i], c.w[i]), c.results(i)):
+                if a is None:
+                    continue
+                if a is c.p[i] and c.w[i] is not None:
+                    a = c.w[i].to(torch.bfloat16)
+                assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_in_place_and_again(bits):
+    """In place as into other tensors; the same seed gives the same bits, another one others."""
+    a, b, other = (Case(*LISTS["types"], bits, False, seed=4) for _ in range(3))
+    L.moe_adamw(a.list(0.1), seed=9, **HYPER)
+    L.moe_adamw(b.list(0.1, in_place=True), seed=9, **HYPER)
+    L.moe_adamw(other.list(0.1), seed=10, **HYPER)
+    differ = False
+    for i in range(a.n):
+        for x, y, z in zip(a.results(i), (b.p[i], b.m[i], b.v[i], b.sc[i]), other.results(i)):
+            if x is not None:
+                assert torch.equal(x, y)
+                differ |= not torch.equal(x, z)
+    assert differ
+
+
+def test_adamw_rounding_has_the_right_mean():
+    """Of n independent roundings, each off by at most a step: six standard deviations, 0.5 / sqrt(n) each."""
+    n = 1 << 18
+    c = Case([n, n], [BF16, F32], [BF16, F32], 8, False, seed=6)
+    L.moe_adamw(c.list(0.0), seed=77, **HYPER)
+    for i in range(2):
+        m0, v0 = states_before(c, i)
+        P, M, V = S.adamw(np64(c.p[i]), np64(c.g[i]), m0, v0, decay=0.0, **HYPER)
+        p, m, v, sc, _ = c.results(i)
+        s = np64(sc).reshape(2, -1)
+        for codes, scale, want in ((m, s[0], M), (v, s[1], np.sqrt(V))):
+            y = want / np.repeat(scale, 128)
+            use = np.abs(y) > 2.0 ** -6   # not the smallest code, which a positive v is kept at
+            e = (S.E4M3[codes.cpu().numpy()] - y)[use] / code_step(y[use])
+            assert abs(e.mean()) < 3 / np.sqrt(use.sum())
+        if i == 0:
+            e = (np64(p) - P) / (2.0 ** (np.floor(np.log2(np.abs(P))) - 7))
+            assert abs(e.mean()) < 3 / np.sqrt(n)
+
+
+def test_adamw_lost_block():
+    """A gradient that is not finite and no norm to stop it: its element, and its block of 8-bit states."""
+    c = Case([300], [F32], [F32], 8, False, seed=8)
+    c.g[0][140] = float("nan")
+    L.moe_adamw(c.list(0.0), **HYPER)
+    p, m, v, sc, _ = c.results(0)
+    bad = torch.isnan(sc).view(2, 3)
+    assert bad[:, 1].all() and bad.sum() == 2
+    assert torch.isnan(p).sum() == 1 and torch.isnan(p[140])
+    again = L.adamw_list([p], c.g, [m], [v], [sc], None, 0.0)
+    L.moe_adamw(again, **HYPER)
+    assert torch.isnan(sc).sum() == 2 and torch.isnan(p).sum() == 128
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_first_steps(bits):
+    """From zero states; a zero gradient leaves zero states and decays the parameter alone."""
+    p, g = [torch.randn(500, device=DEV)], [torch.zeros(500, device=DEV)]
+    m, v, sc, _ = L.adamw_states(p, bits)
+    p0 = np64(p[0])
+    t = L.adamw_list(p, g, m, v, sc, None, 0.5)
+    L.moe_adamw(t, lr=0.1, beta1=0.9, beta2=0.99, eps=1e-8, step=1)
+    assert np.all(np.abs(np64(p[0]) - 0.95 * p0) <= 4 * F * np.abs(p0)) and not m[0].any() and not v[0].any()
+    g[0].fill_(1e-3)
+    L.moe_adamw(t, lr=0.1, beta1=0.9, beta2=0.99, eps=1e-8, step=1)
+    # m / (1 - beta1) = g and v / (1 - beta2) = g^2 exactly: a step of lr g / (g + eps)
+    want = 0.95 * 0.95 * p0 - 0.1 * 1e-3 / (1e-3 + 1e-8)
+    assert np.all(np.abs(np64(p[0]) - want) <= 40 * F * (np.abs(p0) + 0.1))
+
+
+# ---- all of them: streams, graphs -----------------------------------------------------------------------
+
+class Step:
+    """Route, quantize, multiply, go back through the router, move the bias, step: on one set of buffers."""
+
+    def __init__(self):
+        g = torch.Generator(device=DEV).manual_seed(3)
+        rnd = lambda *s: torch.randn(*s, device=DEV, generator=g)
+        self.T, self.E, self.k, self.d, self.N = 300, 16, 2, 256, 256
+        T, E, k, d, N = self.T, self.E, self.k, self.d, self.N
+        self.x, self.wr, self.bias = rnd(T, d).bfloat16(), (0.1 * rnd(E, d)).bfloat16(), 0.01 * rnd(E)
+        self.w = (0.05 * rnd(E, N, d)).bfloat16()
+        self.logits, self.idx, self.gate = rnd(T, E), torch.zeros(T, k, dtype=torch.int32, device=DEV), rnd(T, k)
+        self.dgate = rnd(T, k)
+        n = T * k
+        # a plan that any choice fits: rows in turn (the products do not depend on the choice)
+        self.offsets = torch.tensor([n * i // E for i in range(E + 1)], dtype=torch.int32, device=DEV)
+        self.src = torch.arange(n, dtype=torch.int32, device=DEV)
+        self.counts = (self.offsets[1:] - self.offsets[:-1]).contiguous()
+        self.rows = rnd(n, d).bfloat16()
+        u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=DEV)
+        self.xq, self.xs = u8(n, d), torch.empty(d // 128, n, device=DEV)
+        self.wq, self.ws = u8(E, N, d), torch.empty(E, N // 128, d // 128, device=DEV)
+        self.y = torch.empty(n, N, dtype=torch.bfloat16, device=DEV)
+        self.dw, self.dx = torch.empty(E, d, device=DEV), torch.empty_like(self.x)
+        self.bytes = max(L.moe_route_balanced_bwd_workspace_size(T, d, E, k, SIG, 1), L.moe_fp8_gemm_workspace_size(E, n, N, d))
+        self.work = workspace(self.bytes)
+        self.params = [self.wr.clone(), self.w.clone()]
+        self.grads = [self.dw, (0.01 * rnd(E, N, d)).bfloat16()]
+        self.m, self.v, self.sc, _ = L.adamw_states(self.params, 8)
+        self.list = L.adamw_list(self.params, self.grads, self.m, self.v, self.sc, None, 0.1)
+        self.sumsq = torch.full((1,), 9.0, dtype=torch.float64, device=DEV)
+
+    def run(self, stream=None):
+        T, E, k, d, N, n = self.T, self.E, self.k, self.d, self.N, self.T * self.k
+        kw = dict(stream=stream)
+        L.moe_route_balanced(self.x, self.wr, self.logits, self.bias, T, d, E, k, 4, 2, SIG, 1, 1.0, L.MOE_BF16, self.idx, self.gate, **kw)
+        L.moe_fp8_quantize_rows(self.rows, n, d, d, self.xq, self.xs, **kw)
+        L.moe_fp8_quantize_weights(self.params[1], E, N, d, self.wq, self.ws, None, None, **kw)
+        L.moe_fp8_gemm_rows(self.xq, self.xs, self.wq, self.ws, None, None, 0, self.offsets, E, n, N, d, L.MOE_MX_EPI_STORE, self.y,
+                            None, None, None, None, self.work, self.bytes, **kw)
+        L.moe_route_balanced_bwd(self.dgate, self.logits, self.idx, self.offsets, self.src, self.x, self.wr, T, d, E, k, SIG, 1,
+                                 1.0, L.MOE_BF16, self.dw, self.dx, self.work, self.bytes, **kw)
+        L.moe_route_bias_update(self.counts, E, 1e-3, self.bias, self.bias, **kw)
+        L.moe_adamw(self.list, 1e-2, 0.9, 0.95, 1e-8, 3, 11, self.sumsq, 1.0, **kw)
+
+    def state(self):
+        return [self.logits, self.gate, self.idx, self.y, self.dw, self.dx, self.bias, *self.params, *self.m, *self.v, *self.sc]
+
+
+def same(a, b):
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+def test_captured_and_replayed():
+    eager, other = Step(), Step()
+    expected = []
+    for _ in range(4):
+        eager.run()
+        expected.append([t.clone() for t in eager.state()])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        other.run()
+    for want in expected:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(other.state(), want)
+        eager.x.normal_()                 # work between the replays
+        eager.run()
+        torch.cuda.synchronize()
+
+
+def test_on_another_stream():
+    eager, other = Step(), Step()
+    eager.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other.run(stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert same(other.state(), eager.state())
+
+
+def test_host_tensors_are_refused():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    with pytest.raises((ValueError, L.MoEError)):
+        L.moe_fp8_quantize_rows(x, 4, 128, 128, torch.empty(4, 128, dtype=torch.uint8, device=DEV), torch.empty(1, 4, device=DEV))
+    t = L.adamw_list([torch.zeros(8)], [torch.zeros(8)], [torch.zeros(8)], [torch.zeros(8)])
+    with pytest.raises((ValueError, L.MoEError)):
+        L.moe_adamw(t, 1e-3, 0.9, 0.95, 1e-8, 1)
