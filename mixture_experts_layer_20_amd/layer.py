@@ -126,6 +126,43 @@ class MxSet:
             self.ws_k = u8(max(nws, 256))
 
 
+class Fp8Set:
+    """Buffers of one expert set in 8-bit floating point with a float scale for each block of 128: the
+    forward products and the data gradients.  Weights are quantized once per pass, their transposed form
+    (the same codes in another order) with them; weight gradients are bf16 products."""
+
+    def __init__(self, offsets, G, M, d, f, device, backward):
+        self.offsets, self.G, self.M, self.d, self.f = offsets, G, M, d, f
+        u8 = lambda *s: torch.empty(*s, dtype=torch.uint8, device=device)
+        f32 = lambda *s: torch.empty(*s, dtype=torch.float32, device=device)
+        rows = lambda K: (u8(max(M, 1), K), f32(K // 128, max(M, 1)))
+        weights = lambda N, K: (u8(G, N, K), f32(G, N // 128, K // 128))
+        self.xq, self.hq = rows(d), rows(f)
+        self.w1q, self.w3q, self.w2q = weights(f, d), weights(f, d), weights(d, f)
+        self.w1t = self.w3t = self.w2t = (None, None)
+        if backward:
+            self.dyq, self.dabq = rows(d), rows(2 * f)
+            self.w1t, self.w3t, self.w2t = weights(d, f), weights(d, f), weights(f, d)
+        sizes = [(f, d), (d, f), (d, 2 * f)]
+        self.ws = u8(max(256, *(L.moe_fp8_gemm_workspace_size(G, M, N, K) for N, K in sizes)))
+
+
+@dataclass(frozen=True)
+class ScoreRouter:
+    """Routing by scores (moe_route_balanced) in place of the softmax over logits.  ``score``: "sigmoid" or
+    "softmax"; a token uses ``topk_groups`` of ``groups`` expert groups; gates are scaled by ``scale``.  The
+    layer's ``params["select_bias"]`` ([E] float, may be absent) takes part in the choice alone and is moved
+    by ``MoELayer.update_select_bias``."""
+    score: str = "sigmoid"
+    groups: int = 1
+    topk_groups: int = 1
+    scale: float = 1.0
+
+    @property
+    def code(self) -> int:
+        return {"softmax": L.MOE_SCORE_SOFTMAX, "sigmoid": L.MOE_SCORE_SIGMOID}[self.score]
+
+
 class MoELayer:
     """One GPU's MoE layer pass over device-resident inputs.
 
@@ -143,6 +180,8 @@ class MoELayer:
     ``precision``: "bf16" (bf16 MFMA products) or "mxfp8" (the MXFP8 recipe of the Ultra runs, "Olmo-core
     DDP MoE examples", "Production throughput runs": every expert product on MX-quantized E4M3
     operands with fp32 accumulation; stored activations and gradients stay bf16).
+    ``precision="fp8"``: forward products and data gradients on E4M3 operands with a float scale for each
+    block of 128 (activations: of a row; weights: 128 x 128); weight gradients are bf16 products.
     ``mx_cached_weights``: quantize the expert weights (both orientations) on the first pass and
     reuse them until ``refresh_mx_weights()`` is called, as when the weights change once per
     optimizer step and several micro-batches pass through the layer in between; otherwise every
@@ -153,12 +192,14 @@ class MoELayer:
     the block has a gate, ``norm_gate`` [ceil(T / gate_rows), d] (``gate_rows``: tokens per gate row,
     by default all of them).  The backward adds the residual's gradient to dx and writes
     ``dnorm_in``, ``dnorm_out`` and ``dnorm_gate`` (float).
+    ``router``: a ScoreRouter, for routing by scores; ``renormalize`` divides the gates by their sum.
     """
 
     def __init__(self, cfg: MoEConfig, params: dict, bufs: Buffers | None = None, renormalize: int = 1,
                  merge_shared: bool = True, recompute: bool = False, lbl_weight: float = 0.0,
                  precision: str = "bf16", mx_cached_weights: bool = False, block_norm: bool = False,
-                 gate_rows: int | None = None, res_scale: float = 1.0, norm_eps: float = 1e-6):
+                 gate_rows: int | None = None, res_scale: float = 1.0, norm_eps: float = 1e-6,
+                 router: ScoreRouter | None = None):
         self.cfg = cfg
         self.p = params
         self.bufs = bufs or Buffers.allocate(cfg, params["x"].device)
@@ -189,7 +230,11 @@ class MoELayer:
                                               dtype=torch.uint8, device=dev)
         self.dt = L.MOE_BF16 if cfg.dtype == "bf16" else L.MOE_F32
         self.events: dict | None = None
-        if precision not in ("bf16", "mxfp8"):
+        self.router = router
+        if router is not None:
+            self._check_router()
+        self._adamw = None
+        if precision not in ("bf16", "mxfp8", "fp8"):
             raise ValueError(f"unknown precision {precision!r}")
         self.precision = precision
         self.mx = None
@@ -202,6 +247,33 @@ class MoELayer:
             self.mx = [MxSet(b["offsets"], cfg.E, cfg.T * cfg.k, cfg.d, cfg.f, dev, cfg.backward)]
             if cfg.fs > 0:
                 self.mx.append(MxSet(b["shared_offsets"], 1, cfg.T, cfg.d, cfg.fs, dev, cfg.backward))
+        self.fp8 = None
+        if precision == "fp8":
+            if cfg.dtype != "bf16" or recompute:
+                raise ValueError("the fp8 expert path takes bf16 workloads without recompute")
+            if cfg.d % 128 or cfg.f % 128 or cfg.fs % 128:
+                raise ValueError("the fp8 expert path needs d, f and fs to be multiples of 128")
+            dev, b = params["x"].device, self.bufs
+            self.fp8 = [Fp8Set(b["offsets"], cfg.E, cfg.T * cfg.k, cfg.d, cfg.f, dev, cfg.backward)]
+            if cfg.fs > 0:
+                self.fp8.append(Fp8Set(b["shared_offsets"], 1, cfg.T, cfg.d, cfg.fs, dev, cfg.backward))
+
+    def _check_router(self):
+        c, p, q = self.cfg, self.p, self.router
+        if q.score not in ("softmax", "sigmoid"):
+            raise ValueError(f"unknown score {q.score!r}")
+        if self.lbl > 0:
+            raise ValueError("the auxiliary loss is that of the softmax router; a ScoreRouter is balanced by its bias")
+        if p.get("bias") is not None:
+            raise ValueError("a ScoreRouter's logits have no bias; params['select_bias'] takes part in the choice")
+        if c.E % q.groups or not 1 <= q.topk_groups <= q.groups or c.k > q.topk_groups * (c.E // q.groups):
+            raise ValueError(f"{q.topk_groups} of {q.groups} groups of {c.E} experts do not hold {c.k} choices")
+        bias = p.get("select_bias")
+        if bias is not None and (tuple(bias.shape) != (c.E,) or bias.dtype != torch.float32):
+            raise ValueError("select_bias must be [E] float")
+        if c.backward and c.routing == "learned":
+            need = L.moe_route_balanced_bwd_workspace_size(c.T, c.d, c.E, c.k, q.code, self.renorm)
+            self._ws_scores = torch.empty(max(256, need), dtype=torch.uint8, device=p["x"].device)
 
     @property
     def x(self) -> torch.Tensor:
@@ -288,9 +360,15 @@ class MoELayer:
         logits = b["logits"] if learned else p["logits"]
         if self.norm:
             self._stage("norm_in", L.moe_norm_in, p["x"], p["norm_in"], T, d, self.norm_eps, dt, b["xn"], b["rstd_in"])
-        self._stage("route", L.moe_route, self.x, p.get("w_router") if learned else None,
-                    p.get("bias") if learned else None, logits, T, d, E, k, self.renorm, dt,
-                    b["topk_idx"], b["gate"])
+        if self.router is not None:
+            q = self.router
+            self._stage("route", L.moe_route_balanced, self.x, p.get("w_router") if learned else None, logits,
+                        p.get("select_bias"), T, d, E, k, q.groups, q.topk_groups, q.code, self.renorm, q.scale, dt,
+                        b["topk_idx"], b["gate"])
+        else:
+            self._stage("route", L.moe_route, self.x, p.get("w_router") if learned else None,
+                        p.get("bias") if learned else None, logits, T, d, E, k, self.renorm, dt,
+                        b["topk_idx"], b["gate"])
         self._stage("permute", L.moe_permute, self.x, b["topk_idx"], T, d, E, k, dt, b["counts"],
                     b["offsets"], b["dest_pos"], b["src_row"], b["x_perm"], b["ws_perm"],
                     b["ws_perm"].numel())
@@ -299,6 +377,8 @@ class MoELayer:
                         b["prob_mean"], b["load_frac"], b["ws_aux"], b["ws_aux"].numel())
         if self.mx is not None:
             self._mx_forward()
+        elif self.fp8 is not None:
+            self._fp8_forward()
         else:
             sets = self._sets(stash=not self.recompute)
             self._gemm("gate_up_fwd", L.MOE_STAGE_GATE_UP_FWD, sets, b["ws_fwd"])
@@ -336,7 +416,13 @@ class MoELayer:
         self._stage("combine_bwd", L.moe_combine_bwd, dout, b["y"], b["gate"], b["dest_pos"], T, d, k, dt,
                     b["dy"], b["dgate"] if learned else None)
         dx_router = None
-        if learned:
+        if learned and self.router is not None:
+            q = self.router
+            self._stage("route_bwd", L.moe_route_balanced_bwd, b["dgate"], b["logits"], b["topk_idx"], b["offsets"],
+                        b["src_row"], self.x, p["w_router"], T, d, E, k, q.code, self.renorm, q.scale, dt, b["dwr"],
+                        b["dx_router"], self._ws_scores, self._ws_scores.numel())
+            dx_router = b["dx_router"]
+        elif learned:
             self._stage("route_bwd", L.moe_route_bwd, b["dgate"], b["gate"], b["topk_idx"], b["offsets"],
                         b["src_row"], self.x, p["w_router"], T, d, E, k, self.renorm, dt, b["dwr"],
                         b["dx_router"], b["ws_route"], b["ws_route"].numel())
@@ -359,8 +445,11 @@ class MoELayer:
         # Each activation gradient is consumed right after it is produced, while it still sits in
         # the last-level cache (dA/dB by the gate/up dgrad, dX_perm by the permute backward); the
         # weight gradients, which nothing downstream reads, go last.
-        self._gemm("down_bwd", L.MOE_STAGE_DOWN_BWD, sets, ws)
-        self._gemm("gate_up_dgrad", L.MOE_STAGE_GATE_UP_DGRAD, sets, ws)
+        if self.fp8 is not None:
+            self._fp8_dgrad(dout)
+        else:
+            self._gemm("down_bwd", L.MOE_STAGE_DOWN_BWD, sets, ws)
+            self._gemm("gate_up_dgrad", L.MOE_STAGE_GATE_UP_DGRAD, sets, ws)
         self._stage("permute_bwd", L.moe_permute_bwd, b["dx_perm"], b["dest_pos"], dx_shared, dx_router, T, d,
                     k, dt, dx)
         self._gemm("down_wgrad", L.MOE_STAGE_DOWN_WGRAD, sets, ws)
@@ -384,7 +473,7 @@ class MoELayer:
         return name if i == 0 else "shared_" + name
 
     def refresh_mx_weights(self):
-        """Cached mode: the weights changed; the next pass quantizes them again."""
+        """Cached mode (MXFP8 or fp8): the weights changed; the next pass quantizes them again."""
         self._mx_w_fresh = False
 
     def _mx_quantize_weights(self):
@@ -453,6 +542,95 @@ class MoELayer:
             self._stage(self._pfx(i, "gate_up_wgrad"), L.moe_mx_gemm_k, m.abc[0], m.abc[1], m.ld, m.xc[0],
                         m.xc[1], m.ld, m.kbase, G, 2 * f, d, f, t["dw1"], t["dw3"], m.ws_k,
                         m.ws_k.numel())
+
+    # ---- 8-bit expert products with scales for blocks of 128 -------------------------------
+    def _fp8_quantize_weights(self):
+        d = self.cfg.d
+        for i, m in enumerate(self.fp8):
+            t, G, f = self._mx_tensors(i), m.G, m.f
+            for name, w, N, K, out, flip in (("q_w1", t["w1"], f, d, m.w1q, m.w1t), ("q_w3", t["w3"], f, d, m.w3q, m.w3t),
+                                             ("q_w2", t["w2"], d, f, m.w2q, m.w2t)):
+                self._stage(self._pfx(i, name), L.moe_fp8_quantize_weights, w, G, N, K, *out, *flip)
+        self._mx_w_fresh = True
+
+    def _fp8_product(self, i, name, m, rows, w, w2, k2, N, K, epilogue, out, aux=(None, None)):
+        self._stage(self._pfx(i, name), L.moe_fp8_gemm_rows, *rows, *w, *(w2 or (None, None)), k2, m.offsets, m.G, m.M, N, K,
+                    epilogue, *out, *aux, m.ws, m.ws.numel())
+
+    def _fp8_forward(self):
+        d, bw = self.cfg.d, self.cfg.backward
+        if not (self.mx_cached and self._mx_w_fresh):
+            self._fp8_quantize_weights()
+        for i, m in enumerate(self.fp8):
+            t, M, f = self._mx_tensors(i), m.M, m.f
+            self._stage(self._pfx(i, "q_x"), L.moe_fp8_quantize_rows, t["x"], M, d, d, *m.xq)
+            self._fp8_product(i, "gate_up_fwd", m, m.xq, m.w1q, m.w3q, 0, f, d, L.MOE_MX_EPI_SWIGLU,
+                              (t["a"] if bw else None, t["b"] if bw else None, t["h"]))
+            self._stage(self._pfx(i, "q_h"), L.moe_fp8_quantize_rows, t["h"], M, f, f, *m.hq)
+            self._fp8_product(i, "down_fwd", m, m.hq, m.w2q, None, 0, d, f, L.MOE_MX_EPI_STORE, (t["y"], None, None))
+
+    def _fp8_dgrad(self, dout):
+        d = self.cfg.d
+        for i, m in enumerate(self.fp8):
+            t, M, f = self._mx_tensors(i, dout), m.M, m.f
+            self._stage(self._pfx(i, "q_dy"), L.moe_fp8_quantize_rows, t["dy"], M, d, d, *m.dyq)
+            self._fp8_product(i, "down_bwd", m, m.dyq, m.w2t, None, 0, f, d, L.MOE_MX_EPI_SWIGLU_BWD,
+                              (t["dab"], None, None), (t["a"], t["b"]))
+            self._stage(self._pfx(i, "q_dab"), L.moe_fp8_quantize_rows, t["dab"], M, 2 * f, 2 * f, *m.dabq)
+            self._fp8_product(i, "gate_up_dgrad", m, m.dabq, m.w1t, m.w3t, f, d, 2 * f, L.MOE_MX_EPI_STORE,
+                              (t["dx"], None, None))
+
+    # ---- the step that follows a pass ------------------------------------------------------
+    def update_select_bias(self, rate: float):
+        """Move the ScoreRouter's bias towards balance by this pass's counts."""
+        if self.router is None or self.p.get("select_bias") is None:
+            raise ValueError("the layer has no ScoreRouter with a select_bias")
+        bias = self.p["select_bias"]
+        self._stage("bias_update", L.moe_route_bias_update, self.bufs["counts"], self.cfg.E, rate, bias, bias)
+
+    def parameters(self) -> list[torch.Tensor]:
+        """The parameters that gradients() are of, in its order."""
+        p, c = self.p, self.cfg
+        names = ["w1", "w3", "w2"]
+        if c.fs > 0:
+            names += ["ws1", "ws3", "ws2"]
+        if c.routing == "learned":
+            names.append("w_router")
+        if self.norm:
+            names += ["norm_in", "norm_out"]
+            if self._dnorm_gate is not None:
+                names.append("norm_gate")
+        return [p[n] for n in names]
+
+    def make_adamw(self, state_bits: int = 32, master: bool = False, weight_decay=0.0):
+        """The optimizer's states (zeros) for adamw_step: 32 or 8 bits, with or without float master copies
+        of bf16 parameters; weight_decay for all parameters or a list in their order."""
+        if not self.cfg.backward:
+            raise ValueError("the layer has no backward")
+        params, grads = self.parameters(), self.gradients()
+        m, v, scales, masters = L.adamw_states(params, state_bits, master)
+        self._adamw = L.adamw_list(params, grads, m, v, scales, masters, weight_decay)
+        self._adamw_grads = L.grad_list(grads)
+        self._adamw_sumsq = torch.empty(1, dtype=torch.float64, device=params[0].device)
+        self._ws_adamw = torch.empty(max(256, L.moe_grad_workspace_size(self._adamw_grads)), dtype=torch.uint8,
+                                     device=params[0].device)
+        self.steps = 0
+
+    def adamw_step(self, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
+                   max_norm: float | None = None, seed: int = 0):
+        """One AdamW step on the parameters, in place, from the gradients of the last backward, clipped in the
+        same pass to a global norm of max_norm if that is given (grad_norm then is the norm).  make_adamw comes
+        first.  Quantized weights are made again by the next pass.  The step's number is an argument of the
+        kernels: a captured graph would repeat it."""
+        if self._adamw is None:
+            raise ValueError("make_adamw comes before adamw_step")
+        if max_norm is not None:
+            self._stage("grad_norm", L.moe_grad_norm, self._adamw_grads, self._adamw_sumsq, self.grad_norm, self._ws_adamw,
+                        self._ws_adamw.numel())
+        self._stage("adamw", L.moe_adamw, self._adamw, lr, beta1, beta2, eps, self.steps + 1, seed + self.steps,
+                    self._adamw_sumsq if max_norm is not None else None, 1.0 if max_norm is None else max_norm)
+        self.steps += 1
+        self._mx_w_fresh = False
 
     def gradients(self) -> list[torch.Tensor]:
         """Every parameter gradient the backward writes (dx, the input's, is not among them)."""
