@@ -237,10 +237,11 @@ def main(argv=None) -> int:
     ap.add_argument("--recompute", action="store_true",
                     help="per-layer recompute variant: no A/B stash in the forward, gate/up GEMM rerun in "
                          "the backward")
-    ap.add_argument("--precision", choices=("bf16", "mxfp8"), default="bf16",
-                    help="expert products in bf16, or in MXFP8 (E4M3 with one E8M0 scale per 32 elements)")
+    ap.add_argument("--precision", choices=("bf16", "mxfp8", "fp8"), default="bf16",
+                    help="expert products in bf16, in MXFP8 (E4M3 with one E8M0 scale per 32 elements), or in fp8 "
+                         "(E4M3 with one float scale per block of 128; weight gradients in bf16)")
     ap.add_argument("--mx-cached-weights", action="store_true",
-                    help="MXFP8: quantize the expert weights once before the timed steps (the optimizer-step "
+                    help="MXFP8 and fp8: quantize the expert weights once before the timed steps (the optimizer-step "
                          "cadence, with several micro-batches per weight update) instead of in every pass")
     ap.add_argument("--no-merge", action="store_true",
                     help="one GEMM call per expert set instead of routed + shared in one call")
@@ -267,7 +268,7 @@ def main(argv=None) -> int:
     print(f"[bench] generating inputs for {cfg.name}", file=sys.stderr, flush=True)
     inp = I.make_inputs(cfg)
     dev = torch.device("cuda:0")
-    mx = a.precision == "mxfp8"
+    mx = a.precision != "bf16"   # quantized operands, a call for each expert set
     merged = not (a.no_merge or mx)
     lay = LY.MoELayer(cfg, LY.upload_inputs(inp, dev), merge_shared=merged, recompute=a.recompute,
                       lbl_weight=a.lbl, precision=a.precision, mx_cached_weights=a.mx_cached_weights)
@@ -299,7 +300,6 @@ def main(argv=None) -> int:
         stages[name] = sum(ms) / len(ms)
     lay.events = None
     flops = stage_flops(cfg, merged=merged, recompute=a.recompute)
-    peak = PEAK_FP8_TFLOPS if mx else PEAK_BF16_TFLOPS
     gemm_ms = sum(stages[s] for s in flops if s in stages)
     gemm_flop = sum(flops.values())
     stage_tflops = {s: flops[s] / (stages[s] * 1e-3) / 1e12 for s in flops if s in stages}
@@ -307,6 +307,7 @@ def main(argv=None) -> int:
     # grouped-GEMM launch (a weight gradient whose reduction is split adds its reduce launch).
     dom = max((s for s in flops if s in stages), key=lambda s: stages[s])
     achieved = stage_tflops[dom]
+    peak = PEAK_FP8_TFLOPS if mx and not (a.precision == "fp8" and dom.endswith("wgrad")) else PEAK_BF16_TFLOPS
     traffic = None
     if os.path.exists(a.traffic_json):
         try:
@@ -327,7 +328,8 @@ def main(argv=None) -> int:
         "higher_is_better": True,
         "scaling": "weak",
         "vs_baseline": None,
-        "dtype": "mxfp8-e4m3 products, bf16 storage" if mx else cfg.dtype,
+        "dtype": {"mxfp8": "mxfp8-e4m3 products, bf16 storage",
+                  "fp8": "fp8-e4m3 products (weight gradients bf16), bf16 storage"}.get(a.precision, cfg.dtype),
         "data": "synthetic (seeded Gaussian inputs and weights; random routing logits drawn per token)"
         if cfg.routing == "random" else "synthetic (seeded Gaussian inputs and weights, learned router)",
         "config": {"workload": cfg.name, "tokens": cfg.T, "d_model": cfg.d, "experts": cfg.E, "top_k": cfg.k,
@@ -353,9 +355,9 @@ def main(argv=None) -> int:
                              for s, by in stage_bytes(cfg).items() if s in stages},
     }
     if mx:
-        # MXFP8 quantization passes (activations each product, weights in both orientations).
+        # Quantization passes (activations each product, weights in both orientations).
         qs = {k: v for k, v in stages.items() if k.startswith("q_") or k.startswith("shared_q_")}
-        line["mxfp8_quantize_ms"] = sum(qs.values())
+        line[a.precision + "_quantize_ms"] = sum(qs.values())
     del lay, flush
     torch.cuda.empty_cache()
     if not a.no_ceilings:
