@@ -16,7 +16,7 @@
 // and the open groups are found by moves between lanes.  The choice works on 32-bit keys, three bits of which
 // are the expert's place in its lane (so that they carry 20 bits of mantissa): every lane sorts its keys once,
 // and a round is then a maximum over the lanes' first keys and a step of the winner's queue.
-// 8192 tokens of 256 experts in 8 groups with k = 8: 14 us (9 MB, 2 us at the rate of a copy; one token 5.7 us, a
+// 8192 tokens of 256 experts in 8 groups with k = 8: 13 us (9 MB, 2 us at the rate of a copy; one token 5.6 us, a
 // launch), 2 of them for the waves that are decided again, whose time the launch waits for; walking the groups
 // in LDS and taking the k largest of 64-bit keys one after the other was 25.
 //
@@ -50,7 +50,7 @@ __device__ __forceinline__ uint64_t order_code(double v) {
   const uint64_t flip = (uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull;
   return (b & 0x7fffffffffffffffull) > 0x7ff0000000000000ull ? 0ull : b ^ flip;
 }
-// A key of `choose` to its value, rounded down; NaN is -inf.
+// A key of `choose` to its value, rounded down.
 __device__ __forceinline__ float key_value(uint32_t key) {
   const uint32_t code = key & ~7u;
   return code < 0x00800000u ? -INFINITY : __uint_as_float(code & 0x80000000u ? code & 0x7fffffffu : ~code);
@@ -94,13 +94,22 @@ __device__ __forceinline__ V over_lanes(int lanes, V v, Op op) {
   if (lanes >= 32) v = op(v, across<16>(v));
   return v;
 }
+// Of floats one instruction, which takes the number where the other is a NaN.
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
 struct Max {
   template <typename V>
   __device__ V operator()(V a, V b) const { return a > b ? a : b; }
+  __device__ float operator()(float a, float b) const { return larger(a, b); }
+  __device__ double operator()(double a, double b) const { return larger(a, b); }
 };
 struct Min {
   template <typename V>
   __device__ V operator()(V a, V b) const { return a < b ? a : b; }
+  __device__ float operator()(float a, float b) const { return smaller(a, b); }
+  __device__ double operator()(double a, double b) const { return smaller(a, b); }
 };
 struct Sum {
   template <typename V>
@@ -155,14 +164,17 @@ __device__ __forceinline__ bool nearby(R high, R low, R tolerance) {
   return !(high - low > tolerance * (R(2) + finite(high) + finite(low)));
 }
 
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return (uint32_t)__shfl((int)v, lane, 64); }
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) { return (uint64_t)__shfl((long long)v, lane, 64); }
+
 // The two largest of a lane's values; a NaN is none.
 template <typename R>
 struct TopTwo {
   R a = -INFINITY, b = -INFINITY;
   __device__ __forceinline__ void take(R c) {
-    const R v = c == c ? c : R(-INFINITY);
-    b = Max()(b, Min()(a, v));
-    a = Max()(a, v);
+    const R v = larger(c, R(-INFINITY));
+    b = larger(b, smaller(a, v));
+    a = larger(a, v);
   }
 };
 // Whether this lane's group is open, from the two largest selection scores of its experts here; at.q lanes a
@@ -183,7 +195,7 @@ __device__ __forceinline__ bool group_open(const RouteScores& r, const Place& at
   const int g = j / at.q, lane0 = ((int)threadIdx.x & 63) - j;
   int rank = 0;
   for (int o = 0; o < r.groups; ++o) {
-    const auto other = order_code((R)__shfl(score, lane0 + o * at.q, 64));
+    const auto other = lane_value(mine, lane0 + o * at.q);
     rank += other > mine || (other == mine && o < g) ? 1 : 0;
   }
   const bool open = rank < r.topk_groups;
@@ -290,8 +302,11 @@ __device__ __forceinline__ void sort_down(uint32_t (&key)[S]) {
 template <int S>
 __device__ __forceinline__ void sorted_keys(const float (&v)[S], uint32_t shut, uint32_t (&key)[S]) {
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    key[s] = (shut >> s & 1u) ? 0u : (max(order_code(v[s]), 0x100u) & ~7u) | (7 - s);
+  for (int s = 0; s < S; ++s) {   // order_code's order, but a NaN is -inf
+    const uint32_t b = __float_as_uint(fmaxf(v[s], -INFINITY) + 0.0f);
+    const uint32_t code = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    key[s] = (shut >> s & 1u) ? 0u : (code & ~7u) | (7 - s);
+  }
   sort_down<S>(key);
 }
 template <int S>
@@ -440,10 +455,18 @@ __global__ __launch_bounds__(256) void route_scores_kernel(RouteScores r, int32_
     load4(r.logits + (size_t)tc * r.E + at.first, at.in_run(s), at.size, r.whole, l + s);
     if (biased) load4(r.bias + at.first, at.in_run(s), at.size, r.whole, b + s);
   }
+  if (r.whole) {
+#pragma unroll
+    for (int s = 0; s < S; s += 4)
+      if (at.has(s)) *reinterpret_cast<float4*>(&logit_s[slot][at.expert(s)]) = make_float4(l[s], l[s + 1], l[s + 2], l[s + 3]);
+  } else {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (at.has(s)) logit_s[slot][at.expert(s)] = l[s];
+  }
 #pragma unroll
   for (int s = 0; s < S; ++s) {
-    if (at.has(s)) logit_s[slot][at.expert(s)] = l[s];
-    else shut |= 1u << s;
+    if (!at.has(s)) shut |= 1u << s;
     if (!biased) b[s] = 0.0f;
   }
   float c[S];
@@ -554,8 +577,8 @@ __global__ __launch_bounds__(256) void route_bias_kernel(const int32_t* counts, 
 // has no cancellation of large terms.
 
 // Logit gradients of the chosen experts [T, k], one thread for each token.
-__global__ __launch_bounds__(256) void scores_grad_kernel(RouteScores r, const float* dgate, const int32_t* idx, float* dl) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
+__global__ __launch_bounds__(64) void scores_grad_kernel(RouteScores r, const float* dgate, const int32_t* idx, float* dl) {
+  const int t = blockIdx.x * 64 + threadIdx.x;
   if (t >= r.T) return;
   float l[8], dg[8];
 #pragma unroll
@@ -663,7 +686,7 @@ hipError_t launch_route_scores_bwd(const RouteScores& r, const float* dgate, con
   void* rest = reinterpret_cast<char*>(ws) + align256((size_t)r.T * (dense ? r.E : r.k) * sizeof(float));
   if (r.T > 0) {
     if (dense) scores_grad_dense_kernel<<<dim3(ceil_div(r.T, 4)), dim3(256), 0, s>>>(r, dgate, topk_idx, dl);
-    else scores_grad_kernel<<<dim3(ceil_div(r.T, 256)), dim3(256), 0, s>>>(r, dgate, topk_idx, dl);
+    else scores_grad_kernel<<<dim3(ceil_div(r.T, 64)), dim3(64), 0, s>>>(r, dgate, topk_idx, dl);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
