@@ -6,9 +6,11 @@
 // instructions (512 cycles of its SIMD), straight from memory: the four waves of a workgroup, side by side in
 // c, read the same Q through the CU's cache.
 //
-// dw sums over T tokens for few outputs: T goes in parts to about 2048 waves, two for each SIMD, whose sums
-// are added in order.  T 1537, d 1000, E 60 in fp32: dw 54 -> 12 us, dx 27 -> 13 us against vector
-// multiply-adds of one column a thread; what bounds it is the latency of 15 to 16 steps a wave.
+// dw sums over T tokens for few outputs: T goes in parts to about 2048 waves, two for each SIMD, of 32 tokens or
+// more, whose sums are added in order.  T 1537, d 1000, E 60 in fp32: both products 17 us in one launch (12 + 13
+// in two) and 4 for the parts' join, against 54 + 27 + 4 with vector multiply-adds of one column a thread; 14 MB
+// and 0.4 GFLOP are 3 us.  What bounds it is the latency of the 15 steps of 4 that a wave of dx takes, 4 of them
+// in flight (with the next 4 loaded while 4 are multiplied: 20 us).
 #include "train_step.h"
 
 #include <algorithm>
@@ -19,22 +21,22 @@ namespace {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int TILE = 64;     // outputs of a wave, each way
-constexpr int AHEAD = 2;     // steps of 4 of k in flight
+constexpr int AHEAD = 4;     // steps of 4 of k in flight
 
 int dw_splits(long long T, long long d, int E) {
   const long long tiles = ceil_div(d, TILE) * (long long)ceil_div(E, TILE);
-  return (int)std::max(1LL, std::min<long long>(ceil_div(T, TILE), 2048 / tiles));
+  return (int)std::max(1LL, std::min<long long>(ceil_div(T, 32), 2048 / tiles));
 }
 
-// DW: Q = G, k the tokens of part blockIdx.y, out the parts' sums [parts, E, d]; else Q[k, n] = G[n, k], out dx.
+// DW: Q = G, k the tokens of a part, out the parts' sums [parts, E, d]; else Q[k, n] = G[n, k], out dx.
 template <typename T, bool DW>
-__global__ __launch_bounds__(256) void dense_product_kernel(const float* G, const T* P, int ntok, int d, int E, void* out) {
+__device__ __forceinline__ void dense_product(const float* G, const T* P, int ntok, int d, int E, int block, int part,
+                                              int parts, void* out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, q = lane >> 4;
   const int cols = (d + 4 * TILE - 1) / (4 * TILE);
-  const int c0 = ((int)(blockIdx.x % cols) * 4 + wave) * TILE, n0 = (int)(blockIdx.x / cols) * TILE;
+  const int c0 = (block % cols * 4 + wave) * TILE, n0 = block / cols * TILE;
   if (c0 >= d) return;
   const int N = DW ? E : ntok, K = DW ? ntok : E;
-  const int part = DW ? (int)blockIdx.y : 0, parts = DW ? (int)gridDim.y : 1;
   const int kb = (int)((long long)K * part / parts), ke = (int)((long long)K * (part + 1) / parts);
   f32x4_t acc[4][4];   // c, n
 #pragma unroll
@@ -94,6 +96,19 @@ __global__ __launch_bounds__(256) void dense_product_kernel(const float* G, cons
   }
 }
 
+// Both in one launch, dw's workgroups first: neither fills the CUs by itself where the tokens are few.
+template <typename T>
+__global__ __launch_bounds__(256) void dense_products_kernel(const float* G, const T* x, const T* w, int ntok, int d, int E,
+                                                             int dw_blocks, int parts, float* sums, T* dx) {
+  const int b = blockIdx.x;
+  if (b < dw_blocks) {
+    const int tiles = dw_blocks / parts;
+    dense_product<T, true>(G, x, ntok, d, E, b % tiles, b / tiles, parts, sums);
+  } else {
+    dense_product<T, false>(G, w, ntok, d, E, b - dw_blocks, 0, 1, dx);
+  }
+}
+
 // The parts' sums in order; no part (no token): zeros.
 __global__ __launch_bounds__(256) void dense_join_kernel(const float* parts, int count, int n, float* dw) {
   const int i = blockIdx.x * 256 + threadIdx.x;
@@ -110,8 +125,8 @@ hipError_t launch_products(const float* G, const T* x, const T* w, int ntok, int
   const int count = ntok > 0 ? dw_splits(ntok, d, E) : 0;
   if (ntok > 0) {
     const int cols = ceil_div(d, 4 * TILE);
-    dense_product_kernel<T, false><<<dim3(cols * ceil_div(ntok, TILE)), dim3(256), 0, s>>>(G, w, ntok, d, E, dx);
-    dense_product_kernel<T, true><<<dim3(cols * ceil_div(E, TILE), count), dim3(256), 0, s>>>(G, x, ntok, d, E, parts);
+    const int dw_blocks = cols * ceil_div(E, TILE) * count, dx_blocks = cols * ceil_div(ntok, TILE);
+    dense_products_kernel<T><<<dim3((unsigned)dw_blocks + dx_blocks), dim3(256), 0, s>>>(G, x, w, ntok, d, E, dw_blocks, count, parts, dx);
   }
   dense_join_kernel<<<dim3(ceil_div((long long)E * d, 256)), dim3(256), 0, s>>>(parts, count, E * d, dw);
   return hipGetLastError();
