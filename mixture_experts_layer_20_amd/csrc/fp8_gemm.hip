@@ -281,7 +281,6 @@ constexpr int W = 4;
 template <int EPI>
 __global__ __launch_bounds__(64 * W) void fp8_few_kernel(Fp8GemmArgs p) {
   constexpr int B = EPI == MX_EPI_SWIGLU ? 2 : 1;   // weight streams
-  constexpr int AHEAD = 4 / B;                      // blocks of 128 in flight
   __shared__ __attribute__((aligned(16))) float red[W][B][16][20];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, q = lane >> 4;
   const int NT = p.N / 16, nt = blockIdx.x % NT;
@@ -301,12 +300,13 @@ __global__ __launch_bounds__(64 * W) void fp8_few_kernel(Fp8GemmArgs p) {
   f32x4_t acc[B];
 #pragma unroll
   for (int s = 0; s < B; ++s) acc[s] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int kb = k0; kb < k1; kb += AHEAD) {
+  auto blocks = [&](auto count, int kb) {   // of 128, all loaded before the first is multiplied
+    constexpr int AHEAD = decltype(count)::value;
     i32x8_t fa[AHEAD], fb[AHEAD][B];
     float sa[AHEAD], sb[AHEAD][B];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      const int k = min(kb + u, k1 - 1);   // one block more than once rather than a load under a condition
+      const int k = kb + u;
 #pragma unroll
       for (int s = 0; s < B; ++s) {
         const bool second = EPI == MX_EPI_SWIGLU ? s == 1 : k * BLK >= K1;
@@ -323,11 +323,18 @@ __global__ __launch_bounds__(64 * W) void fp8_few_kernel(Fp8GemmArgs p) {
       for (int s = 0; s < B; ++s) {
         const f32x4_t part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
             fb[u][s], fa[u], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, ONE, 0, ONE);
-        const float f = kb + u < k1 ? sa[u] * sb[u][s] : 0.0f;
+        const float f = sa[u] * sb[u][s];
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[s][e] = __builtin_fmaf(f, part[e], acc[s][e]);
       }
-  }
+  };
+  // Short runs too: a wave of K = 1024 has two blocks, and two more loads of each cost it the same again (48 for
+  // 26 us, 244 rows by 64 weights of 2048 x 1024).
+  int kb = k0;
+  if constexpr (B == 1)
+    for (; kb + 4 <= k1; kb += 4) blocks(std::integral_constant<int, 4>(), kb);
+  for (; kb + 2 <= k1; kb += 2) blocks(std::integral_constant<int, 2>(), kb);
+  if (kb < k1) blocks(std::integral_constant<int, 1>(), kb);
   // lane: row li of each 16, columns 4 q .. 4 q + 3
 #pragma unroll
   for (int s = 0; s < B; ++s) *reinterpret_cast<f32x4_t*>(&red[wave][s][li][4 * q]) = acc[s];
@@ -852,12 +859,16 @@ hipError_t launch_pipe(const Fp8GemmArgs& a, hipStream_t s) {
 
 template <int EPI>
 hipError_t launch_epi(const Fp8GemmArgs& a, hipStream_t s) {
-  // A wave's 16 rows read a group's weights at the rate of memory, but each further 16 read them again: 64
-  // groups of 2048 x 2048, microseconds of few rows / of 256-row tiles, at 1, 4, 8, 16 rows a group 46 / 51,
-  // 50 / 50, 55 / 52, 68 / 52; with SwiGLU (N 1024) 28 / 46, 40 / 52, 48 / 54, 66 / 60.  And a tile's workgroup
-  // reads its weights alone: one group, K 7168, N 2048, at 16 and 64 rows 10 / 46 and 18 / 47.
+  // A wave's 16 rows read a group's weights at the rate of memory, but each further 16 read them again; a tile's
+  // workgroup reads its weights alone, and has one block of them in flight.  Microseconds of few rows / of
+  // 256-row tiles, 64 groups of random sizes, at 1, 4 and 8 rows a group on average: K 2048, N 2048 32 / 42,
+  // 45 / 43, 57 / 44, but with a quarter of the columns (128 tiles, half the CUs) 11 / 21, 16 / 22, 19 / 22, and
+  // with K 4096, weights that pass the last-level cache, 58 / 114, 88 / 126, 113 / 130.  With SwiGLU, whose two
+  // products share the rows' loads, N 1024 28 / 45, 40 / 46, 48 / 53.  One group, K 7168, N 2048, at 16 and 64
+  // rows 10 / 46 and 18 / 47.
   const bool fits = ((a.M + 15) / 16 + a.G) * (long long)(a.N / 16) <= 1 << 22;   // below 2^31 threads
-  if ((a.M <= 64 || a.M <= 8LL * a.G) && fits) return launch_few<EPI>(a, s);
+  const bool longer = EPI == MX_EPI_SWIGLU || (long long)a.G * a.N < 256LL * PN || (long long)a.G * a.N * a.K > 256LL << 20;
+  if ((a.M <= 64 || a.M <= (longer ? 8LL : 2LL) * a.G) && fits) return launch_few<EPI>(a, s);
   // a tile's columns: 256 of N, or 128 gate and 128 up columns
   if (a.N % (EPI == MX_EPI_SWIGLU ? 128 : PN) == 0) return launch_pipe<EPI>(a, s);
   return launch_tiles<EPI>(a, s);
