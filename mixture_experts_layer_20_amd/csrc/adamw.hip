@@ -418,7 +418,12 @@ __global__ __launch_bounds__(NT, BITS8 ? 5 : 8) void adamw_kernel(Table<CAP> t) 
   if (t.step.sumsq) {
     const double norm = sqrt(*t.step.sumsq);
     if (!((float)norm <= 3.4028234664e38f)) {   // no step: the outputs are the inputs
-      if (k.param) copy_chunk(k.param, k.param_out, k.n, bf16 ? 2 : 4);
+      if (k.param) {
+        copy_chunk(k.param, k.param_out, k.n, bf16 ? 2 : 4);
+      } else {   // a master copy stands for it
+        for (uint32_t e = threadIdx.x; e < k.n; e += NT)
+          reinterpret_cast<bf16_t*>(k.param_out)[e] = f32_to_bf16(reinterpret_cast<const float*>(k.master)[e]);
+      }
       copy_chunk(k.m, k.m_out, k.n, BITS8 ? 1 : 4);
       copy_chunk(k.v, k.v_out, k.n, BITS8 ? 1 : 4);
       if (k.master) copy_chunk(k.master, k.master_out, k.n, 4);

@@ -604,7 +604,8 @@ class MoELayer:
 
     def make_adamw(self, state_bits: int = 32, master: bool = False, weight_decay=0.0):
         """The optimizer's states (zeros) for adamw_step: 32 or 8 bits, with or without float master copies
-        of bf16 parameters; weight_decay for all parameters or a list in their order."""
+        of bf16 parameters; weight_decay for all parameters or a list in their order.  The tensors that params
+        holds now are the ones that adamw_step changes."""
         if not self.cfg.backward:
             raise ValueError("the layer has no backward")
         params, grads = self.parameters(), self.gradients()

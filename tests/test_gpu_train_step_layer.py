@@ -132,6 +132,15 @@ def test_layer_routed_by_scores(score, renorm, groups, topk_groups, dtype):
     np.testing.assert_allclose(np64(params["select_bias"]), S.move_bias(b["counts"].cpu().numpy(), 1e-3, bias), rtol=0, atol=1e-7)
 
 
+def test_given_logits_routed_by_scores():
+    """Random routing: the caller's logits, no router to train."""
+    cfg = I.CONFIGS["tiny64e_random"].with_(name="rnd", T=300, d=128, E=16, k=4, f=128, fs=0)
+    lay, inp = make(cfg, router=LY.ScoreRouter("softmax", 4, 2), precision="fp8")
+    lay.step()
+    l = np64(lay.p["logits"])
+    np.testing.assert_array_equal(lay.bufs["topk_idx"].cpu().numpy(), S.choose(l, None, cfg.k, 4, 2, False))
+
+
 @pytest.mark.parametrize("bits,master,precision,norm", [(32, False, "fp8", True), (8, True, "fp8", False), (8, False, "bf16", True),
                                                         (32, True, "mxfp8", False)])
 def test_steps_of_training(bits, master, precision, norm):
