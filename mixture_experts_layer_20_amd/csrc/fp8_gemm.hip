@@ -32,6 +32,27 @@ constexpr int ONE = 0x7f7f7f7f;   // scale bytes of the matrix instruction: 2^0
 constexpr int TB = 128;
 constexpr int OPBYTES = TB * TB;
 
+// Two floats to bf16, to nearest, by the instruction for it.  (Rounding in integers with a branch for NaN, and the
+// exact exponential and division for a sigmoid, lengthened a tile's end by 1200 and 3000 instructions: 140 us
+// instead of 127 for 32768 x 1024 by 64 weights of 2048 x 1024, 878 instead of 805 for the prompt's product.)
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+__device__ __forceinline__ u32x4_t pack_row(const float (&v)[8]) {
+  u32x4_t w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = pack2(v[2 * e], v[2 * e + 1]);
+  return w;
+}
+// 1 / (1 + exp(-a)) by the hardware's exponential and reciprocal, a unit in the last place each, for results that
+// are rounded to bf16.  Of the two exponentials the one that is at most 1 is formed; below a = -87 it is 0.
+__device__ __forceinline__ float sigmoid_of(float a) {
+  const float t = __builtin_amdgcn_exp2f(fabsf(a) * -1.44269504088896340736f), r = __builtin_amdgcn_rcpf(1.0f + t);
+  return a < 0.0f ? t * r : r;
+}
+
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
 
 // The group of row tile mt and its rows, from the group offsets: rows of a group in tiles of TM, groups in
@@ -208,10 +229,10 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float a = acc[i][0][4 * q + r];
-          hv[r] = a * sigmoid_f32(a) * acc[i][1][4 * q + r];
+          hv[r] = a * sigmoid_of(a) * acc[i][1][4 * q + r];
         }
         auto put = [&](void* out, float v0, float v1, float v2, float v3) {
-          *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + o) = make_uint2(bf16pack(v0, v1), bf16pack(v2, v3));
+          *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + o) = make_uint2(pack2(v0, v1), pack2(v2, v3));
         };
         if (p.out0) put(p.out0, acc[i][0][4 * q], acc[i][0][4 * q + 1], acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]);
         if (p.out1) put(p.out1, acc[i][1][4 * q], acc[i][1][4 * q + 1], acc[i][1][4 * q + 2], acc[i][1][4 * q + 3]);
@@ -233,16 +254,16 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
             for (int r = 0; r < 4; ++r) {
               const float a = bf16_to_f32((bf16_t)(aw[r >> 1] >> (16 * (r & 1))));
               const float bb = bf16_to_f32((bf16_t)(bw[r >> 1] >> (16 * (r & 1))));
-              const float sg = sigmoid_f32(a);
+              const float sg = sigmoid_of(a);
               da[r] = v[r] * bb * sg * (1.0f + a * (1.0f - sg));
               db[r] = v[r] * a * sg;
             }
             bf16_t* dab = reinterpret_cast<bf16_t*>(p.out0) + (long long)row * (2 * p.N);
-            *reinterpret_cast<uint2*>(dab + col) = make_uint2(bf16pack(da[0], da[1]), bf16pack(da[2], da[3]));
-            *reinterpret_cast<uint2*>(dab + p.N + col) = make_uint2(bf16pack(db[0], db[1]), bf16pack(db[2], db[3]));
+            *reinterpret_cast<uint2*>(dab + col) = make_uint2(pack2(da[0], da[1]), pack2(da[2], da[3]));
+            *reinterpret_cast<uint2*>(dab + p.N + col) = make_uint2(pack2(db[0], db[1]), pack2(db[2], db[3]));
           } else {
             *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(p.out0) + (long long)row * p.N + col) =
-                make_uint2(bf16pack(v[0], v[1]), bf16pack(v[2], v[3]));
+                make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
           }
         }
       }
@@ -274,7 +295,7 @@ __device__ __forceinline__ i32x8_t load32(const uint8_t* p) {
   return r;
 }
 
-__device__ __forceinline__ uint2 pack4(const f32x4_t& v) { return make_uint2(bf16pack(v[0], v[1]), bf16pack(v[2], v[3])); }
+__device__ __forceinline__ uint2 pack4(const f32x4_t& v) { return make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3])); }
 
 constexpr int W = 4;
 
@@ -359,7 +380,7 @@ __global__ __launch_bounds__(64 * W) void fp8_few_kernel(Fp8GemmArgs p) {
     if constexpr (EPI == MX_EPI_SWIGLU) {
       f32x4_t hv;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) hv[e] = v[0][e] * sigmoid_f32(v[0][e]) * v[B - 1][e];
+      for (int e = 0; e < 4; ++e) hv[e] = v[0][e] * sigmoid_of(v[0][e]) * v[B - 1][e];
       if (p.out0) *at(p.out0, o) = pack4(v[0]);
       if (p.out1) *at(p.out1, o) = pack4(v[B - 1]);
       *at(p.out2, o) = pack4(hv);
@@ -371,7 +392,7 @@ __global__ __launch_bounds__(64 * W) void fp8_few_kernel(Fp8GemmArgs p) {
       for (int e = 0; e < 4; ++e) {
         const uint32_t ua = e < 2 ? aw.x : aw.y, ub = e < 2 ? bw.x : bw.y;
         const float a = bf16_to_f32((bf16_t)(ua >> (16 * (e & 1)))), b = bf16_to_f32((bf16_t)(ub >> (16 * (e & 1))));
-        const float sg = sigmoid_f32(a);
+        const float sg = sigmoid_of(a);
         da[e] = v[0][e] * b * sg * (1.0f + a * (1.0f - sg));
         db[e] = v[0][e] * a * sg;
       }
@@ -401,8 +422,8 @@ hipError_t launch_few(const Fp8GemmArgs& a, hipStream_t s) {
 // Wave (wm, wn) multiplies 64 columns at 64 wn and the rows 64 i + 32 wm .. + 31 of every quarter i of the
 // tile: a group's last tile leaves out the quarters that it does not fill, loads, products and stores, and
 // all waves leave out the same.  (128 x 256 tiles in three stages, whose waves of 64 x 64 read a third more of
-// LDS for a product and meet at twice as many barriers: 1002 us for 950, 32768 x 3584 by 64 weights of 3584 x
-// 2560 with SwiGLU.)
+// LDS for a product and meet at twice as many barriers: 1002 us for 950, 32768 x 4096 by 128 weights of 2048 x
+// 4096 with SwiGLU, here "the prompt's product".)
 constexpr int PM = 256, PN = 256;
 constexpr int PSCALE = (PM + PN) * BLK;   // a stage's scales: 8 runs of 64 floats, one for each wave's load
 constexpr int PSTAGE = PSCALE + 8 * 256;
@@ -590,7 +611,7 @@ __device__ __forceinline__ void pipe_epilogue(const Fp8GemmArgs& p, const PTile&
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) hv[b][e] = c[2 * b][e] * sigmoid_f32(c[2 * b][e]) * c[2 * b + 1][e];
+          for (int e = 0; e < 4; ++e) hv[b][e] = c[2 * b][e] * sigmoid_of(c[2 * b][e]) * c[2 * b + 1][e];
         float g[8], up[8], x[8];
         side_by_side(c[0], c[2], g);
         side_by_side(c[1], c[3], up);
@@ -598,9 +619,9 @@ __device__ __forceinline__ void pipe_epilogue(const Fp8GemmArgs& p, const PTile&
         const int row = r0 + 16 * u;
         if (row >= t.m_end) continue;
         const long long o = (long long)row * p.N + t.nt * 128 + wn * 32 + cl;
-        if (p.out0) *at(p.out0, o) = pack8(g);
-        if (p.out1) *at(p.out1, o) = pack8(up);
-        *at(p.out2, o) = pack8(x);
+        if (p.out0) *at(p.out0, o) = pack_row(g);
+        if (p.out1) *at(p.out1, o) = pack_row(up);
+        *at(p.out2, o) = pack_row(x);
       }
     } else {
       // the stash of 32 rows is loaded before their first store, which it may alias as far as the compiler
@@ -630,15 +651,15 @@ __device__ __forceinline__ void pipe_epilogue(const Fp8GemmArgs& p, const PTile&
             unpack8(sb[u][b], bb);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float sg = sigmoid_f32(a[e]);
+              const float sg = sigmoid_of(a[e]);
               da[e] = x[e] * bb[e] * sg * (1.0f + a[e] * (1.0f - sg));
               db[e] = x[e] * a[e] * sg;
             }
             const long long o = (long long)row * (2 * p.N) + col;
-            *at(p.out0, o) = pack8(da);
-            *at(p.out0, o + p.N) = pack8(db);
+            *at(p.out0, o) = pack_row(da);
+            *at(p.out0, o + p.N) = pack_row(db);
           } else {
-            *at(p.out0, (long long)row * p.N + col) = pack8(x);
+            *at(p.out0, (long long)row * p.N + col) = pack_row(x);
           }
         }
     }
