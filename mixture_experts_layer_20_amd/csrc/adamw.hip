@@ -307,14 +307,16 @@ __device__ __forceinline__ void update(const Chunk& k, uint32_t at) {
         root[e] = at + e <= last ? root[e] : 0.0f;
       }
     }
+    // The largest magnitudes, a NaN above all (`maximum` hands it on).  Where the root is lost, so is m; m can be by
+    // itself, from a state that holds a NaN or an infinity.
     float top = 0.0f;
-    uint32_t most = 0;   // root's bits: not negative, and a NaN, which m then is too, is above all
+    uint32_t most = 0;   // root's bits: not negative
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      top = fmaxf(top, fabsf(m[e]));
+      top = __builtin_elementwise_maximum(top, __builtin_fabsf(m[e]));
       most = max(most, __float_as_uint(root[e]));
     }
-    sm = encode8<false>(m, most >= 0x7f800000u ? most : __float_as_uint(top), bits, cm);
+    sm = encode8<false>(m, most >= 0x7f800000u ? most : __float_as_uint(top) & 0x7fffffffu, bits, cm);
     sv = encode8<true>(root, most, bits, cv);
     store8_codes<FULL>(reinterpret_cast<uint8_t*>(k.m_out), at, last, cm);
     store8_codes<FULL>(reinterpret_cast<uint8_t*>(k.v_out), at, last, cv);
