@@ -299,6 +299,9 @@ __device__ __forceinline__ void update(const Chunk& k, uint32_t at) {
 #pragma unroll
     for (int e = 0; e < N; ++e) bits[e] = h = h * 1664525u + 1013904223u;
   }
+  uint32_t width[N];   // of the random bits added to a bf16 parameter: to a NaN, whose bits may all be set, none
+#pragma unroll
+  for (int e = 0; e < N; ++e) width[e] = w[e] == w[e] ? 16 : 0;
   if constexpr (BITS8) {
     if (!FULL) {   // what stood in for the elements behind the last is no part of their block
 #pragma unroll
@@ -316,7 +319,12 @@ __device__ __forceinline__ void update(const Chunk& k, uint32_t at) {
       top = __builtin_elementwise_maximum(top, __builtin_fabsf(m[e]));
       most = max(most, __float_as_uint(root[e]));
     }
-    sm = encode8<false>(m, most >= 0x7f800000u ? most : __float_as_uint(top) & 0x7fffffffu, bits, cm);
+    const uint32_t lost = most >= 0x7f800000u ? most : __float_as_uint(top) & 0x7fffffffu;
+    // One comparison for the lane's 8: a NaN of a state or a gradient is among them, and one of the parameter itself
+    // has a lower half of zeros.  The other seven are cut off; their block is lost.
+#pragma unroll
+    for (int e = 0; e < N; ++e) width[e] = lost >= 0x7f800000u ? 0 : 16;
+    sm = encode8<false>(m, lost, bits, cm);
     sv = encode8<true>(root, most, bits, cv);
     store8_codes<FULL>(reinterpret_cast<uint8_t*>(k.m_out), at, last, cm);
     store8_codes<FULL>(reinterpret_cast<uint8_t*>(k.v_out), at, last, cv);
@@ -340,13 +348,12 @@ __device__ __forceinline__ void update(const Chunk& k, uint32_t at) {
       const f32x2_t pair = {w[2 * e], w[2 * e + 1]};
       p[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(pair, bf16x2_t));
     }
-  } else {   // infinities stay: their lower bits are zero
+  } else {
+    // Infinities stay: their lower bits are zero.  So do NaNs: with bits added, 0x7fffffff would carry into a zero.
+    // (A result of arithmetic, a NaN has its upper half's quiet bit.)
+    auto up = [&](int e) { return __float_as_uint(w[e]) + __builtin_amdgcn_ubfe(bits[e], 8, width[e]); };
 #pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-      const uint32_t lo = __float_as_uint(w[2 * e]) + (bits[2 * e] >> 8 & 0xffffu);
-      const uint32_t hi = __float_as_uint(w[2 * e + 1]) + (bits[2 * e + 1] >> 8 & 0xffffu);
-      p[e] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);   // the upper halves
-    }
+    for (int e = 0; e < N / 2; ++e) p[e] = __builtin_amdgcn_perm(up(2 * e + 1), up(2 * e), 0x07060302u);   // the upper halves
   }
   store_pairs<FULL>(reinterpret_cast<bf16_t*>(k.param_out), at, last, p);
 }

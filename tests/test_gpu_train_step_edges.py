@@ -38,3 +38,32 @@ def test_adamw_keeps_a_lost_first_moment(what):
     else:
         where = lost.repeat_interleave(128)[:n]
     assert torch.equal(ends, where)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("nan", [0x7FFFFFFF, 0xFFFFFFFF, 0x7FC00000, 0x7FC0FFFF])
+def test_adamw_keeps_nan_in_random_rounding(nan, bits):
+    """A NaN gradient makes its bf16 parameter, which has no master copy, a NaN: whatever the NaN's payload and
+    the random bits that are added to it."""
+    n = 2048 + 77   # wide accesses and a tail
+    c = Case([n], [torch.bfloat16], [torch.float32], bits, False, seed=9)
+    at = torch.arange(0, n, 3, device=DEV)
+    c.g[0].view(torch.int32)[at] = nan - (1 << 32) if nan >= 1 << 31 else nan
+    L.moe_adamw(c.list(0.0), seed=3, **HYPER)
+    c.check_guards()
+    bad = torch.isnan(c.results(0)[0])
+    assert bad[at].all() and bad.sum() == len(at)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("nan", [0x7FFFFFFF, 0xFFFFFFFF])
+def test_adamw_keeps_nan_of_a_state_in_random_rounding(nan, bits):
+    """As before, with the NaN in m, or in the scale of one of its blocks."""
+    n = 2048 + 77
+    c = Case([n], [torch.bfloat16], [torch.float32], bits, False, seed=11)
+    state, at = (c.m[0], torch.arange(0, n, 3, device=DEV)) if bits == 32 else (c.sc[0], torch.arange(0, 17, 2, device=DEV))
+    state.view(torch.int32)[at] = nan - (1 << 32) if nan >= 1 << 31 else nan
+    L.moe_adamw(c.list(0.0), seed=3, **HYPER)
+    where = torch.zeros(n if bits == 32 else 17, dtype=torch.bool, device=DEV)
+    where[at] = True
+    assert torch.equal(torch.isnan(c.results(0)[0]), where if bits == 32 else where.repeat_interleave(128)[:n])
