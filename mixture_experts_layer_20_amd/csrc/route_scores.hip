@@ -163,6 +163,11 @@ template <typename R>
 __device__ __forceinline__ bool nearby(R high, R low, R tolerance) {
   return !(high - low > tolerance * (R(2) + finite(high) + finite(low)));
 }
+// How far a group's score may be off, from its two largest: what they lose goes by their own sizes, however small
+// their sum is.  Two sigmoids 2^-21, or softmax scores, which sum to 1 at most, 2^-19; the sums with the bias and
+// the group's 2^-23 (|a| + |b|).  Twice that.
+template <typename R>
+__device__ __forceinline__ R group_error(R a, R b) { return R(2 * NEAR) + R(0x1p-22f) * (finite(a) + finite(b)); }
 
 __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) { return (uint32_t)__shfl((int)v, lane, 64); }
 __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) { return (uint64_t)__shfl((long long)v, lane, 64); }
@@ -201,17 +206,18 @@ __device__ __forceinline__ bool group_open(const RouteScores& r, const Place& at
   const bool open = rank < r.topk_groups;
   if (r.topk_groups < r.groups) {
     const bool number = score == score;
-    const R least = over_lanes(L, open && number ? score : R(INFINITY), Min());
-    const R most = over_lanes(L, !open && number ? score : R(-INFINITY), Max());
-    near = nearby<R>(least, most, 2 * NEAR);
+    const R off = group_error<R>(a, at.size > 1 ? b : a);
+    const R least = over_lanes(L, open && number ? score - off : R(INFINITY), Min());
+    const R most = over_lanes(L, !open && number ? score + off : R(-INFINITY), Max());
+    near = !(least > most);
   }
   return open;
 }
 
-// The same for any number of groups: cs holds the token's selection scores, gsc the groups' scores and open
-// their flags, in LDS.  q lanes walk a group (a power of two, at most L / groups).
+// The same for any number of groups: cs holds the token's selection scores, gsc the groups' scores, goff how far
+// these may be off and open their flags, in LDS.  q lanes walk a group (a power of two, at most L / groups).
 template <int L, typename R>
-__device__ __forceinline__ void walk_groups(const RouteScores& r, int j, const R* cs, R* gsc, uint8_t* open, bool& near) {
+__device__ __forceinline__ void walk_groups(const RouteScores& r, int j, const R* cs, R* gsc, float* goff, uint8_t* open, bool& near) {
   const int size = r.E / r.groups;
   int q = 1;
   while (q * 2 * r.groups <= L) q *= 2;
@@ -235,7 +241,10 @@ __device__ __forceinline__ void walk_groups(const RouteScores& r, int j, const R
       b = Max()(Max()(b, ob), Min()(a, oa));
       a = Max()(a, oa);
     }
-    if (sub == 0 && g < r.groups) gsc[g] = size > 1 ? a + b : a;
+    if (sub == 0 && g < r.groups) {
+      gsc[g] = size > 1 ? a + b : a;
+      goff[g] = group_error<float>((float)a, (float)(size > 1 ? b : a));
+    }
   }
   wave_fence();
   R least = INFINITY, most = -INFINITY;   // of the open groups, of the shut ones
@@ -247,13 +256,14 @@ __device__ __forceinline__ void walk_groups(const RouteScores& r, int j, const R
       rank += other > mine || (other == mine && o < g) ? 1 : 0;
     }
     open[g] = rank < r.topk_groups;
-    if (rank < r.topk_groups) least = gsc[g] < least ? gsc[g] : least;
-    else most = gsc[g] > most ? gsc[g] : most;
+    const R low = gsc[g] - goff[g], high = gsc[g] + goff[g];
+    if (rank < r.topk_groups) least = low < least ? low : least;
+    else most = high > most ? high : most;
   }
   wave_fence();
   least = over_lanes(L, least, Min());
   most = over_lanes(L, most, Max());
-  near = r.topk_groups < r.groups && nearby<R>(least, most, 2 * NEAR);
+  near = r.topk_groups < r.groups && !(least > most);
 }
 
 // Selection scores in double, one at a time from a token's logits in LDS: the code of one exponential, which
@@ -436,6 +446,7 @@ __global__ __launch_bounds__(256) void route_scores_kernel(RouteScores r, int32_
   __shared__ uint8_t chosen_s[TOK][16];
   __shared__ double score_s[WTOK][WMAX];   // the groups' walk: floats first, doubles where they do not tell
   __shared__ double group_s[WTOK][WMAX];
+  __shared__ float off_s[WTOK][WMAX];
   __shared__ uint8_t open_s[WTOK][WMAX];
   const long long gl = (long long)blockIdx.x * 256 + threadIdx.x;
   const int t = (int)(gl / L), j = (int)(gl % L), slot = threadIdx.x / L;
@@ -483,13 +494,13 @@ __global__ __launch_bounds__(256) void route_scores_kernel(RouteScores r, int32_
       for (int s = 0; s < S; ++s)
         if (at.has(s)) cs[at.expert(s)] = c[s];
       wave_fence();
-      walk_groups<L, float>(r, j, cs, reinterpret_cast<float*>(group_s[slot]), open_s[slot], near);
+      walk_groups<L, float>(r, j, cs, reinterpret_cast<float*>(group_s[slot]), off_s[slot], open_s[slot], near);
       if (__any(near)) {
         const Exact<L> exact(r, logit_s[slot], j);
         wave_fence();
         for (int e = j; e < r.E; e += L) score_s[slot][e] = exact(e);
         wave_fence();
-        walk_groups<L, double>(r, j, score_s[slot], group_s[slot], open_s[slot], near);
+        walk_groups<L, double>(r, j, score_s[slot], group_s[slot], off_s[slot], open_s[slot], near);
       }
       const int size = r.E / r.groups;
 #pragma unroll

@@ -1,10 +1,11 @@
 """Values and sizes at which routing by scores, the block-scaled 8-bit products and AdamW could go wrong, on the
 GPU against the float64 oracle."""
+import numpy as np
 import pytest
 import torch
 
 from mixture_experts_layer_20_amd import libmoe as L
-from tests.test_gpu_train_step import DEV, HYPER, Case
+from tests.test_gpu_train_step import DEV, HYPER, SIG, SOFT, Case, check_route
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,19 @@ def test_adamw_keeps_nan_of_a_state_in_random_rounding(nan, bits):
     where = torch.zeros(n if bits == 32 else 17, dtype=torch.bool, device=DEV)
     where[at] = True
     assert torch.equal(torch.isnan(c.results(0)[0]), where if bits == 32 else where.repeat_interleave(128)[:n])
+
+
+# ---- routing by scores --------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("E,groups,topk_groups", [(32, 4, 2), (96, 8, 3), (256, 8, 4), (48, 6, 3), (255, 15, 4)])
+@pytest.mark.parametrize("size", [8.0, 4096.0, 2.0 ** 20])
+def test_route_groups_of_opposite_biases(E, groups, topk_groups, score, size):
+    """A group's two largest scores that cancel: their sum is small, what fp32 loses of each of them is not."""
+    r = np.random.default_rng(int(size) + E)
+    T, k = 1024, 2
+    l = r.standard_normal((T, E)).astype(np.float32)
+    b = np.full((groups, E // groups), -4 * size, np.float32)
+    b[:, 0], b[:, 1] = size, -size
+    b = np.take_along_axis(b, np.argsort(r.random(b.shape), axis=1), axis=1)
+    check_route(l, b.reshape(-1), k, groups, topk_groups, score, 1, 1.0)
