@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from mixture_experts_layer_20_amd import libmoe as L
-from tests.test_gpu_train_step import DEV, HYPER, SIG, SOFT, Case, check_route
+from oracle import train_step as S
+from tests.test_gpu_train_step import BF, DEV, F, HYPER, SIG, SOFT, Case, check_route, put, sums_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,194 @@ def test_route_groups_of_opposite_biases(E, groups, topk_groups, score, size):
     b[:, 0], b[:, 1] = size, -size
     b = np.take_along_axis(b, np.argsort(r.random(b.shape), axis=1), axis=1)
     check_route(l, b.reshape(-1), k, groups, topk_groups, score, 1, 1.0)
+
+
+# ---- products -------------------------------------------------------------------------------------------
+
+VALUES = torch.from_numpy(S.E4M3)
+
+
+def rows_of(codes, scales):
+    return VALUES.to(DEV)[codes.long()] * scales.double().t().repeat_interleave(128, 1)
+
+
+def weights_of(codes, scales):
+    return VALUES.to(DEV)[codes.long()] * scales.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
+
+
+def grouped_product(a, b, offsets):
+    """S.grouped_product on the device: the product, the sum of magnitudes, the sum of each eight's largest."""
+    M, N = a.shape[0], b.shape[1]
+    out, size, tops = (torch.full((M, N), float("nan"), dtype=torch.float64, device=DEV) for _ in range(3))
+    top = lambda t: t.abs().view(*t.shape[:-1], -1, 8).amax(-1)
+    for g, (r0, r1) in enumerate(zip(offsets, offsets[1:])):
+        if r1 > r0:
+            out[r0:r1] = a[r0:r1] @ b[g].t()
+            size[r0:r1] = a[r0:r1].abs() @ b[g].abs().t()
+            tops[r0:r1] = top(a[r0:r1]) @ top(b[g]).t()
+    return out, size, tops
+
+
+def cut(sizes, first, behind):
+    """Offsets of groups of these sizes, with rows before and behind them that belong to none."""
+    offsets = [first]
+    for n in sizes:
+        offsets.append(offsets[-1] + n)
+    return offsets[-1] + behind, offsets
+
+
+# Row tiles of 256 whose last ones fill 1 to 4 quarters in turn, groups of one tile and of several, empty ones.
+RAGGED = [300, 70, 0, 513, 190, 250, 1, 400, 129, 256, 0, 60, 700, 64, 65, 333, 512, 128, 449, 5, 210, 600, 90, 385]
+TILED = [(*cut(RAGGED, 3, 7), 8192, 128), (*cut(RAGGED, 0, 0), 8192, 384), (*cut([2000, 1900, 30, 2100], 0, 1), 8192, 256)]
+
+
+def row_tiles(offsets):
+    return sum(-(-(b - a) // 256) for a, b in zip(offsets, offsets[1:]))
+
+
+def operands(M, G, N, K, seed, sources=1, scale=1.0):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    codes = lambda *s: torch.randint(0, 256, s, device=DEV, generator=gen, dtype=torch.int32).to(torch.uint8)
+    keep = lambda c: torch.where((c & 0x7F) == 0x7F, c - 1, c)   # no NaN
+    factor = lambda *s: scale * torch.exp(0.5 * torch.randn(*s, device=DEV, generator=gen))
+    t = [keep(codes(M, K)), factor(K // 128, M)]
+    for _ in range(sources):
+        t += [keep(codes(G, N, K)), factor(G, N // 128, K // 128)]
+    return t
+
+
+def outputs(M, N, count=1):
+    return [torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(count)]
+
+
+def within(got, want, e, M):
+    """got against want, whose rows of no group are NaN, with an error of e before the one rounding to bf16."""
+    inside = ~torch.isnan(want[:, 0])
+    assert (got[:M][~inside] == 7.0).all() and (got[M] == 7.0).all()
+    err = (got[:M].double() - want).abs()[inside]
+    tol = (e * (1 + BF) + BF * want.abs())[inside] + 1e-30
+    assert (err <= tol).all(), (err / tol).max().item()
+
+
+def several_tiles(offsets, columns):
+    """Whether every workgroup of the persistent product, one for each CU, gets two tiles at least."""
+    assert row_tiles(offsets) * columns >= 2 * torch.cuda.get_device_properties(0).multi_processor_count + 8
+
+
+@pytest.mark.parametrize("M,offsets,N,K", TILED)
+def test_product_of_many_tiles(M, offsets, N, K):
+    several_tiles(offsets, N // 256)
+    G = len(offsets) - 1
+    t, off = operands(M, G, N, K, M + K), put(np.array(offsets), torch.int32)
+    out, = outputs(M, N)
+    L.moe_fp8_gemm_rows(*t, None, None, 0, off, G, M, N, K, L.MOE_MX_EPI_STORE, out, None, None, None, None, None, 0)
+    want, size, tops = grouped_product(rows_of(*t[:2]), weights_of(*t[2:]), offsets)
+    within(out, want, sums_bound(size, tops, K), M)
+
+
+@pytest.mark.parametrize("M,offsets,N,K", TILED)
+def test_product_of_many_tiles_and_two_sources(M, offsets, N, K):
+    several_tiles(offsets, N // 256)
+    G, kb = len(offsets) - 1, K // 128
+    for K2 in (128, 256):
+        Ks = K + K2
+        t, off = operands(M, G, N, Ks, M + Ks), put(np.array(offsets), torch.int32)
+        one, two = outputs(M, N, 2)
+        part = lambda v, lo, hi: v[:, :, lo:hi].clone(memory_format=torch.contiguous_format)
+        tail = (off, G, M, N, Ks, L.MOE_MX_EPI_STORE)
+        L.moe_fp8_gemm_rows(*t[:2], part(t[2], 0, K), part(t[3], 0, kb), part(t[2], K, Ks), part(t[3], kb, Ks // 128), K, *tail,
+                            two, None, None, None, None, None, 0)
+        want, size, tops = grouped_product(rows_of(*t[:2]), weights_of(*t[2:]), offsets)
+        within(two, want, sums_bound(size, tops, Ks), M)
+        L.moe_fp8_gemm_rows(*t, None, None, 0, *tail, one, None, None, None, None, None, 0)
+        assert torch.equal(one, two)
+
+
+@pytest.mark.parametrize("M,offsets,N,K", TILED)
+def test_product_of_many_tiles_swiglu(M, offsets, N, K):
+    several_tiles(offsets, N // 128)
+    G = len(offsets) - 1
+    # E4M3's codes have a root mean square of 90: gates of a few units
+    t, off = operands(M, G, N, K, M + K + 1, 2, K ** -0.25 / 90.0), put(np.array(offsets), torch.int32)
+    o = outputs(M, N, 3)
+    L.moe_fp8_gemm_rows(*t, 0, off, G, M, N, K, L.MOE_MX_EPI_SWIGLU, *o, None, None, None, 0)
+    A = rows_of(*t[:2])
+    (ga, size_a, top_a), (up, size_u, top_u) = (grouped_product(A, weights_of(*w), offsets) for w in (t[2:4], t[4:]))
+    ea, eu = sums_bound(size_a, top_a, K), sums_bound(size_u, top_u, K)
+    act = ga / (1.0 + torch.exp(-ga))
+    h = act * up
+    # silu's slope is below 1.1; an exponential of an argument rounded |a| half steps, a reciprocal, two products
+    eh = 1.1 * ea * (up.abs() + eu) + act.abs() * eu + (8 * ga.abs() + 24) * F * h.abs()
+    for got, want, e in zip(o, (ga, up, h), (ea, eu, eh)):
+        within(got, want, e, M)
+
+
+@pytest.mark.parametrize("M,offsets,N,K", TILED)
+def test_product_of_many_tiles_swiglu_backward(M, offsets, N, K):
+    several_tiles(offsets, N // 256)
+    G = len(offsets) - 1
+    t, off = operands(M, G, N, K, M + K + 2, 1, K ** -0.25 / 90.0), put(np.array(offsets), torch.int32)
+    gen = torch.Generator(device=DEV).manual_seed(M)
+    ga, up = ((2 * torch.randn(M, N, device=DEV, generator=gen)).to(torch.bfloat16) for _ in range(2))
+    out, = outputs(M, 2 * N)
+    L.moe_fp8_gemm_rows(*t, None, None, 0, off, G, M, N, K, L.MOE_MX_EPI_SWIGLU_BWD, out, None, None, ga, up, None, 0)
+    dh, size, tops = grouped_product(rows_of(*t[:2]), weights_of(*t[2:]), offsets)
+    e, A, U = sums_bound(size, tops, K), ga.double(), up.double()
+    sg = 1.0 / (1.0 + torch.exp(-A))
+    fa, fb = U * sg * (1.0 + A * (1.0 - sg)), A * sg
+    # 1 + a (1 - sg) cancels where it is near zero: its terms are counted by themselves
+    slack_a = (8 * A.abs() + 24) * F * dh.abs() * U.abs() * sg * (1.0 + A.abs())
+    slack_b = (8 * A.abs() + 24) * F * (dh * fb).abs()
+    within(out[:, :N], dh * fa, e * fa.abs() + slack_a, M)
+    within(out[:, N:], dh * fb, e * fb.abs() + slack_b, M)
+
+
+FEW = [(1, [0, 1]), (9, [0, 9]), (40, [0, 3, 3, 20, 40])]
+
+
+@pytest.mark.parametrize("K", [2048, 2944])
+@pytest.mark.parametrize("M,offsets", FEW)
+def test_product_of_few_rows_and_long_sums(M, offsets, K):
+    """A wave's share of K in steps of 4, 2 and 1 blocks; a second source from within a step of 4 on."""
+    G, N = len(offsets) - 1, 256
+    t, off = operands(M, G, N, K, M + K, 2, K ** -0.25 / 90.0), put(np.array(offsets), torch.int32)
+    A = rows_of(*t[:2])
+    (ga, size_a, top_a), (up, size_u, top_u) = (grouped_product(A, weights_of(*w), offsets) for w in (t[2:4], t[4:]))
+    ea, eu = sums_bound(size_a, top_a, K), sums_bound(size_u, top_u, K)
+    one, = outputs(M, N)
+    tail = (off, G, M, N, K)
+    L.moe_fp8_gemm_rows(*t[:4], None, None, 0, *tail, L.MOE_MX_EPI_STORE, one, None, None, None, None, None, 0)
+    within(one, ga, ea, M)
+    part = lambda v, lo, hi: v[:, :, lo:hi].clone(memory_format=torch.contiguous_format)
+    for kb in (1, 2, 7, K // 128 - 1):
+        two, = outputs(M, N)
+        L.moe_fp8_gemm_rows(*t[:2], part(t[2], 0, 128 * kb), part(t[3], 0, kb), part(t[2], 128 * kb, K), part(t[3], kb, K // 128),
+                            128 * kb, *tail, L.MOE_MX_EPI_STORE, two, None, None, None, None, None, 0)
+        assert torch.equal(one, two)
+    o = outputs(M, N, 3)
+    L.moe_fp8_gemm_rows(*t, 0, *tail, L.MOE_MX_EPI_SWIGLU, *o, None, None, None, 0)
+    act = ga / (1.0 + torch.exp(-ga))
+    eh = 1.1 * ea * (up.abs() + eu) + act.abs() * eu + (8 * ga.abs() + 24) * F * (act * up).abs()
+    for got, want, e in zip(o, (ga, up, act * up), (ea, eu, eh)):
+        within(got, want, e, M)
+
+
+@pytest.mark.parametrize("G", [65, 129, 1024])
+@pytest.mark.parametrize("N,per", [(256, 2), (256, 12), (384, 12)])
+def test_product_of_many_groups(N, per, G):
+    """More groups than a wave has lanes, most of them of few rows, a third of them empty: all three kernels' lists."""
+    r, K = np.random.default_rng(G + N), 256
+    sizes = (r.poisson(1.5 * per, G) * (r.random(G) < 0.67)).tolist()
+    M, offsets = cut(sizes, 5, 9)
+    assert (M > 8 * G) == (per == 12)
+    t, off = operands(M, G, N, K, G, 2, K ** -0.25 / 90.0), put(np.array(offsets), torch.int32)
+    A = rows_of(*t[:2])
+    (ga, size_a, top_a), (up, size_u, top_u) = (grouped_product(A, weights_of(*w), offsets) for w in (t[2:4], t[4:]))
+    ea, eu = sums_bound(size_a, top_a, K), sums_bound(size_u, top_u, K)
+    one, o = outputs(M, N)[0], outputs(M, N, 3)
+    L.moe_fp8_gemm_rows(*t[:4], None, None, 0, off, G, M, N, K, L.MOE_MX_EPI_STORE, one, None, None, None, None, None, 0)
+    L.moe_fp8_gemm_rows(*t, 0, off, G, M, N, K, L.MOE_MX_EPI_SWIGLU, *o, None, None, None, 0)
+    act = ga / (1.0 + torch.exp(-ga))
+    eh = 1.1 * ea * (up.abs() + eu) + act.abs() * eu + (8 * ga.abs() + 24) * F * (act * up).abs()
+    for got, want, e in zip((one, *o), (ga, ga, up, act * up), (ea, ea, eu, eh)):
+        within(got, want, e, M)
