@@ -9,6 +9,7 @@ from oracle import train_step as S
 from tests.test_gpu_train_step import BF, DEV, F, HYPER, SIG, SOFT, Case, check_route, put, sums_bound
 
 pytestmark = pytest.mark.gpu
+VALUES = torch.from_numpy(S.E4M3)
 
 
 # ---- AdamW --------------------------------------------------------------------------------------------
@@ -71,6 +72,91 @@ def test_adamw_keeps_nan_of_a_state_in_random_rounding(nan, bits):
     assert torch.equal(torch.isnan(c.results(0)[0]), where if bits == 32 else where.repeat_interleave(128)[:n])
 
 
+def quantized_at_random(y, gen):
+    """E4M3 values around y in [0, 448], up with the probability of the rest; a positive one not to zero."""
+    step = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -6))) - 3)
+    q = torch.floor(y / step + torch.rand(y.shape, dtype=y.dtype, device=DEV, generator=gen)) * step
+    return torch.where(y > 0, q.clamp(min=2.0 ** -9), q).clamp(max=448.0)
+
+
+@pytest.mark.parametrize("beta2,steps", [(0.95, 200), (0.999, 2000)])
+def test_adamw_long_runs_of_8_bit_states(beta2, steps):
+    """What accumulates in v over many steps: the mean of the root is kept in each rounding, so v's own comes out a few
+    per cent high, as it does for the rule in float64 with other random bits.  Blocks of 128 are independent: the mean
+    over n / 128 of them is within six of its standard deviations, of either side."""
+    n = 1 << 17
+    gen = torch.Generator(device=DEV).manual_seed(13)
+    p, g = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    m, v, sc, _ = L.adamw_states([p], 8)
+    t = L.adamw_list([p], [g], m, v, sc)
+    rule, exact, first = (torch.zeros(n, dtype=torch.float64, device=DEV) for _ in range(3))
+    for step in range(1, steps + 1):
+        g.normal_(0.0, 1e-3, generator=gen)
+        L.moe_adamw(t, 1e-3, 0.9, beta2, 1e-8, step, seed=step)
+        sq = g.double().square()
+        exact = beta2 * exact + (1 - beta2) * sq
+        first = 0.9 * first + 0.1 * g.double()
+        root = (beta2 * rule + (1 - beta2) * sq).sqrt().view(-1, 128)
+        scale = root.amax(1, keepdim=True) / 448
+        rule = (quantized_at_random(root / scale, gen) * scale).view(-1).square()
+    s = sc[0].double().view(2, -1).repeat_interleave(128, 1)
+    values = VALUES.to(DEV)
+    got, moment = (values[v[0].long()] * s[1]).square(), values[m[0].long()] * s[0]
+    per = lambda x: (x / exact).view(-1, 128).mean(1)
+    a, b = per(got), per(rule)
+    off = 6 * (a.var() / a.numel() + b.var() / b.numel()).sqrt()
+    assert (a.mean() - b.mean()).abs() <= off, (a.mean().item(), b.mean().item(), off.item())
+    assert 1.0 <= b.mean() <= 1.1
+    d = ((moment - first) / exact.sqrt()).view(-1, 128).mean(1)   # m's own roundings have the right mean
+    assert d.mean().abs() <= 6 * (d.var() / d.numel()).sqrt()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_more_than_2_32_elements(bits):
+    """Chunks of two steps and offsets beyond 32 bits: contents that repeat give results that repeat."""
+    P, n = 1 << 20, (1 << 32) + (3 << 20) + 2 * 2048 + 77
+    c = Case([P], [torch.float32], [torch.float32], bits, False, seed=14)
+
+    def repeated(t, period, size):
+        out = torch.empty(size, dtype=t.dtype, device=DEV)
+        whole = size // period * period
+        out[:whole].view(-1, period).copy_(t[:period])
+        out[whole:].copy_(t[:size - whole])
+        return out
+
+    def repeats(t, want, equal):
+        whole = t.numel() // want.numel() * want.numel()
+        for part in t[:whole].view(-1, want.numel()).split(512):
+            assert equal(part, want)
+        return equal(t[whole:], want[:t.numel() - whole])
+
+    blocks, whole = -(-n // 128), P // 128
+    p, g = repeated(c.p[0], P, n), repeated(c.g[0], P, n)
+    m, v = repeated(c.m[0], P, n), repeated(c.v[0], P, n)
+    sc = None
+    if bits == 8:
+        sc = torch.empty(2, blocks, device=DEV)
+        for row in range(2):
+            sc[row] = repeated(c.sc[0].view(2, -1)[row], whole, blocks)
+        sc = sc.view(-1)
+    big = L.adamw_list([p], [g], [m], [v], [sc])
+    L.moe_adamw(c.list(0.0), seed=3, **HYPER)
+    L.moe_adamw(big, seed=3, **HYPER)
+    same = lambda a, b: torch.equal(a, b.expand_as(a))
+    want = c.results(0)
+    assert repeats(p, want[0], same)
+    if bits == 32:
+        assert repeats(m, want[1], same) and repeats(v, want[2], same)
+        return
+    # codes of the same values with other random bits: the one below or the one above
+    near = lambda a, b: ((a & 0x7F).to(torch.int8) - (b & 0x7F).to(torch.int8)).abs().amax() <= 1
+    last = blocks - 1   # the last block is part of one: its scale is its own
+    for row in range(2):
+        assert repeats(sc.view(2, -1)[row][:last], want[3].view(2, -1)[row], same)
+    cut = last * 128
+    assert repeats(m[:cut], want[1], near) and repeats(v[:cut], want[2], near)
+
+
 # ---- routing by scores --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("score", [SIG, SOFT])
@@ -88,9 +174,6 @@ def test_route_groups_of_opposite_biases(E, groups, topk_groups, score, size):
 
 
 # ---- products -------------------------------------------------------------------------------------------
-
-VALUES = torch.from_numpy(S.E4M3)
-
 
 def rows_of(codes, scales):
     return VALUES.to(DEV)[codes.long()] * scales.double().t().repeat_interleave(128, 1)
