@@ -623,7 +623,7 @@ moe_status_t moe_fp8_gemm_rows(const uint8_t* a_codes, const float* a_scales, co
  *   p = (1 - lr weight_decay) p - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
  * all in fp32.  c = 1 without sumsq; with it (moe_grad_norm) c = min(1, max_norm / (sqrt(sumsq) + 1e-6)),
  * and a norm that is infinite as a float or NaN makes no step: every output is its input (of a parameter
- * that is not given, its master copy, rounded).
+ * that is not given, its master copy, rounded).  Such a call does not count: the next one gets the same number.
  *   state_bits 32: m, v [n] float, scale NULL.
  *   state_bits 8:  m, v [n] uint8, E4M3 codes of m and of sqrt(v); scale [2, ceil(n / 128)] float, m's and
  *     then those of sqrt(v): a code stands for itself times its block's scale (largest magnitude / 448).

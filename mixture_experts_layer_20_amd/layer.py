@@ -7,6 +7,7 @@ HIP kernels.
 """
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass, field
 
 import numpy as np
@@ -615,22 +616,49 @@ class MoELayer:
         self._adamw_sumsq = torch.empty(1, dtype=torch.float64, device=params[0].device)
         self._ws_adamw = torch.empty(max(256, L.moe_grad_workspace_size(self._adamw_grads)), dtype=torch.uint8,
                                      device=params[0].device)
+        # the last clipped step's norm on the host, and when it is there
+        cuda = params[0].is_cuda
+        self._norm_host = torch.empty(1, pin_memory=True) if cuda else None
+        self._norm_there = torch.cuda.Event() if cuda else None
         self.steps = 0
+
+    @property
+    def steps(self) -> int:
+        """The steps that adamw_step has made.  One whose norm is infinite or NaN is none and counts for nothing: the
+        next one's bias corrections are those of the states that it finds.  Only the device knows that norm, so this
+        waits for the last step's if it was clipped."""
+        if self._norm_awaited:
+            self._norm_there.synchronize()
+            self._norm_awaited = False
+            if not math.isfinite(self._norm_host.item()):
+                self._steps -= 1
+        return self._steps
+
+    @steps.setter
+    def steps(self, made: int):
+        self._steps, self._norm_awaited = made, False
 
     def adamw_step(self, lr: float, beta1: float = 0.9, beta2: float = 0.95, eps: float = 1e-8,
                    max_norm: float | None = None, seed: int = 0):
         """One AdamW step on the parameters, in place, from the gradients of the last backward, clipped in the
-        same pass to a global norm of max_norm if that is given (grad_norm then is the norm).  make_adamw comes
-        first.  Quantized weights are made again by the next pass.  The step's number is an argument of the
-        kernels: a captured graph would repeat it."""
+        same pass to a global norm of max_norm if that is given (grad_norm then is the norm; one that is infinite
+        or NaN makes no step).  make_adamw comes first.  Quantized weights are made again by the next pass.  The
+        step's number and its seed are arguments of the kernels: a captured graph repeats them.  A clipped step is
+        preceded by a wait for the norm of the one before (see steps), but not while a graph is captured."""
         if self._adamw is None:
             raise ValueError("make_adamw comes before adamw_step")
+        captured = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+        made = self._steps if captured else self.steps
         if max_norm is not None:
             self._stage("grad_norm", L.moe_grad_norm, self._adamw_grads, self._adamw_sumsq, self.grad_norm, self._ws_adamw,
                         self._ws_adamw.numel())
-        self._stage("adamw", L.moe_adamw, self._adamw, lr, beta1, beta2, eps, self.steps + 1, seed + self.steps,
+        self._stage("adamw", L.moe_adamw, self._adamw, lr, beta1, beta2, eps, made + 1, seed + made,
                     self._adamw_sumsq if max_norm is not None else None, 1.0 if max_norm is None else max_norm)
-        self.steps += 1
+        self._steps = made + 1
+        if max_norm is not None and not captured:
+            self._norm_host.copy_(self.grad_norm, non_blocking=True)
+            self._norm_there.record()
+            self._norm_awaited = True
         self._mx_w_fresh = False
 
     def gradients(self) -> list[torch.Tensor]:
