@@ -548,7 +548,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 
 /* x, w_router, logits, E <= 256, k <= 8, dt as for moe_route (w_router NULL: logits [T, E] float are an
  * input, x is not read); select_bias [E] float or NULL; 1 <= topk_groups <= groups, groups divides E,
- * k <= topk_groups * E / groups; scale finite.  topk_idx [T, k] int32, topk_gate [T, k] float OUTPUT. */
+ * k <= topk_groups * E / groups; scale finite.  topk_idx [T, k] int32, topk_gate [T, k] float OUTPUT.  Sizes whose
+ * launch would have 2^32 threads or more are refused, here and in the backward. */
 moe_status_t moe_route_balanced(const void* x, const void* w_router, float* logits, const float* select_bias,
                                 int64_t T, int64_t d, int32_t E, int32_t k, int32_t groups, int32_t topk_groups,
                                 int32_t score, int32_t renormalize, float scale, moe_dtype_t dt, int32_t* topk_idx,

@@ -1131,6 +1131,7 @@ moe_status_t moe_route_balanced(const void* x, const void* w_router, float* logi
         "topk_groups must be in [1, groups] (got %d of %d)", topk_groups, groups);
   CHECK(k <= topk_groups * (E / groups), MOE_ERR_INVALID_VALUE, "k = %d, but %d open groups have %d experts", k,
         topk_groups, topk_groups * (E / groups));
+  CHECK(moe::route_scores_fits(T, E), MOE_ERR_UNSUPPORTED, "T = %lld is too large for a launch", (long long)T);
   CHECK(!w_router || x, MOE_ERR_INVALID_VALUE, "x is NULL with a learned router");
   if (T == 0) return MOE_OK;
   CHECK(logits && topk_idx && topk_gate, MOE_ERR_INVALID_VALUE, "logits/topk_idx/topk_gate is NULL");
@@ -1165,6 +1166,8 @@ moe_status_t moe_route_balanced_bwd(const float* dgate, const float* logits, con
   const bool dense = dense_scores(score, renormalize);
   CHECK(!dense || d % 8 == 0, MOE_ERR_UNSUPPORTED,
         "softmax scores without renormalization need d %% 8 == 0 (got %lld)", (long long)d);
+  CHECK(moe::route_scores_bwd_fits(T, d, E, k, dense, dt == MOE_BF16), MOE_ERR_UNSUPPORTED,
+        "T = %lld and d = %lld are too large for a launch", (long long)T, (long long)d);
   CHECK(dw_router && offsets && w_router, MOE_ERR_INVALID_VALUE, "dw_router/offsets/w_router is NULL");
   CHECK(T == 0 || (dgate && logits && topk_idx && src_row && x && dx_router), MOE_ERR_INVALID_VALUE,
         "dgate/logits/topk_idx/src_row/x/dx_router is NULL");

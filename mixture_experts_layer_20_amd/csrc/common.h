@@ -41,6 +41,8 @@ hipError_t launch_router_logits(const void* x, const void* w, const float* bias,
 hipError_t launch_topk_gate(const float* logits, int T, int E, int k, int renormalize,
                             int32_t* topk_idx, float* topk_gate, hipStream_t s);
 size_t route_bwd_ws_bytes(long long T, long long d, int E, int k);
+// Whether the launches fit: fewer than 2^32 threads along a grid's first axis, 2^16 blocks along its second.
+bool route_bwd_fits(long long T, long long d, int E, int k, bool bf16);
 // gate NULL: dgate holds the gradients of the chosen experts' logits.
 hipError_t launch_route_bwd(const float* dgate, const float* gate, const int32_t* topk_idx,
                             const int32_t* offsets, const int32_t* src_row, const void* x,
@@ -58,6 +60,7 @@ hipError_t launch_router_aux_bwd(const float* logits, const float* load_frac, co
 
 // dw = G^T x and dx = G w of a dense logit gradient G [T, E] (both written, not added to)
 size_t router_dense_bwd_ws_bytes(long long T, long long d, int E);
+bool router_dense_bwd_fits(long long T, long long d, int E);
 hipError_t launch_router_dense_bwd(const float* G, const void* x, const void* w, int T, int d, int E, bool bf16,
                                    float* dw, void* dx, void* ws, hipStream_t s);
 

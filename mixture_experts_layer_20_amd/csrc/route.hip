@@ -10,6 +10,7 @@
 // specified bitwise, so this runs on the vector ALUs.
 #include "common.h"
 
+#include <algorithm>
 #include <type_traits>
 
 #pragma clang fp contract(off)
@@ -781,6 +782,17 @@ static inline long long max_segments(long long Tk, int E) { return (Tk + SEG - 1
 size_t route_bwd_ws_bytes(long long T, long long d, int E, int k) {
   const long long Tk = T * k;
   return align256((size_t)max_segments(Tk, E) * d * sizeof(float));
+}
+
+bool route_bwd_fits(long long T, long long d, int E, int k, bool bf16) {
+  const long long blocks = 1LL << 24;   // of 256 threads
+  const long long segs = max_segments(T * k, E);
+  if ((d + DWCOLS - 1) / DWCOLS >= 1 << 16) return false;
+  if (d % 8 == 0) {
+    const int kk = k <= 2 ? k : k <= 4 ? 4 : 8, nt = std::max(1, DXL / (kk * (bf16 ? 1 : 2)));
+    return segs * ((d + DWCOLS8 - 1) / DWCOLS8) + (T + nt - 1) / nt * ((d + DXCOLS - 1) / DXCOLS) < blocks;
+  }
+  return T < blocks && segs < blocks;
 }
 
 template <typename T>

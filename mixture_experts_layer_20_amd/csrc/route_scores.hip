@@ -689,6 +689,13 @@ size_t route_scores_bwd_ws_bytes(long long T, long long d, int E, int k, bool de
          (dense ? router_dense_bwd_ws_bytes(T, d, E) : route_bwd_ws_bytes(T, d, E, k));
 }
 
+bool route_scores_fits(long long T, int E) { return T * (E <= 128 ? 16 : 32) <= (1LL << 32) - 256; }
+
+bool route_scores_bwd_fits(long long T, long long d, int E, int k, bool dense, bool bf16) {
+  if (dense) return T <= (1LL << 26) - 4 && router_dense_bwd_fits(T, d, E);   // a wave of the gates' gradient a token
+  return route_bwd_fits(T, d, E, k, bf16);
+}
+
 hipError_t launch_route_scores_bwd(const RouteScores& r, const float* dgate, const int32_t* topk_idx,
                                    const int32_t* offsets, const int32_t* src_row, const void* x, const void* w, int d,
                                    bool bf16, float* dw, void* dx, void* ws, hipStream_t s) {

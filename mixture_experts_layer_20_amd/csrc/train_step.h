@@ -15,6 +15,9 @@ struct RouteScores {
   bool whole;            // set by the launcher
   float scale;
 };
+// Whether the launches fit (grids of fewer than 2^32 threads).
+bool route_scores_fits(long long T, int E);
+bool route_scores_bwd_fits(long long T, long long d, int E, int k, bool dense, bool bf16);
 hipError_t launch_route_scores(const RouteScores& r, int32_t* topk_idx, float* topk_gate, hipStream_t s);
 // Every logit has a gradient (softmax scores that are not renormalised): dense.
 inline bool route_scores_dense(bool sigmoid, bool renormalize) { return !sigmoid && !renormalize; }

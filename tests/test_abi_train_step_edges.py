@@ -1,0 +1,32 @@
+"""Sizes and settings at the ends of what routing by scores and AdamW take: refused on the host past them (CPU)."""
+import pytest
+
+from mixture_experts_layer_20_amd import libmoe as L
+from tests.test_abi_train_step import BF, F32, FAKE, INVALID, SIG, SOFT, UNSUPPORTED, WORKSPACE, expect
+
+
+def test_route_balanced_of_too_many_tokens():
+    """16 threads a token: 2^28 tokens are a grid of 2^32.  (A pointer out of line ends the last call that is not
+    refused for its size.)"""
+    f = lambda T, E: L.moe_route_balanced(None, None, FAKE + 4, None, T, 8, E, 1, 1, 1, SIG, 1, 1.0, F32, FAKE, FAKE)
+    for E in (1, 4, 7):
+        expect(UNSUPPORTED, f, 1 << 28, E)
+        expect(UNSUPPORTED, f, (1 << 28) - 15, E)
+        expect(INVALID, f, (1 << 28) - 16, E)
+
+
+@pytest.mark.parametrize("score,renorm,dt,T,d,E,k", [
+    (SIG, 1, BF, 1 << 24, 9, 4, 1),          # a workgroup a token where d is no multiple of 8
+    (SIG, 1, BF, (1 << 28) - 1, 8, 4, 1),    # 16 tokens a workgroup, and the segments of the weights' gradient
+    (SOFT, 1, F32, 1 << 24, 8, 8, 8),        # one
+    (SIG, 0, BF, 1 << 16, 1 << 20, 8, 8),    # 512 of them for a token's columns
+    (SIG, 1, BF, 16, 1 << 27, 8, 8),         # 2^17 blocks along a grid's second axis
+    (SOFT, 0, BF, 1 << 26, 8, 8, 8),         # a wave a token
+    (SOFT, 0, BF, (1 << 26) - 3, 8, 8, 8),
+    (SOFT, 0, F32, 1 << 22, 1 << 16, 8, 8),  # 2^24 workgroups of dx
+])
+def test_route_balanced_bwd_of_too_large_sizes(score, renorm, dt, T, d, E, k):
+    f = lambda t, n: L.moe_route_balanced_bwd(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, t, n, E, k, score, renorm, 1.0, dt, FAKE,
+                                              FAKE, FAKE, 0)
+    expect(UNSUPPORTED, f, T, d)
+    expect(WORKSPACE, f, T // 4 if T > 16 else T, d if T > 16 else d // 4)
