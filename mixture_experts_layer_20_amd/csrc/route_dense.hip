@@ -138,11 +138,11 @@ size_t router_dense_bwd_ws_bytes(long long T, long long d, int E) {
   return T > 0 ? (size_t)dw_splits(T, d, E) * E * d * sizeof(float) : 0;
 }
 
-// Both products in one grid of fewer than 2^24 workgroups.
+// Both products in one grid of fewer than 2^24 workgroups, dw's elements counted in an int.
 bool router_dense_bwd_fits(long long T, long long d, int E) {
   const long long cols = (d + 4 * TILE - 1) / (4 * TILE), etiles = (E + TILE - 1) / TILE;
   const long long dw_blocks = T > 0 ? cols * etiles * dw_splits(T, d, E) : 0;
-  return dw_blocks + cols * ((T + TILE - 1) / TILE) < 1LL << 24;
+  return E * d < 1LL << 31 && dw_blocks + cols * ((T + TILE - 1) / TILE) < 1LL << 24;
 }
 
 hipError_t launch_router_dense_bwd(const float* G, const void* x, const void* w, int T, int d, int E, bool bf16,

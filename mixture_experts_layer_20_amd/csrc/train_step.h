@@ -15,7 +15,7 @@ struct RouteScores {
   bool whole;            // set by the launcher
   float scale;
 };
-// Whether the launches fit (grids of fewer than 2^32 threads).
+// Whether the launches fit (grids of fewer than 2^32 threads, E d an int).
 bool route_scores_fits(long long T, int E);
 bool route_scores_bwd_fits(long long T, long long d, int E, int k, bool dense, bool bf16);
 hipError_t launch_route_scores(const RouteScores& r, int32_t* topk_idx, float* topk_gate, hipStream_t s);

@@ -24,6 +24,7 @@ def test_route_balanced_of_too_many_tokens():
     (SOFT, 0, BF, 1 << 26, 8, 8, 8),         # a wave a token
     (SOFT, 0, BF, (1 << 26) - 3, 8, 8, 8),
     (SOFT, 0, F32, 1 << 22, 1 << 16, 8, 8),  # 2^24 workgroups of dx
+    (SOFT, 0, BF, 16, 1 << 23, 256, 8),      # 2^31 elements of dw
 ])
 def test_route_balanced_bwd_of_too_large_sizes(score, renorm, dt, T, d, E, k):
     f = lambda t, n: L.moe_route_balanced_bwd(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, t, n, E, k, score, renorm, 1.0, dt, FAKE,
