@@ -26,7 +26,8 @@ constexpr int BLK = 128;
 constexpr int ONE = 0x7f7f7f7f;   // scale bytes of the matrix instruction: 2^0
 
 // ---- Products: 128 x 128 tiles ------------------------------------------------------------------
-// Four waves, 64 x 64 each; K goes in blocks of 128 through a double-buffered LDS tile, 16-byte chunks
+// For many rows where N is no multiple of 256 (with SwiGLU every N fits the tiles further down, 128 columns of
+// either product).  Four waves, 64 x 64 each; K goes in blocks of 128 through a double-buffered LDS tile, 16-byte chunks
 // XOR-swizzled by (row >> 1) & 7.  The weights are the instruction's first operand, so a lane's
 // accumulators hold 4 consecutive output columns of one row: its row's scale is one register.
 constexpr int TB = 128;
@@ -108,14 +109,13 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][OPBYTES];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1, li = lane & 31, h = lane >> 5;
-  constexpr int OC = EPI == MX_EPI_SWIGLU ? 64 : 128;   // the SwiGLU tile: 64 gate and 64 up columns
-  const int NT = p.N / OC;
+  const int NT = p.N / TB;
   const int nt = blockIdx.x % NT;
   int g, m0, m_end;
   if (!find_rows<TB>(p.offsets, p.G, p.M, blockIdx.x / NT, g, m0, m_end)) return;
   const int nk = p.K / TB;
-  const bool split = EPI != MX_EPI_SWIGLU && p.b2 != nullptr;
-  const int K1 = split ? p.ksplit : p.K, K2 = EPI == MX_EPI_SWIGLU ? p.K : p.K - K1;
+  const bool split = p.b2 != nullptr;
+  const int K1 = split ? p.ksplit : p.K, K2 = p.K - K1;
 
   // Loads: rows (tid >> 3) + 32 j, 16-byte chunk tid & 7, of both operands.
   const int lrow = tid >> 3, lch = tid & 7;
@@ -126,22 +126,16 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
   for (int j = 0; j < 4; ++j) {
     const int r = lrow + 32 * j;
     ga[j] = p.a + (long long)min(m0 + r, m_end - 1) * p.K + 16 * lch;
-    if constexpr (EPI == MX_EPI_SWIGLU) {
-      const long long br = (long long)g * p.N + nt * 64 + (r >> 6) * 32 + (r & 31);
-      gb[j] = (((r >> 5) & 1) ? p.b2 : p.b) + br * p.K + 16 * lch;
-      gb2[j] = gb[j];
-    } else {
-      const long long br = (long long)g * p.N + nt * TB + r;
-      gb[j] = p.b + br * K1 + 16 * lch;
-      gb2[j] = split ? p.b2 + br * K2 + 16 * lch - K1 : gb[j];
-    }
+    const long long br = (long long)g * p.N + nt * TB + r;
+    gb[j] = p.b + br * K1 + 16 * lch;
+    gb2[j] = split ? p.b2 + br * K2 + 16 * lch - K1 : gb[j];
   }
   const int lofs = lrow * TB + 16 * (lch ^ swz(lrow));
-  // Scales: one of each of the lane's two rows, one of each of the wave's column blocks of 128.
+  // Scales: one of each of the lane's two rows, one of the tile's columns.
   const float* sa_p[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) sa_p[i] = p.as + min(m0 + wm * 64 + i * 32 + li, m_end - 1);
-  const long long nblk = (long long)g * (p.N / BLK) + (EPI == MX_EPI_SWIGLU ? nt / 2 : nt);
+  const long long nblk = (long long)g * (p.N / BLK) + nt;
   const float* sb_p = p.bs + nblk * (K1 / BLK);
   const float* sb2_p = p.bs2 ? p.bs2 + nblk * (K2 / BLK) : nullptr;
 
@@ -175,15 +169,10 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
   for (int kt = 0; kt < nk; ++kt) {
     const int cur = kt & 1;
     if (kt + 1 < nk) fetch(kt + 1);
-    float sa[2], sb[2];
+    float sa[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) sa[i] = sa_p[i][(long long)kt * p.M];
-    if constexpr (EPI == MX_EPI_SWIGLU) {
-      sb[0] = sb_p[kt];
-      sb[1] = sb2_p[kt];
-    } else {
-      sb[0] = sb[1] = kt * TB >= K1 ? sb2_p[kt - K1 / TB] : sb_p[kt];
-    }
+    const float sb = kt * TB >= K1 ? sb2_p[kt - K1 / TB] : sb_p[kt];
     f32x16_t part[2][2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -208,7 +197,7 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float f = sa[i] * sb[j];
+        const float f = sa[i] * sb;
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] += f * part[i][j][r];
       }
@@ -223,48 +212,32 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
     if (row >= m_end) continue;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      if constexpr (EPI == MX_EPI_SWIGLU) {
-        const long long o = (long long)row * p.N + nt * 64 + wn * 32 + 8 * q + 4 * h;
-        float hv[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float a = acc[i][0][4 * q + r];
-          hv[r] = a * sigmoid_of(a) * acc[i][1][4 * q + r];
-        }
-        auto put = [&](void* out, float v0, float v1, float v2, float v3) {
-          *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(out) + o) = make_uint2(pack2(v0, v1), pack2(v2, v3));
-        };
-        if (p.out0) put(p.out0, acc[i][0][4 * q], acc[i][0][4 * q + 1], acc[i][0][4 * q + 2], acc[i][0][4 * q + 3]);
-        if (p.out1) put(p.out1, acc[i][1][4 * q], acc[i][1][4 * q + 1], acc[i][1][4 * q + 2], acc[i][1][4 * q + 3]);
-        put(p.out2, hv[0], hv[1], hv[2], hv[3]);
-      } else {
+      for (int j = 0; j < 2; ++j) {
+        const int col = nt * TB + wn * 64 + j * 32 + 8 * q + 4 * h;
+        float v[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = nt * TB + wn * 64 + j * 32 + 8 * q + 4 * h;
-          float v[4];
+        for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r];
+        if constexpr (EPI == MX_EPI_SWIGLU_BWD) {
+          const long long o = (long long)row * p.N + col;
+          const uint2 av = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux0) + o);
+          const uint2 bv = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux1) + o);
+          const uint32_t aw[2] = {av.x, av.y}, bw[2] = {bv.x, bv.y};
+          float da[4], db[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * q + r];
-          if constexpr (EPI == MX_EPI_SWIGLU_BWD) {
-            const long long o = (long long)row * p.N + col;
-            const uint2 av = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux0) + o);
-            const uint2 bv = *reinterpret_cast<const uint2*>(reinterpret_cast<const bf16_t*>(p.aux1) + o);
-            const uint32_t aw[2] = {av.x, av.y}, bw[2] = {bv.x, bv.y};
-            float da[4], db[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float a = bf16_to_f32((bf16_t)(aw[r >> 1] >> (16 * (r & 1))));
-              const float bb = bf16_to_f32((bf16_t)(bw[r >> 1] >> (16 * (r & 1))));
-              const float sg = sigmoid_of(a);
-              da[r] = v[r] * bb * sg * (1.0f + a * (1.0f - sg));
-              db[r] = v[r] * a * sg;
-            }
-            bf16_t* dab = reinterpret_cast<bf16_t*>(p.out0) + (long long)row * (2 * p.N);
-            *reinterpret_cast<uint2*>(dab + col) = make_uint2(pack2(da[0], da[1]), pack2(da[2], da[3]));
-            *reinterpret_cast<uint2*>(dab + p.N + col) = make_uint2(pack2(db[0], db[1]), pack2(db[2], db[3]));
-          } else {
-            *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(p.out0) + (long long)row * p.N + col) =
-                make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+          for (int r = 0; r < 4; ++r) {
+            const float a = bf16_to_f32((bf16_t)(aw[r >> 1] >> (16 * (r & 1))));
+            const float bb = bf16_to_f32((bf16_t)(bw[r >> 1] >> (16 * (r & 1))));
+            const float sg = sigmoid_of(a);
+            da[r] = v[r] * bb * sg * (1.0f + a * (1.0f - sg));
+            db[r] = v[r] * a * sg;
           }
+          bf16_t* dab = reinterpret_cast<bf16_t*>(p.out0) + (long long)row * (2 * p.N);
+          *reinterpret_cast<uint2*>(dab + col) = make_uint2(pack2(da[0], da[1]), pack2(da[2], da[3]));
+          *reinterpret_cast<uint2*>(dab + p.N + col) = make_uint2(pack2(db[0], db[1]), pack2(db[2], db[3]));
+        } else {
+          *reinterpret_cast<uint2*>(reinterpret_cast<bf16_t*>(p.out0) + (long long)row * p.N + col) =
+              make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
         }
       }
     }
@@ -274,7 +247,7 @@ __global__ __launch_bounds__(256, 2) void fp8_gemm_kernel(Fp8GemmArgs p) {
 template <int EPI>
 hipError_t launch_tiles(const Fp8GemmArgs& a, hipStream_t s) {
   const long long rows = (a.M + TB - 1) / TB + std::min(a.G, a.M);
-  const long long tiles = rows * (a.N / (EPI == MX_EPI_SWIGLU ? 64 : 128));
+  const long long tiles = rows * (a.N / TB);
   fp8_gemm_kernel<EPI><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -890,17 +863,12 @@ hipError_t launch_epi(const Fp8GemmArgs& a, hipStream_t s) {
   const bool fits = ((a.M + 15) / 16 + a.G) * (long long)(a.N / 16) <= 1 << 22;   // below 2^31 threads
   const bool longer = EPI == MX_EPI_SWIGLU || (long long)a.G * a.N < 256LL * PN || (long long)a.G * a.N * a.K > 256LL << 20;
   if ((a.M <= 64 || a.M <= (longer ? 8LL : 2LL) * a.G) && fits) return launch_few<EPI>(a, s);
-  // a tile's columns: 256 of N, or 128 gate and 128 up columns
-  if (a.N % (EPI == MX_EPI_SWIGLU ? 128 : PN) == 0) return launch_pipe<EPI>(a, s);
-  return launch_tiles<EPI>(a, s);
+  // a tile's columns: 128 gate and 128 up columns, or 256 of N
+  if constexpr (EPI == MX_EPI_SWIGLU) return launch_pipe<EPI>(a, s);
+  else return a.N % PN == 0 ? launch_pipe<EPI>(a, s) : launch_tiles<EPI>(a, s);
 }
 
 }  // namespace
-
-size_t fp8_gemm_ws_bytes(int G, long long M, long long N, long long K) {
-  (void)G; (void)M; (void)N; (void)K;
-  return 0;
-}
 
 hipError_t launch_fp8_gemm(int epi, const Fp8GemmArgs& a, hipStream_t s) {
   if (a.M == 0) return hipSuccess;

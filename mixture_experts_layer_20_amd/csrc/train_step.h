@@ -47,9 +47,7 @@ struct Fp8GemmArgs {
   void* out2;
   const void* aux0;
   const void* aux1;
-  void* ws;
 };
-size_t fp8_gemm_ws_bytes(int G, long long M, long long N, long long K);
 hipError_t launch_fp8_gemm(int epi, const Fp8GemmArgs& a, hipStream_t s);   // epi: MxEpilogue
 
 // AdamW over a list of tensors
