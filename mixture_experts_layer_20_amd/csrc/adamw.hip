@@ -20,6 +20,8 @@
 // lanes, whose largest value is found with row rotations in registers.
 #include "train_step.h"
 
+#include "lanes.h"
+
 #include <algorithm>
 #include <memory>
 #include <new>
@@ -30,8 +32,6 @@
 namespace moe {
 namespace {
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
@@ -48,16 +48,6 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
   h ^= h >> 15;
   h *= 0xC5A1E6B7u;
   return h ^ (h >> 16);
-}
-
-// The largest of the 16 lanes of a row, in every one of them: bits of magnitudes, which order as the
-// values do, a NaN above all.
-__device__ __forceinline__ uint32_t row_max(uint32_t b) {
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0xB1, 0xf, 0xf, false));    // quad_perm 1,0,3,2
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x4E, 0xf, 0xf, false));    // quad_perm 2,3,0,1
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x124, 0xf, 0xf, false));   // row_ror 4
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x128, 0xf, 0xf, false));   // row_ror 8
-  return b;
 }
 
 // sqrt(v), v >= 0, from the reciprocal root with one correction, nearly always rounded to nearest; the
@@ -172,7 +162,7 @@ __device__ __forceinline__ void store8_codes(uint8_t* p, uint32_t at, uint32_t l
 // code above zero.  A block with an infinity or a NaN gets a scale of NaN, and stays so.
 template <bool POSITIVE>
 __device__ __forceinline__ float encode8(const float (&x)[RUN], uint32_t b, const uint32_t (&bits)[RUN], u32x2_t& codes) {
-  b = row_max(b);
+  b = row16_max(b);
   const bool lost = b >= 0x7f800000u;
   const float top = __uint_as_float(b);
   const bool fine = top >= TINY && !lost;

@@ -32,6 +32,19 @@ __device__ __forceinline__ float sigmoid_f32(float a) { return 1.0f / (1.0f + ex
 
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
+// Compute units of the current device (one persistent workgroup each).
+inline int device_cus() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
 // ----------------------------------------------------------------------------------------------
 // Launchers (host side).  All enqueue on `s` and return the launch status.
 

@@ -10,7 +10,7 @@
 // weights' scale is the same for all of them.
 #include "train_step.h"
 
-#include "block_store.h"
+#include "lanes.h"
 #include "mxfp8.h"
 
 #include <algorithm>
@@ -820,18 +820,6 @@ __global__ __launch_bounds__(512, 2) void fp8_pipe_kernel(Fp8GemmArgs p) {
     }
     pipe_epilogue<EPI>(p, t, acc, wm, wn, lane);
   }
-}
-
-int device_cus() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 template <int EPI>

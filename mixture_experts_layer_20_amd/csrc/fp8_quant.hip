@@ -12,25 +12,16 @@
 // exactly, the others on their own side of them, and the codes are those of the exact quotient.
 #include "train_step.h"
 
+#include "lanes.h"
+
 #include <algorithm>
 
 namespace moe {
 namespace {
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-
 constexpr int BLK = 128;
 constexpr float TOP = 448.0f;
 constexpr float TINY = 0x1p-100f;
-
-__device__ __forceinline__ uint32_t row16_max(uint32_t b) {   // of a row of 16 lanes
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0xB1, 0xf, 0xf, false));    // quad_perm 1,0,3,2
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x4E, 0xf, 0xf, false));    // quad_perm 2,3,0,1
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x124, 0xf, 0xf, false));   // row_ror 4
-  b = max(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x128, 0xf, 0xf, false));   // row_ror 8
-  return b;
-}
 
 // Bits of the largest magnitude of 8 bf16 values (as fp32 bits; a NaN is above all).
 __device__ __forceinline__ uint32_t max8(const u32x4_t& w) {

@@ -34,7 +34,7 @@
 // groups.  In both, the B operand is the instruction's first operand, so each lane's accumulators
 // hold 4 consecutive output columns of one row.
 #include "common.h"
-#include "block_store.h"
+#include "lanes.h"
 #include "mxfp8.h"
 
 #include <algorithm>
@@ -222,6 +222,10 @@ constexpr int TB = 128;               // tile rows = tile columns = K step (byte
 constexpr int OPBYTES = TB * TB;      // one operand tile of one buffer: 16 KiB
 
 __device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+
+__device__ __forceinline__ uint32_t bf16pack(float a, float b) {
+  return (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
+}
 
 // Operand fragment of a 32-row block for K step half s: row i = lane & 31, chunks 4s + h and
 // 4s + 2 + h (h = lane >> 5) of the 128-byte row.
@@ -704,6 +708,40 @@ __device__ __forceinline__ void pipe_issue(const PLoad& L, long long kb0, int j,
   }
 }
 
+// Accumulator block exchange for wide stores.  After the transposed MFMA, lane l holds row l % 32 and,
+// for element v, column 8 (v / 4) + 4 (l / 32) + v % 4 of the 32x32 block: a store covers 32 rows
+// with 16 bytes each.  v_permlane32_swap of the 4-column pieces of each 16-column half gives lane l
+// 8 consecutive columns 16 H + 8 (l / 32) of its row; v_permlane16_swap of the two halves then
+// leaves x0 = row l % 16 and x1 = row 16 + l % 16, both at columns 16 ((l / 16) % 2) + 8 (l / 32):
+// each 16-byte store covers 16 rows with 64 contiguous bytes.
+__device__ __forceinline__ int xcol(int lane) { return 16 * ((lane >> 4) & 1) + 8 * (lane >> 5); }
+
+__device__ __forceinline__ void xchg_block(const f32x16_t& c, float (&x0)[8], float (&x1)[8]) {
+  float hv[2][8];
+#pragma unroll
+  for (int H = 0; H < 2; ++H)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[8 * H + e]), __float_as_uint(c[8 * H + 4 + e]),
+                                                      false, false);
+      hv[H][e] = __uint_as_float(r[0]);
+      hv[H][4 + e] = __uint_as_float(r[1]);
+    }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(hv[0][e]), __float_as_uint(hv[1][e]), false, false);
+    x0[e] = __uint_as_float(r[0]);
+    x1[e] = __uint_as_float(r[1]);
+  }
+}
+
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
+  u32x4_t w;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) w[e] = bf16pack(v[2 * e], v[2 * e + 1]);
+  return w;
+}
+
 // MXFP8 of 8 consecutive bf16 values of a row (packed in w) whose 32-column block is spread over
 // lanes l, l ^ 16, l ^ 32, l ^ 48 (the exchanged layout): codes to dst (8 bytes), the scale byte by
 // the lane holding the block's first columns.
@@ -990,19 +1028,6 @@ __global__ __launch_bounds__(512, 1) void mx_gemm_pipe_kernel(MxGemmArgs p) {
     pipe_epilogue<EPI, RK>(p, t, acc, wm, wn, lane);
     after_epi = true;
   }
-}
-
-// Compute units of the current device (one persistent workgroup each).
-int device_cus() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
-    int n = 0;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    cached[dev] = n;
-  }
-  return cached[dev];
 }
 
 template <int EPI, bool RK, int SW>
