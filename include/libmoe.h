@@ -654,7 +654,8 @@ typedef struct {
   moe_dtype_t dt, grad_dt;
 } moe_adamw_t;
 typedef struct {
-  double lr, beta1, beta2, eps;   /* lr >= 0, betas in [0, 1), eps > 0 */
+  double lr, beta1, beta2, eps;   /* lr >= 0, betas in [0, 1), eps > 0; lr / (1 - beta1^step), lr weight_decay and
+                                   * eps are used as floats and have to be finite as such */
   int64_t step;                   /* 1 for the first */
   uint32_t seed;
   int32_t state_bits;             /* 32 or 8 */

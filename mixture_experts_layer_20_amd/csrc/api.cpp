@@ -1395,6 +1395,8 @@ moe_status_t moe_adamw(const moe_adamw_t* tensors, int32_t count, const moe_adam
   CHECK((float)step->eps >= 1.17549435e-38f && std::isfinite((float)step->eps), MOE_ERR_INVALID_VALUE,
         "eps must be a normal float > 0");
   CHECK(step->step >= 1, MOE_ERR_INVALID_VALUE, "step must be >= 1 (got %lld)", (long long)step->step);
+  const float step_size = (float)(step->lr / (1.0 - std::pow(step->beta1, (double)step->step)));
+  CHECK(std::isfinite(step_size), MOE_ERR_INVALID_VALUE, "lr / (1 - beta1^step) must be finite as a float");
   if (sumsq && (st = check_max_norm(max_norm)) != MOE_OK) return st;
   CHECK_ALIGN16(sumsq);
   if (count == 0) return MOE_OK;
@@ -1402,6 +1404,8 @@ moe_status_t moe_adamw(const moe_adamw_t* tensors, int32_t count, const moe_adam
   CHECK(items, MOE_ERR_UNSUPPORTED, "no host memory for a list of %d tensors", count);
   for (int i = 0; i < count; ++i) {
     const moe_adamw_t& a = tensors[i];
+    CHECK(std::isfinite((float)(step->lr * a.weight_decay)), MOE_ERR_INVALID_VALUE,
+          "tensor %d: lr weight_decay must be finite as a float", i);
     items[i] = moe::AdamWItem{a.param,     a.grad,       a.m,          a.v,
                               a.scale,     a.master,     a.param_out,  a.m_out,
                               a.v_out,     a.scale_out,  a.master_out, (long long)a.n,
@@ -1414,7 +1418,7 @@ moe_status_t moe_adamw(const moe_adamw_t* tensors, int32_t count, const moe_adam
   s.beta2 = (float)step->beta2;
   s.one_minus_beta2 = (float)(1.0 - step->beta2);
   s.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(1.0 - std::pow(step->beta2, (double)step->step)));
-  s.step_size = (float)(step->lr / (1.0 - std::pow(step->beta1, (double)step->step)));
+  s.step_size = step_size;
   s.eps = (float)step->eps;
   s.sumsq = sumsq;
   s.max_norm = max_norm;

@@ -2,7 +2,7 @@
 import pytest
 
 from mixture_experts_layer_20_amd import libmoe as L
-from tests.test_abi_train_step import BF, F32, FAKE, INVALID, SIG, SOFT, UNSUPPORTED, WORKSPACE, expect
+from tests.test_abi_train_step import BF, F32, FAKE, INVALID, SIG, SOFT, UNSUPPORTED, WORKSPACE, expect, host_list
 
 
 def test_route_balanced_of_too_many_tokens():
@@ -31,3 +31,11 @@ def test_route_balanced_bwd_of_too_large_sizes(score, renorm, dt, T, d, E, k):
                                               FAKE, FAKE, 0)
     expect(UNSUPPORTED, f, T, d)
     expect(WORKSPACE, f, T // 4 if T > 16 else T, d if T > 16 else d // 4)
+
+
+def test_adamw_of_factors_past_float():
+    """The kernels' factors are floats: ones that would be infinite there are refused."""
+    t, decayed = host_list(), host_list(weight_decay=1e30)
+    expect(INVALID, L.moe_adamw, t, 1e39, 0.0, 0.95, 1e-8, 1)
+    expect(INVALID, L.moe_adamw, t, 1e30, 1.0 - 1e-9, 0.95, 1e-8, 1)   # over 1 - beta1
+    expect(INVALID, L.moe_adamw, decayed, 1e10, 0.9, 0.95, 1e-8, 100)
