@@ -157,6 +157,21 @@ def test_adamw_of_more_than_2_32_elements(bits):
     assert repeats(m[:cut], want[1], near) and repeats(v[:cut], want[2], near)
 
 
+def test_adamw_of_32_bit_states_rounds_to_nearest():
+    """From a parameter of zero, a step is -(lr / bc1) m / (sqrt(v) / sqrt(bc2) + eps) of the new m and v, each operation
+    rounded once.  (numpy's roots of doubles, rounded to float, are roots rounded to nearest; torch's of floats on the CPU
+    need not be.  The sum with eps is formed in double and rounded twice, which differs once in 2^29.)"""
+    n = 20000
+    c = Case([n], [torch.float32], [torch.float32], 32, False, seed=15)
+    c.p[0].zero_()
+    L.moe_adamw(c.list(0.0), seed=3, **HYPER)
+    p, m, v = (t.cpu().numpy() for t in c.results(0)[:3])
+    f32 = np.float32
+    root, factor = np.sqrt(v.astype(np.float64)).astype(f32), f32((1.0 - HYPER["beta2"] ** HYPER["step"]) ** -0.5)
+    den = (root.astype(np.float64) * np.float64(factor) + np.float64(f32(HYPER["eps"]))).astype(f32)
+    np.testing.assert_array_equal(p, -f32(HYPER["lr"] / (1.0 - HYPER["beta1"] ** HYPER["step"])) * (m / den))
+
+
 # ---- routing by scores --------------------------------------------------------------------------------
 
 @pytest.mark.parametrize("score", [SIG, SOFT])
