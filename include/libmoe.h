@@ -556,8 +556,8 @@ moe_status_t moe_route_balanced(const void* x, const void* w_router, float* logi
                                 float* topk_gate, moe_stream_t stream);
 
 /* Backward of the gates with respect to the logits, and through them to the router and its input.  dgate
- * [T, k] float, logits [T, E] float and topk_idx [T, k] (of the forward call), offsets [E+1] and src_row
- * [T*k] from moe_permute, x [T, d], w_router [E, d] (dt) INPUT:
+ * [T, k] float, logits [T, E] float and topk_idx [T, k] (of the forward call, or another choice: an expert may
+ * stand in two of a token's places), offsets [E+1] and src_row [T*k] from moe_permute, x [T, d], w_router [E, d] (dt) INPUT:
  *   dw_router = dL^T x  [E, d] float OUTPUT;   dx_router = dL w_router  [T, d] (dt) OUTPUT
  * The choice carries no gradient, nor does the bias.  dL is zero outside the chosen experts, but for
  * softmax scores with renormalize = 0, whose every logit has a gradient: that form needs d to be a

@@ -670,7 +670,7 @@ __global__ __launch_bounds__(256) void scores_grad_dense_kernel(RouteScores r, c
 #pragma unroll
     for (int s = 0; s < 4; ++s)
       if (e == lane + 64 * s) {
-        own[s] = dg;
+        own[s] += dg;
         all += p[s] * inv * dg;
       }
   }

@@ -6,7 +6,7 @@ import torch
 
 from mixture_experts_layer_20_amd import libmoe as L
 from oracle import train_step as S
-from tests.test_gpu_train_step import BF, DEV, F, HYPER, SIG, SOFT, Case, check_route, put, sums_bound
+from tests.test_gpu_train_step import BF, DEV, F, HYPER, SIG, SOFT, Case, check_route, np64, put, route_bwd, sums_bound
 
 pytestmark = pytest.mark.gpu
 VALUES = torch.from_numpy(S.E4M3)
@@ -186,6 +186,33 @@ def test_route_groups_of_opposite_biases(E, groups, topk_groups, score, size):
     b[:, 0], b[:, 1] = size, -size
     b = np.take_along_axis(b, np.argsort(r.random(b.shape), axis=1), axis=1)
     check_route(l, b.reshape(-1), k, groups, topk_groups, score, 1, 1.0)
+
+
+@pytest.mark.parametrize("score,renorm", [(SIG, 1), (SIG, 0), (SOFT, 1), (SOFT, 0)])
+def test_route_backward_of_an_expert_named_twice(score, renorm):
+    """A choice that a caller made: each of a token's places has its own gate and gradient, also where two name one
+    expert."""
+    r = np.random.default_rng(21)
+    T, d, E, k, scale = 70, 64, 12, 4, 1.5
+    logits, idx = put(r.standard_normal((T, E)) * 2), put(r.integers(0, E, (T, k)), torch.int32)
+    idx[:, 2] = idx[:, 0]
+    x, w, dgate = put(r.standard_normal((T, d))), put(r.standard_normal((E, d)) * 0.3), put(r.standard_normal((T, k)))
+    dw, dx = route_bwd(dgate, logits, idx, x, w, score, renorm, scale)
+    l, dg, i = np64(logits), np64(dgate), idx.cpu().numpy().astype(np.int64)
+    dl, g = S.gates_bwd(dg, l, i, score == SIG, renorm, scale), S.gates(l, i, score == SIG, renorm, 1.0)
+    # terms of a logit's gradient, and their roundings: the gates' own, k differences and products
+    size = np.zeros_like(dl)
+    if score == SOFT and not renorm:
+        size += scale * S.scores(l, False) * (g * np.abs(dg)).sum(1, keepdims=True)
+    inner = np.abs(dg) + ((g * np.abs(dg)).sum(1, keepdims=True) if renorm else 0.0)
+    np.add.at(size, (np.arange(T)[:, None], i), scale * g * inner)
+    e_dl = (12 * np.abs(l).max() + 100) * F * size
+    x64, w64 = np64(x), np64(w)
+    # each place is a term of its own in the sums: their magnitudes, not those of what is left of two
+    tol_dw = e_dl.T @ np.abs(x64) + (T + 8) * F * (size.T @ np.abs(x64))
+    tol_dx = e_dl @ np.abs(w64) + (E + 8) * F * (size @ np.abs(w64))
+    assert np.all(np.abs(np64(dw) - dl.T @ x64) <= tol_dw * 1.01 + 1e-30)
+    assert np.all(np.abs(np64(dx) - dl @ w64) <= tol_dx * 1.01 + 1e-30)
 
 
 # ---- products -------------------------------------------------------------------------------------------
