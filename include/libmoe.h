@@ -540,8 +540,9 @@ moe_status_t moe_mx_gemm_k(const uint8_t* a_codes, const uint8_t* a_scales, int6
  * groups, it is decided in double wherever fp32 does not tell.  Of equal values the lower index comes
  * first.  A NaN ranks after every number; whatever logits and bias hold, topk_idx has k different values
  * in [0, E), and the gates of a token with a NaN or +inf are unspecified.  A logit of -inf is a score of
- * 0; where every chosen score is 0 the gates are 0.  Scores of -inf from the bias shut an expert as long
- * as k others are open.
+ * 0; where every chosen score is 0 the gates are 0.  A bias of -inf shuts an expert: it is chosen only where the
+ * token's open groups have fewer than k others.  (A group whose second best is shut scores -inf, and of such groups
+ * the first ones are open.)
  * Source: "Olmo-core DDP MoE examples", "Other experiments in the report" (load-balancing experiments); the
  * pages do not print the router: the formulas above are the reading. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
@@ -585,7 +586,9 @@ moe_status_t moe_route_bias_update(const int32_t* counts, int32_t E, float rate,
  * A block that holds an infinity or a NaN gets a scale of NaN, and what is multiplied with it is NaN.
  * A product is that of the matrices which codes and scales stand for: each block's 128 products are summed
  * by the matrix instruction (8 neighbours at a time with 13 bits below the largest of them, those sums in
- * fp32), scaled, and the blocks are added in fp32; outputs are bf16, rounded once.
+ * fp32), scaled by the product of its two scales, which is formed in fp32 and should be a normal number there, and the
+ * blocks are added in fp32; outputs are bf16, rounded once.  The SwiGLU epilogues' sigmoid comes from the hardware's
+ * exponential and reciprocal, a few units in the last place of fp32.
  * Source: the pages' 8-bit recipe ("Olmo-core DDP MoE examples", "Other experiments in the report") in the
  * form with longer blocks. */
 
@@ -622,17 +625,21 @@ moe_status_t moe_fp8_gemm_rows(const uint8_t* a_codes, const float* a_scales, co
 /* The step that follows the gradients' norm, with the clipping in the same pass over the gradients:
  *   g = c grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p = (1 - lr weight_decay) p - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
- * all in fp32.  c = 1 without sumsq; with it (moe_grad_norm) c = min(1, max_norm / (sqrt(sumsq) + 1e-6)),
+ * all in fp32, with 32-bit states each operation rounded to nearest, with 8-bit states the root and the quotient within
+ * units in the last place.  c = 1 without sumsq; with it (moe_grad_norm) c = min(1, max_norm / (sqrt(sumsq) + 1e-6)),
  * and a norm that is infinite as a float or NaN makes no step: every output is its input (of a parameter
  * that is not given, its master copy, rounded).  Such a call does not count: the next one gets the same number.
  *   state_bits 32: m, v [n] float, scale NULL.
  *   state_bits 8:  m, v [n] uint8, E4M3 codes of m and of sqrt(v); scale [2, ceil(n / 128)] float, m's and
  *     then those of sqrt(v): a code stands for itself times its block's scale (largest magnitude / 448).
- *     Rounded up or down at random with the right mean, a positive v not to zero.  The step uses m and v
- *     before that.  A block that gets an infinity or a NaN gets a scale of NaN.
+ *     Rounded up or down at random, so that m and sqrt(v) keep their mean, but a positive v not to zero.  Its square
+ *     does not: v itself, which accumulates, comes out 3 to 6% too large on average and spread by a quarter to a third
+ *     (beta2 0.95 to 0.999, steady gradients), and no further however long the run.  The step uses m and v before
+ *     that.  A block that gets an infinity or a NaN gets a scale of NaN.
  *   A bf16 parameter with a master copy is that copy, rounded to nearest, and not read; without one it is
  *     rounded at random like the 8-bit states.  fp32 parameters have no master copy (NULL).
- * Random bits are a function of seed, the tensor's place in the list and the element's place in it.
+ * Random bits are a function of seed, the tensor's place in the list and the element's place in it: give every step
+ * another seed.  step and seed are arguments of the kernels: a captured graph repeats them at every replay.
  * Every out is the same tensor as its input (in place) or overlaps nothing else of the list: two tensors of
  * the list must not share memory either, which moe_adamw_check finds and moe_adamw does not look for.
  * Tensors are contiguous and 16-byte aligned; n may be 0.  Zeros are the state before the first step.

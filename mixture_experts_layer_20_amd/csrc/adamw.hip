@@ -11,13 +11,15 @@
 // probability of the rest.  A positive v keeps at least the smallest code: m over a v that was rounded to
 // zero would be a step of m / eps.  A bf16 parameter without a master copy is rounded in the same way.  The
 // random bits are a hash of the element's run of 8 and the tensor's seed, and a linear congruential sequence
-// inside the run: the same call gives the same bits.
+// (Knuth's and Lewis's) inside the run: the same call gives the same bits.  What keeps its mean in each rounding is
+// the root; v's is then larger by the rounding's variance, which over many steps comes to 3 to 6% of it (a quarter
+// to a third of spread, beta2 0.95 to 0.999): it stays there, since a root that hardly moves is near its code.
 //
 // Bound by memory: one pass, nothing read or written twice, parameters that have a master copy not read.
-// 409 M bf16 parameters out of place: fp32 states and master copies 2104 us (12.3 GB, 5.8 TB/s), 8-bit states
-// 720 us (4.1 GB, 5.7 TB/s), against 5.1 TB/s of a device copy; what the 8-bit form computes, about 430
-// vector instructions for 8 elements of a wave, would take 0.6 ms by itself.  128 elements (a block) lie in 16
-// lanes, whose largest value is found with row rotations in registers.
+// 409 M bf16 parameters out of place: fp32 states and master copies, 28 bytes each, 2069 to 2117 us (11.5 GB, 5.4 to
+// 5.5 TB/s), 8-bit states 713 to 733 us (4.1 GB, 5.6 to 5.8 TB/s), against 5.2 TB/s of a device copy; what the 8-bit
+// form computes, about 430 vector instructions for 8 elements of a wave, would take 0.6 ms by itself.  128
+// elements (a block) lie in 16 lanes, whose largest value is found with row rotations in registers.
 #include "train_step.h"
 
 #include "lanes.h"
@@ -52,8 +54,10 @@ __device__ __forceinline__ uint32_t mix(uint32_t h) {
 
 // sqrt(v), v >= 0, from the reciprocal root with one correction, nearly always rounded to nearest; the
 // hardware's own, which is within a unit in the last place, would decide four times as many of the stored
-// roots' roundings differently from the exact value.  NaN for infinity.  Below 2^-126, the squares of
-// gradients below 2^-63, the root comes out small.
+// roots' roundings differently from the exact value.  (Of 200 M stored codes 131 of v and 250 of m differ from those
+// of the formulas in 64 bits, the same ones with a root rounded to nearest, which takes 790 us for 733; in plain fp32
+// operations it is 158 and 319.)  NaN for infinity.  Below 2^-126, the squares of gradients below 2^-63, the root comes
+// out small.
 __device__ __forceinline__ float root_of(float v) {
   const float q = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-126f));
   const float r = v * q;
@@ -453,7 +457,7 @@ __global__ __launch_bounds__(NT, BITS8 ? 5 : 8) void adamw_kernel(Table<CAP> t) 
 // Elements per chunk: one step of a workgroup, so that workgroups that run together work on neighbouring
 // memory (409 M parameters with 8-bit states: 720 us, against 880 us with 64 Ki chunks over the list and 1010 us
 // with 8 Ki; with fp32 states and master copies 2109 us, 2205 in chunks of two steps); more only where the grid
-// of a launch would pass 2^30 threads.
+// of a launch would pass 2^30 threads, for lists of more than 2^32 elements.
 long long chunk_size(long long total, bool bits8) {
   const long long step = NT * (bits8 ? lane_elements<true>() : lane_elements<false>());
   const long long c = (total + (1 << 22) - 1) >> 22;

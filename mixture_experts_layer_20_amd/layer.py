@@ -606,7 +606,8 @@ class MoELayer:
     def make_adamw(self, state_bits: int = 32, master: bool = False, weight_decay=0.0):
         """The optimizer's states (zeros) for adamw_step: 32 or 8 bits, with or without float master copies
         of bf16 parameters; weight_decay for all parameters or a list in their order.  The tensors that params
-        holds now are the ones that adamw_step changes."""
+        holds now are the ones that adamw_step changes; one with a master copy is that copy, rounded: weights are
+        loaded before."""
         if not self.cfg.backward:
             raise ValueError("the layer has no backward")
         params, grads = self.parameters(), self.gradients()
@@ -642,8 +643,9 @@ class MoELayer:
                    max_norm: float | None = None, seed: int = 0):
         """One AdamW step on the parameters, in place, from the gradients of the last backward, clipped in the
         same pass to a global norm of max_norm if that is given (grad_norm then is the norm; one that is infinite
-        or NaN makes no step).  make_adamw comes first.  Quantized weights are made again by the next pass.  The
-        step's number and its seed are arguments of the kernels: a captured graph repeats them.  A clipped step is
+        or NaN makes no step).  make_adamw comes first.  Quantized weights are made again by the next pass, but not
+        by a graph that was captured with cached ones.  The step's number and its seed are arguments of the
+        kernels: a captured graph repeats them.  A clipped step is
         preceded by a wait for the norm of the one before (see steps), but not while a graph is captured."""
         if self._adamw is None:
             raise ValueError("make_adamw comes before adamw_step")
