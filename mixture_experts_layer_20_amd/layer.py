@@ -619,7 +619,7 @@ class MoELayer:
                                      device=params[0].device)
         # the last clipped step's norm on the host, and when it is there
         cuda = params[0].is_cuda
-        self._norm_host = torch.empty(1, pin_memory=True) if cuda else None
+        self._norm_host = torch.empty(1, dtype=torch.float32, pin_memory=True) if cuda else None
         self._norm_there = torch.cuda.Event() if cuda else None
         self.steps = 0
 
@@ -645,8 +645,8 @@ class MoELayer:
         same pass to a global norm of max_norm if that is given (grad_norm then is the norm; one that is infinite
         or NaN makes no step).  make_adamw comes first.  Quantized weights are made again by the next pass, but not
         by a graph that was captured with cached ones.  The step's number and its seed are arguments of the
-        kernels: a captured graph repeats them.  A clipped step is
-        preceded by a wait for the norm of the one before (see steps), but not while a graph is captured."""
+        kernels: a captured graph repeats them.  A clipped step is preceded by a wait for the norm of the one before
+        (see steps), but not while a graph is captured."""
         if self._adamw is None:
             raise ValueError("make_adamw comes before adamw_step")
         captured = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()

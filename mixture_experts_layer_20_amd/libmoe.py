@@ -627,7 +627,8 @@ def adamw_states(params, bits=32, master=False):
     params = list(params)
     m = [torch.zeros(p.numel(), dtype=kind, device=p.device) for p in params]
     v = [torch.zeros(p.numel(), dtype=kind, device=p.device) for p in params]
-    scales = [torch.zeros(2 * -(-p.numel() // STATE_BLOCK), device=p.device) if bits == 8 else None for p in params]
+    scales = [torch.zeros(2 * -(-p.numel() // STATE_BLOCK), dtype=torch.float32, device=p.device) if bits == 8 else None
+              for p in params]
     masters = [p.detach().float().reshape(-1).clone() if master and p.dtype == torch.bfloat16 else None for p in params]
     return m, v, scales, masters
 

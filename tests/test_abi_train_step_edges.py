@@ -1,5 +1,6 @@
 """Sizes and settings at the ends of what routing by scores and AdamW take: refused on the host past them (CPU)."""
 import pytest
+import torch
 
 from mixture_experts_layer_20_amd import libmoe as L
 from tests.test_abi_train_step import BF, F32, FAKE, INVALID, SIG, SOFT, UNSUPPORTED, WORKSPACE, expect, host_list
@@ -39,3 +40,14 @@ def test_adamw_of_factors_past_float():
     expect(INVALID, L.moe_adamw, t, 1e39, 0.0, 0.95, 1e-8, 1)
     expect(INVALID, L.moe_adamw, t, 1e30, 1.0 - 1e-9, 0.95, 1e-8, 1)   # over 1 - beta1
     expect(INVALID, L.moe_adamw, decayed, 1e10, 0.9, 0.95, 1e-8, 100)
+
+
+def test_adamw_states_are_float_whatever_torch_makes_by_default():
+    try:
+        torch.set_default_dtype(torch.bfloat16)
+        p = [torch.zeros(300), torch.zeros(5, dtype=torch.float32)]
+        for bits in (8, 32):
+            m, v, scales, masters = L.adamw_states(p, bits, True)
+            L.adamw_list(p, [torch.zeros(300), torch.zeros(5)], m, v, scales, masters)
+    finally:
+        torch.set_default_dtype(torch.float32)
