@@ -537,7 +537,8 @@ moe_status_t moe_mx_gemm_k(const uint8_t* a_codes, const uint8_t* a_scales, int6
  *   topk_idx: the k largest c of the open groups, largest first.
  *   gate_j = scale * s_j, or with renormalize = 1 scale * s_j / sum of the chosen s.
  * The order is that of the exact values: without a bias c orders as the logits do, with one, and for the
- * groups, it is decided in double wherever fp32 does not tell.  Of equal values the lower index comes
+ * groups, it is decided in double wherever fp32 does not tell (two groups' sums that are equal as real numbers, not
+ * term by term, go by their roundings there).  Of equal values the lower index comes
  * first.  A NaN ranks after every number; whatever logits and bias hold, topk_idx has k different values
  * in [0, E), and the gates of a token with a NaN or +inf are unspecified.  A logit of -inf is a score of
  * 0; where every chosen score is 0 the gates are 0.  A bias of -inf shuts an expert: it is chosen only where the
